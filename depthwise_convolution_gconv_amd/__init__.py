@@ -1,5 +1,7 @@
 """Grouped-convolution forward engine for AMD Instinct MI355X (gfx950), with the
-backward of the (batch, steps, channels) depthwise conv1d.
+backward of the (batch, steps, channels) depthwise conv1d, and the sequence operators
+beside that conv in a mixing block: its causal form with a carried state, linear
+attention with a decay for each head, and RMS norm with the residual's addition.
 
 The compute runs in libgconv.so (hand-written HIP kernels behind the C ABI in
 include/gconv.h); this package is its Python binding.  Importing the package
@@ -31,4 +33,16 @@ from ._binding import (  # noqa: F401
     gconv_status_string,
     lib,
     lib_path,
+)
+from ._sequence import (  # noqa: F401
+    dwconv1d_causal,
+    dwconv1d_causal_backward,
+    dwconv1d_causal_step,
+    linear_attention,
+    linear_attention_backward,
+    linear_attention_step,
+    linear_attention_workspace,
+    rms_norm,
+    rms_norm_backward,
+    rms_norm_e4m3,
 )

@@ -1,0 +1,422 @@
+"""Sequence operators of libgconv.so: linear attention with a decay for each head, RMS
+norm with the residual's addition (16/32-bit or e4m3 output), and the causal depthwise
+conv1d that carries its state.
+
+Like the convolution binding: argument checks and marshalling only, on the caller's
+current device and stream, outputs and workspaces from torch.  Every function takes
+`stream` (default: the current stream).  With another stream than the current one, the
+call's outputs and workspace are recorded on it; its inputs are the caller's to keep.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from ._binding import (DTYPES, ERR_INVALID_ARG, ERR_SHAPE, GconvError, _check, _i32, _i64, _i64p, _vp, lib)
+
+ACTIVATIONS = {None: 0, "silu": 1}
+_f32 = ctypes.c_float
+_size = ctypes.c_size_t
+
+_fns = None
+
+
+def _library():
+    """The entry points with their argument types set."""
+    global _fns
+    if _fns is None:
+        L = lib()
+        sizep = ctypes.POINTER(_size)
+        for name, args in {
+            "gconv_linear_attention_workspace": [_i64p, _i32, _i32, sizep],
+            "gconv_linear_attention": [_vp] * 4 + [_i64p, _i64p, _vp, _f32] + [_vp] * 3 + [_i32, _vp, _size, _vp],
+            "gconv_linear_attention_backward": [_vp] * 7 + [_i64p, _i64p, _vp, _f32] + [_vp] * 4 + [_i32, _vp, _size, _vp],
+            "gconv_linear_attention_step": [_vp] * 5 + [_i64p, _i64p, _vp, _f32, _vp, _i32, _vp],
+            "gconv_rms_norm": [_vp] * 5 + [_i64, _i64, _i64p, _f32, _i32, _vp],
+            "gconv_rms_norm_e4m3": [_vp] * 6 + [_i64, _i64, _i64p, _f32, _i32, _i32, _vp],
+            "gconv_rms_norm_backward_workspace": [_i64, _i64, _i32, sizep],
+            "gconv_rms_norm_backward": [_vp] * 6 + [_i64, _i64, _i64p, _f32, _i32, _vp, _size, _vp],
+            "gconv_dw1d_causal": [_vp] * 7 + [_i64p, _i64p, _i32, _i32, _vp],
+            "gconv_dw1d_causal_backward_workspace": [_i64p, _i32, sizep],
+            "gconv_dw1d_causal_backward": [_vp] * 11 + [_i64p, _i64p, _i32, _i32, _vp, _size, _vp],
+            "gconv_dw1d_causal_step": [_vp] * 6 + [_i64p, _i64, _i32, _i32, _vp],
+        }.items():
+            fn = getattr(L, name)
+            fn.argtypes = args
+            fn.restype = _i32
+        _fns = L
+    return _fns
+
+
+_arrays = {n: _i64 * n for n in (1, 2, 3, 4, 6, 8, 12, 21)}
+
+
+def _bad(text: str, status: int = ERR_INVALID_ARG):
+    raise GconvError(status, text)
+
+
+def _dtype(name: str, t: torch.Tensor) -> int:
+    d = DTYPES.get(t.dtype)
+    if d is None:
+        _bad(f"{name}: unsupported dtype {t.dtype}")
+    if not t.is_cuda:
+        _bad(f"{name} must be a GPU tensor")
+    return d
+
+
+def _view(name: str, t: torch.Tensor, ref: torch.Tensor, shape) -> torch.Tensor:
+    """A tensor of ref's dtype and device whose last axis is contiguous."""
+    if t.dtype != ref.dtype or t.device != ref.device:
+        _bad(f"{name} must match the dtype and device of the other tensors")
+    if t.shape != shape:
+        _bad(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}", ERR_SHAPE)
+    if t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1:
+        _bad(f"{name}: the last axis must be contiguous")
+    return t
+
+
+def _whole(name: str, t: Optional[torch.Tensor], dtype, device, shape) -> int:
+    """Address of a contiguous tensor of that dtype, device and shape (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.device != device:
+        _bad(f"{name} must be a {dtype} tensor on {device}")
+    if t.shape != shape:
+        _bad(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}", ERR_SHAPE)
+    if not t.is_contiguous():
+        _bad(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+class _On:
+    """The device and stream a call runs on."""
+
+    __slots__ = ("device", "stream", "handle", "_guard")
+
+    def __init__(self, device: torch.device, stream):
+        self.device = device
+        self.stream = stream
+        self._guard = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.device.index:
+            self._guard = torch.cuda.device(self.device)
+            self._guard.__enter__()
+        self.handle = (self.stream if self.stream is not None else torch.cuda.current_stream()).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+    def made(self, *tensors):
+        """Tensors this call allocated: their memory is in use on the call's stream."""
+        if self.stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+def _workspace(need: int, device) -> Optional[torch.Tensor]:
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def _ptr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+# ---------------------------------------------------------------- linear attention
+
+def _attn_args(q, k, v, log_decay, lengths):
+    dt = _dtype("q", q)
+    if q.dim() != 4 or v.dim() != 4:
+        _bad("q and k must be [B, T, Hk, Dk], v [B, T, H, Dv]")
+    B, T, Hk, Dk = q.shape
+    H, Dv = v.shape[2], v.shape[3]
+    _view("q", q, q, q.shape)
+    _view("k", k, q, q.shape)
+    _view("v", v, q, (B, T, H, Dv))
+    g = _whole("log_decay", log_decay, torch.float32, q.device, (H,))
+    n = _whole("lengths", lengths, torch.int32, q.device, (B,))
+    return dt, (B, T, Hk, H, Dk, Dv), g, n
+
+
+def linear_attention_workspace(shape, dtype: torch.dtype, backward: bool = False) -> int:
+    """Workspace bytes of linear_attention (or its backward) for shape (B, T, Hk, H, Dk, Dv)."""
+    n = _size(0)
+    _check(_library().gconv_linear_attention_workspace(_arrays[6](*shape), DTYPES[dtype], int(backward),
+                                                       ctypes.byref(n)))
+    return n.value
+
+
+def linear_attention(q, k, v, log_decay, scale: Optional[float] = None, initial_state=None, lengths=None,
+                     return_state: bool = False, stream=None):
+    """Linear attention with a decay for each head over whole prompts.
+
+        S_t = exp(log_decay[h]) S_(t-1) + k_t v_t^T,   o_t = scale * q_t S_t
+
+    q, k [B, T, Hk, Dk], v [B, T, H, Dv] with H a multiple of Hk (each key head serves
+    H / Hk value heads), any strides but a contiguous last axis; log_decay fp32 [H];
+    scale defaults to Dk**-0.5.  initial_state: fp32 [B, H, Dk, Dv].  lengths: int32 [B],
+    the tokens of each sequence that exist; the outputs of the others are zero.
+    Returns o [B, T, H, Dv], or (o, state) with the fp32 state after each sequence's last
+    token, which linear_attention_step carries on from."""
+    dt, shape, g, n = _attn_args(q, k, v, log_decay, lengths)
+    B, T, Hk, H, Dk, Dv = shape
+    dev = q.device
+    s0 = _whole("initial_state", initial_state, torch.float32, dev, (B, H, Dk, Dv))
+    sh = _arrays[6](*shape)
+    need = _size(0)
+    L = _library()
+    _check(L.gconv_linear_attention_workspace(sh, dt, 0, ctypes.byref(need)))
+    with _On(dev, stream) as on:
+        o = torch.empty((B, T, H, Dv), dtype=q.dtype, device=dev)
+        st = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if return_state else None
+        ws = _workspace(need.value, dev)
+        on.made(o, st, ws)
+        _check(L.gconv_linear_attention(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), sh,
+            _arrays[12](*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *o.stride()[:3]), g,
+            Dk ** -0.5 if scale is None else scale, s0, _ptr(st), n, dt, _ptr(ws), need.value, on.handle))
+    return (o, st) if return_state else o
+
+
+def linear_attention_backward(q, k, v, log_decay, do, scale: Optional[float] = None, initial_state=None,
+                              lengths=None, dstate=None, stream=None):
+    """(dq, dk, dv, dinitial) of linear_attention from the gradients `do` of its output and
+    `dstate` (fp32, or None: zero) of its final state.  dinitial is None without an
+    initial_state.  log_decay is a constant: it gets no gradient."""
+    dt, shape, g, n = _attn_args(q, k, v, log_decay, lengths)
+    B, T, Hk, H, Dk, Dv = shape
+    dev = q.device
+    _view("do", do, q, (B, T, H, Dv))
+    s0 = _whole("initial_state", initial_state, torch.float32, dev, (B, H, Dk, Dv))
+    sf = _whole("dstate", dstate, torch.float32, dev, (B, H, Dk, Dv))
+    sh = _arrays[6](*shape)
+    need = _size(0)
+    L = _library()
+    _check(L.gconv_linear_attention_workspace(sh, dt, 1, ctypes.byref(need)))
+    with _On(dev, stream) as on:
+        dq = torch.empty((B, T, Hk, Dk), dtype=q.dtype, device=dev)
+        dk = torch.empty((B, T, Hk, Dk), dtype=q.dtype, device=dev)
+        dv = torch.empty((B, T, H, Dv), dtype=q.dtype, device=dev)
+        ds = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if initial_state is not None else None
+        ws = _workspace(need.value, dev)
+        on.made(dq, dk, dv, ds, ws)
+        _check(L.gconv_linear_attention_backward(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), sh,
+            _arrays[21](*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *do.stride()[:3], *dq.stride()[:3],
+                        *dk.stride()[:3], *dv.stride()[:3]), g, Dk ** -0.5 if scale is None else scale, s0, sf,
+            _ptr(ds), n, dt, _ptr(ws), need.value, on.handle))
+    return dq, dk, dv, ds
+
+
+def linear_attention_step(q, k, v, log_decay, state, scale: Optional[float] = None, slots=None, stream=None):
+    """The next token of each sequence: q, k [B, Hk, Dk], v [B, H, Dv]; state fp32
+    [n, H, Dk, Dv] is updated in place.  slots: int32 [B], the row of `state` that each
+    sequence owns, each row at most once (default: row b); a slot outside [0, n) leaves
+    the pool alone and gives a zero output.  Returns o [B, H, Dv]."""
+    dt = _dtype("q", q)
+    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+        _bad("q and k must be [B, Hk, Dk], v [B, H, Dv], state [n, H, Dk, Dv]")
+    B, Hk, Dk = q.shape
+    H, Dv = v.shape[1], v.shape[2]
+    dev = q.device
+    _view("q", q, q, q.shape)
+    _view("k", k, q, q.shape)
+    _view("v", v, q, (B, H, Dv))
+    g = _whole("log_decay", log_decay, torch.float32, dev, (H,))
+    sp = _whole("state", state, torch.float32, dev, (state.shape[0], H, Dk, Dv))
+    sl = _whole("slots", slots, torch.int32, dev, (B,))
+    with _On(dev, stream) as on:
+        o = torch.empty((B, H, Dv), dtype=q.dtype, device=dev)
+        on.made(o)
+        _check(_library().gconv_linear_attention_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), sp, _arrays[6](B, Hk, H, Dk, Dv, state.shape[0]),
+            _arrays[8](*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2]), g,
+            Dk ** -0.5 if scale is None else scale, sl, dt, on.handle))
+    return o
+
+
+# ---------------------------------------------------------------- RMS norm
+
+def _rows(name: str, t: torch.Tensor, ref: torch.Tensor) -> int:
+    """The one stride that leads from row to row of t's last axis."""
+    _view(name, t, ref, ref.shape)
+    if t.dim() == 2:
+        return t.stride(0)
+    if t.dim() == 1 or t.numel() == 0 or t.is_contiguous():
+        return t.shape[-1]
+    step = None          # from the last row axis on: each longer axis goes on where the shorter ones end
+    for n, s in reversed(list(zip(t.shape[:-1], t.stride()[:-1]))):
+        if n == 1:
+            continue
+        if step is None:
+            row = step = s
+        elif s != step:
+            _bad(f"{name}: its rows must lie at one stride")
+        step = s * n
+    return t.shape[-1] if step is None else row
+
+
+def _norm(x, weight, residual, eps, q8, block, stream):
+    dt = _dtype("x", x)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        _bad("x must be [..., C] with C >= 1")
+    C = x.shape[-1]
+    rows = x.numel() // C
+    dev = x.device
+    with _On(dev, stream) as on:
+        xs = _rows("x", x, x)
+        w = _whole("weight", weight, x.dtype, dev, (C,))
+        if not w:
+            _bad("weight is needed")
+        if residual is not None:
+            rs = _rows("residual", residual, x)
+            h = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        else:
+            rs, h = 0, None
+        L = _library()
+        if not q8:
+            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            on.made(y, h)
+            _check(L.gconv_rms_norm(x.data_ptr(), _ptr(residual), w, y.data_ptr(), _ptr(h), rows, C, _arrays[2](xs, rs), eps,
+                                    dt, on.handle))
+            return y, h
+        y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+        nb = -(-C // block) if block > 0 else 1
+        scales = torch.empty((*x.shape[:-1], nb), dtype=torch.float32, device=dev)
+        on.made(y, scales, h)
+        _check(L.gconv_rms_norm_e4m3(x.data_ptr(), _ptr(residual), w, y.data_ptr(), scales.data_ptr(), _ptr(h), rows, C,
+                                     _arrays[2](xs, rs), eps, block, dt, on.handle))
+        return y, scales, h
+
+
+def rms_norm(x, weight, residual=None, eps: float = 1e-6, stream=None):
+    """y = weight * h / sqrt(mean(h^2) + eps) over the last axis of x [..., C], where h is x,
+    or x + residual rounded to the dtype.  Returns y, or (y, h) with a residual."""
+    y, h = _norm(x, weight, residual, eps, False, 0, stream)
+    return y if residual is None else (y, h)
+
+
+def rms_norm_e4m3(x, weight, residual=None, eps: float = 1e-6, block: int = 0, stream=None):
+    """rms_norm with its output as e4m3 values q (float8_e4m3fn [..., C]) and fp32 scales,
+    y = q * scale: one scale for a row (block 0, scales [..., 1]) or for each `block`
+    columns (32, 64, 128 or 256; scales [..., ceil(C / block)]).
+    Returns (q, scales), or (q, scales, h) with a residual."""
+    y, scales, h = _norm(x, weight, residual, eps, True, int(block), stream)
+    return (y, scales) if residual is None else (y, scales, h)
+
+
+def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, stream=None):
+    """(dx, dw) of rms_norm: dx is the gradient of x and of residual alike, from the gradient
+    dy of y, the normed rows h (x itself without a residual) and the gradient dh of the h
+    output (or None)."""
+    dt = _dtype("h", h)
+    if h.dim() < 1 or h.shape[-1] < 1:
+        _bad("h must be [..., C] with C >= 1")
+    C = h.shape[-1]
+    rows = h.numel() // C
+    dev = h.device
+    L = _library()
+    need = _size(0)
+    _check(L.gconv_rms_norm_backward_workspace(rows, C, dt, ctypes.byref(need)))
+    with _On(dev, stream) as on:
+        w = _whole("weight", weight, h.dtype, dev, (C,))
+        if not w:
+            _bad("weight is needed")
+        ys, hs = _rows("dy", dy, h), _rows("h", h, h)
+        es = _rows("dh", dh, h) if dh is not None else 0
+        dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
+        dw = torch.empty((C,), dtype=h.dtype, device=dev)
+        ws = _workspace(need.value, dev)
+        on.made(dx, dw, ws)
+        _check(L.gconv_rms_norm_backward(dy.data_ptr(), h.data_ptr(), w, _ptr(dh), dx.data_ptr(), dw.data_ptr(), rows,
+                                         C, _arrays[3](ys, hs, es), eps, dt, _ptr(ws), need.value, on.handle))
+    return dx, dw
+
+
+# ---------------------------------------------------------------- causal depthwise conv1d
+
+def _conv_args(x, weight, bias, activation, dims):
+    dt = _dtype("x", x)
+    if x.dim() != dims or weight.dim() != 3:
+        _bad(f"x must be {dims}-D with channels last and weight [C, 1, K]")
+    C, K = x.shape[-1], weight.shape[2]
+    if activation not in ACTIVATIONS:
+        _bad(f"unknown activation {activation!r}")
+    _view("x", x, x, x.shape)
+    w = _whole("weight", weight, x.dtype, x.device, (C, 1, K))
+    b = _whole("bias", bias, x.dtype, x.device, (C,))
+    return dt, C, K, w, b, ACTIVATIONS[activation]
+
+
+def dwconv1d_causal(x, weight, bias=None, activation: Optional[str] = None, initial_state=None, lengths=None,
+                    return_state: bool = False, stream=None):
+    """Causal depthwise conv1d over x [B, T, C] (any strides, channels contiguous) with weight
+    [C, 1, K]: y[t] = act(bias + sum_k weight[k] * xs[t - (K-1) + k]), where the K-1 inputs
+    before the first token come from initial_state [B, K-1, C] (default: zeros).
+    activation: None or "silu".  lengths: int32 [B]; the outputs past them are zero.
+    Returns y, or (y, state) with the last K-1 inputs of each sequence, which
+    dwconv1d_causal_step carries on from."""
+    dt, C, K, w, b, act = _conv_args(x, weight, bias, activation, 3)
+    B, T, _ = x.shape
+    dev = x.device
+    s0 = _whole("initial_state", initial_state, x.dtype, dev, (B, K - 1, C))
+    n = _whole("lengths", lengths, torch.int32, dev, (B,))
+    with _On(dev, stream) as on:
+        y = torch.empty((B, T, C), dtype=x.dtype, device=dev)
+        st = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if return_state else None
+        on.made(y, st)
+        _check(_library().gconv_dw1d_causal(x.data_ptr(), w, b, y.data_ptr(), s0, _ptr(st), n, _arrays[4](B, T, C, K),
+                                            _arrays[2](*x.stride()[:2]), act, dt, on.handle))
+    return (y, st) if return_state else y
+
+
+def dwconv1d_causal_backward(x, weight, bias, dy, activation: Optional[str] = None, initial_state=None, lengths=None,
+                             dstate=None, stream=None):
+    """(dx, dw, db, dinitial) of dwconv1d_causal from the gradients dy of its output and
+    dstate (or None: zero) of its final state.  db is None without a bias, dinitial
+    without an initial_state."""
+    dt, C, K, w, b, act = _conv_args(x, weight, bias, activation, 3)
+    B, T, _ = x.shape
+    dev = x.device
+    _view("dy", dy, x, x.shape)
+    s0 = _whole("initial_state", initial_state, x.dtype, dev, (B, K - 1, C))
+    sf = _whole("dstate", dstate, x.dtype, dev, (B, K - 1, C))
+    n = _whole("lengths", lengths, torch.int32, dev, (B,))
+    L = _library()
+    sh = _arrays[4](B, T, C, K)
+    need = _size(0)
+    _check(L.gconv_dw1d_causal_backward_workspace(sh, dt, ctypes.byref(need)))
+    with _On(dev, stream) as on:
+        dx = torch.empty((B, T, C), dtype=x.dtype, device=dev)
+        dw = torch.empty((C, 1, K), dtype=x.dtype, device=dev)
+        db = torch.empty((C,), dtype=x.dtype, device=dev) if bias is not None else None
+        ds = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if initial_state is not None else None
+        ws = _workspace(need.value, dev)
+        on.made(dx, dw, db, ds, ws)
+        _check(L.gconv_dw1d_causal_backward(x.data_ptr(), w, b, dy.data_ptr(), s0, sf, dx.data_ptr(), dw.data_ptr(),
+                                            _ptr(db), _ptr(ds), n, sh, _arrays[4](*x.stride()[:2], *dy.stride()[:2]),
+                                            act, dt, _ptr(ws), need.value, on.handle))
+    return dx, dw, db, ds
+
+
+def dwconv1d_causal_step(x, weight, bias, state, activation: Optional[str] = None, slots=None, stream=None):
+    """The next token of each sequence: x [B, C]; state [n, K-1, C] moves up by one row in
+    place.  slots as for linear_attention_step.  Returns y [B, C]."""
+    dt, C, K, w, b, act = _conv_args(x, weight, bias, activation, 2)
+    B = x.shape[0]
+    dev = x.device
+    if state.dim() != 3:
+        _bad("state must be [n, K-1, C]")
+    sp = _whole("state", state, x.dtype, dev, (state.shape[0], K - 1, C))
+    sl = _whole("slots", slots, torch.int32, dev, (B,))
+    with _On(dev, stream) as on:
+        y = torch.empty((B, C), dtype=x.dtype, device=dev)
+        on.made(y)
+        _check(_library().gconv_dw1d_causal_step(x.data_ptr(), w, b, sp, y.data_ptr(), sl,
+                                                 _arrays[4](B, C, K, state.shape[0]), x.stride(0), act, dt, on.handle))
+    return y

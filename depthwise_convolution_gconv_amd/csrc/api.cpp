@@ -13,6 +13,7 @@
 
 #include "common.hpp"
 #include "gconv.h"
+#include "seq.hpp"
 
 namespace {
 
@@ -309,6 +310,9 @@ gconv::Dw1dArgs dw1d_args(const Geometry &g, const void *w, gconv_dtype_t dtype,
 }
 
 }  // namespace
+
+void gconv::set_last_error(const char *text) { std::snprintf(g_last_error, sizeof(g_last_error), "%s", text); }
+void gconv::set_last_kernel(const char *name) { g_last_kernel = name; }
 
 extern "C" {
 

@@ -1,0 +1,519 @@
+// dw1d_causal.hip -- causal depthwise conv1d over (batch, steps, channels) that carries
+// its state: prompts, gradients and single tokens.
+//
+//     z[b,t,c] = bias[c] + sum_k w[c,0,k] xs[b, t-(K-1)+k, c],   y = z or z / (1 + exp(-z))
+//
+// where xs[b, -1 .. -(K-1)] are the K-1 inputs before the first token (the state, or
+// zeros).  The state after n tokens is xs[b, n-(K-1) .. n-1].  Tokens from lengths[b] on
+// are padding: their y is zero, and neither the state nor a gradient depends on them.
+//
+// causal_run<T, K>: K <= 4.  Lanes run along channels in 16-byte loads, a thread slides
+//   its K taps down kRun tokens in registers.  Bound by HBM.
+// causal_tile<T>: any K <= 64.  64 channels x 64 tokens and the K-1 inputs before them in
+//   LDS as fp32; a thread takes 16 tokens of a channel and goes through the taps 4 at a
+//   time, so 19 LDS reads feed 64 multiplications.
+// causal_bwd_tile<T, NT>: one tile of the gradients: z is computed again, dz = dy act'(z)
+//   goes to LDS with the K-1 rows behind the tile, then dx is the correlation of dz with
+//   the reversed taps and dw, db are the tile's sums, which a second kernel adds over the
+//   tiles in a fixed order.
+// causal_step<T>: one token; the state moves up by one row in place.
+#include <algorithm>
+
+#include "seq.hpp"
+#include "vecio.hpp"
+
+namespace gconv {
+namespace {
+
+constexpr int kThreads = 256;
+
+// z / (1 + exp(-z)): fp32 tensors take the library's exponential, 16-bit ones the
+// hardware's (relative error 2^-21 at |z| = 8, far below half a step of either).
+template <typename T> __device__ __forceinline__ float silu(float z)
+{
+    if constexpr (sizeof(T) == 4) return z / (1.0f + expf(-z));
+    else return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+
+// d silu(z) / dz
+template <typename T> __device__ __forceinline__ float silu_grad(float z)
+{
+    const float s = sizeof(T) == 4 ? 1.0f / (1.0f + expf(-z)) : __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+    return s * (1.0f + z * (1.0f - s));
+}
+
+__device__ __forceinline__ int seq_len(const int32_t *lengths, int64_t b, int64_t T)
+{
+    if (!lengths) return (int)T;
+    const int n = lengths[b];
+    return n < 0 ? 0 : n > T ? (int)T : n;
+}
+
+// Pointer to xs[b, t, c] (t >= -(K-1)): an input, a state row, or nullptr for a zero.
+template <typename T>
+__device__ __forceinline__ const T *xs_at(const CausalArgs &a, int64_t b, int64_t t, int64_t c)
+{
+    if (t >= 0) return (const T *)a.x + b * a.xsb + t * a.xst + c;
+    return a.s0 ? (const T *)a.s0 + (b * (a.K - 1) + t + a.K - 1) * a.C + c : nullptr;
+}
+
+constexpr int kRun = 16;    // tokens for each thread of causal_run
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads)
+causal_run(const CausalArgs a, int cx, int cblocks, int tblocks)
+{
+    constexpr int VE = 16 / sizeof(T);
+    const int ty = threadIdx.x / cx;                       // cx channel runs by 256 / cx token runs
+    int64_t id = blockIdx.x;
+    const int cb = (int)(id % cblocks);
+    id /= cblocks;
+    const int tb = (int)(id % tblocks);
+    const int64_t b = id / tblocks;
+    const int64_t c = ((int64_t)cb * cx + threadIdx.x % cx) * VE;
+    const int t0 = (tb * (kThreads / cx) + ty) * kRun, T_in = (int)a.T;
+    if (c >= a.C) return;
+    const int left = (int)min(a.C - c, (int64_t)VE), n = seq_len(a.lengths, b, a.T);
+
+    if (t0 == 0 && a.sf) {   // the state after the sequence
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            const T *src = xs_at<T>(a, b, (int64_t)n - (K - 1) + j, c);
+            const Run<T, VE> r = load_raw<T, VE>(src, src ? left : 0);
+            store_raw<T, VE>((T *)a.sf + (b * (K - 1) + j) * a.C + c, left, r);
+        }
+    }
+    if (t0 >= T_in) return;
+    float w[VE * K], z0[VE];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        float f[VE];
+        load_run<T, VE>((const T *)a.w + c * K + j * VE, left * K - j * VE, f);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) w[j * VE + e] = f[e];
+    }
+    load_run<T, VE>((const T *)a.bias + c, a.bias ? left : 0, z0);
+
+    float win[K][VE];        // xs of the K tokens up to the current one
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+        const T *src = xs_at<T>(a, b, (int64_t)t0 - (K - 1) + j, c);
+        load_run<T, VE>(src, src ? left : 0, win[j]);
+    }
+    const T *xp = (const T *)a.x + b * a.xsb + (int64_t)t0 * a.xst + c;
+    T *yp = (T *)a.y + (b * a.T + t0) * a.C + c;
+    constexpr int U = 8;     // rows in flight
+#pragma unroll
+    for (int t1 = 0; t1 < kRun; t1 += U) {
+        Run<T, VE> xr[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) xr[u] = load_raw<T, VE>(xp + (int64_t)(t1 + u) * a.xst, t0 + t1 + u < T_in ? left : 0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t1 + u;
+            float y[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                win[K - 1][e] = to_f32(xr[u].v[e]);
+                float z = z0[e];
+#pragma unroll
+                for (int j = 0; j < K; ++j) z = fmaf(w[e * K + j], win[j][e], z);
+                y[e] = t0 + t < n ? (a.silu ? silu<T>(z) : z) : 0.0f;
+            }
+            if (t0 + t < T_in) store_run<T, VE>(yp + (int64_t)t * a.C, left, y);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) win[j][e] = win[j + 1][e];
+        }
+    }
+}
+
+constexpr int kCT = 64;     // channels of a tile (lanes)
+constexpr int kTT = 64;     // tokens of a tile
+constexpr int kWaves = kThreads / 64;
+
+// out[r] = bias + sum_k w[k] xs[row0 + r + k] for R rows of the staged inputs (stride kCT).
+// Taps go 4 at a time through a register window of R + 3 rows; REV reads them from the end.
+template <int R, bool REV>
+__device__ __forceinline__ void taps(const float *xs, const float *ws, int K, int lane, float (&acc)[R])
+{
+    int k = 0;
+    for (; k + 4 <= K; k += 4) {
+        float x[R + 3], w[4];
+#pragma unroll
+        for (int i = 0; i < R + 3; ++i) x[i] = xs[(k + i) * kCT + lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = ws[(REV ? K - 1 - k - i : k + i) * kCT + lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[r] = fmaf(x[r + i], w[i], acc[r]);
+    }
+    for (; k < K; ++k) {
+        const float w = ws[(REV ? K - 1 - k : k) * kCT + lane];
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r] = fmaf(xs[(k + r) * kCT + lane], w, acc[r]);
+    }
+}
+
+// Stages `rows` rows of 64 channels from row(r) (nullptr: zeros) as fp32.  T elements go in
+// runs of VE; UN runs of a thread are in flight together.
+template <typename T, typename F>
+__device__ __forceinline__ void stage(float *dst, int rows, int64_t c0, int64_t C, F row)
+{
+    constexpr int VE = 16 / sizeof(T), PR = kCT / VE, UN = 4;
+    for (int base = 0; base < rows * PR; base += UN * kThreads) {
+        Run<T, VE> v[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int i = base + u * kThreads + (int)threadIdx.x, r = i / PR;
+            const int64_t c = c0 + i % PR * VE;
+            const T *src = i < rows * PR ? row(r) : nullptr;
+            v[u] = load_raw<T, VE>(src + c, src ? (int)max((int64_t)0, min(C - c, (int64_t)VE)) : 0);
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int i = base + u * kThreads + (int)threadIdx.x;
+            if (i < rows * PR) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) dst[i / PR * kCT + i % PR * VE + e] = to_f32(v[u].v[e]);
+            }
+        }
+    }
+}
+
+// Filters of 64 channels as [K][64].
+template <typename T>
+__device__ __forceinline__ void stage_taps(float *ws, const CausalArgs &a, int64_t c0)
+{
+    const int K = (int)a.K, total = (int)min(a.C - c0, (int64_t)kCT) * K;
+    for (int i = threadIdx.x; i < kCT * K; i += kThreads) {
+        const int c = i / K;
+        ws[(i - c * K) * kCT + c] = i < total ? to_f32(((const T *)a.w)[c0 * K + i]) : 0.0f;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+causal_tile(const CausalArgs a, int cblocks, int tblocks)
+{
+    constexpr int R = kTT / kWaves;
+    extern __shared__ float sm[];
+    const int K = (int)a.K, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float *xs = sm, *ws = sm + (kTT + K - 1) * kCT;
+    int64_t id = blockIdx.x;
+    const int64_t c0 = id % cblocks * kCT;
+    id /= cblocks;
+    const int t0 = (int)(id % tblocks) * kTT, T_in = (int)a.T;
+    const int64_t b = id / tblocks, c = c0 + lane;
+    const int n = seq_len(a.lengths, b, a.T);
+    stage<T>(xs, kTT + K - 1, c0, a.C, [&](int r) -> const T * {
+        const int t = t0 - (K - 1) + r;
+        return t < n ? xs_at<T>(a, b, t, 0) : nullptr;
+    });
+    stage_taps<T>(ws, a, c0);
+    __syncthreads();
+    if (t0 == 0 && a.sf && c < a.C)
+        for (int j = wave; j < K - 1; j += kWaves) {
+            const T *src = xs_at<T>(a, b, (int64_t)n - (K - 1) + j, c);
+            ((T *)a.sf)[(b * (K - 1) + j) * a.C + c] = src ? *src : (T)0.0f;
+        }
+    if (c >= a.C) return;
+    const float b0 = a.bias ? to_f32(((const T *)a.bias)[c]) : 0.0f;
+    float acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[r] = b0;
+    taps<R, false>(xs + wave * R * kCT, ws, K, lane, acc);
+    T *yp = (T *)a.y + (b * a.T + t0 + wave * R) * a.C + c;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int t = t0 + wave * R + r;
+        if (t < T_in) store_nt(yp + (int64_t)r * a.C, from_f32<T>(t < n ? (a.silu ? silu<T>(acc[r]) : acc[r]) : 0.0f));
+    }
+}
+
+// Tile of rows s0 .. s0 + 63 of the inputs with their state (s = -(K-1) .. T-1).
+// NT: taps for each wave (K <= 4 NT).
+template <typename T, int NT>
+__global__ void __launch_bounds__(kThreads)
+causal_bwd_tile(const CausalArgs a, int cblocks, int tblocks)
+{
+    constexpr int R = 8, NX = kTT + (NT == 1 ? 12 : 8 * NT), ND = kTT + 4 * NT;
+    __shared__ float xs[NX * kCT];        // x at s0 - (K-1) ..
+    __shared__ float dz[ND * kCT];        // dz at s0 ..
+    __shared__ float ws[4 * NT * kCT];
+    const int K = (int)a.K, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int64_t id = blockIdx.x;
+    const int64_t c0 = id % cblocks * kCT;
+    id /= cblocks;
+    const int tb = (int)(id % tblocks), s0 = tb * kTT - (a.s0 ? K - 1 : 0);
+    const int64_t b = id / tblocks, c = c0 + lane;
+    const int n = seq_len(a.lengths, b, a.T), rows_dz = kTT + K - 1;
+    const bool cok = c < a.C;
+
+    // Rows past what the tile needs are zeroed: the weight sums read them beside zero dz.
+    stage<T>(xs, NX, c0, a.C, [&](int r) -> const T * {
+        const int t = s0 - (K - 1) + r;
+        return t < n && t >= -(K - 1) ? xs_at<T>(a, b, t, 0) : nullptr;
+    });
+    stage<T>(dz, ND, c0, a.C, [&](int r) -> const T * {
+        const int t = s0 + r;
+        return t >= 0 && t < n && r < rows_dz ? (const T *)a.dy + b * a.dysb + (int64_t)t * a.dyst : nullptr;
+    });
+    stage_taps<T>(ws, a, c0);
+    __syncthreads();
+
+    if (a.silu) {   // dz = dy silu'(z), each element by the thread that reads it here
+        const float b0 = a.bias && cok ? to_f32(((const T *)a.bias)[c]) : 0.0f;
+        for (int r0 = wave * R; r0 < rows_dz; r0 += kWaves * R) {
+            float z[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) z[r] = b0;
+            taps<R, false>(xs + r0 * kCT, ws, K, lane, z);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int t = s0 + r0 + r;
+                if (r0 + r < rows_dz && t >= 0 && t < n) dz[(r0 + r) * kCT + lane] *= silu_grad<T>(z[r]);
+            }
+        }
+        __syncthreads();
+    }
+
+    // dx[s] = sum_j dz[s + j] w[K-1-j], and the gradient of the final state's inputs.
+    for (int r0 = wave * R; r0 < kTT; r0 += kWaves * R) {
+        float acc[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r] = 0.0f;
+        taps<R, true>(dz + r0 * kCT, ws, K, lane, acc);
+        if (!cok) continue;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int s = s0 + r0 + r;
+            if (s >= a.T) continue;
+            float v = s < n ? acc[r] : 0.0f;
+            if (a.dsf && s < n && s >= n - (K - 1))
+                v += to_f32(((const T *)a.dsf)[(b * (K - 1) + s - n + K - 1) * a.C + c]);
+            if (s >= 0) ((T *)a.dx)[(b * a.T + s) * a.C + c] = from_f32<T>(v);
+            else if (a.ds0) ((T *)a.ds0)[(b * (K - 1) + s + K - 1) * a.C + c] = from_f32<T>(v);
+        }
+    }
+
+    // dw[k] = sum over the tile's tokens of dz[t] xs[t-(K-1)+k]: wave g takes the taps from
+    // g NT on and slides a window of NT inputs down the tile.  Row i of xs is input
+    // s0 - (K-1) + i, so token s0 + i meets tap k at row i + k.
+    float acc[NT], accb = 0.0f, win[NT];
+    const float *xr = xs + wave * NT * kCT + lane;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        acc[j] = 0.0f;
+        win[j] = xr[j * kCT];
+    }
+    for (int t = 0; t < kTT; t += NT) {
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            const float d = dz[(t + u) * kCT + lane];   // zero outside [0, n)
+            accb += d;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[j] = fmaf(d, win[(j + u) % NT], acc[j]);
+            win[u] = xr[(t + u + NT) * kCT];
+        }
+    }
+    if (!cok) return;
+    float *pt = a.ws + (b * tblocks + tb) * (int64_t)(K + 1) * a.C + c;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+        if (wave * NT + j < K) pt[(int64_t)(wave * NT + j) * a.C] = acc[j];
+    if (wave == 0) pt[(int64_t)K * a.C] = accb;
+}
+
+// dw[c,0,k] and db[c] from the tiles' sums: 64 columns of the (K+1) x C sums and 16 slices
+// of the tiles for each workgroup, added in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(1024)
+causal_bwd_reduce(const float *__restrict__ ws, T *__restrict__ dw, T *__restrict__ db, int64_t tiles, int64_t C, int K)
+{
+    __shared__ float part[16][64];
+    const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+    const int64_t cols = (K + 1) * C, x = (int64_t)blockIdx.x * 64 + lane;
+    float s = 0.0f;
+    if (x < cols) {
+        int64_t g = slice;
+        for (; g + 48 < tiles; g += 64) {
+            const float v0 = ws[g * cols + x], v1 = ws[(g + 16) * cols + x];
+            const float v2 = ws[(g + 32) * cols + x], v3 = ws[(g + 48) * cols + x];
+            s += (v0 + v1) + (v2 + v3);
+        }
+        for (; g < tiles; g += 16) s += ws[g * cols + x];
+    }
+    part[slice][lane] = s;
+    __syncthreads();
+    if (slice != 0 || x >= cols) return;
+    for (int i = 1; i < 16; ++i) s += part[i][lane];
+    const int64_t k = x / C, c = x - k * C;
+    if (k < K) dw[c * K + k] = from_f32<T>(s);
+    else if (db) db[c] = from_f32<T>(s);
+}
+
+// One token for each sequence: 4 channels for each thread.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+causal_step(const CausalStepArgs a, int cblocks)
+{
+    constexpr int VE = 4;
+    const int64_t b = blockIdx.x / cblocks;
+    const int64_t c = ((int64_t)(blockIdx.x % cblocks) * kThreads + threadIdx.x) * VE;
+    if (c >= a.C) return;
+    const int left = (int)min(a.C - c, (int64_t)VE), K = (int)a.K;
+    const int64_t slot = a.slots ? a.slots[b] : b;
+    T *yp = (T *)a.y + b * a.C + c;
+    float x[VE], z[VE];
+    if (slot < 0 || slot >= a.n) {   // no state: nothing to update, the token's output is zero
+#pragma unroll
+        for (int e = 0; e < VE; ++e) z[e] = 0.0f;
+        store_run<T, VE>(yp, left, z);
+        return;
+    }
+    T *sp = (T *)a.state + slot * (K - 1) * a.C + c;
+    const T *wp = (const T *)a.w + c * K;
+    load_run<T, VE>((const T *)a.x + b * a.xsb + c, left, x);
+    load_run<T, VE>((const T *)a.bias + c, a.bias ? left : 0, z);
+    constexpr int U = 4;     // state rows in flight
+    for (int j0 = 0; j0 < K; j0 += U) {
+        Run<T, VE> row[U];
+        float w[U][VE];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u;
+            row[u] = load_raw<T, VE>(sp + (int64_t)j * a.C, j < K - 1 ? left : 0);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) w[u][e] = j < K && e < left ? to_f32(wp[e * K + j]) : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u;
+            if (j >= K) continue;
+            if (j == K - 1) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) row[u].v[e] = from_f32<T>(x[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < VE; ++e) z[e] = fmaf(w[u][e], to_f32(row[u].v[e]), z[e]);
+            if (j > 0) store_raw<T, VE>(sp + (int64_t)(j - 1) * a.C, left, row[u]);
+        }
+    }
+    if (a.silu) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) z[e] = silu<T>(z[e]);
+    }
+    store_run<T, VE>(yp, left, z);
+}
+
+template <typename T, int K> hipError_t run_short(const CausalArgs &a)
+{
+    constexpr int VE = 16 / sizeof(T);
+    const int64_t runs = ceil_div(a.C, VE);
+    int cx = 8;
+    while (cx < kThreads && cx < runs) cx *= 2;
+    const int64_t cblocks = ceil_div(runs, cx);
+    const int64_t tblocks = std::max<int64_t>(1, ceil_div(a.T, (int64_t)(kThreads / cx) * kRun));
+    const int64_t blocks = a.B * cblocks * tblocks;
+    if (blocks > kGridMax) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((causal_run<T, K>), dim3((unsigned)blocks), dim3(kThreads), 0, a.stream, a, cx, (int)cblocks,
+                       (int)tblocks);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t run_fwd(const CausalArgs &a, const char **kname)
+{
+    *kname = "causal_run";
+    switch (a.K) {
+    case 1: return run_short<T, 1>(a);
+    case 2: return run_short<T, 2>(a);
+    case 3: return run_short<T, 3>(a);
+    case 4: return run_short<T, 4>(a);
+    default: break;
+    }
+    *kname = "causal_tile";
+    const int64_t cblocks = ceil_div(a.C, kCT), tblocks = std::max<int64_t>(1, ceil_div(a.T, kTT));
+    const int64_t blocks = a.B * cblocks * tblocks;
+    if (blocks > kGridMax) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((causal_tile<T>), dim3((unsigned)blocks), dim3(kThreads),
+                       (unsigned)((kTT + 2 * a.K - 1) * kCT * sizeof(float)), a.stream, a, (int)cblocks, (int)tblocks);
+    return hipGetLastError();
+}
+
+template <typename T, int NT> hipError_t run_bwd_tile(const CausalArgs &a, int64_t blocks, int64_t cblocks, int64_t tblocks)
+{
+    hipLaunchKernelGGL((causal_bwd_tile<T, NT>), dim3((unsigned)blocks), dim3(kThreads), 0, a.stream, a, (int)cblocks,
+                       (int)tblocks);
+    return hipGetLastError();
+}
+
+// Tiles along the sequence: its tokens and, for the state's gradient, the K-1 before them.
+int64_t bwd_tblocks(int64_t T, int64_t K) { return ceil_div(T + K - 1, kTT); }
+
+template <typename T> hipError_t run_bwd(const CausalArgs &a, const char **kname)
+{
+    *kname = "causal_bwd_tile";
+    const int64_t cblocks = ceil_div(a.C, kCT), tblocks = a.s0 ? bwd_tblocks(a.T, a.K) : ceil_div(a.T, kTT);
+    const int64_t tiles = a.B * tblocks, blocks = tiles * cblocks;
+    if (blocks > kGridMax) return hipErrorInvalidValue;
+    hipError_t err = hipSuccess;
+    if (blocks > 0) {
+        if (a.K <= 4) err = run_bwd_tile<T, 1>(a, blocks, cblocks, tblocks);
+        else if (a.K <= 8) err = run_bwd_tile<T, 2>(a, blocks, cblocks, tblocks);
+        else if (a.K <= 16) err = run_bwd_tile<T, 4>(a, blocks, cblocks, tblocks);
+        else if (a.K <= 32) err = run_bwd_tile<T, 8>(a, blocks, cblocks, tblocks);
+        else err = run_bwd_tile<T, 16>(a, blocks, cblocks, tblocks);
+    }
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL((causal_bwd_reduce<T>), dim3((unsigned)ceil_div((a.K + 1) * a.C, 64)), dim3(1024), 0, a.stream,
+                       a.ws, (T *)a.dw, (T *)a.db, tiles, a.C, (int)a.K);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t run_step(const CausalStepArgs &a)
+{
+    const int64_t cblocks = ceil_div(a.C, kThreads * 4), blocks = a.B * cblocks;
+    if (blocks > kGridMax) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((causal_step<T>), dim3((unsigned)blocks), dim3(kThreads), 0, a.stream, a, (int)cblocks);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_causal(const CausalArgs &a, const char **kname)
+{
+    switch (a.dtype) {
+    case DT_F32: return run_fwd<float>(a, kname);
+    case DT_F16: return run_fwd<_Float16>(a, kname);
+    default: return run_fwd<__bf16>(a, kname);
+    }
+}
+
+size_t causal_bwd_workspace(int64_t B, int64_t T, int64_t C, int64_t K)
+{
+    return sizeof(float) * (size_t)(B * bwd_tblocks(T, K) * (K + 1) * C);
+}
+
+hipError_t launch_causal_bwd(const CausalArgs &a, const char **kname)
+{
+    switch (a.dtype) {
+    case DT_F32: return run_bwd<float>(a, kname);
+    case DT_F16: return run_bwd<_Float16>(a, kname);
+    default: return run_bwd<__bf16>(a, kname);
+    }
+}
+
+hipError_t launch_causal_step(const CausalStepArgs &a, const char **kname)
+{
+    *kname = "causal_step";
+    switch (a.dtype) {
+    case DT_F32: return run_step<float>(a);
+    case DT_F16: return run_step<_Float16>(a);
+    default: return run_step<__bf16>(a);
+    }
+}
+
+}  // namespace gconv

@@ -1,0 +1,88 @@
+// linattn.hpp -- the one pass that every direction of linear attention is made of.
+//
+// With lam = exp(log_decay[head]) and logical token index u = 0 .. n-1,
+//
+//     out_u = p_scale * sum_{s <= u} lam^(u-s) (a_u . b_s) c_s  +  inter_scale * lam^(u+e0) a_u R_0
+//     R_n   = upd_scale * sum_s lam^(n-s-e0) b_s c_s^T  +  lam^n R_0
+//
+// forward      a = q,  b = k,  c = v,  out = o,  R_0 = initial state, e0 = 1
+// gradient dq  a = do, b = v,  c = k,  out = dq, R_0 = initial state transposed, e0 = 1
+// gradient dv  a = k,  b = q,  c = do, out = dv, tokens reversed, R_0 = the final state's gradient, e0 = 0
+// gradient dk  a = v,  b = do, c = q,  out = dk, the same with the states transposed
+//
+// R_n of the third line is the initial state's gradient.  In a reversed pass u counts
+// from the sequence's last token.
+#pragma once
+
+#include "common.hpp"
+
+namespace gconv {
+
+struct LinWalk {
+    const void *a, *b, *c;
+    void *out;
+    int64_t asb, ast, ash, bsb, bst, bsh, csb, cst, csh, osb, ost, osh;   // element strides: batch, token, head
+    int32_t ra, rb, rc;          // value heads for each head of a, b, c
+    int32_t B, T, H, Da, Dc;     // a, b have Da columns, c and out Dc
+    const float *log_decay;      // [H]
+    const int32_t *lengths;      // [B] or nullptr: T
+    const float *s0;             // state before the first token, or nullptr: zero
+    int64_t s0b, s0h, s0r, s0c;  // its element strides: batch, head, row (a's column), column (c's)
+    float *sf;                   // state after the last token, or nullptr
+    int64_t sfb, sfh, sfr, sfc;
+    float *ws;                   // [B*H][nseg] states of Da x Dc, strides wsr, wsc
+    int64_t wsr, wsc;
+    float p_scale, inter_scale, upd_scale;
+    int32_t e0, reverse;
+    int32_t nseg, seg_len;       // segments of seg_len tokens (a multiple of 64), walked by one workgroup each
+    int32_t ndv;                 // column tiles of c
+    int64_t blocks;              // workgroups with work
+    int dtype;                   // of a, b, c
+    int out_f32;                 // out is fp32 (partial gradients of a shared head) rather than dtype
+    hipStream_t stream;
+};
+
+__device__ __forceinline__ float lin_pow(float g, int e) { return e == 0 ? 1.0f : (float)exp((double)g * e); }
+
+// Length of sequence b.
+__device__ __forceinline__ int lin_len(const LinWalk &p, int b)
+{
+    if (!p.lengths) return p.T;
+    const int n = p.lengths[b];
+    return n < 0 ? 0 : n > p.T ? p.T : n;
+}
+
+// Token of logical index u; indices past the length stand for the padding tokens.
+__device__ __forceinline__ int lin_token(const LinWalk &p, int u, int n)
+{
+    return p.reverse && u < n ? n - 1 - u : u;
+}
+
+// The segment states of p (nseg > 1): local sums into p.ws, then the scan that turns
+// them into the states before each segment and writes p.sf.
+hipError_t launch_lin_states(const LinWalk &p, const char **kname);
+// The outputs (with nseg == 1 also p.sf).
+hipError_t launch_lin_walk(const LinWalk &p, const char **kname);
+// Scan alone (T == 0 or nseg segments already summed).
+hipError_t launch_lin_scan(const LinWalk &p);
+// out[b,t,g,:] = sum over j < r of part[b,t,g*r+j,:] (contiguous), rounded to dtype; ost: out's
+// element strides (batch, token, head).
+hipError_t launch_lin_group_sum(const float *part, void *out, const int64_t *ost, int64_t B, int64_t T, int Hk, int r,
+                                int D, int dtype, hipStream_t stream);
+
+struct LinStep {
+    const void *q, *k, *v;
+    void *o;
+    float *state;
+    const float *log_decay;
+    const int32_t *slots;
+    int64_t qsb, qsh, ksb, ksh, vsb, vsh, osb, osh;
+    int64_t n;                   // states in the pool
+    int32_t B, Hk, H, Dk, Dv;
+    float scale;
+    int dtype;
+    hipStream_t stream;
+};
+hipError_t launch_lin_step(const LinStep &p, const char **kname);
+
+}  // namespace gconv

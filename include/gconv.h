@@ -271,6 +271,118 @@ gconv_status_t gconv_autotune(const void *x, const int64_t *x_shape,
 /* Forgets every route gconv_autotune recorded. */
 void gconv_autotune_clear(void);
 
+/* ---------------------------------------------------------------------------
+ * Sequence operators: what stands beside the depthwise conv1d in a mixing block.
+ *
+ * Conventions as above (device pointers, caller's stream, no allocation, errors found
+ * on the host before anything is enqueued), and:
+ *  - Tensors named with strides may be views: the last axis is contiguous, the other
+ *    axes take the given ELEMENT strides; any element alignment.  The rest is contiguous.
+ *  - lengths: int32 [B] on the device or NULL (all T).  Tokens from lengths[b] on are
+ *    padding: their outputs and gradients are zero, whatever their inputs hold (NaN
+ *    included).  Values outside [0, T] are taken as 0 and T.
+ *  - slots: int32 [B] on the device or NULL (slot b for sequence b): the row of a pool of
+ *    n states that sequence b owns, each at most once.  A slot outside [0, n) has no
+ *    state: the token's output is zero and nothing is updated.
+ *  - Sums and states are fp32; outputs are rounded once to the dtype.
+ *  - No output may overlap an input or another output.
+ * Results do not depend on the launch: no atomics, fixed orders of addition. */
+
+/* Linear attention with a decay for each head.  shape = {B, T, Hk, H, Dk, Dv}: q, k
+ * [B,T,Hk,Dk], v, o [B,T,H,Dv], H a multiple of Hk (value head h reads key head
+ * h / (H/Hk)), Dk and Dv in [1, 256].  log_decay: fp32 [H] on the device, a constant
+ * <= 0 for each head (-infinity allowed: lam = 0).  With lam = exp(log_decay[h]):
+ *     S_t = lam S_(t-1) + k_t v_t^T,   o_t = scale * q_t S_t
+ * initial_state: fp32 [B,H,Dk,Dv] = S_(-1), or NULL (zero).  final_state: the same shape,
+ * S after lengths[b] tokens, or NULL.  strides = {q: batch, token, head; k; v; o}, 12
+ * values.  Tokens are taken in chunks of 64: a non-finite q, k or v of a real token can
+ * reach the outputs of its whole chunk.  workspace: gconv_linear_attention_workspace
+ * bytes (may be 0), 16-byte aligned. */
+gconv_status_t gconv_linear_attention_workspace(const int64_t *shape, gconv_dtype_t dtype, int32_t backward,
+                                                size_t *bytes);
+gconv_status_t gconv_linear_attention(const void *q, const void *k, const void *v, void *o, const int64_t *shape,
+                                      const int64_t *strides, const float *log_decay, float scale,
+                                      const float *initial_state, float *final_state, const int32_t *lengths,
+                                      gconv_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                      void *hip_stream);
+
+/* Its gradients: dq, dk [B,T,Hk,Dk] (the value heads of a key head added), dv [B,T,H,Dv]
+ * and, if dinitial is not NULL, the gradient of initial_state (fp32), from the gradients
+ * d_o of o and dfinal (fp32, or NULL: zero) of final_state.  strides = {q, k, v, d_o, dq,
+ * dk, dv: batch, token, head}, 21 values.  log_decay is a constant: it has no gradient. */
+gconv_status_t gconv_linear_attention_backward(const void *q, const void *k, const void *v, const void *d_o,
+                                               void *dq, void *dk, void *dv, const int64_t *shape,
+                                               const int64_t *strides, const float *log_decay, float scale,
+                                               const float *initial_state, const float *dfinal, float *dinitial,
+                                               const int32_t *lengths, gconv_dtype_t dtype, void *workspace,
+                                               size_t workspace_bytes, void *hip_stream);
+
+/* One token for each sequence: shape = {B, Hk, H, Dk, Dv, n}; q, k [B,Hk,Dk], v, o
+ * [B,H,Dv], state fp32 [n,H,Dk,Dv] updated in place.  strides = {q: batch, head; k; v; o},
+ * 8 values. */
+gconv_status_t gconv_linear_attention_step(const void *q, const void *k, const void *v, void *o, float *state,
+                                           const int64_t *shape, const int64_t *strides, const float *log_decay,
+                                           float scale, const int32_t *slots, gconv_dtype_t dtype,
+                                           void *hip_stream);
+
+/* Root-mean-square norm over the last axis of x [rows, C], with the residual's addition:
+ *     h = x + residual (rounded to the dtype),   y = weight * h / sqrt(mean(h^2) + eps)
+ * residual NULL: h is x and the h output must be NULL.  strides = {x row, residual row};
+ * weight [C], y and h [rows, C] contiguous.  C in [1, 2^24]. */
+gconv_status_t gconv_rms_norm(const void *x, const void *residual, const void *weight, void *y, void *h,
+                              int64_t rows, int64_t C, const int64_t *strides, float eps, gconv_dtype_t dtype,
+                              void *hip_stream);
+
+/* The same with y as 8-bit e4m3 values q [rows, C] and fp32 scales: y = q * scale.
+ * scales [rows, ceil(C/block)], one for each `block` columns (32, 64, 128 or 256), or
+ * [rows, 1] for block 0 (one a row):
+ *     scale = max(max|y|, 2^-100) / 448,   q = e4m3(y / scale)
+ * A NaN among the columns of a scale makes the scale NaN. */
+gconv_status_t gconv_rms_norm_e4m3(const void *x, const void *residual, const void *weight, void *q, float *scales,
+                                   void *h, int64_t rows, int64_t C, const int64_t *strides, float eps,
+                                   int32_t block, gconv_dtype_t dtype, void *hip_stream);
+
+/* Gradients of gconv_rms_norm: dx [rows, C] (of x and of residual alike) and dw [C] from
+ * the gradient dy of y, the normed rows h and, if not NULL, the gradient dh of the h
+ * output.  strides = {dy row, h row, dh row}.  workspace: fp32 partial sums,
+ * gconv_rms_norm_backward_workspace bytes, 16-byte aligned. */
+gconv_status_t gconv_rms_norm_backward_workspace(int64_t rows, int64_t C, gconv_dtype_t dtype, size_t *bytes);
+gconv_status_t gconv_rms_norm_backward(const void *dy, const void *h, const void *weight, const void *dh, void *dx,
+                                       void *dw, int64_t rows, int64_t C, const int64_t *strides, float eps,
+                                       gconv_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                       void *hip_stream);
+
+/* Activation applied to a causal conv1d's sums. */
+typedef enum { GCONV_ACT_NONE = 0, GCONV_ACT_SILU = 1 } gconv_act_t;
+
+/* Causal depthwise conv1d over (batch, steps, channels) that carries its state.
+ * shape = {B, T, C, K}, K in [1, 64]: x [B,T,C] (strides = {x batch, x token}),
+ * w [C,1,K], bias [C] or NULL, y [B,T,C].
+ *     y[b,t,c] = act(bias[c] + sum_k w[c,0,k] xs[b, t-(K-1)+k, c])
+ * xs is x with initial_state [B,K-1,C] (or zeros) before its first token.  final_state
+ * [B,K-1,C], or NULL: the last K-1 rows of xs after lengths[b] tokens. */
+gconv_status_t gconv_dw1d_causal(const void *x, const void *w, const void *bias, void *y, const void *initial_state,
+                                 void *final_state, const int32_t *lengths, const int64_t *shape,
+                                 const int64_t *strides, gconv_act_t activation, gconv_dtype_t dtype,
+                                 void *hip_stream);
+
+/* Its gradients: dx [B,T,C], dw [C,1,K], db [C] (or NULL) and dinitial [B,K-1,C] (or NULL;
+ * only with initial_state) from dy [B,T,C] and dfinal [B,K-1,C] (or NULL: zero).
+ * strides = {x batch, x token, dy batch, dy token}.  workspace: fp32 partial sums,
+ * gconv_dw1d_causal_backward_workspace bytes, 16-byte aligned. */
+gconv_status_t gconv_dw1d_causal_backward_workspace(const int64_t *shape, gconv_dtype_t dtype, size_t *bytes);
+gconv_status_t gconv_dw1d_causal_backward(const void *x, const void *w, const void *bias, const void *dy,
+                                          const void *initial_state, const void *dfinal, void *dx, void *dw,
+                                          void *db, void *dinitial, const int32_t *lengths, const int64_t *shape,
+                                          const int64_t *strides, gconv_act_t activation, gconv_dtype_t dtype,
+                                          void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/* One token for each sequence: shape = {B, C, K, n}; x [B,C] (row stride x_stride),
+ * state [n,K-1,C] moved up by one row in place, y [B,C]. */
+gconv_status_t gconv_dw1d_causal_step(const void *x, const void *w, const void *bias, void *state, void *y,
+                                      const int32_t *slots, const int64_t *shape, int64_t x_stride,
+                                      gconv_act_t activation, gconv_dtype_t dtype, void *hip_stream);
+
 /* Name of the kernel the last successful gconv_fwd / gconv_fwd_route / gconv_fwd_ex /
  * gconv_dw1d_bwd_data / gconv_dw1d_bwd_filter call on this host thread launched
  * (the first of two for the filter gradient; "" before the first call or after
