@@ -25,8 +25,8 @@ PEAKS_SRC = "peaks.hip"
 PEAKS_LIB = os.path.join(PKG, "libgconv_peaks.so")
 
 SOURCES = ["api.cpp", "direct2d.hip", "dw2d.hip", "dw1d_ntc.hip", "dw1d_wgrad.hip", "nhwc.hip", "igemm_nhwc.hip", "igemm.hip", "igemm_rows.hip", "igemm_defer.hip", "igemm_f32.hip",
-           "seq_api.cpp", "linattn.hip", "rmsnorm.hip", "dw1d_causal.hip"]
-HEADERS = ["common.hpp", "fastdiv.hpp", "rows_common.hpp", "linattn.hpp", "seq.hpp", "vecio.hpp"]
+           "seq_api.cpp", "linattn.hip", "linattn_f32.hip", "linattn_f16.hip", "linattn_bf16.hip", "rmsnorm.hip", "dw1d_causal.hip"]
+HEADERS = ["common.hpp", "fastdiv.hpp", "rows_common.hpp", "linattn.hpp", "linattn_walk.hpp", "seq.hpp", "vecio.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -58,6 +58,11 @@ __device__ __forceinline__ int lin_token(const LinWalk &p, int u, int n)
     return p.reverse && u < n ? n - 1 - u : u;
 }
 
+// One walk of all segments, outputs (full) or local states only, for each dtype (linattn_walk.hpp).
+hipError_t run_lin_walk_f32(const LinWalk &p, bool full);
+hipError_t run_lin_walk_f16(const LinWalk &p, bool full);
+hipError_t run_lin_walk_bf16(const LinWalk &p, bool full);
+
 // The segment states of p (nseg > 1): local sums into p.ws, then the scan that turns
 // them into the states before each segment and writes p.sf.
 hipError_t launch_lin_states(const LinWalk &p, const char **kname);

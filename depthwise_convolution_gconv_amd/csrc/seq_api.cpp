@@ -101,7 +101,7 @@ constexpr int64_t kChunk = 64;
 void lin_segments(const LinShape &s, int32_t *nseg, int32_t *seg_len)
 {
     const int64_t chunks = std::max<int64_t>(1, gconv::ceil_div(s.T, kChunk));
-    const int64_t wide = std::max<int64_t>(1, s.B * s.H * gconv::ceil_div(std::min(s.Dk, s.Dv), 64));
+    const int64_t wide = std::max<int64_t>(1, s.B * s.H * gconv::ceil_div(std::min(s.Dk, s.Dv), 128));
     int64_t n = wide >= 256 ? 1 : std::min<int64_t>({gconv::ceil_div(512, wide), std::max<int64_t>(1, chunks / 4), 1024});
     const int64_t each = gconv::ceil_div(chunks, n);
     *nseg = (int32_t)gconv::ceil_div(chunks, each);
