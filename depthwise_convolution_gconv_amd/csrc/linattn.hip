@@ -15,18 +15,20 @@ constexpr int kThreads = 256;
 // One thread for each state element, 8 segments' loads in flight.
 constexpr int kMaxSeg = 1024;
 __global__ void __launch_bounds__(kThreads)
-lin_scan(const LinWalk p)
+lin_scan(const LinWalks all)
 {
     __shared__ float lam[kMaxSeg];
     const int tid = threadIdx.x;
-    const int64_t cells = (int64_t)p.Da * p.Dc, tiles = (cells + kThreads - 1) / kThreads;
-    const int64_t bh = blockIdx.x / tiles;
+    // Every walk's states have as many elements.
+    const int64_t cells = (int64_t)all.w[0].Da * all.w[0].Dc, tiles = (cells + kThreads - 1) / kThreads;
+    const LinWalk &p = all.w[blockIdx.x / all.blocks];
+    const int64_t bh = blockIdx.x % all.blocks / tiles;
     const int h = (int)(bh % p.H), bi = (int)(bh / p.H);
     const int n = lin_len(p, bi);
     for (int g = tid; g < p.nseg; g += kThreads)
         lam[g] = lin_pow(p.log_decay[h], max(0, min(n - g * p.seg_len, p.seg_len)));
     __syncthreads();
-    const int64_t x = (blockIdx.x % tiles) * kThreads + tid;
+    const int64_t x = (blockIdx.x % all.blocks % tiles) * kThreads + tid;
     if (x >= cells) return;
     const int64_t d = x / p.Dc, c = x % p.Dc;
     float r = p.s0 ? p.s0[bi * p.s0b + h * p.s0h + d * p.s0r + c * p.s0c] : 0.0f;
@@ -134,34 +136,47 @@ template <typename T> hipError_t run_step(const LinStep &p)
 
 }  // namespace
 
-hipError_t launch_lin_scan(const LinWalk &p)
+hipError_t launch_lin_scan(const LinWalks &walks)
 {
-    const int64_t blocks = (int64_t)p.B * p.H * ceil_div((int64_t)p.Da * p.Dc, kThreads);
-    if (blocks >= (int64_t(1) << 31) || p.nseg > kMaxSeg) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(lin_scan, dim3((unsigned)blocks), dim3(kThreads), 0, p.stream, p);
+    LinWalks all = walks;
+    const LinWalk &p = all.w[0];
+    all.blocks = (int64_t)p.B * p.H * ceil_div((int64_t)p.Da * p.Dc, kThreads);
+    if (all.count * all.blocks >= (int64_t(1) << 31) || p.nseg > kMaxSeg) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(lin_scan, dim3((unsigned)(all.count * all.blocks)), dim3(kThreads), 0, p.stream, all);
     return hipGetLastError();
 }
 
-static hipError_t run_walk(const LinWalk &p, bool full)
+// One launch for the walks of each class.
+static hipError_t run_walks(const LinWalks &all, bool full)
 {
-    switch (p.dtype) {
-    case DT_F32: return run_lin_walk_f32(p, full);
-    case DT_F16: return run_lin_walk_f16(p, full);
-    default: return run_lin_walk_bf16(p, full);
+    for (int i = 0; i < all.count; ++i) {
+        LinWalks some = {};
+        bool first = true;
+        for (int j = 0; j < all.count; ++j)
+            if (lin_class(all.w[j]) == lin_class(all.w[i])) {
+                first = first && j >= i;
+                some.w[some.count++] = all.w[j];
+            }
+        if (!first) continue;
+        const hipError_t err = all.w[0].dtype == DT_F32   ? run_lin_walks_f32(some, full)
+                               : all.w[0].dtype == DT_F16 ? run_lin_walks_f16(some, full)
+                                                          : run_lin_walks_bf16(some, full);
+        if (err != hipSuccess) return err;
     }
+    return hipSuccess;
 }
 
-hipError_t launch_lin_states(const LinWalk &p, const char **kname)
+hipError_t launch_lin_states(const LinWalks &all, const char **kname)
 {
     *kname = "lin_walk";
-    const hipError_t err = run_walk(p, false);
-    return err != hipSuccess ? err : launch_lin_scan(p);
+    const hipError_t err = run_walks(all, false);
+    return err != hipSuccess ? err : launch_lin_scan(all);
 }
 
-hipError_t launch_lin_walk(const LinWalk &p, const char **kname)
+hipError_t launch_lin_walks(const LinWalks &all, const char **kname)
 {
     *kname = "lin_walk";
-    return run_walk(p, true);
+    return run_walks(all, true);
 }
 
 hipError_t launch_lin_group_sum(const float *part, void *out, const int64_t *ost, int64_t B, int64_t T, int Hk, int r,

@@ -36,7 +36,7 @@ struct LinWalk {
     int32_t e0, reverse;
     int32_t nseg, seg_len;       // segments of seg_len tokens (a multiple of 64), walked by one workgroup each
     int32_t ndv;                 // column tiles of c
-    int64_t blocks;              // workgroups with work
+    int64_t blocks;              // workgroups
     int dtype;                   // of a, b, c
     int out_f32;                 // out is fp32 (partial gradients of a shared head) rather than dtype
     hipStream_t stream;
@@ -58,18 +58,33 @@ __device__ __forceinline__ int lin_token(const LinWalk &p, int u, int n)
     return p.reverse && u < n ? n - 1 - u : u;
 }
 
-// One walk of all segments, outputs (full) or local states only, for each dtype (linattn_walk.hpp).
-hipError_t run_lin_walk_f32(const LinWalk &p, bool full);
-hipError_t run_lin_walk_f16(const LinWalk &p, bool full);
-hipError_t run_lin_walk_bf16(const LinWalk &p, bool full);
+// Walks that one launch makes together: they share B, T, H, dtype, nseg, seg_len and stream.
+constexpr int kMaxWalks = 3;
+struct LinWalks {
+    LinWalk w[kMaxWalks];
+    int32_t count;
+    int64_t blocks;
+};
 
-// The segment states of p (nseg > 1): local sums into p.ws, then the scan that turns
-// them into the states before each segment and writes p.sf.
-hipError_t launch_lin_states(const LinWalk &p, const char **kname);
-// The outputs (with nseg == 1 also p.sf).
-hipError_t launch_lin_walk(const LinWalk &p, const char **kname);
+// Which kernel walks p: columns of a and of c that a workgroup holds.  Two waves where 64
+// columns are all there are, but for wide rows: their staging is shared by four.
+inline int lin_class(const LinWalk &p)
+{
+    return p.Da > 128 ? 4 : 2 * (p.Da > 64) + (p.Dc > 64);
+}
+
+// The walks of all segments, outputs (full) or local states only, for each dtype; all of one class.
+hipError_t run_lin_walks_f32(const LinWalks &all, bool full);
+hipError_t run_lin_walks_f16(const LinWalks &all, bool full);
+hipError_t run_lin_walks_bf16(const LinWalks &all, bool full);
+
+// The segment states (nseg > 1): local sums into ws, then the scan that turns them into
+// the states before each segment and writes sf.
+hipError_t launch_lin_states(const LinWalks &all, const char **kname);
+// The outputs (with nseg == 1 also sf).
+hipError_t launch_lin_walks(const LinWalks &all, const char **kname);
 // Scan alone (T == 0 or nseg segments already summed).
-hipError_t launch_lin_scan(const LinWalk &p);
+hipError_t launch_lin_scan(const LinWalks &all);
 // out[b,t,g,:] = sum over j < r of part[b,t,g*r+j,:] (contiguous), rounded to dtype; ost: out's
 // element strides (batch, token, head).
 hipError_t launch_lin_group_sum(const float *part, void *out, const int64_t *ost, int64_t B, int64_t T, int Hk, int r,

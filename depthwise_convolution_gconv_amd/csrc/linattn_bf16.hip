@@ -3,10 +3,9 @@
 
 namespace gconv {
 
-hipError_t run_lin_walk_bf16(const LinWalk &p, bool full)
+hipError_t run_lin_walks_bf16(const LinWalks &all, bool full)
 {
-    if (!full) return run_walk<__bf16, __bf16, false>(p);
-    return p.out_f32 ? run_walk<__bf16, float, true>(p) : run_walk<__bf16, __bf16, true>(p);
+    return full ? run_walks<__bf16, true>(all) : run_walks<__bf16, false>(all);
 }
 
 }  // namespace gconv

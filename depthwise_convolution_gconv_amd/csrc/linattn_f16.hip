@@ -3,10 +3,9 @@
 
 namespace gconv {
 
-hipError_t run_lin_walk_f16(const LinWalk &p, bool full)
+hipError_t run_lin_walks_f16(const LinWalks &all, bool full)
 {
-    if (!full) return run_walk<_Float16, _Float16, false>(p);
-    return p.out_f32 ? run_walk<_Float16, float, true>(p) : run_walk<_Float16, _Float16, true>(p);
+    return full ? run_walks<_Float16, true>(all) : run_walks<_Float16, false>(all);
 }
 
 }  // namespace gconv

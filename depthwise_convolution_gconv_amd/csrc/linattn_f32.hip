@@ -3,9 +3,9 @@
 
 namespace gconv {
 
-hipError_t run_lin_walk_f32(const LinWalk &p, bool full)
+hipError_t run_lin_walks_f32(const LinWalks &all, bool full)
 {
-    return full ? run_walk<float, float, true>(p) : run_walk<float, float, false>(p);
+    return full ? run_walks<float, true>(all) : run_walks<float, false>(all);
 }
 
 }  // namespace gconv

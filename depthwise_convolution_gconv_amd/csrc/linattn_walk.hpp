@@ -25,9 +25,11 @@
 //
 // Nothing but the inputs goes through LDS.  Products run transposed (columns of the
 // accumulators are tokens i, rows are j or columns of c): scores and the state leave the
-// matrix cores with four consecutive rows in a lane, and as the order of a reduction is
-// free, the other operand is read in that same order (rows 4h .. 4h+3 and 8+4h .. 8+4h+3
-// of each 16 for the lane's half h).  A wave keeps the state of its 32 columns in
+// matrix cores with four consecutive rows in a lane (rows 4h .. 4h+3 and 8+4h .. 8+4h+3 of
+// each 16 for the lane's half h), and as the order of a reduction is free, the other
+// operand is read in that same order: for the scores by reading c's rows so, for the state
+// by giving row 16 s + r of its tile the column kRowCol[r] = 0-3, 8-11, 4-7, 12-15, so that
+// a lane's eight are eight neighbours of a.  A wave keeps the state of its 32 columns in
 // accumulators for the whole walk.
 #pragma once
 
@@ -40,22 +42,22 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 template <typename T> constexpr int kParts = sizeof(T) == 4 ? 3 : 2;
 template <> constexpr int kParts<__bf16> = 1;
 constexpr int kUpdParts = 3;
-// Tokens in a chunk: more parts take more LDS, more columns more registers.
-template <typename T, int DK, int NW> constexpr int kLen = kParts<T> == 1 && DK / NW <= 32 ? 64 : 32;
+constexpr int kLen = 32;     // tokens in a chunk
 
-// A tile of D columns in LDS: rows 16 banks apart within each four and groups of four two
-// banks apart, so the 32 rows of an operand read (8 bytes each) and the 4 rows x 64 bytes
-// of a transposing read both cover all 64 banks.
+// A tile of D columns in LDS: rows 16 banks apart within each four and groups of four rows
+// four banks apart, so the 16-byte reads of 16 rows and the transposing reads of 4 rows x
+// 64 bytes both cover all 64 banks.
 template <int D> struct Tile {
     static constexpr int row = D == 64 ? 96 : D == 128 ? 160 : 288;
-    static constexpr int group = D == 64 ? 388 : D == 128 ? 644 : 1156;
+    static constexpr int group = D == 64 ? 392 : D == 128 ? 648 : 1160;
+    static constexpr int size = kLen / 4 * group;
     static __device__ __forceinline__ int at(int j, int d) { return (j >> 2) * group + (j & 3) * row + d; }
-    static constexpr int size(int rows) { return rows / 4 * group; }
 };
 
 template <int NP> struct Part8 { bf16x8 p[NP]; };
@@ -90,32 +92,27 @@ __device__ __forceinline__ f32x16 mma(const Part8<NA> &a, const Part8<NB> &b, f3
     return acc;
 }
 
-// 8 values of row j at columns d + 4h .. and d + 8 + 4h .. (the caller's d holds 4h).
-template <int D, int NP>
-__device__ __forceinline__ Part8<NP> read_rows(const __bf16 *t, int size, int at)
+// 8 neighbours of a row (16-byte aligned).
+template <int D, int NP> __device__ __forceinline__ Part8<NP> read_row(const __bf16 *t, int at)
 {
     Part8<NP> r;
 #pragma unroll
-    for (int q = 0; q < NP; ++q) {
-        const bf16x4 lo = *reinterpret_cast<const bf16x4 *>(t + q * size + at);
-        const bf16x4 hi = *reinterpret_cast<const bf16x4 *>(t + q * size + at + 8);
-        r.p[q] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
+    for (int q = 0; q < NP; ++q) r.p[q] = *reinterpret_cast<const bf16x8 *>(t + q * Tile<D>::size + at);
     return r;
 }
 
-// The same of column (lane) over rows: two transposing reads of 4 rows each, `at` and
-// two groups of rows further.
-template <int D, int NP>
-__device__ __forceinline__ Part8<NP> read_cols(const __bf16 *t, int size, int at)
+// Rows 4h .. 4h+3 and 8+4h .. of a column each lane: two transposing reads.  Of 16 lanes,
+// lane t names row t / 4 and the t % 4-th four columns, and gets its column of all four rows.
+template <int D, int NP> __device__ __forceinline__ Part8<NP> read_col(const __bf16 *t, int at)
 {
     typedef __attribute__((address_space(3))) s16x4 lds4;
     Part8<NP> r;
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
-        const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(t + q * size + at)));
-        const bf16x4 hi = __builtin_bit_cast(
-            bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(t + q * size + at + 2 * Tile<D>::group)));
+        const __bf16 *x = t + q * Tile<D>::size + at;
+        const bf16x4 lo = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)x));
+        const bf16x4 hi =
+            __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(x + 2 * Tile<D>::group)));
         r.p[q] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     return r;
@@ -123,6 +120,15 @@ __device__ __forceinline__ Part8<NP> read_cols(const __bf16 *t, int size, int at
 
 // 8 elements on their way from memory to LDS.
 template <typename T> struct Raw8 { RunVec<T, 16 / (int)sizeof(T)> w[sizeof(T) / 2]; };
+
+template <typename T> __device__ __forceinline__ Raw8<T> load8_whole(const T *src)
+{
+    constexpr int N = 16 / sizeof(T);
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < 8 / N; ++i) r.w[i] = *reinterpret_cast<const RunVec<T, N> *>(src + N * i);
+    return r;
+}
 
 template <typename T> __device__ __forceinline__ Raw8<T> load8(const T *src, int valid)
 {
@@ -134,8 +140,9 @@ template <typename T> __device__ __forceinline__ Raw8<T> load8(const T *src, int
 }
 
 // They go to their parts' tiles.
-template <typename T, int NP> __device__ __forceinline__ void stage8(__bf16 *t, int size, int at, const Raw8<T> &v)
+template <typename T, int D> __device__ __forceinline__ void stage8(__bf16 *t, int at, const Raw8<T> &v)
 {
+    constexpr int NP = kParts<T>;
     Part8<NP> r;
     if constexpr (NP == 1) {
         r.p[0] = __builtin_bit_cast(bf16x8, v);
@@ -147,42 +154,90 @@ template <typename T, int NP> __device__ __forceinline__ void stage8(__bf16 *t, 
         r = split8<NP>(f);
     }
 #pragma unroll
-    for (int q = 0; q < NP; ++q) {
-        *reinterpret_cast<bf16x4 *>(t + q * size + at) = __builtin_shufflevector(r.p[q], r.p[q], 0, 1, 2, 3);
-        *reinterpret_cast<bf16x4 *>(t + q * size + at + 4) = __builtin_shufflevector(r.p[q], r.p[q], 4, 5, 6, 7);
+    for (int q = 0; q < NP; ++q) *reinterpret_cast<bf16x8 *>(t + q * Tile<D>::size + at) = r.p[q];
+}
+
+// A thread's share of a tile of kLen tokens by D columns: NR runs of 8 of one column block,
+// every STEP tokens.
+template <typename T, int D, int NTH> struct Share {
+    static constexpr int NR = kLen * D / 8 / NTH, STEP = NTH / (D / 8);
+    Raw8<T> r[NR];
+    const T *p;              // its first run of the next chunk
+    int64_t step;            // elements from token to token of the walk
+    int j, left;             // first token; columns from its block on
+    __device__ __forceinline__ void init(const T *base, int64_t stride, int cols, int u0, int n, int reverse)
+    {
+        const int d = threadIdx.x % (D / 8) * 8;
+        j = threadIdx.x / (D / 8);
+        left = cols - d;
+        step = reverse ? -stride : stride;
+        p = base + d + (int64_t)(reverse ? n - 1 - u0 - j : u0 + j) * stride;
+    }
+    // The chunk's `live` tokens; even: whole blocks only (columns divide by 8).
+    __device__ __forceinline__ void fetch(int live, bool even)
+    {
+        if (live >= kLen && even) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                r[i] = Raw8<T>{};
+                if (left > 0) r[i] = load8_whole<T>(p + i * STEP * step);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) r[i] = load8<T>(p + i * STEP * step, j + i * STEP < live ? left : 0);
+        }
+        p += kLen * step;
+    }
+    __device__ __forceinline__ void stage(__bf16 *t) const
+    {
+        const int d = threadIdx.x % (D / 8) * 8;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) stage8<T, D>(t, Tile<D>::at(j + i * STEP, d), r[i]);
+    }
+};
+
+// A lane's 16 values of a token, four columns of every eight.
+template <typename TO> __device__ __forceinline__ void store_tile(TO *o, int left, const f32x16 &acc)
+{
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const float f[4] = {acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
+        if (left > 8 * g) store_run<TO, 4>(o + 8 * g, left - 8 * g, f);
     }
 }
 
 template <typename T, int DK, int NW, bool FULL> struct WalkLds {
-    static constexpr int NP = kParts<T>, L = kLen<T, DK, NW>, NT = 32 * NW;
-    static constexpr int AB = Tile<DK>::size(L), C = Tile<NT>::size(L);
-    __bf16 a[FULL ? NP * AB : 4];
-    __bf16 b[NP * AB];
-    __bf16 c[NP * C];
-    float pw[L + 1];         // lam^0 .. lam^L
-    float upd[L];            // upd_scale lam^(m-j-e0)
-    float off[32];           // lam^(32-j)
+    static constexpr int NP = kParts<T>;
+    __bf16 a[FULL ? NP * Tile<DK>::size : 8];
+    __bf16 b[NP * Tile<DK>::size];
+    __bf16 c[NP * Tile<32 * NW>::size];
+    float diag[FULL ? 16 * 64 : 4];     // weights of a tile of scores, [r / 4][lane][r % 4]
+    uint32_t mask[FULL ? 8 * 64 : 4];   // halves of ones for the pairs of them with j <= i, [r / 8][lane][r / 2 % 4]
+    float upd[kLen];                    // upd_scale lam^(m-j-e0)
+    float pw[kLen + 1];                 // lam^0 .. lam^kLen
 };
 
-// Two workgroups of four waves share a compute unit where their registers and LDS allow.
-template <typename T, int DK, int NW> constexpr int kWavesPerSimd = DK == 256 || kParts<T> == 3 ? 1 : 2;
+// Waves of a SIMD that registers are kept for: two or three workgroups share a compute unit.
+template <typename T, int DK, int NW>
+constexpr int kWavesPerSimd = DK == 256 ? 1 : kParts<T> == 1 && DK / NW <= 32 ? 3 : 2;
 
-template <typename T, typename TO, int DK, int NW, bool FULL>
+template <typename T, int DK, int NW, bool FULL>
 __global__ void __launch_bounds__(64 * NW, (kWavesPerSimd<T, DK, NW>))
-lin_walk(const LinWalk p)
+lin_walk(const LinWalks all)
 {
-    constexpr int NP = kParts<T>, L = kLen<T, DK, NW>, NT = 32 * NW, NTH = 64 * NW;
-    typedef WalkLds<T, DK, NW, FULL> Lds;
-    constexpr int NBR = L * DK / 8 / NTH, NCR = L * NT / 8 / NTH;   // staging runs of 8 for each thread
+    constexpr int NP = kParts<T>, L = kLen, NT = 32 * NW, NTH = 64 * NW;
     constexpr int NX = DK / 32, NS = DK / 16, NG = L / 16;          // state tiles, steps along columns, along tokens
-    __shared__ __attribute__((aligned(16))) Lds sm;
+    __shared__ __attribute__((aligned(16))) WalkLds<T, DK, NW, FULL> sm;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l32 = lane & 31, half = lane >> 5;
 
     // Workgroups go round the 8 XCDs; a contiguous run of ids on one XCD keeps the column
     // tiles and heads that share a's and b's rows on one L2.
-    const int64_t per = (p.blocks + 7) / 8;
+    const int64_t per = (all.blocks + 7) / 8;
     int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (id >= p.blocks) return;
+    if (id >= all.blocks) return;
+    int which = 0;
+    while (id >= all.w[which].blocks) id -= all.w[which++].blocks;
+    const LinWalk &p = all.w[which];
     const int dv = (int)(id % p.ndv);
     id /= p.ndv;
     const int seg = (int)(id % p.nseg);
@@ -193,34 +248,44 @@ lin_walk(const LinWalk p)
     const int utop = min(useg + p.seg_len, FULL ? p.T : n);   // tokens [useg, utop) of this workgroup
     const int ulive = min(n, utop);
     const bool mine = n0 + wave * 32 < p.Dc;                  // this wave has columns
+    const bool even = p.Da % 8 == 0 && p.Dc % 8 == 0;
 
-    for (int e = tid; e <= L; e += NTH) sm.pw[e] = lin_pow(p.log_decay[h], e);
-    if (tid < 32) sm.off[tid] = lin_pow(p.log_decay[h], 32 - tid);
-    const T *ab = (const T *)p.a + bi * p.asb + (h / p.ra) * p.ash;
-    const T *bb = (const T *)p.b + bi * p.bsb + (h / p.rb) * p.bsh;
-    const T *cb = (const T *)p.c + bi * p.csb + (h / p.rc) * p.csh + n0;
+    Share<T, DK, NTH> sa, sb;
+    Share<T, NT, NTH> sc;
+    if constexpr (FULL)
+        sa.init((const T *)p.a + bi * p.asb + (h / p.ra) * p.ash, p.ast, p.Da, useg, n, p.reverse);
+    sb.init((const T *)p.b + bi * p.bsb + (h / p.rb) * p.bsh, p.bst, p.Da, useg, n, p.reverse);
+    sc.init((const T *)p.c + bi * p.csb + (h / p.rc) * p.csh + n0, p.cst, p.Dc - n0, useg, n, p.reverse);
+    auto fetch = [&](int u0) {
+        if constexpr (FULL) sa.fetch(ulive - u0, even);
+        sb.fetch(ulive - u0, even);
+        sc.fetch(ulive - u0, even);
+    };
+    fetch(useg);
+    if (tid <= L) sm.pw[tid] = lin_pow(p.log_decay[h], tid);
 
-    // The state: column n0 + 32 wave + l32, rows 32x + 8 (r / 4) + 4 half + r % 4.
+    // The state: column scol, rows 4 half + 32 x + 8 (r / 4) + r % 4 of the tiles, which stand
+    // for the columns of b that d_of gives.
     const int scol = n0 + wave * 32 + l32;
+    auto d_of = [&](int x, int r) { return 32 * x + 16 * (r / 8) + 8 * half + 4 * (r / 4 % 2) + r % 4; };
     f32x16 st[NX];
     const float *sp = nullptr;
-    int64_t sr = 0, sc = 0;
+    int64_t sr = 0, scs = 0;
     if (FULL && p.nseg > 1) {
         sp = p.ws + (bh * p.nseg + seg) * (int64_t)p.Da * p.Dc;
-        sr = p.wsr; sc = p.wsc;
+        sr = p.wsr; scs = p.wsc;
     } else if (FULL && p.s0) {
         sp = p.s0 + bi * p.s0b + h * p.s0h;
-        sr = p.s0r; sc = p.s0c;
+        sr = p.s0r; scs = p.s0c;
     }
     if (sp && scol < p.Dc) {
-        sp += scol * sc;
+        sp += scol * scs;
 #pragma unroll
         for (int x = 0; x < NX; ++x)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {     // rows past the last read that one
-                const int d = 32 * x + 8 * (r / 4) + 4 * half + r % 4;
-                const float v = sp[min(d, p.Da - 1) * sr];
-                st[x][r] = d < p.Da ? v : 0.0f;
+                const float v = sp[min(d_of(x, r), p.Da - 1) * sr];
+                st[x][r] = d_of(x, r) < p.Da ? v : 0.0f;
             }
     } else {
 #pragma unroll
@@ -229,44 +294,30 @@ lin_walk(const LinWalk p)
             for (int r = 0; r < 16; ++r) st[x][r] = 0.0f;
     }
 
-    Raw8<T> ar[FULL ? NBR : 1], br[NBR], cr[NCR];
-    auto fetch = [&](int u0) {
-#pragma unroll
-        for (int i = 0; i < NBR; ++i) {
-            const int x = tid + i * NTH, j = x / (DK / 8), d = x % (DK / 8) * 8, u = u0 + j;
-            const int left = u < ulive ? p.Da - d : 0;
-            const int64_t tok = lin_token(p, u, n);
-            if constexpr (FULL) ar[i] = load8<T>(ab + tok * p.ast + d, left);
-            br[i] = load8<T>(bb + tok * p.bst + d, left);
-        }
-#pragma unroll
-        for (int i = 0; i < NCR; ++i) {
-            const int x = tid + i * NTH, j = x / (NT / 8), d = x % (NT / 8) * 8, u = u0 + j;
-            cr[i] = load8<T>(cb + (int64_t)lin_token(p, u, n) * p.cst + d, u < ulive ? p.Dc - n0 - d : 0);
-        }
-    };
-    fetch(useg);
     __syncthreads();     // the powers
-
-    const int row_at = Tile<DK>::at(l32, 4 * half);                                   // row l32
+    if constexpr (FULL) {
+        for (int e = tid; e < 16 * 64; e += NTH) {
+            const int i = e / 4 % 32, j = 8 * (e / 256) + 4 * (e / 128 % 2) + e % 4;
+            sm.diag[e] = j <= i ? p.p_scale * sm.pw[i - j] : 0.0f;
+        }
+        for (int e = tid; e < 8 * 64; e += NTH) {
+            const int i = e / 4 % 32, j = 16 * (e / 256) + 8 * (e / 2 % 2) + 4 * (e / 128 % 2) + e % 2 * 2;
+            sm.mask[e] = (j <= i ? 0xffffu : 0u) | (j + 1 <= i ? 0xffff0000u : 0u);
+        }
+    }
+    const int row_at = Tile<DK>::at(l32, 8 * half);
     const int col_row = 4 * half + ((lane & 15) >> 2), col_d = (lane & 16) + (lane & 3) * 4;
-    const int bcol_at = Tile<DK>::at(col_row, col_d), ccol_at = Tile<NT>::at(col_row, 32 * wave + col_d);
+    // b's columns of a lane group in the order 0-3, 8-11, 4-7, 12-15
+    const int bcol_at = Tile<DK>::at(col_row, (lane & 16) + (lane & 1) * 8 + (lane & 2) * 2);
+    const int ccol_at = Tile<NT>::at(col_row, 32 * wave + col_d);
 
     int mset = -1;
     for (int u0 = useg; u0 < utop; u0 += L) {
         const int m = max(0, min(n - u0, L));
         // The previous chunk's readers are done (barrier at the loop's end).
-#pragma unroll
-        for (int i = 0; i < NBR; ++i) {
-            const int x = tid + i * NTH, at = Tile<DK>::at(x / (DK / 8), x % (DK / 8) * 8);
-            if constexpr (FULL) stage8<T, NP>(sm.a, Lds::AB, at, ar[i]);
-            stage8<T, NP>(sm.b, Lds::AB, at, br[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < NCR; ++i) {
-            const int x = tid + i * NTH;
-            stage8<T, NP>(sm.c, Lds::C, Tile<NT>::at(x / (NT / 8), x % (NT / 8) * 8), cr[i]);
-        }
+        if constexpr (FULL) sa.stage(sm.a);
+        sb.stage(sm.b);
+        sc.stage(sm.c);
         if (m != mset) {
             if (tid < L) sm.upd[tid] = p.upd_scale * sm.pw[max(m - tid - p.e0, 0)];
             mset = m;
@@ -274,110 +325,81 @@ lin_walk(const LinWalk p)
         __syncthreads();
         if (u0 + L < utop) fetch(u0 + L);
 
-        if (mine && m > 0) {
-            auto cols_c = [&](int g) { return read_cols<NT, NP>(sm.c, Lds::C, ccol_at + 4 * g * Tile<NT>::group); };
-            if constexpr (FULL) {
-                // Rolled: the copies would keep each other's operands alive.
-#pragma unroll 1
-                for (int it = 0; 32 * it < m; ++it) {
-                    const int a_at = row_at + it * 8 * Tile<DK>::group;
-                    f32x16 acc, sc;
+        if (FULL && mine) {
+            f32x16 acc;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[r] = sc[r] = 0.0f;
-                    // a_i R, and the scores of the tile on the diagonal.
+            for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
+            if (m > 0) {
+                // a_i R and the scores a_i . b_j share the reads of a.
+                f32x16 sco;
 #pragma unroll
-                    for (int s = 0; s < NS; ++s) {
-                        const Part8<NP> aq = read_rows<DK, NP>(sm.a, Lds::AB, a_at + 16 * s);
-                        float f[8];
+                for (int r = 0; r < 16; ++r) sco[r] = 0.0f;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = st[s / 2][s % 2 * 8 + e];
-                        acc = mma<NP - 1>(split8<NP>(f), aq, acc);
-                        sc = mma<NP - 1>(read_rows<DK, NP>(sm.b, Lds::AB, a_at + 16 * s), aq, sc);
-                    }
-                    const float fi = p.inter_scale * sm.pw[min(it * 32 + l32 + p.e0, L)];
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int j = 8 * (r / 4) + 4 * half + r % 4;
-                        acc[r] *= fi;
-                        // Scores of later tokens are dropped, not multiplied by zero: they may be infinite.
-                        sc[r] = j <= l32 ? sc[r] * (p.p_scale * sm.pw[max(l32 - j, 0)]) : 0.0f;
-                    }
-                    auto add = [&](int jt) {
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            float f[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) f[e] = sc[8 * g + e];
-                            acc = mma<NP - 1>(cols_c(2 * jt + g), split8<NP>(f), acc);
-                        }
-                    };
-                    add(it);
-                    if (L > 32 && it > 0) {   // the tile before it
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) sc[r] = 0.0f;
-#pragma unroll
-                        for (int s = 0; s < NS; ++s)
-                            sc = mma<NP - 1>(read_rows<DK, NP>(sm.b, Lds::AB, row_at + 16 * s),
-                                             read_rows<DK, NP>(sm.a, Lds::AB, a_at + 16 * s), sc);
-                        const float fs = p.p_scale * sm.pw[l32];
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) sc[r] *= fs * sm.off[8 * (r / 4) + 4 * half + r % 4];
-                        add(0);
-                    }
-                    const int i = it * 32 + l32, u = u0 + i;
-                    if (u < utop) {
-                        TO *op = (TO *)p.out + bi * p.osb + (int64_t)lin_token(p, u, n) * p.ost + h * p.osh + n0 +
-                                 wave * 32 + 4 * half;
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            float f[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) f[e] = i < m ? acc[4 * g + e] : 0.0f;
-                            const int left = p.Dc - n0 - wave * 32 - 4 * half - 8 * g;
-                            if (left > 0) store_run<TO, 4>(op + 8 * g, left, f);
-                        }
-                    }
-                }
-            }
-
-            if (!FULL || u0 + L < utop || (p.nseg == 1 && p.sf)) {
-                const float lm = sm.pw[m];
-#pragma unroll
-                for (int x = 0; x < NX; ++x)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) st[x][r] *= lm;
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    if (16 * g >= m) break;
-                    const Part8<NP> cT = cols_c(g);
+                for (int s = 0; s < NS; ++s) {
+                    const Part8<NP> aq = read_row<DK, NP>(sm.a, row_at + 16 * s);
                     float f[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float v = (float)cT.p[NP - 1][e];
+                    for (int e = 0; e < 8; ++e) f[e] = st[s / 2][s % 2 * 8 + e];
+                    sco = mma<NP - 1>(read_row<DK, NP>(sm.b, row_at + 16 * s), aq, sco);
+                    acc = mma<NP - 1>(split8<NP>(f), aq, acc);
+                }
+                const float fi = p.inter_scale * sm.pw[min(l32 + p.e0, L)];
 #pragma unroll
-                        for (int q = NP - 2; q >= 0; --q) v += (float)cT.p[q][e];
-                        f[e] = v * sm.upd[16 * g + 4 * half + 8 * (e / 4) + e % 4];
+                for (int r = 0; r < 16; ++r) acc[r] *= fi;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        const float4 w = *reinterpret_cast<const float4 *>(&sm.diag[256 * (2 * g + e / 4) + 4 * lane]);
+                        f[e] = sco[8 * g + e] * w.x;
+                        f[e + 1] = sco[8 * g + e + 1] * w.y;
+                        f[e + 2] = sco[8 * g + e + 2] * w.z;
+                        f[e + 3] = sco[8 * g + e + 3] * w.w;
                     }
-                    const Part8<kUpdParts> wc = split8<kUpdParts>(f);
+                    // Scores of later tokens are masked, not only multiplied by zero: they may be infinite.
+                    Part8<NP> pr = split8<NP>(f);
+                    const u32x4 mask = *reinterpret_cast<const u32x4 *>(&sm.mask[256 * g + 4 * lane]);
 #pragma unroll
-                    for (int x = 0; x < NX; ++x)
-                        st[x] = mma<2>(read_cols<DK, NP>(sm.b, Lds::AB, bcol_at + 4 * g * Tile<DK>::group + 32 * x), wc, st[x]);
+                    for (int q = 0; q < NP; ++q)
+                        pr.p[q] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, pr.p[q]) & mask);
+                    acc = mma<NP - 1>(read_col<NT, NP>(sm.c, ccol_at + 4 * g * Tile<NT>::group), pr, acc);
                 }
             }
+            if (m < L) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[r] = l32 < m ? acc[r] : 0.0f;
+            }
+            const int u = u0 + l32;
+            if (u < utop) {
+                const int64_t at = bi * p.osb + (int64_t)lin_token(p, u, n) * p.ost + h * p.osh + n0 + wave * 32 + 4 * half;
+                const int left = p.Dc - n0 - wave * 32 - 4 * half;
+                if (sizeof(T) == 4 || p.out_f32) store_tile<float>((float *)p.out + at, left, acc);
+                else store_tile<T>((T *)p.out + at, left, acc);
+            }
         }
-        if (FULL && mine) {
-            // Tokens past the sequence's end, in 32-token tiles that held none that exist: zeros.
+
+        if (mine && m > 0 && (!FULL || u0 + L < utop || (p.nseg == 1 && p.sf))) {
+            const float lm = sm.pw[m];
 #pragma unroll
-            for (int it = 0; it < L / 32; ++it) {
-                const int u = u0 + it * 32 + l32;
-                if (32 * it < m || u >= utop) continue;
-                TO *op = (TO *)p.out + bi * p.osb + (int64_t)u * p.ost + h * p.osh + n0 + wave * 32 + 4 * half;
+            for (int x = 0; x < NX; ++x)
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    const int left = p.Dc - n0 - wave * 32 - 4 * half - 8 * g;
-                    if (left > 0) store_run<TO, 4>(op + 8 * g, left, z);
+                for (int r = 0; r < 16; ++r) st[x][r] *= lm;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const Part8<NP> cT = read_col<NT, NP>(sm.c, ccol_at + 4 * g * Tile<NT>::group);
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float v = (float)cT.p[NP - 1][e];
+#pragma unroll
+                    for (int q = NP - 2; q >= 0; --q) v += (float)cT.p[q][e];
+                    f[e] = v * sm.upd[16 * g + 4 * half + 8 * (e / 4) + e % 4];
                 }
+                const Part8<kUpdParts> wc = split8<kUpdParts>(f);
+#pragma unroll
+                for (int x = 0; x < NX; ++x)
+                    st[x] = mma<2>(read_col<DK, NP>(sm.b, bcol_at + 4 * g * Tile<DK>::group + 32 * x), wc, st[x]);
             }
         }
         __syncthreads();
@@ -393,38 +415,44 @@ lin_walk(const LinWalk p)
         dr = p.sfr; dc = p.sfc;
     }
     if (dp && scol < p.Dc) {
-        int d0 = 4 * half;
+        int d0 = 8 * half;
         asm("" : "+v"(d0));      // the addresses are made here, not kept through the walk
         dp += d0 * dr + scol * dc;
 #pragma unroll
         for (int x = 0; x < NX; ++x)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int d = 32 * x + 8 * (r / 4) + r % 4;
+                const int d = 32 * x + 16 * (r / 8) + 4 * (r / 4 % 2) + r % 4;
                 if (d0 + d < p.Da) dp[d * dr] = st[x][r];
             }
     }
 }
 
-template <typename T, typename TO, int DK, bool FULL>
-hipError_t run_walk_waves(const LinWalk &p0)
+template <typename T, int DK, int NW, bool FULL> hipError_t run_walk_on(LinWalks all)
 {
-    LinWalk p = p0;
-    const int nw = p.Dc <= 64 ? 2 : 4;
-    p.ndv = (int32_t)ceil_div(p.Dc, 32 * nw);
-    p.blocks = (int64_t)p.B * p.H * p.nseg * p.ndv;
-    const int64_t grid = 8 * ceil_div(p.blocks, 8);
+    all.blocks = 0;
+    for (int i = 0; i < all.count; ++i) {
+        LinWalk &p = all.w[i];
+        p.ndv = (int32_t)ceil_div(p.Dc, 32 * NW);
+        p.blocks = (int64_t)p.B * p.H * p.nseg * p.ndv;
+        all.blocks += p.blocks;
+    }
+    const int64_t grid = 8 * ceil_div(all.blocks, 8);
     if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-    if (nw == 2) hipLaunchKernelGGL((lin_walk<T, TO, DK, 2, FULL>), dim3((unsigned)grid), dim3(128), 0, p.stream, p);
-    else hipLaunchKernelGGL((lin_walk<T, TO, DK, 4, FULL>), dim3((unsigned)grid), dim3(256), 0, p.stream, p);
+    hipLaunchKernelGGL((lin_walk<T, DK, NW, FULL>), dim3((unsigned)grid), dim3(64 * NW), 0, all.w[0].stream, all);
     return hipGetLastError();
 }
 
-template <typename T, typename TO, bool FULL> hipError_t run_walk(const LinWalk &p)
+// The walks of `all` have Da and Dc in one class (lin_class).
+template <typename T, bool FULL> hipError_t run_walks(const LinWalks &all)
 {
-    if (p.Da <= 64) return run_walk_waves<T, TO, 64, FULL>(p);
-    if (p.Da <= 128) return run_walk_waves<T, TO, 128, FULL>(p);
-    return run_walk_waves<T, TO, 256, FULL>(p);
+    switch (lin_class(all.w[0])) {
+    case 0: return run_walk_on<T, 64, 2, FULL>(all);
+    case 1: return run_walk_on<T, 64, 4, FULL>(all);
+    case 2: return run_walk_on<T, 128, 2, FULL>(all);
+    case 3: return run_walk_on<T, 128, 4, FULL>(all);
+    default: return run_walk_on<T, 256, 4, FULL>(all);
+    }
 }
 
 }  // namespace

@@ -95,23 +95,28 @@ gconv_status_t check_strides(const int64_t *strides, int n)
     return GCONV_OK;
 }
 
-// Segments of a sequence: workgroups for twice the 256 compute units while a segment
-// keeps at least 4 chunks (a cut sequence reads two of its three inputs again).
+// Segments of a sequence: three workgroups for each of the 256 compute units over the
+// `walks` that a launch makes, while a segment keeps at least 4 chunks of 64 tokens (a cut
+// sequence reads two of its three inputs again).
 constexpr int64_t kChunk = 64;
-void lin_segments(const LinShape &s, int32_t *nseg, int32_t *seg_len)
+void lin_segments(const LinShape &s, int walks, int32_t *nseg, int32_t *seg_len)
 {
     const int64_t chunks = std::max<int64_t>(1, gconv::ceil_div(s.T, kChunk));
-    const int64_t wide = std::max<int64_t>(1, s.B * s.H * gconv::ceil_div(std::min(s.Dk, s.Dv), 128));
-    int64_t n = wide >= 256 ? 1 : std::min<int64_t>({gconv::ceil_div(512, wide), std::max<int64_t>(1, chunks / 4), 1024});
+    const int64_t wide = std::max<int64_t>(1, walks * s.B * s.H * gconv::ceil_div(std::min(s.Dk, s.Dv), 128));
+    int64_t n = wide >= 384 ? 1 : std::min<int64_t>({gconv::ceil_div(768, wide), std::max<int64_t>(1, chunks / 4), 1024});
     const int64_t each = gconv::ceil_div(chunks, n);
     *nseg = (int32_t)gconv::ceil_div(chunks, each);
     *seg_len = (int32_t)(each * kChunk);
 }
 
-size_t lin_states_bytes(const LinShape &s)
+// Walks of a call: the output; or dv, dk and dq, over the states of two of them.
+int lin_walks(bool backward) { return backward ? 3 : 1; }
+
+// One set of segment states.
+size_t lin_states_bytes(const LinShape &s, bool backward)
 {
     int32_t nseg, len;
-    lin_segments(s, &nseg, &len);
+    lin_segments(s, lin_walks(backward), &nseg, &len);
     return nseg > 1 ? sizeof(float) * (size_t)(s.B * s.H * nseg * s.Dk * s.Dv) : 0;
 }
 
@@ -124,12 +129,13 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 size_t lin_workspace(const LinShape &s, bool backward)
 {
-    return align256(lin_states_bytes(s)) + (backward ? align256(lin_part_bytes(s)) : 0);
+    const size_t states = align256(lin_states_bytes(s, backward));
+    return backward ? 2 * states + 2 * align256(lin_part_bytes(s)) : states;
 }
 
 // What every pass over these heads shares.
-gconv::LinWalk lin_base(const LinShape &s, const float *log_decay, const int32_t *lengths, gconv_dtype_t dtype,
-                        void *stream)
+gconv::LinWalk lin_base(const LinShape &s, bool backward, const float *log_decay, const int32_t *lengths,
+                        gconv_dtype_t dtype, void *stream)
 {
     gconv::LinWalk p = {};
     p.B = (int32_t)s.B; p.T = (int32_t)s.T; p.H = (int32_t)s.H;
@@ -137,7 +143,7 @@ gconv::LinWalk lin_base(const LinShape &s, const float *log_decay, const int32_t
     p.lengths = lengths;
     p.dtype = (int)dtype;
     p.stream = (hipStream_t)stream;
-    lin_segments(s, &p.nseg, &p.seg_len);
+    lin_segments(s, lin_walks(backward), &p.nseg, &p.seg_len);
     return p;
 }
 
@@ -228,7 +234,10 @@ gconv_status_t gconv_linear_attention(const void *q, const void *k, const void *
     };
     if ((st = check_ranges(r, sizeof(r) / sizeof(r[0]))) != GCONV_OK) return st;
     if (s.B == 0) return done(hipSuccess, "");
-    gconv::LinWalk p = lin_base(s, log_decay, lengths, dtype, hip_stream);
+    gconv::LinWalks all = {};
+    all.count = 1;
+    gconv::LinWalk &p = all.w[0];
+    p = lin_base(s, false, log_decay, lengths, dtype, hip_stream);
     set_a(p, View{q, strides, s.Hk, s.Dk});
     set_b(p, View{k, strides + 3, s.Hk, s.Dk});
     set_c(p, View{v, strides + 6, s.H, s.Dv});
@@ -243,11 +252,11 @@ gconv_status_t gconv_linear_attention(const void *q, const void *k, const void *
     if (s.T == 0) {   // no token: the state stays
         if (!final_state) return done(hipSuccess, "");
         p.nseg = 0;
-        return done(gconv::launch_lin_scan(p), kname);
+        return done(gconv::launch_lin_scan(all), kname);
     }
     hipError_t err = hipSuccess;
-    if (p.nseg > 1) err = gconv::launch_lin_states(p, &kname);
-    if (err == hipSuccess) err = gconv::launch_lin_walk(p, &kname);
+    if (p.nseg > 1) err = gconv::launch_lin_states(all, &kname);
+    if (err == hipSuccess) err = gconv::launch_lin_walks(all, &kname);
     return done(err, kname);
 }
 
@@ -285,71 +294,83 @@ gconv_status_t gconv_linear_attention_backward(const void *q, const void *k, con
     const View vq{q, strides, s.Hk, s.Dk}, vk{k, strides + 3, s.Hk, s.Dk}, vv{v, strides + 6, s.H, s.Dv},
         vdo{d_o, strides + 9, s.H, s.Dv};
     const int32_t rep = (int32_t)(s.H / s.Hk);
-    float *states = (float *)workspace, *part = (float *)((char *)workspace + align256(lin_states_bytes(s)));
-    const char *kname = "lin_scan", *first = nullptr;
-    const gconv::LinWalk base = lin_base(s, log_decay, lengths, dtype, hip_stream);
+    const size_t nstates = align256(lin_states_bytes(s, true)), npart = align256(lin_part_bytes(s));
+    float *ahead = (float *)workspace, *behind = (float *)((char *)workspace + nstates);
+    char *part = (char *)workspace + 2 * nstates;
+    const char *kname = "lin_scan";
+    const gconv::LinWalk base = lin_base(s, true, log_decay, lengths, dtype, hip_stream);
+    gconv::LinWalks all = {};
+    all.count = 3;
+    gconv::LinWalk &pv = all.w[0], &pq = all.w[1], &pk = all.w[2];
 
     // Gradients of later tokens: states of q do^T from the end, which dv reads by row and
     // dk transposed; their value before the first token is the initial state's gradient.
-    gconv::LinWalk p = base;
-    set_a(p, vk);
-    set_b(p, vq);
-    set_c(p, vdo);
-    set_s0(p, dfinal, s, false);
-    set_sf(p, dinitial, s);
-    p.ws = states; p.wsr = s.Dv; p.wsc = 1;
-    p.p_scale = p.upd_scale = scale;
-    p.inter_scale = 1.0f;
-    p.e0 = 0;
-    p.reverse = 1;
+    pv = base;
+    set_a(pv, vk);
+    set_b(pv, vq);
+    set_c(pv, vdo);
+    set_s0(pv, dfinal, s, false);
+    set_sf(pv, dinitial, s);
+    pv.ws = behind; pv.wsr = s.Dv; pv.wsc = 1;
+    pv.p_scale = pv.upd_scale = scale;
+    pv.inter_scale = 1.0f;
+    pv.e0 = 0;
+    pv.reverse = 1;
     if (s.T == 0) {
         if (!dinitial) return done(hipSuccess, "");
-        p.nseg = 0;
-        return done(gconv::launch_lin_scan(p), kname);
+        pv.nseg = 0;
+        all.count = 1;
+        return done(gconv::launch_lin_scan(all), kname);
     }
-    hipError_t err = hipSuccess;
-    if (p.nseg > 1) err = gconv::launch_lin_states(p, &kname);
-    p.out = dv; p.osb = strides[18]; p.ost = strides[19]; p.osh = strides[20];
-    if (err == hipSuccess) err = gconv::launch_lin_walk(p, &first);
+    pv.out = dv; pv.osb = strides[18]; pv.ost = strides[19]; pv.osh = strides[20];
+
+    // Gradient of q: the forward states, transposed.
+    pq = base;
+    set_a(pq, vdo);
+    set_b(pq, vv);
+    set_c(pq, vk);
+    set_s0(pq, initial_state, s, true);
+    pq.ws = ahead; pq.wsr = s.Dk; pq.wsc = 1;
+    pq.p_scale = pq.inter_scale = scale;
+    pq.upd_scale = 1.0f;
+    pq.e0 = 1;
+
+    pk = pv;
+    set_a(pk, vv);
+    set_b(pk, vdo);
+    set_c(pk, vq);
+    set_s0(pk, dfinal, s, true);
+    pk.sf = nullptr;
+    pk.wsr = 1; pk.wsc = s.Dv;
 
     // A key head that serves several value heads: each writes its share in fp32, then the
     // shares are added and rounded once.
-    auto key_grad = [&](gconv::LinWalk &w, void *out, const int64_t *st) {
-        if (err != hipSuccess) return;
-        if (rep == 1) {
-            w.out = out; w.osb = st[0]; w.ost = st[1]; w.osh = st[2];
-            err = gconv::launch_lin_walk(w, &kname);
-            return;
-        }
-        w.out = part;
+    auto key_grad = [&](gconv::LinWalk &w, void *out, const int64_t *st, float *shares) {
+        w.out = out; w.osb = st[0]; w.ost = st[1]; w.osh = st[2];
+        if (rep == 1) return;
+        w.out = shares;
         w.osb = s.T * s.H * s.Dk; w.ost = s.H * s.Dk; w.osh = s.Dk;
         w.out_f32 = 1;
-        err = gconv::launch_lin_walk(w, &kname);
-        if (err == hipSuccess)
-            err = gconv::launch_lin_group_sum(part, out, st, s.B, s.T, (int)s.Hk, rep, (int)s.Dk, (int)dtype, base.stream);
     };
-    gconv::LinWalk w = p;
-    set_a(w, vv);
-    set_b(w, vdo);
-    set_c(w, vq);
-    set_s0(w, dfinal, s, true);
-    w.sf = nullptr;
-    w.wsr = 1; w.wsc = s.Dv;
-    key_grad(w, dk, strides + 15);
-
-    // Gradient of q: the forward states, transposed.
-    w = base;
-    set_a(w, vdo);
-    set_b(w, vv);
-    set_c(w, vk);
-    set_s0(w, initial_state, s, true);
-    w.ws = states; w.wsr = s.Dk; w.wsc = 1;
-    w.p_scale = w.inter_scale = scale;
-    w.upd_scale = 1.0f;
-    w.e0 = 1;
-    if (err == hipSuccess && w.nseg > 1) err = gconv::launch_lin_states(w, &kname);
-    key_grad(w, dq, strides + 12);
-    return done(err, first);
+    key_grad(pq, dq, strides + 12, (float *)part);
+    key_grad(pk, dk, strides + 15, (float *)(part + npart));
+    hipError_t err = hipSuccess;
+    if (base.nseg > 1) {
+        gconv::LinWalks states = all;
+        states.count = 2;    // dk's are dv's
+        err = gconv::launch_lin_states(states, &kname);
+    }
+    if (err == hipSuccess) err = gconv::launch_lin_walks(all, &kname);
+    if (rep > 1) {
+        auto sum = [&](const void *shares, void *out, const int64_t *st) {
+            if (err == hipSuccess)
+                err = gconv::launch_lin_group_sum((const float *)shares, out, st, s.B, s.T, (int)s.Hk, rep, (int)s.Dk,
+                                                  (int)dtype, base.stream);
+        };
+        sum(part, dq, strides + 12);
+        sum(part + npart, dk, strides + 15);
+    }
+    return done(err, kname);
 }
 
 gconv_status_t gconv_linear_attention_step(const void *q, const void *k, const void *v, void *o, float *state,
