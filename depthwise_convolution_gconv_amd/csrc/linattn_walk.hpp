@@ -40,6 +40,8 @@ namespace gconv {
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -66,16 +68,21 @@ template <int NP> struct Part8 { bf16x8 p[NP]; };
 template <int NP> __device__ __forceinline__ Part8<NP> split8(const float (&x)[8])
 {
     Part8<NP> r;
-    float left[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) left[e] = x[e];
+    for (int e = 0; e < 8; e += 2) {
+        f32x2 left = {x[e], x[e + 1]};
 #pragma unroll
-    for (int q = 0; q < NP; ++q)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            r.p[q][e] = (__bf16)left[e];
-            if (q + 1 < NP) left[e] -= (float)r.p[q][e];
+        for (int q = 0; q < NP; ++q) {
+            const bf16x2 two = __builtin_convertvector(left, bf16x2);   // one instruction
+            r.p[q][e] = two[0];
+            r.p[q][e + 1] = two[1];
+            if (q + 1 < NP) {
+                const uint32_t bits = __builtin_bit_cast(uint32_t, two);
+                left[0] -= __builtin_bit_cast(float, bits << 16);
+                left[1] -= __builtin_bit_cast(float, bits & 0xffff0000u);
+            }
         }
+    }
     return r;
 }
 
@@ -118,25 +125,35 @@ template <int D, int NP> __device__ __forceinline__ Part8<NP> read_col(const __b
     return r;
 }
 
-// 8 elements on their way from memory to LDS.
-template <typename T> struct Raw8 { RunVec<T, 16 / (int)sizeof(T)> w[sizeof(T) / 2]; };
+// 8 elements on their way from memory to LDS, in loads of 16 bytes.
+template <typename T> struct Raw8 {
+    static constexpr int N = 16 / sizeof(T);     // elements of a load
+    RunVec<T, N> w[8 / N];
+};
 
-template <typename T> __device__ __forceinline__ Raw8<T> load8_whole(const T *src)
+// Where a row ends inside a load, the load ends with the row instead (rows of N columns or
+// more): offset of its address from the block's first column, and later the shift that puts
+// its elements in their places and zeros after them.  Both take the columns left from the
+// block's first one on; a load past the row's end reads the one before it.
+template <typename T> __device__ __forceinline__ int load_at(int left, int i)
 {
-    constexpr int N = 16 / sizeof(T);
-    Raw8<T> r;
-#pragma unroll
-    for (int i = 0; i < 8 / N; ++i) r.w[i] = *reinterpret_cast<const RunVec<T, N> *>(src + N * i);
-    return r;
+    constexpr int N = Raw8<T>::N;
+    if (left <= N * i) i = 0;
+    return N * i + min(left - N * i - N, 0);
 }
-
-template <typename T> __device__ __forceinline__ Raw8<T> load8(const T *src, int valid)
+template <typename T> __device__ __forceinline__ void shift_tail(Raw8<T> &r, int left)
 {
-    constexpr int N = 16 / sizeof(T);
-    Raw8<T> r;
+    constexpr int N = Raw8<T>::N;
 #pragma unroll
-    for (int i = 0; i < 8 / N; ++i) r.w[i] = load_words<T, N>(src + N * i, valid - N * i);
-    return r;
+    for (int i = 0; i < 8 / N; ++i) {
+        const int sh = min(max(N * i + N - left, 0), N) * (128 / N);
+        typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+        u64x2 v = __builtin_bit_cast(u64x2, r.w[i]);
+        const uint64_t lo = sh & 63 ? v[0] >> (sh & 63) | v[1] << (64 - (sh & 63)) : v[0], hi = v[1] >> (sh & 63);
+        v[0] = sh < 64 ? lo : sh < 128 ? hi : 0;
+        v[1] = sh < 64 ? hi : 0;
+        r.w[i] = __builtin_bit_cast(RunVec<T, N>, v);
+    }
 }
 
 // They go to their parts' tiles.
@@ -158,9 +175,9 @@ template <typename T, int D> __device__ __forceinline__ void stage8(__bf16 *t, i
 }
 
 // A thread's share of a tile of kLen tokens by D columns: NR runs of 8 of one column block,
-// every STEP tokens.
+// every STEP tokens.  Blocks past the last column are neither read nor staged.
 template <typename T, int D, int NTH> struct Share {
-    static constexpr int NR = kLen * D / 8 / NTH, STEP = NTH / (D / 8);
+    static constexpr int NR = kLen * D / 8 / NTH, STEP = NTH / (D / 8), N = Raw8<T>::N;
     Raw8<T> r[NR];
     const T *p;              // its first run of the next chunk
     int64_t step;            // elements from token to token of the walk
@@ -173,24 +190,43 @@ template <typename T, int D, int NTH> struct Share {
         step = reverse ? -stride : stride;
         p = base + d + (int64_t)(reverse ? n - 1 - u0 - j : u0 + j) * stride;
     }
-    // The chunk's `live` tokens; even: whole blocks only (columns divide by 8).
-    __device__ __forceinline__ void fetch(int live, bool even)
+    // A whole chunk of a row of N columns or more.
+    __device__ __forceinline__ void fetch()
     {
-        if (live >= kLen && even) {
+        if (left > 0) {
 #pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                r[i] = Raw8<T>{};
-                if (left > 0) r[i] = load8_whole<T>(p + i * STEP * step);
-            }
-        } else {
+            for (int i = 0; i < NR; ++i)
 #pragma unroll
-            for (int i = 0; i < NR; ++i) r[i] = load8<T>(p + i * STEP * step, j + i * STEP < live ? left : 0);
+                for (int e = 0; e < 8 / N; ++e)
+                    r[i].w[e] = *reinterpret_cast<const RunVec<T, N> *>(p + i * STEP * step + load_at<T>(left, e));
         }
         p += kLen * step;
     }
-    __device__ __forceinline__ void stage(__bf16 *t) const
+    // The chunk's first `live` tokens; narrow: a row of fewer columns, element by element.
+    __device__ __forceinline__ void fetch(int live, bool narrow)
     {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) r[i] = Raw8<T>{};
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            if (left <= 0 || j + i * STEP >= live) continue;
+#pragma unroll
+            for (int e = 0; e < 8 / N; ++e) {
+                if (!narrow) r[i].w[e] = *reinterpret_cast<const RunVec<T, N> *>(p + i * STEP * step + load_at<T>(left, e));
+                else if (e == 0) r[i].w[e] = load_words<T, N>(p + i * STEP * step, left);
+            }
+        }
+        p += kLen * step;
+    }
+    // shift: row ends inside a load have to be moved (not for narrow rows).
+    __device__ __forceinline__ void stage(__bf16 *t, bool shift)
+    {
+        if (left <= 0) return;
         const int d = threadIdx.x % (D / 8) * 8;
+        if (shift) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) shift_tail<T>(r[i], left);
+        }
 #pragma unroll
         for (int i = 0; i < NR; ++i) stage8<T, D>(t, Tile<D>::at(j + i * STEP, d), r[i]);
     }
@@ -208,6 +244,7 @@ template <typename TO> __device__ __forceinline__ void store_tile(TO *o, int lef
 
 template <typename T, int DK, int NW, bool FULL> struct WalkLds {
     static constexpr int NP = kParts<T>;
+    static constexpr int tiles = 2 * NP * ((FULL ? 2 : 1) * Tile<DK>::size + Tile<32 * NW>::size) + (FULL ? 0 : 16);
     __bf16 a[FULL ? NP * Tile<DK>::size : 8];
     __bf16 b[NP * Tile<DK>::size];
     __bf16 c[NP * Tile<32 * NW>::size];
@@ -226,8 +263,9 @@ __global__ void __launch_bounds__(64 * NW, (kWavesPerSimd<T, DK, NW>))
 lin_walk(const LinWalks all)
 {
     constexpr int NP = kParts<T>, L = kLen, NT = 32 * NW, NTH = 64 * NW;
+    typedef WalkLds<T, DK, NW, FULL> Lds;
     constexpr int NX = DK / 32, NS = DK / 16, NG = L / 16;          // state tiles, steps along columns, along tokens
-    __shared__ __attribute__((aligned(16))) WalkLds<T, DK, NW, FULL> sm;
+    __shared__ __attribute__((aligned(16))) Lds sm;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l32 = lane & 31, half = lane >> 5;
 
     // Workgroups go round the 8 XCDs; a contiguous run of ids on one XCD keeps the column
@@ -248,7 +286,10 @@ lin_walk(const LinWalks all)
     const int utop = min(useg + p.seg_len, FULL ? p.T : n);   // tokens [useg, utop) of this workgroup
     const int ulive = min(n, utop);
     const bool mine = n0 + wave * 32 < p.Dc;                  // this wave has columns
-    const bool even = p.Da % 8 == 0 && p.Dc % 8 == 0;
+    // Row ends inside a load, and rows shorter than one.
+    constexpr int N = Raw8<T>::N;
+    const bool narrow_ab = p.Da < N, narrow_c = p.Dc < N, narrow = narrow_ab || narrow_c;
+    const bool shift_ab = p.Da % 8 != 0 && !narrow_ab, shift_c = p.Dc % 8 != 0 && !narrow_c;
 
     Share<T, DK, NTH> sa, sb;
     Share<T, NT, NTH> sc;
@@ -257,11 +298,22 @@ lin_walk(const LinWalks all)
     sb.init((const T *)p.b + bi * p.bsb + (h / p.rb) * p.bsh, p.bst, p.Da, useg, n, p.reverse);
     sc.init((const T *)p.c + bi * p.csb + (h / p.rc) * p.csh + n0, p.cst, p.Dc - n0, useg, n, p.reverse);
     auto fetch = [&](int u0) {
-        if constexpr (FULL) sa.fetch(ulive - u0, even);
-        sb.fetch(ulive - u0, even);
-        sc.fetch(ulive - u0, even);
+        const int live = ulive - u0;
+        if (live >= L && !narrow) {
+            if constexpr (FULL) sa.fetch();
+            sb.fetch();
+            sc.fetch();
+        } else {
+            if constexpr (FULL) sa.fetch(live, narrow_ab);
+            sb.fetch(live, narrow_ab);
+            sc.fetch(live, narrow_c);
+        }
     };
     fetch(useg);
+    {   // columns past the last stay zero
+        u32x4 *z = reinterpret_cast<u32x4 *>(&sm);
+        for (int e = tid; e < Lds::tiles / 16; e += NTH) z[e] = u32x4{0, 0, 0, 0};
+    }
     if (tid <= L) sm.pw[tid] = lin_pow(p.log_decay[h], tid);
 
     // The state: column scol, rows 4 half + 32 x + 8 (r / 4) + r % 4 of the tiles, which stand
@@ -315,9 +367,9 @@ lin_walk(const LinWalks all)
     for (int u0 = useg; u0 < utop; u0 += L) {
         const int m = max(0, min(n - u0, L));
         // The previous chunk's readers are done (barrier at the loop's end).
-        if constexpr (FULL) sa.stage(sm.a);
-        sb.stage(sm.b);
-        sc.stage(sm.c);
+        if constexpr (FULL) sa.stage(sm.a, shift_ab);
+        sb.stage(sm.b, shift_ab);
+        sc.stage(sm.c, shift_c);
         if (m != mset) {
             if (tid < L) sm.upd[tid] = p.upd_scale * sm.pw[max(m - tid - p.e0, 0)];
             mset = m;
