@@ -12,15 +12,16 @@ namespace {
 constexpr int kThreads = 256;
 // States before each segment from the segments' own sums, in place:
 //     R_(g+1) = lam^(tokens of g) R_g + local_g,  R_0 = s0.
-// One thread for each state element, 8 segments' loads in flight.
+// Two neighbouring elements for each thread, 8 segments' loads in flight.
 constexpr int kMaxSeg = 1024;
+constexpr int kScan = 2;
 __global__ void __launch_bounds__(kThreads)
 lin_scan(const LinWalks all)
 {
     __shared__ float lam[kMaxSeg];
     const int tid = threadIdx.x;
     // Every walk's states have as many elements.
-    const int64_t cells = (int64_t)all.w[0].Da * all.w[0].Dc, tiles = (cells + kThreads - 1) / kThreads;
+    const int64_t cells = (int64_t)all.w[0].Da * all.w[0].Dc, tiles = (cells + kScan * kThreads - 1) / (kScan * kThreads);
     const LinWalk &p = all.w[blockIdx.x / all.blocks];
     const int64_t bh = blockIdx.x % all.blocks / tiles;
     const int h = (int)(bh % p.H), bi = (int)(bh / p.H);
@@ -28,23 +29,35 @@ lin_scan(const LinWalks all)
     for (int g = tid; g < p.nseg; g += kThreads)
         lam[g] = lin_pow(p.log_decay[h], max(0, min(n - g * p.seg_len, p.seg_len)));
     __syncthreads();
-    const int64_t x = (blockIdx.x % all.blocks % tiles) * kThreads + tid;
-    if (x >= cells) return;
-    const int64_t d = x / p.Dc, c = x % p.Dc;
-    float r = p.s0 ? p.s0[bi * p.s0b + h * p.s0h + d * p.s0r + c * p.s0c] : 0.0f;
+    const int64_t x = ((blockIdx.x % all.blocks % tiles) * kThreads + tid) * kScan;
+    const int left = (int)min(cells - x, (int64_t)kScan);
+    if (left <= 0) return;
+    float r[kScan];
+#pragma unroll
+    for (int e = 0; e < kScan; ++e) {
+        const int64_t d = (x + e) / p.Dc, c = (x + e) % p.Dc;
+        r[e] = p.s0 && e < left ? p.s0[bi * p.s0b + h * p.s0h + d * p.s0r + c * p.s0c] : 0.0f;
+    }
     float *w = p.ws + bh * p.nseg * cells + x;
     for (int g0 = 0; g0 < p.nseg; g0 += 8) {
-        float loc[8];
+        float loc[8][kScan];
 #pragma unroll
-        for (int g = 0; g < 8; ++g) loc[g] = g0 + g < p.nseg ? w[(g0 + g) * cells] : 0.0f;
+        for (int g = 0; g < 8; ++g) load_run<float, kScan>(w + (g0 + g) * cells, g0 + g < p.nseg ? left : 0, loc[g]);
 #pragma unroll
         for (int g = 0; g < 8; ++g)
             if (g0 + g < p.nseg) {
-                w[(g0 + g) * cells] = r;
-                r = fmaf(lam[g0 + g], r, loc[g]);
+                store_run<float, kScan>(w + (g0 + g) * cells, left, r);
+#pragma unroll
+                for (int e = 0; e < kScan; ++e) r[e] = fmaf(lam[g0 + g], r[e], loc[g][e]);
             }
     }
-    if (p.sf) p.sf[bi * p.sfb + h * p.sfh + d * p.sfr + c * p.sfc] = r;
+    if (p.sf) {
+#pragma unroll
+        for (int e = 0; e < kScan; ++e) {
+            const int64_t d = (x + e) / p.Dc, c = (x + e) % p.Dc;
+            if (e < left) p.sf[bi * p.sfb + h * p.sfh + d * p.sfr + c * p.sfc] = r[e];
+        }
+    }
 }
 
 template <typename T>
@@ -140,7 +153,7 @@ hipError_t launch_lin_scan(const LinWalks &walks)
 {
     LinWalks all = walks;
     const LinWalk &p = all.w[0];
-    all.blocks = (int64_t)p.B * p.H * ceil_div((int64_t)p.Da * p.Dc, kThreads);
+    all.blocks = (int64_t)p.B * p.H * ceil_div((int64_t)p.Da * p.Dc, kScan * kThreads);
     if (all.count * all.blocks >= (int64_t(1) << 31) || p.nseg > kMaxSeg) return hipErrorInvalidValue;
     hipLaunchKernelGGL(lin_scan, dim3((unsigned)(all.count * all.blocks)), dim3(kThreads), 0, p.stream, all);
     return hipGetLastError();
@@ -170,7 +183,7 @@ hipError_t launch_lin_states(const LinWalks &all, const char **kname)
 {
     *kname = "lin_walk";
     const hipError_t err = run_walks(all, false);
-    return err != hipSuccess ? err : launch_lin_scan(all);
+    return err != hipSuccess || all.w[0].nseg <= kFoldSegs ? err : launch_lin_scan(all);
 }
 
 hipError_t launch_lin_walks(const LinWalks &all, const char **kname)

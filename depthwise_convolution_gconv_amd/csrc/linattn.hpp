@@ -78,10 +78,14 @@ hipError_t run_lin_walks_f32(const LinWalks &all, bool full);
 hipError_t run_lin_walks_f16(const LinWalks &all, bool full);
 hipError_t run_lin_walks_bf16(const LinWalks &all, bool full);
 
-// The segment states (nseg > 1): local sums into ws, then the scan that turns them into
-// the states before each segment and writes sf.
+// Up to this many segments, each walk adds up the local states before its own, and the last
+// one writes sf: a mean of half as many reads as there are segments, and no scan.
+constexpr int kFoldSegs = 8;
+
+// The segment states (nseg > 1): local sums into ws, then past kFoldSegs the scan that turns
+// them into the states before each segment and writes sf.
 hipError_t launch_lin_states(const LinWalks &all, const char **kname);
-// The outputs (with nseg == 1 also sf).
+// The outputs (up to kFoldSegs also sf).
 hipError_t launch_lin_walks(const LinWalks &all, const char **kname);
 // Scan alone (T == 0 or nseg segments already summed).
 hipError_t launch_lin_scan(const LinWalks &all);

@@ -180,14 +180,15 @@ template <typename T, int D, int NTH> struct Share {
     static constexpr int NR = kLen * D / 8 / NTH, STEP = NTH / (D / 8), N = Raw8<T>::N;
     Raw8<T> r[NR];
     const T *p;              // its first run of the next chunk
-    int64_t step;            // elements from token to token of the walk
+    int64_t step, chunk;     // elements from token to token of the walk, from chunk to chunk
     int j, left;             // first token; columns from its block on
-    __device__ __forceinline__ void init(const T *base, int64_t stride, int cols, int u0, int n, int reverse)
+    __device__ __forceinline__ void init(const T *base, int64_t stride, int cols, int u0, int du, int n, int reverse)
     {
         const int d = threadIdx.x % (D / 8) * 8;
         j = threadIdx.x / (D / 8);
         left = cols - d;
         step = reverse ? -stride : stride;
+        chunk = du * step;
         p = base + d + (int64_t)(reverse ? n - 1 - u0 - j : u0 + j) * stride;
     }
     // A whole chunk of a row of N columns or more.
@@ -200,7 +201,7 @@ template <typename T, int D, int NTH> struct Share {
                 for (int e = 0; e < 8 / N; ++e)
                     r[i].w[e] = *reinterpret_cast<const RunVec<T, N> *>(p + i * STEP * step + load_at<T>(left, e));
         }
-        p += kLen * step;
+        p += chunk;
     }
     // The chunk's first `live` tokens; narrow: a row of fewer columns, element by element.
     __device__ __forceinline__ void fetch(int live, bool narrow)
@@ -216,7 +217,7 @@ template <typename T, int D, int NTH> struct Share {
                 else if (e == 0) r[i].w[e] = load_words<T, N>(p + i * STEP * step, left);
             }
         }
-        p += kLen * step;
+        p += chunk;
     }
     // shift: row ends inside a load have to be moved (not for narrow rows).
     __device__ __forceinline__ void stage(__bf16 *t, bool shift)
@@ -232,13 +233,32 @@ template <typename T, int D, int NTH> struct Share {
     }
 };
 
-// A lane's 16 values of a token, four columns of every eight.
-template <typename TO> __device__ __forceinline__ void store_tile(TO *o, int left, const f32x16 &acc)
+// A lane's 16 values of a token: four columns of every eight.  Of two 16-bit runs the lane
+// gives one to the other half's lane and takes the rest of the other, so stores are 16 bytes.
+template <typename TO> __device__ __forceinline__ void store_tile(TO *o, int half, int left, const f32x16 &acc)
 {
+    if constexpr (sizeof(TO) == 4) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const float f[4] = {acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
-        if (left > 8 * g) store_run<TO, 4>(o + 8 * g, left - 8 * g, f);
+        for (int g = 0; g < 4; ++g) {
+            const float f[4] = {acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
+            const int at = 8 * g + 4 * half;
+            if (left > at) store_run<TO, 4>(o + at, left - at, f);
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+            union { Run<TO, 8> v; uint32_t w[4]; } x;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x.v.v[e] = from_f32<TO>(acc[4 * g + e]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const auto y = __builtin_amdgcn_permlane32_swap(x.w[i], x.w[2 + i], false, false);
+                x.w[i] = y[0];
+                x.w[2 + i] = y[1];
+            }
+            const int at = 8 * g + 8 * half;
+            if (left > at) store_raw<TO, 8>(o + at, left - at, x.v);
+        }
     }
 }
 
@@ -285,6 +305,11 @@ lin_walk(const LinWalks all)
     const int useg = seg * p.seg_len;
     const int utop = min(useg + p.seg_len, FULL ? p.T : n);   // tokens [useg, utop) of this workgroup
     const int ulive = min(n, utop);
+    // Outputs go from the first chunk on.  Local states go from the last one back: each chunk
+    // then adds its tokens with their weights at the segment's end, the state itself is never
+    // scaled, and what was read last, the segments' first halves, is what the outputs' walk
+    // finds in the last-level cache.
+    const int nchunk = (utop - useg + L - 1) / L, ufirst = FULL ? useg : useg + (nchunk - 1) * L, du = FULL ? L : -L;
     const bool mine = n0 + wave * 32 < p.Dc;                  // this wave has columns
     // Row ends inside a load, and rows shorter than one.
     constexpr int N = Raw8<T>::N;
@@ -294,9 +319,9 @@ lin_walk(const LinWalks all)
     Share<T, DK, NTH> sa, sb;
     Share<T, NT, NTH> sc;
     if constexpr (FULL)
-        sa.init((const T *)p.a + bi * p.asb + (h / p.ra) * p.ash, p.ast, p.Da, useg, n, p.reverse);
-    sb.init((const T *)p.b + bi * p.bsb + (h / p.rb) * p.bsh, p.bst, p.Da, useg, n, p.reverse);
-    sc.init((const T *)p.c + bi * p.csb + (h / p.rc) * p.csh + n0, p.cst, p.Dc - n0, useg, n, p.reverse);
+        sa.init((const T *)p.a + bi * p.asb + (h / p.ra) * p.ash, p.ast, p.Da, ufirst, du, n, p.reverse);
+    sb.init((const T *)p.b + bi * p.bsb + (h / p.rb) * p.bsh, p.bst, p.Da, ufirst, du, n, p.reverse);
+    sc.init((const T *)p.c + bi * p.csb + (h / p.rc) * p.csh + n0, p.cst, p.Dc - n0, ufirst, du, n, p.reverse);
     auto fetch = [&](int u0) {
         const int live = ulive - u0;
         if (live >= L && !narrow) {
@@ -309,7 +334,6 @@ lin_walk(const LinWalks all)
             sc.fetch(live, narrow_c);
         }
     };
-    fetch(useg);
     {   // columns past the last stay zero
         u32x4 *z = reinterpret_cast<u32x4 *>(&sm);
         for (int e = tid; e < Lds::tiles / 16; e += NTH) z[e] = u32x4{0, 0, 0, 0};
@@ -319,33 +343,40 @@ lin_walk(const LinWalks all)
     // The state: column scol, rows 4 half + 32 x + 8 (r / 4) + r % 4 of the tiles, which stand
     // for the columns of b that d_of gives.
     const int scol = n0 + wave * 32 + l32;
-    auto d_of = [&](int x, int r) { return 32 * x + 16 * (r / 8) + 8 * half + 4 * (r / 4 % 2) + r % 4; };
+    auto d_of = [](int x, int r) { return 32 * x + 16 * (r / 8) + 4 * (r / 4 % 2) + r % 4; };     // + 8 half
     f32x16 st[NX];
-    const float *sp = nullptr;
-    int64_t sr = 0, scs = 0;
-    if (FULL && p.nseg > 1) {
-        sp = p.ws + (bh * p.nseg + seg) * (int64_t)p.Da * p.Dc;
-        sr = p.wsr; scs = p.wsc;
-    } else if (FULL && p.s0) {
-        sp = p.s0 + bi * p.s0b + h * p.s0h;
-        sr = p.s0r; scs = p.s0c;
-    }
-    if (sp && scol < p.Dc) {
-        sp += scol * scs;
+    auto read_state = [&](const float *sp, int sr, int sc, float keep) {   // st = keep st + *sp
+        int d0 = 8 * half;
+        asm volatile("" : "+v"(d0));     // the offsets are made here, not kept from call to call
 #pragma unroll
-        for (int x = 0; x < NX; ++x)
+        for (int x = 0; x < NX; ++x) {
+            float v[16];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {     // rows past the last read that one
-                const float v = sp[min(d_of(x, r), p.Da - 1) * sr];
-                st[x][r] = d_of(x, r) < p.Da ? v : 0.0f;
+            for (int r = 0; r < 16; ++r)       // rows past the last read that one
+                v[r] = sp[min(d0 + d_of(x, r), p.Da - 1) * sr + scol * sc];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                asm volatile("" : "+v"(v[r]));     // a load inside the condition would wait for each
+                st[x][r] = d0 + d_of(x, r) < p.Da ? fmaf(keep, st[x][r], v[r]) : 0.0f;
             }
-    } else {
+        }
+    };
 #pragma unroll
-        for (int x = 0; x < NX; ++x)
+    for (int x = 0; x < NX; ++x)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) st[x][r] = 0.0f;
+        for (int r = 0; r < 16; ++r) st[x][r] = 0.0f;
+    const bool fold = p.nseg <= kFoldSegs, ends = FULL && fold && p.sf && seg + 1 == p.nseg;
+    if (FULL && scol < p.Dc) {
+        const int64_t cells = (int64_t)p.Da * p.Dc;
+        if (p.s0 && fold) read_state(p.s0 + bi * p.s0b + h * p.s0h, (int)p.s0r, (int)p.s0c, 0.0f);
+        const int last = fold ? seg : seg + 1;     // else the scan has summed them up
+        #pragma unroll 1
+        for (int g = fold ? 0 : seg; g < last; ++g)
+            read_state(p.ws + (bh * p.nseg + g) * cells, (int)p.wsr, (int)p.wsc,
+                       fold ? lin_pow(p.log_decay[h], max(0, min(n - g * p.seg_len, p.seg_len))) : 0.0f);
     }
 
+    if (nchunk > 0) fetch(ufirst);
     __syncthreads();     // the powers
     if constexpr (FULL) {
         for (int e = tid; e < 16 * 64; e += NTH) {
@@ -363,19 +394,22 @@ lin_walk(const LinWalks all)
     const int bcol_at = Tile<DK>::at(col_row, (lane & 16) + (lane & 1) * 8 + (lane & 2) * 2);
     const int ccol_at = Tile<NT>::at(col_row, 32 * wave + col_d);
 
-    int mset = -1;
-    for (int u0 = useg; u0 < utop; u0 += L) {
-        const int m = max(0, min(n - u0, L));
+    // Outputs: the state is scale times its registers, so that it need not be scaled for every
+    // chunk's decay.  Local states: scale is the weight of the next chunk's last token.
+    float scale = 1.0f;
+    for (int k = 0; k < nchunk; ++k) {
+        const int u0 = ufirst + k * du;
+        const int m = max(0, min(ulive - u0, L));
+        const float faded = scale * sm.pw[m];
+        const bool settle = FULL && !(faded >= 0x1p-10f && faded <= 0x1p10f);   // registers take the scale
         // The previous chunk's readers are done (barrier at the loop's end).
         if constexpr (FULL) sa.stage(sm.a, shift_ab);
         sb.stage(sm.b, shift_ab);
         sc.stage(sm.c, shift_c);
-        if (m != mset) {
-            if (tid < L) sm.upd[tid] = p.upd_scale * sm.pw[max(m - tid - p.e0, 0)];
-            mset = m;
-        }
+        if (tid < L)
+            sm.upd[tid] = p.upd_scale * sm.pw[max(m - tid - p.e0, 0)] * (!FULL ? scale : settle ? 1.0f : 1.0f / faded);
         __syncthreads();
-        if (u0 + L < utop) fetch(u0 + L);
+        if (k + 1 < nchunk) fetch(u0 + du);
 
         if (FULL && mine) {
             f32x16 acc;
@@ -395,7 +429,7 @@ lin_walk(const LinWalks all)
                     sco = mma<NP - 1>(read_row<DK, NP>(sm.b, row_at + 16 * s), aq, sco);
                     acc = mma<NP - 1>(split8<NP>(f), aq, acc);
                 }
-                const float fi = p.inter_scale * sm.pw[min(l32 + p.e0, L)];
+                const float fi = scale * p.inter_scale * sm.pw[min(l32 + p.e0, L)];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[r] *= fi;
 #pragma unroll
@@ -422,21 +456,23 @@ lin_walk(const LinWalks all)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[r] = l32 < m ? acc[r] : 0.0f;
             }
+            // Both lanes of a token store or neither: they hold each other's values.
             const int u = u0 + l32;
             if (u < utop) {
-                const int64_t at = bi * p.osb + (int64_t)lin_token(p, u, n) * p.ost + h * p.osh + n0 + wave * 32 + 4 * half;
-                const int left = p.Dc - n0 - wave * 32 - 4 * half;
-                if (sizeof(T) == 4 || p.out_f32) store_tile<float>((float *)p.out + at, left, acc);
-                else store_tile<T>((T *)p.out + at, left, acc);
+                const int64_t at = bi * p.osb + (int64_t)lin_token(p, u, n) * p.ost + h * p.osh + n0 + wave * 32;
+                const int left = p.Dc - n0 - wave * 32;
+                if (sizeof(T) == 4 || p.out_f32) store_tile<float>((float *)p.out + at, half, left, acc);
+                else store_tile<T>((T *)p.out + at, half, left, acc);
             }
         }
 
-        if (mine && m > 0 && (!FULL || u0 + L < utop || (p.nseg == 1 && p.sf))) {
-            const float lm = sm.pw[m];
+        if (mine && m > 0 && (!FULL || k + 1 < nchunk || ends)) {
+            if (settle) {
 #pragma unroll
-            for (int x = 0; x < NX; ++x)
+                for (int x = 0; x < NX; ++x)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) st[x][r] *= lm;
+                    for (int r = 0; r < 16; ++r) st[x][r] *= faded;
+            }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const Part8<NP> cT = read_col<NT, NP>(sm.c, ccol_at + 4 * g * Tile<NT>::group);
@@ -454,28 +490,28 @@ lin_walk(const LinWalks all)
                     st[x] = mma<2>(read_col<DK, NP>(sm.b, bcol_at + 4 * g * Tile<DK>::group + 32 * x), wc, st[x]);
             }
         }
+        scale = settle ? 1.0f : faded;
         __syncthreads();
     }
 
     float *dp = nullptr;
-    int64_t dr = 0, dc = 0;
+    int dr = 0, dc = 0;      // a state's offsets stay below 2^16
     if (!FULL) {
         dp = p.ws + (bh * p.nseg + seg) * (int64_t)p.Da * p.Dc;
-        dr = p.wsr; dc = p.wsc;
-    } else if (p.nseg == 1 && p.sf) {
+        dr = (int)p.wsr; dc = (int)p.wsc;
+    } else if (ends) {
         dp = p.sf + bi * p.sfb + h * p.sfh;
-        dr = p.sfr; dc = p.sfc;
+        dr = (int)p.sfr; dc = (int)p.sfc;
     }
     if (dp && scol < p.Dc) {
         int d0 = 8 * half;
-        asm("" : "+v"(d0));      // the addresses are made here, not kept through the walk
-        dp += d0 * dr + scol * dc;
+        asm volatile("" : "+v"(d0));
 #pragma unroll
         for (int x = 0; x < NX; ++x)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int d = 32 * x + 16 * (r / 8) + 4 * (r / 4 % 2) + r % 4;
-                if (d0 + d < p.Da) dp[d * dr] = st[x][r];
+                const int d = d0 + d_of(x, r);
+                if (d < p.Da) dp[d * dr + scol * dc] = FULL ? st[x][r] * scale : st[x][r];
             }
     }
 }
