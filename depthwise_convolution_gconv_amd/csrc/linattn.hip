@@ -159,14 +159,14 @@ hipError_t launch_lin_scan(const LinWalks &walks)
     return hipGetLastError();
 }
 
-// One launch for the walks of each class.
+// One launch for walks that are alike.
 static hipError_t run_walks(const LinWalks &all, bool full)
 {
     for (int i = 0; i < all.count; ++i) {
         LinWalks some = {};
         bool first = true;
         for (int j = 0; j < all.count; ++j)
-            if (lin_class(all.w[j]) == lin_class(all.w[i])) {
+            if (lin_alike(all.w[j], all.w[i])) {
                 first = first && j >= i;
                 some.w[some.count++] = all.w[j];
             }

@@ -35,8 +35,7 @@ struct LinWalk {
     float p_scale, inter_scale, upd_scale;
     int32_t e0, reverse;
     int32_t nseg, seg_len;       // segments of seg_len tokens (a multiple of 64), walked by one workgroup each
-    int32_t ndv;                 // column tiles of c
-    int64_t blocks;              // workgroups
+    int32_t rep;                 // value heads for each key head
     int dtype;                   // of a, b, c
     int out_f32;                 // out is fp32 (partial gradients of a shared head) rather than dtype
     hipStream_t stream;
@@ -63,17 +62,14 @@ constexpr int kMaxWalks = 3;
 struct LinWalks {
     LinWalk w[kMaxWalks];
     int32_t count;
-    int64_t blocks;
+    int32_t ndv;                 // column tiles of c
+    int64_t blocks;              // workgroups
 };
 
-// Which kernel walks p: columns of a and of c that a workgroup holds.  Two waves where 64
-// columns are all there are, but for wide rows: their staging is shared by four.
-inline int lin_class(const LinWalk &p)
-{
-    return p.Da > 128 ? 4 : 2 * (p.Da > 64) + (p.Dc > 64);
-}
+// Walks of the same column counts: one kernel and one number of workgroups for each.
+inline bool lin_alike(const LinWalk &p, const LinWalk &q) { return p.Da == q.Da && p.Dc == q.Dc; }
 
-// The walks of all segments, outputs (full) or local states only, for each dtype; all of one class.
+// The walks of all segments, outputs (full) or local states only, for each dtype; all alike.
 hipError_t run_lin_walks_f32(const LinWalks &all, bool full);
 hipError_t run_lin_walks_f16(const LinWalks &all, bool full);
 hipError_t run_lin_walks_bf16(const LinWalks &all, bool full);

@@ -288,21 +288,22 @@ lin_walk(const LinWalks all)
     typedef WalkLds<T, DK, NW, FULL> Lds;
     constexpr int NX = DK / 32, NS = DK / 16, NG = L / 16;          // state tiles, steps along columns, along tokens
     __shared__ __attribute__((aligned(16))) Lds sm;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l32 = lane & 31, half = lane >> 5;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, l32 = lane & 31, half = lane >> 5;
 
-    // Workgroups go round the 8 XCDs; a contiguous run of ids on one XCD keeps the column
-    // tiles and heads that share a's and b's rows on one L2.
+    // Workgroups go round the 8 XCDs, a contiguous run of ids on each.  Neighbours read the same
+    // rows: column tiles, a launch's walks, the value heads of a key head.
     const int64_t per = (all.blocks + 7) / 8;
     int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if (id >= all.blocks) return;
-    int which = 0;
-    while (id >= all.w[which].blocks) id -= all.w[which++].blocks;
-    const LinWalk &p = all.w[which];
-    const int dv = (int)(id % p.ndv);
-    id /= p.ndv;
-    const int seg = (int)(id % p.nseg);
-    const int64_t bh = id / p.nseg;
-    const int h = (int)(bh % p.H), bi = (int)(bh / p.H);
+    auto next = [&](int count) {
+        const int x = (int)(id % count);
+        id /= count;
+        return x;
+    };
+    const int dv = next(all.ndv);
+    const LinWalk &p = all.w[next(all.count)];
+    const int hr = next(p.rep), seg = next(p.nseg), h = next(p.H / p.rep) * p.rep + hr, bi = (int)id;
+    const int64_t bh = (int64_t)bi * p.H + h;
     const int n = lin_len(p, bi), n0 = dv * NT;
     const int useg = seg * p.seg_len;
     const int utop = min(useg + p.seg_len, FULL ? p.T : n);   // tokens [useg, utop) of this workgroup
@@ -540,29 +541,23 @@ lin_walk(const LinWalks all)
 
 template <typename T, int DK, int NW, bool FULL> hipError_t run_walk_on(LinWalks all)
 {
-    all.blocks = 0;
-    for (int i = 0; i < all.count; ++i) {
-        LinWalk &p = all.w[i];
-        p.ndv = (int32_t)ceil_div(p.Dc, 32 * NW);
-        p.blocks = (int64_t)p.B * p.H * p.nseg * p.ndv;
-        all.blocks += p.blocks;
-    }
+    const LinWalk &p = all.w[0];
+    all.ndv = (int32_t)ceil_div(p.Dc, 32 * NW);
+    all.blocks = (int64_t)all.count * p.B * p.H * p.nseg * all.ndv;
     const int64_t grid = 8 * ceil_div(all.blocks, 8);
     if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((lin_walk<T, DK, NW, FULL>), dim3((unsigned)grid), dim3(64 * NW), 0, all.w[0].stream, all);
+    hipLaunchKernelGGL((lin_walk<T, DK, NW, FULL>), dim3((unsigned)grid), dim3(64 * NW), 0, p.stream, all);
     return hipGetLastError();
 }
 
-// The walks of `all` have Da and Dc in one class (lin_class).
+// The walks of `all` are alike (lin_alike).
 template <typename T, bool FULL> hipError_t run_walks(const LinWalks &all)
 {
-    switch (lin_class(all.w[0])) {
-    case 0: return run_walk_on<T, 64, 2, FULL>(all);
-    case 1: return run_walk_on<T, 64, 4, FULL>(all);
-    case 2: return run_walk_on<T, 128, 2, FULL>(all);
-    case 3: return run_walk_on<T, 128, 4, FULL>(all);
-    default: return run_walk_on<T, 256, 4, FULL>(all);
-    }
+    // Two waves where 64 columns are all there are, but for wide rows: their staging is shared by four.
+    const LinWalk &p = all.w[0];
+    if (p.Da <= 64) return p.Dc <= 64 ? run_walk_on<T, 64, 2, FULL>(all) : run_walk_on<T, 64, 4, FULL>(all);
+    if (p.Da <= 128) return p.Dc <= 64 ? run_walk_on<T, 128, 2, FULL>(all) : run_walk_on<T, 128, 4, FULL>(all);
+    return run_walk_on<T, 256, 4, FULL>(all);
 }
 
 }  // namespace

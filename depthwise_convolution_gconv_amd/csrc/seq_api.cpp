@@ -138,7 +138,7 @@ gconv::LinWalk lin_base(const LinShape &s, bool backward, const float *log_decay
                         gconv_dtype_t dtype, void *stream)
 {
     gconv::LinWalk p = {};
-    p.B = (int32_t)s.B; p.T = (int32_t)s.T; p.H = (int32_t)s.H;
+    p.B = (int32_t)s.B; p.T = (int32_t)s.T; p.H = (int32_t)s.H; p.rep = (int32_t)(s.H / s.Hk);
     p.log_decay = log_decay;
     p.lengths = lengths;
     p.dtype = (int)dtype;
