@@ -10,6 +10,7 @@ call's outputs and workspace are recorded on it; its inputs are the caller's to 
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -50,7 +51,10 @@ def _library():
     return _fns
 
 
-_arrays = {n: _i64 * n for n in (1, 2, 3, 4, 6, 8, 12, 21)}
+@functools.lru_cache(maxsize=4096)
+def _array(*values):
+    """Sizes or strides for the C entry points; those of a serving loop's calls repeat."""
+    return (_i64 * len(values))(*values)
 
 
 def _bad(text: str, status: int = ERR_INVALID_ARG):
@@ -66,23 +70,24 @@ def _dtype(name: str, t: torch.Tensor) -> int:
     return d
 
 
-def _view(name: str, t: torch.Tensor, ref: torch.Tensor, shape) -> torch.Tensor:
-    """A tensor of ref's dtype and device whose last axis is contiguous."""
-    if t.dtype != ref.dtype or t.device != ref.device:
+def _view(name: str, t: torch.Tensor, dtype, dev: int, shape):
+    """Strides of a tensor of that dtype, device and shape whose last axis is contiguous."""
+    if t.dtype is not dtype or t.get_device() != dev:
         _bad(f"{name} must match the dtype and device of the other tensors")
     if t.shape != shape:
         _bad(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}", ERR_SHAPE)
-    if t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1:
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1 and t.numel():
         _bad(f"{name}: the last axis must be contiguous")
-    return t
+    return st
 
 
-def _whole(name: str, t: Optional[torch.Tensor], dtype, device, shape) -> int:
+def _whole(name: str, t: Optional[torch.Tensor], dtype, dev: int, shape) -> int:
     """Address of a contiguous tensor of that dtype, device and shape (0 for None)."""
     if t is None:
         return 0
-    if t.dtype != dtype or t.device != device:
-        _bad(f"{name} must be a {dtype} tensor on {device}")
+    if t.dtype is not dtype or t.get_device() != dev:
+        _bad(f"{name} must be a {dtype} tensor on device {dev}")
     if t.shape != shape:
         _bad(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}", ERR_SHAPE)
     if not t.is_contiguous():
@@ -90,21 +95,24 @@ def _whole(name: str, t: Optional[torch.Tensor], dtype, device, shape) -> int:
     return t.data_ptr()
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream     # current_stream() without its Python object
+
+
 class _On:
     """The device and stream a call runs on."""
 
     __slots__ = ("device", "stream", "handle", "_guard")
 
-    def __init__(self, device: torch.device, stream):
+    def __init__(self, device: int, stream):
         self.device = device
         self.stream = stream
         self._guard = None
 
     def __enter__(self):
-        if torch.cuda.current_device() != self.device.index:
+        if torch.cuda.current_device() != self.device:
             self._guard = torch.cuda.device(self.device)
             self._guard.__enter__()
-        self.handle = (self.stream if self.stream is not None else torch.cuda.current_stream()).cuda_stream
+        self.handle = _raw_stream(self.device) if self.stream is None else self.stream.cuda_stream
         return self
 
     def __exit__(self, *exc):
@@ -119,8 +127,13 @@ class _On:
                     t.record_stream(self.stream)
 
 
-def _workspace(need: int, device) -> Optional[torch.Tensor]:
-    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+def _workspace(need: int, ref: torch.Tensor) -> Optional[torch.Tensor]:
+    return ref.new_empty(need, dtype=torch.uint8) if need else None
+
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of t's shape and dtype."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> int:
@@ -135,18 +148,18 @@ def _attn_args(q, k, v, log_decay, lengths):
         _bad("q and k must be [B, T, Hk, Dk], v [B, T, H, Dv]")
     B, T, Hk, Dk = q.shape
     H, Dv = v.shape[2], v.shape[3]
-    _view("q", q, q, q.shape)
-    _view("k", k, q, q.shape)
-    _view("v", v, q, (B, T, H, Dv))
-    g = _whole("log_decay", log_decay, torch.float32, q.device, (H,))
-    n = _whole("lengths", lengths, torch.int32, q.device, (B,))
-    return dt, (B, T, Hk, H, Dk, Dv), g, n
+    dtype, dev = q.dtype, q.get_device()
+    st = (*_view("q", q, dtype, dev, q.shape)[:3], *_view("k", k, dtype, dev, q.shape)[:3],
+          *_view("v", v, dtype, dev, (B, T, H, Dv))[:3])
+    g = _whole("log_decay", log_decay, torch.float32, dev, (H,))
+    n = _whole("lengths", lengths, torch.int32, dev, (B,))
+    return dt, (B, T, Hk, H, Dk, Dv), st, g, n
 
 
 def linear_attention_workspace(shape, dtype: torch.dtype, backward: bool = False) -> int:
     """Workspace bytes of linear_attention (or its backward) for shape (B, T, Hk, H, Dk, Dv)."""
     n = _size(0)
-    _check(_library().gconv_linear_attention_workspace(_arrays[6](*shape), DTYPES[dtype], int(backward),
+    _check(_library().gconv_linear_attention_workspace(_array(*shape), DTYPES[dtype], int(backward),
                                                        ctypes.byref(n)))
     return n.value
 
@@ -163,22 +176,22 @@ def linear_attention(q, k, v, log_decay, scale: Optional[float] = None, initial_
     the tokens of each sequence that exist; the outputs of the others are zero.
     Returns o [B, T, H, Dv], or (o, state) with the fp32 state after each sequence's last
     token, which linear_attention_step carries on from."""
-    dt, shape, g, n = _attn_args(q, k, v, log_decay, lengths)
+    dt, shape, strides, g, n = _attn_args(q, k, v, log_decay, lengths)
     B, T, Hk, H, Dk, Dv = shape
-    dev = q.device
+    dev = q.get_device()
     s0 = _whole("initial_state", initial_state, torch.float32, dev, (B, H, Dk, Dv))
-    sh = _arrays[6](*shape)
+    sh = _array(*shape)
     need = _size(0)
     L = _library()
     _check(L.gconv_linear_attention_workspace(sh, dt, 0, ctypes.byref(need)))
     with _On(dev, stream) as on:
-        o = torch.empty((B, T, H, Dv), dtype=q.dtype, device=dev)
-        st = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if return_state else None
-        ws = _workspace(need.value, dev)
+        o = _like(v)
+        st = q.new_empty((B, H, Dk, Dv), dtype=torch.float32) if return_state else None
+        ws = _workspace(need.value, q)
         on.made(o, st, ws)
         _check(L.gconv_linear_attention(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), sh,
-            _arrays[12](*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *o.stride()[:3]), g,
+            _array(*strides, *o.stride()[:3]), g,
             Dk ** -0.5 if scale is None else scale, s0, _ptr(st), n, dt, _ptr(ws), need.value, on.handle))
     return (o, st) if return_state else o
 
@@ -188,27 +201,24 @@ def linear_attention_backward(q, k, v, log_decay, do, scale: Optional[float] = N
     """(dq, dk, dv, dinitial) of linear_attention from the gradients `do` of its output and
     `dstate` (fp32, or None: zero) of its final state.  dinitial is None without an
     initial_state.  log_decay is a constant: it gets no gradient."""
-    dt, shape, g, n = _attn_args(q, k, v, log_decay, lengths)
+    dt, shape, strides, g, n = _attn_args(q, k, v, log_decay, lengths)
     B, T, Hk, H, Dk, Dv = shape
-    dev = q.device
-    _view("do", do, q, (B, T, H, Dv))
+    dev = q.get_device()
+    strides += _view("do", do, q.dtype, dev, (B, T, H, Dv))[:3]
     s0 = _whole("initial_state", initial_state, torch.float32, dev, (B, H, Dk, Dv))
     sf = _whole("dstate", dstate, torch.float32, dev, (B, H, Dk, Dv))
-    sh = _arrays[6](*shape)
+    sh = _array(*shape)
     need = _size(0)
     L = _library()
     _check(L.gconv_linear_attention_workspace(sh, dt, 1, ctypes.byref(need)))
     with _On(dev, stream) as on:
-        dq = torch.empty((B, T, Hk, Dk), dtype=q.dtype, device=dev)
-        dk = torch.empty((B, T, Hk, Dk), dtype=q.dtype, device=dev)
-        dv = torch.empty((B, T, H, Dv), dtype=q.dtype, device=dev)
-        ds = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if initial_state is not None else None
-        ws = _workspace(need.value, dev)
+        dq, dk, dv = _like(q), _like(k), _like(v)
+        ds = q.new_empty((B, H, Dk, Dv), dtype=torch.float32) if initial_state is not None else None
+        ws = _workspace(need.value, q)
         on.made(dq, dk, dv, ds, ws)
         _check(L.gconv_linear_attention_backward(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), sh,
-            _arrays[21](*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *do.stride()[:3], *dq.stride()[:3],
-                        *dk.stride()[:3], *dv.stride()[:3]), g, Dk ** -0.5 if scale is None else scale, s0, sf,
+            _array(*strides, *dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3]), g, Dk ** -0.5 if scale is None else scale, s0, sf,
             _ptr(ds), n, dt, _ptr(ws), need.value, on.handle))
     return dq, dk, dv, ds
 
@@ -223,19 +233,18 @@ def linear_attention_step(q, k, v, log_decay, state, scale: Optional[float] = No
         _bad("q and k must be [B, Hk, Dk], v [B, H, Dv], state [n, H, Dk, Dv]")
     B, Hk, Dk = q.shape
     H, Dv = v.shape[1], v.shape[2]
-    dev = q.device
-    _view("q", q, q, q.shape)
-    _view("k", k, q, q.shape)
-    _view("v", v, q, (B, H, Dv))
+    dtype, dev = q.dtype, q.get_device()
+    strides = (*_view("q", q, dtype, dev, q.shape)[:2], *_view("k", k, dtype, dev, q.shape)[:2],
+               *_view("v", v, dtype, dev, (B, H, Dv))[:2])
     g = _whole("log_decay", log_decay, torch.float32, dev, (H,))
     sp = _whole("state", state, torch.float32, dev, (state.shape[0], H, Dk, Dv))
     sl = _whole("slots", slots, torch.int32, dev, (B,))
     with _On(dev, stream) as on:
-        o = torch.empty((B, H, Dv), dtype=q.dtype, device=dev)
+        o = _like(v)
         on.made(o)
         _check(_library().gconv_linear_attention_step(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), sp, _arrays[6](B, Hk, H, Dk, Dv, state.shape[0]),
-            _arrays[8](*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2]), g,
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), sp, _array(B, Hk, H, Dk, Dv, state.shape[0]),
+            _array(*strides, *o.stride()[:2]), g,
             Dk ** -0.5 if scale is None else scale, sl, dt, on.handle))
     return o
 
@@ -244,7 +253,7 @@ def linear_attention_step(q, k, v, log_decay, state, scale: Optional[float] = No
 
 def _rows(name: str, t: torch.Tensor, ref: torch.Tensor) -> int:
     """The one stride that leads from row to row of t's last axis."""
-    _view(name, t, ref, ref.shape)
+    _view(name, t, ref.dtype, ref.get_device(), ref.shape)
     if t.dim() == 2:
         return t.stride(0)
     if t.dim() == 1 or t.numel() == 0 or t.is_contiguous():
@@ -267,7 +276,7 @@ def _norm(x, weight, residual, eps, q8, block, stream):
         _bad("x must be [..., C] with C >= 1")
     C = x.shape[-1]
     rows = x.numel() // C
-    dev = x.device
+    dev = x.get_device()
     with _On(dev, stream) as on:
         xs = _rows("x", x, x)
         w = _whole("weight", weight, x.dtype, dev, (C,))
@@ -275,22 +284,22 @@ def _norm(x, weight, residual, eps, q8, block, stream):
             _bad("weight is needed")
         if residual is not None:
             rs = _rows("residual", residual, x)
-            h = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            h = _like(x)
         else:
             rs, h = 0, None
         L = _library()
         if not q8:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            y = _like(x)
             on.made(y, h)
-            _check(L.gconv_rms_norm(x.data_ptr(), _ptr(residual), w, y.data_ptr(), _ptr(h), rows, C, _arrays[2](xs, rs), eps,
+            _check(L.gconv_rms_norm(x.data_ptr(), _ptr(residual), w, y.data_ptr(), _ptr(h), rows, C, _array(xs, rs), eps,
                                     dt, on.handle))
             return y, h
-        y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+        y = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
         nb = -(-C // block) if block > 0 else 1
-        scales = torch.empty((*x.shape[:-1], nb), dtype=torch.float32, device=dev)
+        scales = x.new_empty((*x.shape[:-1], nb), dtype=torch.float32)
         on.made(y, scales, h)
         _check(L.gconv_rms_norm_e4m3(x.data_ptr(), _ptr(residual), w, y.data_ptr(), scales.data_ptr(), _ptr(h), rows, C,
-                                     _arrays[2](xs, rs), eps, block, dt, on.handle))
+                                     _array(xs, rs), eps, block, dt, on.handle))
         return y, scales, h
 
 
@@ -319,7 +328,7 @@ def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, stream=None):
         _bad("h must be [..., C] with C >= 1")
     C = h.shape[-1]
     rows = h.numel() // C
-    dev = h.device
+    dev = h.get_device()
     L = _library()
     need = _size(0)
     _check(L.gconv_rms_norm_backward_workspace(rows, C, dt, ctypes.byref(need)))
@@ -329,12 +338,11 @@ def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, stream=None):
             _bad("weight is needed")
         ys, hs = _rows("dy", dy, h), _rows("h", h, h)
         es = _rows("dh", dh, h) if dh is not None else 0
-        dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
-        dw = torch.empty((C,), dtype=h.dtype, device=dev)
-        ws = _workspace(need.value, dev)
+        dx, dw = _like(h), _like(weight)
+        ws = _workspace(need.value, h)
         on.made(dx, dw, ws)
         _check(L.gconv_rms_norm_backward(dy.data_ptr(), h.data_ptr(), w, _ptr(dh), dx.data_ptr(), dw.data_ptr(), rows,
-                                         C, _arrays[3](ys, hs, es), eps, dt, _ptr(ws), need.value, on.handle))
+                                         C, _array(ys, hs, es), eps, dt, _ptr(ws), need.value, on.handle))
     return dx, dw
 
 
@@ -347,9 +355,10 @@ def _conv_args(x, weight, bias, activation, dims):
     C, K = x.shape[-1], weight.shape[2]
     if activation not in ACTIVATIONS:
         _bad(f"unknown activation {activation!r}")
-    _view("x", x, x, x.shape)
-    w = _whole("weight", weight, x.dtype, x.device, (C, 1, K))
-    b = _whole("bias", bias, x.dtype, x.device, (C,))
+    dtype, dev = x.dtype, x.get_device()
+    _view("x", x, dtype, dev, x.shape)
+    w = _whole("weight", weight, dtype, dev, (C, 1, K))
+    b = _whole("bias", bias, dtype, dev, (C,))
     return dt, C, K, w, b, ACTIVATIONS[activation]
 
 
@@ -363,15 +372,15 @@ def dwconv1d_causal(x, weight, bias=None, activation: Optional[str] = None, init
     dwconv1d_causal_step carries on from."""
     dt, C, K, w, b, act = _conv_args(x, weight, bias, activation, 3)
     B, T, _ = x.shape
-    dev = x.device
+    dev = x.get_device()
     s0 = _whole("initial_state", initial_state, x.dtype, dev, (B, K - 1, C))
     n = _whole("lengths", lengths, torch.int32, dev, (B,))
     with _On(dev, stream) as on:
-        y = torch.empty((B, T, C), dtype=x.dtype, device=dev)
-        st = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if return_state else None
+        y = _like(x)
+        st = x.new_empty((B, K - 1, C)) if return_state else None
         on.made(y, st)
-        _check(_library().gconv_dw1d_causal(x.data_ptr(), w, b, y.data_ptr(), s0, _ptr(st), n, _arrays[4](B, T, C, K),
-                                            _arrays[2](*x.stride()[:2]), act, dt, on.handle))
+        _check(_library().gconv_dw1d_causal(x.data_ptr(), w, b, y.data_ptr(), s0, _ptr(st), n, _array(B, T, C, K),
+                                            _array(*x.stride()[:2]), act, dt, on.handle))
     return (y, st) if return_state else y
 
 
@@ -382,24 +391,23 @@ def dwconv1d_causal_backward(x, weight, bias, dy, activation: Optional[str] = No
     without an initial_state."""
     dt, C, K, w, b, act = _conv_args(x, weight, bias, activation, 3)
     B, T, _ = x.shape
-    dev = x.device
-    _view("dy", dy, x, x.shape)
+    dev = x.get_device()
+    _view("dy", dy, x.dtype, dev, x.shape)
     s0 = _whole("initial_state", initial_state, x.dtype, dev, (B, K - 1, C))
     sf = _whole("dstate", dstate, x.dtype, dev, (B, K - 1, C))
     n = _whole("lengths", lengths, torch.int32, dev, (B,))
     L = _library()
-    sh = _arrays[4](B, T, C, K)
+    sh = _array(B, T, C, K)
     need = _size(0)
     _check(L.gconv_dw1d_causal_backward_workspace(sh, dt, ctypes.byref(need)))
     with _On(dev, stream) as on:
-        dx = torch.empty((B, T, C), dtype=x.dtype, device=dev)
-        dw = torch.empty((C, 1, K), dtype=x.dtype, device=dev)
-        db = torch.empty((C,), dtype=x.dtype, device=dev) if bias is not None else None
-        ds = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if initial_state is not None else None
-        ws = _workspace(need.value, dev)
+        dx, dw = _like(x), _like(weight)
+        db = _like(bias) if bias is not None else None
+        ds = x.new_empty((B, K - 1, C)) if initial_state is not None else None
+        ws = _workspace(need.value, x)
         on.made(dx, dw, db, ds, ws)
         _check(L.gconv_dw1d_causal_backward(x.data_ptr(), w, b, dy.data_ptr(), s0, sf, dx.data_ptr(), dw.data_ptr(),
-                                            _ptr(db), _ptr(ds), n, sh, _arrays[4](*x.stride()[:2], *dy.stride()[:2]),
+                                            _ptr(db), _ptr(ds), n, sh, _array(*x.stride()[:2], *dy.stride()[:2]),
                                             act, dt, _ptr(ws), need.value, on.handle))
     return dx, dw, db, ds
 
@@ -409,14 +417,14 @@ def dwconv1d_causal_step(x, weight, bias, state, activation: Optional[str] = Non
     place.  slots as for linear_attention_step.  Returns y [B, C]."""
     dt, C, K, w, b, act = _conv_args(x, weight, bias, activation, 2)
     B = x.shape[0]
-    dev = x.device
+    dev = x.get_device()
     if state.dim() != 3:
         _bad("state must be [n, K-1, C]")
     sp = _whole("state", state, x.dtype, dev, (state.shape[0], K - 1, C))
     sl = _whole("slots", slots, torch.int32, dev, (B,))
     with _On(dev, stream) as on:
-        y = torch.empty((B, C), dtype=x.dtype, device=dev)
+        y = _like(x)
         on.made(y)
         _check(_library().gconv_dw1d_causal_step(x.data_ptr(), w, b, sp, y.data_ptr(), sl,
-                                                 _arrays[4](B, C, K, state.shape[0]), x.stride(0), act, dt, on.handle))
+                                                 _array(B, C, K, state.shape[0]), x.stride(0), act, dt, on.handle))
     return y

@@ -133,36 +133,37 @@ constexpr int kCT = 64;     // channels of a tile (lanes)
 constexpr int kTT = 64;     // tokens of a tile
 constexpr int kWaves = kThreads / 64;
 
-// out[r] = bias + sum_k w[k] xs[row0 + r + k] for R rows of the staged inputs (stride kCT).
-// Taps go 4 at a time through a register window of R + 3 rows; REV reads them from the end.
-template <int R, bool REV>
+// out[r] = bias + sum_k w[k] xs[row0 + r + k] for R rows of the staged inputs (stride S) and
+// filters (stride C).  Taps go 4 at a time through a register window of R + 3 rows; REV reads
+// them from the end.
+template <int R, bool REV, int S = kCT, int C = kCT>
 __device__ __forceinline__ void taps(const float *xs, const float *ws, int K, int lane, float (&acc)[R])
 {
     int k = 0;
     for (; k + 4 <= K; k += 4) {
         float x[R + 3], w[4];
 #pragma unroll
-        for (int i = 0; i < R + 3; ++i) x[i] = xs[(k + i) * kCT + lane];
+        for (int i = 0; i < R + 3; ++i) x[i] = xs[(k + i) * S + lane];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = ws[(REV ? K - 1 - k - i : k + i) * kCT + lane];
+        for (int i = 0; i < 4; ++i) w[i] = ws[(REV ? K - 1 - k - i : k + i) * C + lane];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int r = 0; r < R; ++r) acc[r] = fmaf(x[r + i], w[i], acc[r]);
     }
     for (; k < K; ++k) {
-        const float w = ws[(REV ? K - 1 - k : k) * kCT + lane];
+        const float w = ws[(REV ? K - 1 - k : k) * C + lane];
 #pragma unroll
-        for (int r = 0; r < R; ++r) acc[r] = fmaf(xs[(k + r) * kCT + lane], w, acc[r]);
+        for (int r = 0; r < R; ++r) acc[r] = fmaf(xs[(k + r) * S + lane], w, acc[r]);
     }
 }
 
-// Stages `rows` rows of 64 channels from row(r) (nullptr: zeros) as fp32.  T elements go in
-// runs of VE; UN runs of a thread are in flight together.
-template <typename T, typename F>
+// Stages `rows` rows of CT channels from row(r) (nullptr: zeros) as fp32, S apart.  T elements
+// go in runs of VE; UN runs of a thread are in flight together.
+template <typename T, int CT = kCT, int S = kCT, typename F>
 __device__ __forceinline__ void stage(float *dst, int rows, int64_t c0, int64_t C, F row)
 {
-    constexpr int VE = 16 / sizeof(T), PR = kCT / VE, UN = 4;
+    constexpr int VE = 16 / sizeof(T), PR = CT / VE, UN = 4;
     for (int base = 0; base < rows * PR; base += UN * kThreads) {
         Run<T, VE> v[UN];
 #pragma unroll
@@ -177,20 +178,20 @@ __device__ __forceinline__ void stage(float *dst, int rows, int64_t c0, int64_t 
             const int i = base + u * kThreads + (int)threadIdx.x;
             if (i < rows * PR) {
 #pragma unroll
-                for (int e = 0; e < VE; ++e) dst[i / PR * kCT + i % PR * VE + e] = to_f32(v[u].v[e]);
+                for (int e = 0; e < VE; ++e) dst[i / PR * S + i % PR * VE + e] = to_f32(v[u].v[e]);
             }
         }
     }
 }
 
-// Filters of 64 channels as [K][64].
-template <typename T>
+// Filters of CT channels as [K][CT].
+template <typename T, int CT = kCT>
 __device__ __forceinline__ void stage_taps(float *ws, const CausalArgs &a, int64_t c0)
 {
-    const int K = (int)a.K, total = (int)min(a.C - c0, (int64_t)kCT) * K;
-    for (int i = threadIdx.x; i < kCT * K; i += kThreads) {
+    const int K = (int)a.K, total = (int)min(a.C - c0, (int64_t)CT) * K;
+    for (int i = threadIdx.x; i < CT * K; i += kThreads) {
         const int c = i / K;
-        ws[(i - c * K) * kCT + c] = i < total ? to_f32(((const T *)a.w)[c0 * K + i]) : 0.0f;
+        ws[(i - c * K) * CT + c] = i < total ? to_f32(((const T *)a.w)[c0 * K + i]) : 0.0f;
     }
 }
 
@@ -233,19 +234,28 @@ causal_tile(const CausalArgs a, int cblocks, int tblocks)
     }
 }
 
+// The gradients' tile: 32 channels x 64 tokens, a wave holds two groups of rows.  Half as
+// wide as the forward one so that four workgroups share a compute unit: its three passes
+// alternate between LDS and arithmetic.  Rows lie kBS apart: groups 8, 24, 40 or 72 rows apart
+// (8 modulo 16) then read the two halves of the 64 banks.
+constexpr int kBT = 32, kBS = 36;
+
 // Tile of rows s0 .. s0 + 63 of the inputs with their state (s = -(K-1) .. T-1).
 // NT: taps for each wave (K <= 4 NT).
 template <typename T, int NT>
 __global__ void __launch_bounds__(kThreads)
-causal_bwd_tile(const CausalArgs a, int cblocks, int tblocks)
+causal_bwd_tile(const CausalArgs a, int cblocks, int tblocks, int64_t blocks)
 {
-    constexpr int R = 8, NX = kTT + (NT == 1 ? 12 : 8 * NT), ND = kTT + 4 * NT;
-    __shared__ float xs[NX * kCT];        // x at s0 - (K-1) ..
-    __shared__ float dz[ND * kCT];        // dz at s0 ..
-    __shared__ float ws[4 * NT * kCT];
-    const int K = (int)a.K, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t id = blockIdx.x;
-    const int64_t c0 = id % cblocks * kCT;
+    constexpr int RZ = NT <= 4 ? 10 : NT == 8 ? 12 : 18;      // rows of z for each group of lanes (8 groups)
+    constexpr int R = kTT / 8, NX = 8 * RZ + 4 * NT, ND = kTT + 4 * NT;
+    __shared__ float xs[NX * kBS];        // x at s0 - (K-1) ..
+    __shared__ float dz[ND * kBS];        // dz at s0 ..
+    __shared__ float ws[4 * NT * kBT];
+    const int K = (int)a.K, lane = threadIdx.x & 31, half = threadIdx.x >> 5 & 1, wave = threadIdx.x >> 6;
+    // A contiguous run of tiles on each XCD: neighbours share lines of 16-bit rows, and halo rows.
+    int64_t id = (int64_t)(blockIdx.x & 7) * ((blocks + 7) / 8) + (blockIdx.x >> 3);
+    if (id >= blocks) return;
+    const int64_t c0 = id % cblocks * kBT;
     id /= cblocks;
     const int tb = (int)(id % tblocks), s0 = tb * kTT - (a.s0 ? K - 1 : 0);
     const int64_t b = id / tblocks, c = c0 + lane;
@@ -253,44 +263,43 @@ causal_bwd_tile(const CausalArgs a, int cblocks, int tblocks)
     const bool cok = c < a.C;
 
     // Rows past what the tile needs are zeroed: the weight sums read them beside zero dz.
-    stage<T>(xs, NX, c0, a.C, [&](int r) -> const T * {
+    stage<T, kBT, kBS>(xs, NX, c0, a.C, [&](int r) -> const T * {
         const int t = s0 - (K - 1) + r;
-        return t < n && t >= -(K - 1) ? xs_at<T>(a, b, t, 0) : nullptr;
+        return t < n && t >= -(K - 1) && r < rows_dz + K - 1 ? xs_at<T>(a, b, t, 0) : nullptr;
     });
-    stage<T>(dz, ND, c0, a.C, [&](int r) -> const T * {
+    stage<T, kBT, kBS>(dz, ND, c0, a.C, [&](int r) -> const T * {
         const int t = s0 + r;
         return t >= 0 && t < n && r < rows_dz ? (const T *)a.dy + b * a.dysb + (int64_t)t * a.dyst : nullptr;
     });
-    stage_taps<T>(ws, a, c0);
+    stage_taps<T, kBT>(ws, a, c0);
     __syncthreads();
 
     if (a.silu) {   // dz = dy silu'(z), each element by the thread that reads it here
         const float b0 = a.bias && cok ? to_f32(((const T *)a.bias)[c]) : 0.0f;
-        for (int r0 = wave * R; r0 < rows_dz; r0 += kWaves * R) {
-            float z[R];
+        const int r0 = NT == 8 ? (wave >> 1) * 4 * RZ + (wave & 1) * RZ + half * 2 * RZ : half * 4 * RZ + wave * RZ;
+        float z[RZ];
 #pragma unroll
-            for (int r = 0; r < R; ++r) z[r] = b0;
-            taps<R, false>(xs + r0 * kCT, ws, K, lane, z);
+        for (int r = 0; r < RZ; ++r) z[r] = b0;
+        taps<RZ, false, kBS, kBT>(xs + r0 * kBS, ws, K, lane, z);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int t = s0 + r0 + r;
-                if (r0 + r < rows_dz && t >= 0 && t < n) dz[(r0 + r) * kCT + lane] *= silu_grad<T>(z[r]);
-            }
+        for (int r = 0; r < RZ; ++r) {
+            const int t = s0 + r0 + r;
+            if (r0 + r < rows_dz && t >= 0 && t < n) dz[(r0 + r) * kBS + lane] *= silu_grad<T>(z[r]);
         }
         __syncthreads();
     }
 
     // dx[s] = sum_j dz[s + j] w[K-1-j], and the gradient of the final state's inputs.
-    for (int r0 = wave * R; r0 < kTT; r0 += kWaves * R) {
+    {
+        const int r0 = wave * 2 * R + half * R;
         float acc[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) acc[r] = 0.0f;
-        taps<R, true>(dz + r0 * kCT, ws, K, lane, acc);
-        if (!cok) continue;
+        taps<R, true, kBS, kBT>(dz + r0 * kBS, ws, K, lane, acc);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int s = s0 + r0 + r;
-            if (s >= a.T) continue;
+            if (s >= a.T || !cok) continue;
             float v = s < n ? acc[r] : 0.0f;
             if (a.dsf && s < n && s >= n - (K - 1))
                 v += to_f32(((const T *)a.dsf)[(b * (K - 1) + s - n + K - 1) * a.C + c]);
@@ -300,26 +309,28 @@ causal_bwd_tile(const CausalArgs a, int cblocks, int tblocks)
     }
 
     // dw[k] = sum over the tile's tokens of dz[t] xs[t-(K-1)+k]: wave g takes the taps from
-    // g NT on and slides a window of NT inputs down the tile.  Row i of xs is input
-    // s0 - (K-1) + i, so token s0 + i meets tap k at row i + k.
-    float acc[NT], accb = 0.0f, win[NT];
-    const float *xr = xs + wave * NT * kCT + lane;
+    // g NT on, the halves every other eight tokens.  Row i of xs is input s0 - (K-1) + i, so
+    // token s0 + i meets tap k at row i + k.
+    float acc[NT], accb = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        acc[j] = 0.0f;
-        win[j] = xr[j * kCT];
-    }
-    for (int t = 0; t < kTT; t += NT) {
+    for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
+    for (int t = half * 8; t < kTT; t += 16) {
+        float x[7 + NT], d[8];
 #pragma unroll
-        for (int u = 0; u < NT; ++u) {
-            const float d = dz[(t + u) * kCT + lane];   // zero outside [0, n)
-            accb += d;
+        for (int i = 0; i < 7 + NT; ++i) x[i] = xs[(t + wave * NT + i) * kBS + lane];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) acc[j] = fmaf(d, win[(j + u) % NT], acc[j]);
-            win[u] = xr[(t + u + NT) * kCT];
+        for (int u = 0; u < 8; ++u) d[u] = dz[(t + u) * kBS + lane];   // zero outside [0, n)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            accb += d[u];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[j] = fmaf(d[u], x[u + j], acc[j]);
         }
     }
-    if (!cok) return;
+    accb += __shfl_xor(accb, 32);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j] += __shfl_xor(acc[j], 32);
+    if (!cok || half) return;
     float *pt = a.ws + (b * tblocks + tb) * (int64_t)(K + 1) * a.C + c;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -355,8 +366,9 @@ causal_bwd_reduce(const float *__restrict__ ws, T *__restrict__ dw, T *__restric
     else if (db) db[c] = from_f32<T>(s);
 }
 
-// One token for each sequence: 4 channels for each thread.
-template <typename T>
+// One token for each sequence: 4 channels for each thread.  KS: the number of taps where it
+// is small enough for a channel run's filters to be loaded as they lie (0: any number).
+template <typename T, int KS>
 __global__ void __launch_bounds__(kThreads)
 causal_step(const CausalStepArgs a, int cblocks)
 {
@@ -364,10 +376,18 @@ causal_step(const CausalStepArgs a, int cblocks)
     const int64_t b = blockIdx.x / cblocks;
     const int64_t c = ((int64_t)(blockIdx.x % cblocks) * kThreads + threadIdx.x) * VE;
     if (c >= a.C) return;
-    const int left = (int)min(a.C - c, (int64_t)VE), K = (int)a.K;
+    const int left = (int)min(a.C - c, (int64_t)VE), K = KS ? KS : (int)a.K;
     const int64_t slot = a.slots ? a.slots[b] : b;
     T *yp = (T *)a.y + b * a.C + c;
     float x[VE], z[VE];
+    const T *wp = (const T *)a.w + c * K;
+    load_run<T, VE>((const T *)a.x + b * a.xsb + c, left, x);
+    load_run<T, VE>((const T *)a.bias + c, a.bias ? left : 0, z);
+    float wk[KS ? KS * VE : 1];
+    if constexpr (KS > 0) {
+#pragma unroll
+        for (int j = 0; j < KS; ++j) load_run<T, VE>(wp + j * VE, left * KS - j * VE, *(float(*)[VE])&wk[j * VE]);
+    }
     if (slot < 0 || slot >= a.n) {   // no state: nothing to update, the token's output is zero
 #pragma unroll
         for (int e = 0; e < VE; ++e) z[e] = 0.0f;
@@ -375,10 +395,8 @@ causal_step(const CausalStepArgs a, int cblocks)
         return;
     }
     T *sp = (T *)a.state + slot * (K - 1) * a.C + c;
-    const T *wp = (const T *)a.w + c * K;
-    load_run<T, VE>((const T *)a.x + b * a.xsb + c, left, x);
-    load_run<T, VE>((const T *)a.bias + c, a.bias ? left : 0, z);
     constexpr int U = 4;     // state rows in flight
+#pragma unroll 1
     for (int j0 = 0; j0 < K; j0 += U) {
         Run<T, VE> row[U];
         float w[U][VE];
@@ -387,7 +405,10 @@ causal_step(const CausalStepArgs a, int cblocks)
             const int j = j0 + u;
             row[u] = load_raw<T, VE>(sp + (int64_t)j * a.C, j < K - 1 ? left : 0);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) w[u][e] = j < K && e < left ? to_f32(wp[e * K + j]) : 0.0f;
+            for (int e = 0; e < VE; ++e) {
+                if constexpr (KS > 0) w[u][e] = u < KS ? wk[e * KS + u] : 0.0f;
+                else w[u][e] = j < K && e < left ? to_f32(wp[e * K + j]) : 0.0f;
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -445,8 +466,8 @@ template <typename T> hipError_t run_fwd(const CausalArgs &a, const char **kname
 
 template <typename T, int NT> hipError_t run_bwd_tile(const CausalArgs &a, int64_t blocks, int64_t cblocks, int64_t tblocks)
 {
-    hipLaunchKernelGGL((causal_bwd_tile<T, NT>), dim3((unsigned)blocks), dim3(kThreads), 0, a.stream, a, (int)cblocks,
-                       (int)tblocks);
+    hipLaunchKernelGGL((causal_bwd_tile<T, NT>), dim3((unsigned)(8 * ceil_div(blocks, 8))), dim3(kThreads), 0, a.stream, a,
+                       (int)cblocks, (int)tblocks, blocks);
     return hipGetLastError();
 }
 
@@ -456,9 +477,9 @@ int64_t bwd_tblocks(int64_t T, int64_t K) { return ceil_div(T + K - 1, kTT); }
 template <typename T> hipError_t run_bwd(const CausalArgs &a, const char **kname)
 {
     *kname = "causal_bwd_tile";
-    const int64_t cblocks = ceil_div(a.C, kCT), tblocks = a.s0 ? bwd_tblocks(a.T, a.K) : ceil_div(a.T, kTT);
+    const int64_t cblocks = ceil_div(a.C, kBT), tblocks = a.s0 ? bwd_tblocks(a.T, a.K) : ceil_div(a.T, kTT);
     const int64_t tiles = a.B * tblocks, blocks = tiles * cblocks;
-    if (blocks > kGridMax) return hipErrorInvalidValue;
+    if (blocks > kGridMax - 8) return hipErrorInvalidValue;
     hipError_t err = hipSuccess;
     if (blocks > 0) {
         if (a.K <= 4) err = run_bwd_tile<T, 1>(a, blocks, cblocks, tblocks);
@@ -477,7 +498,13 @@ template <typename T> hipError_t run_step(const CausalStepArgs &a)
 {
     const int64_t cblocks = ceil_div(a.C, kThreads * 4), blocks = a.B * cblocks;
     if (blocks > kGridMax) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((causal_step<T>), dim3((unsigned)blocks), dim3(kThreads), 0, a.stream, a, (int)cblocks);
+    const dim3 grid((unsigned)blocks), block(kThreads);
+    switch (a.K) {
+    case 2: hipLaunchKernelGGL((causal_step<T, 2>), grid, block, 0, a.stream, a, (int)cblocks); break;
+    case 3: hipLaunchKernelGGL((causal_step<T, 3>), grid, block, 0, a.stream, a, (int)cblocks); break;
+    case 4: hipLaunchKernelGGL((causal_step<T, 4>), grid, block, 0, a.stream, a, (int)cblocks); break;
+    default: hipLaunchKernelGGL((causal_step<T, 0>), grid, block, 0, a.stream, a, (int)cblocks); break;
+    }
     return hipGetLastError();
 }
 

@@ -413,31 +413,33 @@ rms_bwd_long_dw(const RmsBwdArgs a, const float *rs, int groups)
     a.ws[g * a.C + c] = s;
 }
 
-// dw from `groups` rows of partial sums: 64 columns and 16 slices of the rows for each
+// dw from `groups` rows of partial sums: 16 columns and 64 slices of the rows for each
 // workgroup, added in a fixed order.
 template <typename T>
 __global__ void __launch_bounds__(1024)
 rms_bwd_reduce(const float *__restrict__ ws, T *__restrict__ dw, int64_t C, int groups)
 {
-    __shared__ float part[16][64];
-    const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    __shared__ float part[64][17];
+    const int col = threadIdx.x & 15, slice = threadIdx.x >> 4;
+    const int64_t c = (int64_t)blockIdx.x * 16 + col;
     float s = 0.0f;
     if (c < C) {
         int g = slice;
-        for (; g + 48 < groups; g += 64) {
-            const float v0 = ws[(int64_t)g * C + c], v1 = ws[(int64_t)(g + 16) * C + c];
-            const float v2 = ws[(int64_t)(g + 32) * C + c], v3 = ws[(int64_t)(g + 48) * C + c];
+        for (; g + 192 < groups; g += 256) {
+            const float v0 = ws[(int64_t)g * C + c], v1 = ws[(int64_t)(g + 64) * C + c];
+            const float v2 = ws[(int64_t)(g + 128) * C + c], v3 = ws[(int64_t)(g + 192) * C + c];
             s += (v0 + v1) + (v2 + v3);
         }
-        for (; g < groups; g += 16) s += ws[(int64_t)g * C + c];
+        for (; g < groups; g += 64) s += ws[(int64_t)g * C + c];
     }
-    part[slice][lane] = s;
+    part[slice][col] = s;
     __syncthreads();
-    if (slice == 0 && c < C) {
-        for (int i = 1; i < 16; ++i) s += part[i][lane];
-        dw[c] = from_f32<T>(s);
-    }
+    if (slice >= 4) return;      // 4 sums of 16 slices, then their sum by lanes
+    s = 0.0f;
+    for (int i = 0; i < 16; ++i) s += part[slice + 4 * i][col];
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (slice == 0 && c < C) dw[c] = from_f32<T>(s);
 }
 
 template <typename T, int TPR, int NV> hipError_t run_rows(const RmsArgs &a)
@@ -509,7 +511,7 @@ template <typename T> hipError_t run_bwd(const RmsBwdArgs &a, const char **kname
         }
     }
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL((rms_bwd_reduce<T>), dim3((unsigned)ceil_div(a.C, 64)), dim3(1024), 0, a.stream, a.ws,
+    hipLaunchKernelGGL((rms_bwd_reduce<T>), dim3((unsigned)ceil_div(a.C, 16)), dim3(1024), 0, a.stream, a.ws,
                        (T *)a.dw, a.C, groups);
     return hipGetLastError();
 }
