@@ -158,12 +158,12 @@ __device__ __forceinline__ void taps(const float *xs, const float *ws, int K, in
     }
 }
 
-// Stages `rows` rows of CT channels from row(r) (nullptr: zeros) as fp32, S apart.  T elements
-// go in runs of VE; UN runs of a thread are in flight together.
-template <typename T, int CT = kCT, int S = kCT, typename F>
+// Stages `rows` rows of 64 channels from row(r) (nullptr: zeros) as fp32.  T elements go in
+// runs of VE; UN runs of a thread are in flight together.
+template <typename T, typename F>
 __device__ __forceinline__ void stage(float *dst, int rows, int64_t c0, int64_t C, F row)
 {
-    constexpr int VE = 16 / sizeof(T), PR = CT / VE, UN = 4;
+    constexpr int VE = 16 / sizeof(T), PR = kCT / VE, UN = 4;
     for (int base = 0; base < rows * PR; base += UN * kThreads) {
         Run<T, VE> v[UN];
 #pragma unroll
@@ -178,22 +178,75 @@ __device__ __forceinline__ void stage(float *dst, int rows, int64_t c0, int64_t 
             const int i = base + u * kThreads + (int)threadIdx.x;
             if (i < rows * PR) {
 #pragma unroll
-                for (int e = 0; e < VE; ++e) dst[i / PR * S + i % PR * VE + e] = to_f32(v[u].v[e]);
+                for (int e = 0; e < VE; ++e) dst[i / PR * kCT + i % PR * VE + e] = to_f32(v[u].v[e]);
             }
         }
     }
 }
 
-// Filters of CT channels as [K][CT].
-template <typename T, int CT = kCT>
-__device__ __forceinline__ void stage_taps(float *ws, const CausalArgs &a, int64_t c0)
-{
-    const int K = (int)a.K, total = (int)min(a.C - c0, (int64_t)CT) * K;
-    for (int i = threadIdx.x; i < CT * K; i += kThreads) {
-        const int c = i / K;
-        ws[(i - c * K) * CT + c] = i < total ? to_f32(((const T *)a.w)[c0 * K + i]) : 0.0f;
+// The same with ROWS known: the loads, then what they brought, so that several stagings wait
+// together.
+template <typename T, int ROWS, int CT, int S> struct Staged {
+    static constexpr int VE = 16 / sizeof(T), PR = CT / VE, NR = (ROWS * PR + kThreads - 1) / kThreads;
+    RunVec<T, VE> v[NR];
+    template <typename F> __device__ __forceinline__ void load(int64_t c0, int64_t C, F row)
+    {
+        const int64_t c = c0 + threadIdx.x % PR * VE;
+        const int left = (int)min(C - c, (int64_t)VE);
+#pragma unroll
+        for (int u = 0; u < NR; ++u) v[u] = RunVec<T, VE>{};
+        if (c0 + CT <= C) {
+#pragma unroll
+            for (int u = 0; u < NR; ++u) {
+                const T *src = row((u * kThreads + (int)threadIdx.x) / PR);
+                if (src) v[u] = *reinterpret_cast<const RunVec<T, VE> *>(src + c);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < NR; ++u) {
+                const T *src = row((u * kThreads + (int)threadIdx.x) / PR);
+                if (src && left > 0) v[u] = load_words<T, VE>(src + c, left);
+            }
+        }
     }
-}
+    __device__ __forceinline__ void put(float *dst) const
+    {
+#pragma unroll
+        for (int u = 0; u < NR; ++u) {
+            const int r = (u * kThreads + (int)threadIdx.x) / PR;
+            if (r >= ROWS) break;
+            const Run<T, VE> x = __builtin_bit_cast(Run<T, VE>, v[u]);
+            float *p = dst + r * S + threadIdx.x % PR * VE;
+#pragma unroll
+            for (int e = 0; e < VE; e += 4)
+                *reinterpret_cast<float4 *>(p + e) = float4{to_f32(x.v[e]), to_f32(x.v[e + 1]), to_f32(x.v[e + 2]), to_f32(x.v[e + 3])};
+        }
+    }
+};
+
+// Filters of CT channels as [K][CT], K <= KM: the loads, then what they brought.
+template <typename T, int CT, int KM> struct StagedTaps {
+    static constexpr int NR = (CT * KM + kThreads - 1) / kThreads;
+    T v[NR];
+    __device__ __forceinline__ void load(const CausalArgs &a, int64_t c0)
+    {
+        const int total = (int)min(a.C - c0, (int64_t)CT) * (int)a.K;
+#pragma unroll
+        for (int u = 0; u < NR; ++u) {
+            const int i = u * kThreads + threadIdx.x;
+            v[u] = (T)0.0f;
+            if (i < total) v[u] = ((const T *)a.w)[c0 * a.K + i];
+        }
+    }
+    __device__ __forceinline__ void put(float *ws, int K) const
+    {
+#pragma unroll
+        for (int u = 0; u < NR; ++u) {
+            const int i = u * kThreads + threadIdx.x, c = i / K;
+            if (c < CT) ws[(i - c * K) * CT + c] = to_f32(v[u]);
+        }
+    }
+};
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
@@ -209,11 +262,13 @@ causal_tile(const CausalArgs a, int cblocks, int tblocks)
     const int t0 = (int)(id % tblocks) * kTT, T_in = (int)a.T;
     const int64_t b = id / tblocks, c = c0 + lane;
     const int n = seq_len(a.lengths, b, a.T);
+    StagedTaps<T, kCT, kCausalMaxK> tp;
+    tp.load(a, c0);
     stage<T>(xs, kTT + K - 1, c0, a.C, [&](int r) -> const T * {
         const int t = t0 - (K - 1) + r;
         return t < n ? xs_at<T>(a, b, t, 0) : nullptr;
     });
-    stage_taps<T>(ws, a, c0);
+    tp.put(ws, K);
     __syncthreads();
     if (t0 == 0 && a.sf && c < a.C)
         for (int j = wave; j < K - 1; j += kWaves) {
@@ -248,8 +303,8 @@ causal_bwd_tile(const CausalArgs a, int cblocks, int tblocks, int64_t blocks)
 {
     constexpr int RZ = NT <= 4 ? 10 : NT == 8 ? 12 : 18;      // rows of z for each group of lanes (8 groups)
     constexpr int R = kTT / 8, NX = 8 * RZ + 4 * NT, ND = kTT + 4 * NT;
-    __shared__ float xs[NX * kBS];        // x at s0 - (K-1) ..
-    __shared__ float dz[ND * kBS];        // dz at s0 ..
+    __shared__ __attribute__((aligned(16))) float xs[NX * kBS];   // x at s0 - (K-1) ..
+    __shared__ __attribute__((aligned(16))) float dz[ND * kBS];   // dz at s0 ..
     __shared__ float ws[4 * NT * kBT];
     const int K = (int)a.K, lane = threadIdx.x & 31, half = threadIdx.x >> 5 & 1, wave = threadIdx.x >> 6;
     // A contiguous run of tiles on each XCD: neighbours share lines of 16-bit rows, and halo rows.
@@ -261,21 +316,29 @@ causal_bwd_tile(const CausalArgs a, int cblocks, int tblocks, int64_t blocks)
     const int64_t b = id / tblocks, c = c0 + lane;
     const int n = seq_len(a.lengths, b, a.T), rows_dz = kTT + K - 1;
     const bool cok = c < a.C;
+    const float b0 = a.bias && cok ? to_f32(((const T *)a.bias)[c]) : 0.0f;
 
     // Rows past what the tile needs are zeroed: the weight sums read them beside zero dz.
-    stage<T, kBT, kBS>(xs, NX, c0, a.C, [&](int r) -> const T * {
-        const int t = s0 - (K - 1) + r;
-        return t < n && t >= -(K - 1) && r < rows_dz + K - 1 ? xs_at<T>(a, b, t, 0) : nullptr;
-    });
-    stage<T, kBT, kBS>(dz, ND, c0, a.C, [&](int r) -> const T * {
-        const int t = s0 + r;
-        return t >= 0 && t < n && r < rows_dz ? (const T *)a.dy + b * a.dysb + (int64_t)t * a.dyst : nullptr;
-    });
-    stage_taps<T, kBT>(ws, a, c0);
+    {
+        Staged<T, NX, kBT, kBS> sx;
+        Staged<T, ND, kBT, kBS> sd;
+        StagedTaps<T, kBT, 4 * NT> tp;
+        sx.load(c0, a.C, [&](int r) -> const T * {
+            const int t = s0 - (K - 1) + r;
+            return t < n && t >= -(K - 1) && r < rows_dz + K - 1 ? xs_at<T>(a, b, t, 0) : nullptr;
+        });
+        sd.load(c0, a.C, [&](int r) -> const T * {
+            const int t = s0 + r;
+            return t >= 0 && t < n && r < rows_dz ? (const T *)a.dy + b * a.dysb + (int64_t)t * a.dyst : nullptr;
+        });
+        tp.load(a, c0);
+        sx.put(xs);
+        sd.put(dz);
+        tp.put(ws, K);
+    }
     __syncthreads();
 
     if (a.silu) {   // dz = dy silu'(z), each element by the thread that reads it here
-        const float b0 = a.bias && cok ? to_f32(((const T *)a.bias)[c]) : 0.0f;
         const int r0 = NT == 8 ? (wave >> 1) * 4 * RZ + (wave & 1) * RZ + half * 2 * RZ : half * 4 * RZ + wave * RZ;
         float z[RZ];
 #pragma unroll
