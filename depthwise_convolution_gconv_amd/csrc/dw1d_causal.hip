@@ -27,18 +27,29 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// z / (1 + exp(-z)): fp32 tensors take the library's exponential, 16-bit ones the
-// hardware's (relative error 2^-21 at |z| = 8, far below half a step of either).
-template <typename T> __device__ __forceinline__ float silu(float z)
+// 1 / (1 + exp(-z)).  16-bit tensors take the hardware's exponential and reciprocal (relative
+// error 2^-21 at |z| = 8, far below half a step).  fp32 ones carry what the product z log2(e)
+// loses, exp(-z) = 2^t (1 + ln2 err), and give the reciprocal a Newton step: a few ulp, at half
+// the instructions of the library's exponential and a division.
+template <typename T> __device__ __forceinline__ float sigmoid(float z)
 {
-    if constexpr (sizeof(T) == 4) return z / (1.0f + expf(-z));
-    else return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+    if constexpr (sizeof(T) == 4) {
+        constexpr float hi = 1.44269502f, lo = 1.92596303e-8f, ln2 = 0.693147182f;     // log2(e) = hi + lo
+        const float t = -z * hi, err = fmaf(-z, lo, fmaf(-z, hi, -t));
+        const float e = __builtin_amdgcn_exp2f(t), d = 1.0f + (fabsf(t) < 126.0f ? fmaf(e, ln2 * err, e) : e);
+        const float r = __builtin_amdgcn_rcpf(d);
+        return d > 0x1p126f ? r : fmaf(r, fmaf(-d, r, 1.0f), r);     // the step would make NaN of infinity
+    } else {
+        return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+    }
 }
+
+template <typename T> __device__ __forceinline__ float silu(float z) { return z * sigmoid<T>(z); }
 
 // d silu(z) / dz
 template <typename T> __device__ __forceinline__ float silu_grad(float z)
 {
-    const float s = sizeof(T) == 4 ? 1.0f / (1.0f + expf(-z)) : __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+    const float s = sigmoid<T>(z);
     return s * (1.0f + z * (1.0f - s));
 }
 
@@ -133,29 +144,31 @@ constexpr int kCT = 64;     // channels of a tile (lanes)
 constexpr int kTT = 64;     // tokens of a tile
 constexpr int kWaves = kThreads / 64;
 
-// out[r] = bias + sum_k w[k] xs[row0 + r + k] for R rows of the staged inputs (stride S) and
-// filters (stride C).  Taps go 4 at a time through a register window of R + 3 rows; REV reads
-// them from the end.
+// acc[r] += sum over N taps from k on of w[k] xs[row0 + r + k], through a register window.
+template <int R, bool REV, int S, int C, int N>
+__device__ __forceinline__ void taps_of(const float *xs, const float *ws, int K, int k, int lane, float (&acc)[R])
+{
+    float x[R + N - 1], w[N];
+#pragma unroll
+    for (int i = 0; i < R + N - 1; ++i) x[i] = xs[(k + i) * S + lane];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = ws[(REV ? K - 1 - k - i : k + i) * C + lane];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r] = fmaf(x[r + i], w[i], acc[r]);
+}
+
+// The same over all K taps, 4 at a time, for R rows of the staged inputs (stride S) and
+// filters (stride C); REV reads the taps from the end.
 template <int R, bool REV, int S = kCT, int C = kCT>
 __device__ __forceinline__ void taps(const float *xs, const float *ws, int K, int lane, float (&acc)[R])
 {
     int k = 0;
-    for (; k + 4 <= K; k += 4) {
-        float x[R + 3], w[4];
-#pragma unroll
-        for (int i = 0; i < R + 3; ++i) x[i] = xs[(k + i) * S + lane];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = ws[(REV ? K - 1 - k - i : k + i) * C + lane];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int r = 0; r < R; ++r) acc[r] = fmaf(x[r + i], w[i], acc[r]);
-    }
-    for (; k < K; ++k) {
-        const float w = ws[(REV ? K - 1 - k : k) * C + lane];
-#pragma unroll
-        for (int r = 0; r < R; ++r) acc[r] = fmaf(xs[(k + r) * S + lane], w, acc[r]);
-    }
+    for (; k + 4 <= K; k += 4) taps_of<R, REV, S, C, 4>(xs, ws, K, k, lane, acc);
+    if (K - k == 3) taps_of<R, REV, S, C, 3>(xs, ws, K, k, lane, acc);
+    else if (K - k == 2) taps_of<R, REV, S, C, 2>(xs, ws, K, k, lane, acc);
+    else if (K - k == 1) taps_of<R, REV, S, C, 1>(xs, ws, K, k, lane, acc);
 }
 
 // Stages `rows` rows of 64 channels from row(r) (nullptr: zeros) as fp32.  T elements go in
@@ -189,19 +202,21 @@ __device__ __forceinline__ void stage(float *dst, int rows, int64_t c0, int64_t 
 template <typename T, int ROWS, int CT, int S> struct Staged {
     static constexpr int VE = 16 / sizeof(T), PR = CT / VE, NR = (ROWS * PR + kThreads - 1) / kThreads;
     RunVec<T, VE> v[NR];
-    template <typename F> __device__ __forceinline__ void load(int64_t c0, int64_t C, F row)
+    // all: every one of the ROWS rows exists, row r at first + r * stride.
+    template <typename F>
+    __device__ __forceinline__ void load(int64_t c0, int64_t C, bool all, const T *first, int64_t stride, F row)
     {
         const int64_t c = c0 + threadIdx.x % PR * VE;
         const int left = (int)min(C - c, (int64_t)VE);
+        if (all && c0 + CT <= C) {
+            const T *p = first + (int64_t)(threadIdx.x / PR) * stride + c;
 #pragma unroll
-        for (int u = 0; u < NR; ++u) v[u] = RunVec<T, VE>{};
-        if (c0 + CT <= C) {
-#pragma unroll
-            for (int u = 0; u < NR; ++u) {
-                const T *src = row((u * kThreads + (int)threadIdx.x) / PR);
-                if (src) v[u] = *reinterpret_cast<const RunVec<T, VE> *>(src + c);
-            }
+            for (int u = 0; u < NR; ++u)
+                if ((u + 1) * kThreads <= ROWS * PR || u * kThreads + (int)threadIdx.x < ROWS * PR)
+                    v[u] = *reinterpret_cast<const RunVec<T, VE> *>(p + u * (kThreads / PR) * stride);
         } else {
+#pragma unroll
+            for (int u = 0; u < NR; ++u) v[u] = RunVec<T, VE>{};
 #pragma unroll
             for (int u = 0; u < NR; ++u) {
                 const T *src = row((u * kThreads + (int)threadIdx.x) / PR);
@@ -240,9 +255,10 @@ template <typename T, int CT, int KM> struct StagedTaps {
     }
     __device__ __forceinline__ void put(float *ws, int K) const
     {
+        const uint32_t inv = ((1u << 19) + K - 1) / K;     // i / K = i inv >> 19 for i < 2^12, K <= 64
 #pragma unroll
         for (int u = 0; u < NR; ++u) {
-            const int i = u * kThreads + threadIdx.x, c = i / K;
+            const int i = u * kThreads + threadIdx.x, c = (int)(i * inv >> 19);
             if (c < CT) ws[(i - c * K) * CT + c] = to_f32(v[u]);
         }
     }
@@ -302,7 +318,7 @@ __global__ void __launch_bounds__(kThreads)
 causal_bwd_tile(const CausalArgs a, int cblocks, int tblocks, int64_t blocks)
 {
     constexpr int RZ = NT <= 4 ? 10 : NT == 8 ? 12 : 18;      // rows of z for each group of lanes (8 groups)
-    constexpr int R = kTT / 8, NX = 8 * RZ + 4 * NT, ND = kTT + 4 * NT;
+    constexpr int R = kTT / 8, NX = 8 * RZ + 4 * NT, ND = 8 * RZ;
     __shared__ __attribute__((aligned(16))) float xs[NX * kBS];   // x at s0 - (K-1) ..
     __shared__ __attribute__((aligned(16))) float dz[ND * kBS];   // dz at s0 ..
     __shared__ float ws[4 * NT * kBT];
@@ -323,11 +339,12 @@ causal_bwd_tile(const CausalArgs a, int cblocks, int tblocks, int64_t blocks)
         Staged<T, NX, kBT, kBS> sx;
         Staged<T, ND, kBT, kBS> sd;
         StagedTaps<T, kBT, 4 * NT> tp;
-        sx.load(c0, a.C, [&](int r) -> const T * {
+        const int x0 = s0 - (K - 1);
+        sx.load(c0, a.C, x0 >= 0 && x0 + NX <= n, (const T *)a.x + b * a.xsb + x0 * a.xst, a.xst, [&](int r) -> const T * {
             const int t = s0 - (K - 1) + r;
             return t < n && t >= -(K - 1) && r < rows_dz + K - 1 ? xs_at<T>(a, b, t, 0) : nullptr;
         });
-        sd.load(c0, a.C, [&](int r) -> const T * {
+        sd.load(c0, a.C, s0 >= 0 && s0 + ND <= n, (const T *)a.dy + b * a.dysb + s0 * a.dyst, a.dyst, [&](int r) -> const T * {
             const int t = s0 + r;
             return t >= 0 && t < n && r < rows_dz ? (const T *)a.dy + b * a.dysb + (int64_t)t * a.dyst : nullptr;
         });
@@ -344,10 +361,15 @@ causal_bwd_tile(const CausalArgs a, int cblocks, int tblocks, int64_t blocks)
 #pragma unroll
         for (int r = 0; r < RZ; ++r) z[r] = b0;
         taps<RZ, false, kBS, kBT>(xs + r0 * kBS, ws, K, lane, z);
+        if (s0 >= 0 && s0 + 8 * RZ <= n) {     // rows past rows_dz are not read
 #pragma unroll
-        for (int r = 0; r < RZ; ++r) {
-            const int t = s0 + r0 + r;
-            if (r0 + r < rows_dz && t >= 0 && t < n) dz[(r0 + r) * kBS + lane] *= silu_grad<T>(z[r]);
+            for (int r = 0; r < RZ; ++r) dz[(r0 + r) * kBS + lane] *= silu_grad<T>(z[r]);
+        } else {
+#pragma unroll
+            for (int r = 0; r < RZ; ++r) {
+                const int t = s0 + r0 + r;
+                if (r0 + r < rows_dz && t >= 0 && t < n) dz[(r0 + r) * kBS + lane] *= silu_grad<T>(z[r]);
+            }
         }
         __syncthreads();
     }
@@ -359,15 +381,23 @@ causal_bwd_tile(const CausalArgs a, int cblocks, int tblocks, int64_t blocks)
 #pragma unroll
         for (int r = 0; r < R; ++r) acc[r] = 0.0f;
         taps<R, true, kBS, kBT>(dz + r0 * kBS, ws, K, lane, acc);
+        // Inside the sequence and away from the final state's inputs a row is its sum.
+        if (s0 >= 0 && s0 + kTT <= n - (K - 1)) {
+            T *p = (T *)a.dx + (b * a.T + s0 + r0) * a.C + c;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int s = s0 + r0 + r;
-            if (s >= a.T || !cok) continue;
-            float v = s < n ? acc[r] : 0.0f;
-            if (a.dsf && s < n && s >= n - (K - 1))
-                v += to_f32(((const T *)a.dsf)[(b * (K - 1) + s - n + K - 1) * a.C + c]);
-            if (s >= 0) ((T *)a.dx)[(b * a.T + s) * a.C + c] = from_f32<T>(v);
-            else if (a.ds0) ((T *)a.ds0)[(b * (K - 1) + s + K - 1) * a.C + c] = from_f32<T>(v);
+            for (int r = 0; r < R; ++r)
+                if (cok) p[r * a.C] = from_f32<T>(acc[r]);
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int s = s0 + r0 + r;
+                if (s >= a.T || !cok) continue;
+                float v = s < n ? acc[r] : 0.0f;
+                if (a.dsf && s < n && s >= n - (K - 1))
+                    v += to_f32(((const T *)a.dsf)[(b * (K - 1) + s - n + K - 1) * a.C + c]);
+                if (s >= 0) ((T *)a.dx)[(b * a.T + s) * a.C + c] = from_f32<T>(v);
+                else if (a.ds0) ((T *)a.ds0)[(b * (K - 1) + s + K - 1) * a.C + c] = from_f32<T>(v);
+            }
         }
     }
 
