@@ -54,14 +54,18 @@ template <> constexpr int kParts<__bf16> = 1;
 constexpr int kUpdParts = 3;
 constexpr int kLen = 32;     // tokens in a chunk
 
-// A tile of D columns in LDS: rows 16 banks apart within each four and groups of four rows
-// four banks apart, so the 16-byte reads of 16 rows and the transposing reads of 4 rows x
-// 64 bytes both cover all 64 banks.
+// A tile of D columns in LDS, laid out so that the 16-byte reads of 16 rows and the transposing
+// reads of 4 rows x 64 bytes both cover all 64 banks: groups of four rows four banks apart, and
+// within each four the 64-byte blocks that one read takes on different banks, by padding, or for
+// 64 columns (where that is half the tile again) by swapping the two blocks of every other pair.
 template <int D> struct Tile {
-    static constexpr int row = D == 64 ? 96 : D == 128 ? 160 : 288;
-    static constexpr int group = D == 64 ? 392 : D == 128 ? 648 : 1160;
+    static constexpr int row = D == 64 ? 64 : D == 128 ? 160 : 288;
+    static constexpr int group = D == 64 ? 264 : D == 128 ? 648 : 1160;
     static constexpr int size = kLen / 4 * group;
-    static __device__ __forceinline__ int at(int j, int d) { return (j >> 2) * group + (j & 3) * row + d; }
+    static __device__ __forceinline__ int row_at(int j) { return (j >> 2) * group + (j & 3) * row; }
+    // where block q (32 columns) of row j is in it
+    static __device__ __forceinline__ int block(int q, int j) { return (D == 64 ? q ^ (j >> 1 & 1) : q) * 32; }
+    static __device__ __forceinline__ int at(int j, int d) { return row_at(j) + block(d / 32, j) + d % 32; }
 };
 
 template <int NP> struct Part8 { bf16x8 p[NP]; };
@@ -411,11 +415,15 @@ lin_walk(const LinWalks all)
             sm.mask[e] = (j <= i ? 0xffffu : 0u) | (j + 1 <= i ? 0xffff0000u : 0u);
         }
     }
-    const int row_at = Tile<DK>::at(l32, 8 * half);
-    const int col_row = 4 * half + ((lane & 15) >> 2), col_d = (lane & 16) + (lane & 3) * 4;
-    // b's columns of a lane group in the order 0-3, 8-11, 4-7, 12-15
-    const int bcol_at = Tile<DK>::at(col_row, (lane & 16) + (lane & 1) * 8 + (lane & 2) * 2);
-    const int ccol_at = Tile<NT>::at(col_row, 32 * wave + col_d);
+    const int row0 = Tile<DK>::row_at(l32) + 8 * half;
+    auto row_at = [&](int s) { return row0 + Tile<DK>::block(s / 2, l32) + s % 2 * 16; };      // columns 16 s + 8 half ..
+    // Columns over rows: the lane's row of its group, and its four columns (b's in the order
+    // 0-3, 8-11, 4-7, 12-15).
+    const int col_row = 4 * half + ((lane & 15) >> 2);
+    const int bcol0 = Tile<DK>::row_at(col_row) + (lane & 16) + (lane & 1) * 8 + (lane & 2) * 2;
+    auto bcol_at = [&](int g, int x) { return bcol0 + Tile<DK>::block(x, col_row) + 4 * g * Tile<DK>::group; };
+    const int ccol0 = Tile<NT>::row_at(col_row) + Tile<NT>::block(wave, col_row) + (lane & 16) + (lane & 3) * 4;
+    auto ccol_at = [&](int g) { return ccol0 + 4 * g * Tile<NT>::group; };
 
     // Outputs: the state is scale times its registers, so that it need not be scaled for every
     // chunk's decay.  Local states: scale is the weight of the next chunk's last token.
@@ -445,11 +453,11 @@ lin_walk(const LinWalks all)
                 for (int r = 0; r < 16; ++r) sco[r] = 0.0f;
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    const Part8<NP> aq = read_row<DK, NP>(sm.a, row_at + 16 * s);
+                    const Part8<NP> aq = read_row<DK, NP>(sm.a, row_at(s));
                     float f[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) f[e] = st[s / 2][s % 2 * 8 + e];
-                    sco = mma<NP - 1>(read_row<DK, NP>(sm.b, row_at + 16 * s), aq, sco);
+                    sco = mma<NP - 1>(read_row<DK, NP>(sm.b, row_at(s)), aq, sco);
                     acc = mma<NP - 1>(split8<NP>(f), aq, acc);
                 }
                 const float fi = scale * p.inter_scale * sm.pw[min(l32 + p.e0, L)];
@@ -472,7 +480,7 @@ lin_walk(const LinWalks all)
 #pragma unroll
                     for (int q = 0; q < NP; ++q)
                         pr.p[q] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, pr.p[q]) & mask);
-                    acc = mma<NP - 1>(read_col<NT, NP>(sm.c, ccol_at + 4 * g * Tile<NT>::group), pr, acc);
+                    acc = mma<NP - 1>(read_col<NT, NP>(sm.c, ccol_at(g)), pr, acc);
                 }
             }
             if (m < L) {
@@ -498,7 +506,7 @@ lin_walk(const LinWalks all)
             }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const Part8<NP> cT = read_col<NT, NP>(sm.c, ccol_at + 4 * g * Tile<NT>::group);
+                const Part8<NP> cT = read_col<NT, NP>(sm.c, ccol_at(g));
                 float f[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -510,7 +518,7 @@ lin_walk(const LinWalks all)
                 const Part8<kUpdParts> wc = split8<kUpdParts>(f);
 #pragma unroll
                 for (int x = 0; x < NX; ++x)
-                    st[x] = mma<2>(read_col<DK, NP>(sm.b, bcol_at + 4 * g * Tile<DK>::group + 32 * x), wc, st[x]);
+                    st[x] = mma<2>(read_col<DK, NP>(sm.b, bcol_at(g, x)), wc, st[x]);
             }
         }
         scale = settle ? 1.0f : faded;
