@@ -284,6 +284,9 @@ template <typename T, int DK, int NW, bool FULL> struct WalkLds {
 template <typename T, int DK, int NW>
 constexpr int kWavesPerSimd = DK == 256 ? 1 : kParts<T> == 1 && DK / NW <= 32 ? 3 : 2;
 
+// Kernels that have registers to spare before their loop (the others would spill into it).
+template <typename T, int DK> constexpr bool kRoomy = DK == 64 ? kParts<T> > 1 : (DK == 128) == (kParts<T> == 3);
+
 template <typename T, int DK, int NW, bool FULL>
 __global__ void __launch_bounds__(64 * NW, (kWavesPerSimd<T, DK, NW>))
 lin_walk(const LinWalks all)
@@ -347,33 +350,42 @@ lin_walk(const LinWalks all)
     }
     if (tid <= L) sm.pw[tid] = lin_pow(p.log_decay[h], tid);
 
+    if (kRoomy<T, DK> && nchunk > 0) fetch(ufirst);
+
     // The state: column scol, rows 4 half + 32 x + 8 (r / 4) + r % 4 of the tiles, which stand
     // for the columns of b that d_of gives.
     const int scol = n0 + wave * 32 + l32;
     auto d_of = [](int x, int r) { return 32 * x + 16 * (r / 8) + 4 * (r / 4 % 2) + r % 4; };     // + 8 half
     f32x16 st[NX];
-    // st = keep st + *sp, whose rows are sr apart (or neighbours, turned).
+    // st = keep st + *sp, whose rows are sr apart (or neighbours, turned).  The loads of two
+    // tiles are in flight together where registers allow.
+    constexpr int TB = kRoomy<T, DK> ? 2 : 1;
     auto read_state = [&](const float *sp, int sr, int sc, float keep, auto turned) {
 #pragma unroll
-        for (int x = 0; x < NX; ++x) {
+        for (int x0 = 0; x0 < NX; x0 += TB) {
             int d0 = 8 * half;
-            asm volatile("" : "+v"(d0));     // the offsets are made here, not kept from tile to tile
-            float v[16];
+            asm volatile("" : "+v"(d0));     // the offsets are made here, not kept from call to call
+            float v[TB][16];
 #pragma unroll
-            for (int r = 0; r < 16; r += turned ? 4 : 1) {     // rows past the last read those before
-                if constexpr (turned) {
-                    const Run<float, 4> w = load_raw<float, 4>(sp + min(d0 + d_of(x, r), p.Da - 4) + scol * sc, 4);
+            for (int x = 0; x < TB; ++x)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[r + e] = w.v[e];
-                } else {
-                    v[r] = sp[min(d0 + d_of(x, r), p.Da - 1) * sr + scol * sc];
+                for (int r = 0; r < 16; r += turned ? 4 : 1) {     // rows past the last read those before
+                    const int d = d0 + d_of(x0 + x, r);
+                    if constexpr (turned) {
+                        const Run<float, 4> w = load_raw<float, 4>(sp + min(d, p.Da - 4) + scol * sc, 4);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[x][r + e] = w.v[e];
+                    } else {
+                        v[x][r] = sp[min(d, p.Da - 1) * sr + scol * sc];
+                    }
                 }
-            }
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                asm volatile("" : "+v"(v[r]));     // a load inside the condition would wait for each
-                st[x][r] = d0 + d_of(x, r) < p.Da ? fmaf(keep, st[x][r], v[r]) : 0.0f;
-            }
+            for (int x = 0; x < TB; ++x)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    asm volatile("" : "+v"(v[x][r]));     // a load inside the condition would wait for each
+                    st[x0 + x][r] = d0 + d_of(x0 + x, r) < p.Da ? fmaf(keep, st[x0 + x][r], v[x][r]) : 0.0f;
+                }
         }
     };
 #pragma unroll
@@ -403,7 +415,7 @@ lin_walk(const LinWalks all)
         }
     }
 
-    if (nchunk > 0) fetch(ufirst);
+    if (!kRoomy<T, DK> && nchunk > 0) fetch(ufirst);
     __syncthreads();     // the powers
     if constexpr (FULL) {
         for (int e = tid; e < 16 * 64; e += NTH) {

@@ -95,28 +95,42 @@ gconv_status_t check_strides(const int64_t *strides, int n)
     return GCONV_OK;
 }
 
-// Segments of a sequence: three workgroups for each of the 256 compute units over the
-// `walks` that a launch makes, while a segment keeps at least 4 chunks of 64 tokens (a cut
-// sequence reads two of its three inputs again).
+// Segments of a sequence: as many workgroups as the compute units hold at once, counted for
+// each launch of a call, while a segment keeps at least 2 chunks of 64 tokens (a cut sequence
+// reads two of its three inputs again, and every segment sets up its tables and reads a state).
+// Measured with 16 heads of 128 over 65536 tokens in bf16: 508 us with 16 segments, 398 with
+// 47, 453 with 64.
 constexpr int64_t kChunk = 64;
-void lin_segments(const LinShape &s, int walks, int32_t *nseg, int32_t *seg_len)
+
+// Workgroups that the 256 compute units hold of the kernel for a walk (Da, Dc), by its
+// registers and LDS: one of the widest and of wide fp32 ones, two of wide fp16 ones, else three.
+int64_t lin_slots(int64_t Da, gconv_dtype_t dtype)
 {
-    const int64_t chunks = std::max<int64_t>(1, gconv::ceil_div(s.T, kChunk));
-    const int64_t wide = std::max<int64_t>(1, walks * s.B * s.H * gconv::ceil_div(std::min(s.Dk, s.Dv), 128));
-    int64_t n = wide >= 384 ? 1 : std::min<int64_t>({gconv::ceil_div(768, wide), std::max<int64_t>(1, chunks / 4), 1024});
+    if (Da > 128 || (Da > 64 && dtype == GCONV_F32)) return 256;
+    return Da > 64 && dtype == GCONV_F16 ? 512 : 768;
+}
+
+void lin_segments(const LinShape &s, bool backward, gconv_dtype_t dtype, int32_t *nseg, int32_t *seg_len)
+{
+    const int64_t chunks = std::max<int64_t>(1, gconv::ceil_div(s.T, kChunk)), heads = std::max<int64_t>(1, s.B * s.H);
+    auto fit = [&](int64_t walks, int64_t Da, int64_t Dc) {
+        return lin_slots(Da, dtype) / (walks * heads * gconv::ceil_div(Dc, 128));
+    };
+    // The output; or dv, and dq and dk, of one launch where heads are square.
+    int64_t n = !backward         ? fit(1, s.Dk, s.Dv)
+                : s.Dk == s.Dv    ? fit(3, s.Dk, s.Dv)
+                                  : std::min(fit(1, s.Dk, s.Dv), fit(2, s.Dv, s.Dk));
+    n = std::max<int64_t>(1, std::min<int64_t>({n, chunks / 2, 1024}));
     const int64_t each = gconv::ceil_div(chunks, n);
     *nseg = (int32_t)gconv::ceil_div(chunks, each);
     *seg_len = (int32_t)(each * kChunk);
 }
 
-// Walks of a call: the output; or dv, dk and dq, over the states of two of them.
-int lin_walks(bool backward) { return backward ? 3 : 1; }
-
 // One set of segment states.
-size_t lin_states_bytes(const LinShape &s, bool backward)
+size_t lin_states_bytes(const LinShape &s, bool backward, gconv_dtype_t dtype)
 {
     int32_t nseg, len;
-    lin_segments(s, lin_walks(backward), &nseg, &len);
+    lin_segments(s, backward, dtype, &nseg, &len);
     return nseg > 1 ? sizeof(float) * (size_t)(s.B * s.H * nseg * s.Dk * s.Dv) : 0;
 }
 
@@ -127,9 +141,9 @@ size_t lin_part_bytes(const LinShape &s)
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-size_t lin_workspace(const LinShape &s, bool backward)
+size_t lin_workspace(const LinShape &s, bool backward, gconv_dtype_t dtype)
 {
-    const size_t states = align256(lin_states_bytes(s, backward));
+    const size_t states = align256(lin_states_bytes(s, backward, dtype));
     return backward ? 2 * states + 2 * align256(lin_part_bytes(s)) : states;
 }
 
@@ -143,7 +157,7 @@ gconv::LinWalk lin_base(const LinShape &s, bool backward, const float *log_decay
     p.lengths = lengths;
     p.dtype = (int)dtype;
     p.stream = (hipStream_t)stream;
-    lin_segments(s, lin_walks(backward), &p.nseg, &p.seg_len);
+    lin_segments(s, backward, dtype, &p.nseg, &p.seg_len);
     return p;
 }
 
@@ -203,7 +217,7 @@ gconv_status_t gconv_linear_attention_workspace(const int64_t *shape, gconv_dtyp
     LinShape s;
     const gconv_status_t st = lin_shape(shape, &s);
     if (st != GCONV_OK) return st;
-    *bytes = lin_workspace(s, backward != 0);
+    *bytes = lin_workspace(s, backward != 0, dtype);
     return GCONV_OK;
 }
 
@@ -219,7 +233,7 @@ gconv_status_t gconv_linear_attention(const void *q, const void *k, const void *
     if (st != GCONV_OK || (st = check_strides(strides, 12)) != GCONV_OK) return st;
     if (!log_decay) return fail(GCONV_ERR_INVALID_ARG, "NULL log_decay");
     if (s.B > 0 && s.T > 0 && (!q || !k || !v || !o)) return fail(GCONV_ERR_INVALID_ARG, "NULL q, k, v or o");
-    const size_t need = lin_workspace(s, false), es = elem(dtype), ns = 4 * (size_t)(s.B * s.H * s.Dk * s.Dv);
+    const size_t need = lin_workspace(s, false, dtype), es = elem(dtype), ns = 4 * (size_t)(s.B * s.H * s.Dk * s.Dv);
     if ((st = check_workspace(workspace, workspace_bytes, need)) != GCONV_OK) return st;
     const Range r[] = {
         {"o", o, extent(s.B, strides[9], s.T, strides[10], s.H, strides[11], s.Dv, es), true},
@@ -275,7 +289,7 @@ gconv_status_t gconv_linear_attention_backward(const void *q, const void *k, con
     if (!log_decay) return fail(GCONV_ERR_INVALID_ARG, "NULL log_decay");
     if (s.B > 0 && s.T > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv))
         return fail(GCONV_ERR_INVALID_ARG, "NULL q, k, v, d_o, dq, dk or dv");
-    const size_t need = lin_workspace(s, true), es = elem(dtype), ns = 4 * (size_t)(s.B * s.H * s.Dk * s.Dv);
+    const size_t need = lin_workspace(s, true, dtype), es = elem(dtype), ns = 4 * (size_t)(s.B * s.H * s.Dk * s.Dv);
     if ((st = check_workspace(workspace, workspace_bytes, need)) != GCONV_OK) return st;
     auto ext = [&](int i, int64_t heads, int64_t D) {
         return extent(s.B, strides[3 * i], s.T, strides[3 * i + 1], heads, strides[3 * i + 2], D, es);
@@ -294,7 +308,7 @@ gconv_status_t gconv_linear_attention_backward(const void *q, const void *k, con
     const View vq{q, strides, s.Hk, s.Dk}, vk{k, strides + 3, s.Hk, s.Dk}, vv{v, strides + 6, s.H, s.Dv},
         vdo{d_o, strides + 9, s.H, s.Dv};
     const int32_t rep = (int32_t)(s.H / s.Hk);
-    const size_t nstates = align256(lin_states_bytes(s, true)), npart = align256(lin_part_bytes(s));
+    const size_t nstates = align256(lin_states_bytes(s, true, dtype)), npart = align256(lin_part_bytes(s));
     float *ahead = (float *)workspace, *behind = (float *)((char *)workspace + nstates);
     char *part = (char *)workspace + 2 * nstates;
     const char *kname = "lin_scan";
