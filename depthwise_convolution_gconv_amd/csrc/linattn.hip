@@ -10,9 +10,10 @@ namespace gconv {
 namespace {
 
 constexpr int kThreads = 256;
-// States before each segment from the segments' own sums, in place:
-//     R_(g+1) = lam^(tokens of g) R_g + local_g,  R_0 = s0.
-// Two neighbouring elements for each thread, 8 segments' loads in flight.
+// States before each segment but the first from the segments' own sums, in place:
+//     R_1 = local_0,  R_(g+1) = lam^(tokens of g) R_g + local_g
+// (local_0 holds what is left of s0).  Two neighbouring elements for each thread, 8
+// segments' loads in flight.
 constexpr int kMaxSeg = 1024;
 constexpr int kScan = 2;
 __global__ void __launch_bounds__(kThreads)
@@ -36,7 +37,7 @@ lin_scan(const LinWalks all)
 #pragma unroll
     for (int e = 0; e < kScan; ++e) {
         const int64_t d = (x + e) / p.Dc, c = (x + e) % p.Dc;
-        r[e] = p.s0 && e < left ? p.s0[bi * p.s0b + h * p.s0h + d * p.s0r + c * p.s0c] : 0.0f;
+        r[e] = p.nseg == 0 && p.s0 && e < left ? p.s0[bi * p.s0b + h * p.s0h + d * p.s0r + c * p.s0c] : 0.0f;
     }
     float *w = p.ws + bh * p.nseg * cells + x;
     for (int g0 = 0; g0 < p.nseg; g0 += 8) {
@@ -46,7 +47,7 @@ lin_scan(const LinWalks all)
 #pragma unroll
         for (int g = 0; g < 8; ++g)
             if (g0 + g < p.nseg) {
-                store_run<float, kScan>(w + (g0 + g) * cells, left, r);
+                if (g0 + g > 0) store_run<float, kScan>(w + (g0 + g) * cells, left, r);
 #pragma unroll
                 for (int e = 0; e < kScan; ++e) r[e] = fmaf(lam[g0 + g], r[e], loc[g][e]);
             }
@@ -181,10 +182,12 @@ static hipError_t run_walks(const LinWalks &all, bool full)
     return hipSuccess;
 }
 
-hipError_t launch_lin_states(const LinWalks &all, const char **kname)
+hipError_t launch_lin_states(const LinWalks &all, int summed, const char **kname)
 {
     *kname = "lin_walk";
-    const hipError_t err = run_walks(all, false);
+    LinWalks some = all;
+    some.count = summed;
+    const hipError_t err = run_walks(some, false);
     return err != hipSuccess || all.w[0].nseg <= kFoldSegs ? err : launch_lin_scan(all);
 }
 

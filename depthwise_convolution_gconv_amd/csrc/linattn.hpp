@@ -30,8 +30,8 @@ struct LinWalk {
     int64_t s0b, s0h, s0r, s0c;  // its element strides: batch, head, row (a's column), column (c's)
     float *sf;                   // state after the last token, or nullptr
     int64_t sfb, sfh, sfr, sfc;
-    float *ws;                   // [B*H][nseg] states of Da x Dc, strides wsr, wsc
-    int64_t wsr, wsc;
+    float *ws;                   // [B*H][nseg] states of Da x Dc
+    float *wst;                  // their transposes for another walk (written with them), or nullptr
     float p_scale, inter_scale, upd_scale;
     int32_t e0, reverse;
     int32_t nseg, seg_len;       // segments of seg_len tokens (a multiple of 64), walked by one workgroup each
@@ -78,12 +78,14 @@ hipError_t run_lin_walks_bf16(const LinWalks &all, bool full);
 // one writes sf: a mean of half as many reads as there are segments, and no scan.
 constexpr int kFoldSegs = 8;
 
-// The segment states (nseg > 1): local sums into ws, then past kFoldSegs the scan that turns
-// them into the states before each segment and writes sf.
-hipError_t launch_lin_states(const LinWalks &all, const char **kname);
+// The segment states (nseg > 1): local sums into ws, the first with what is left of s0, then
+// past kFoldSegs the scan that turns them into the states before each segment but the first
+// and writes sf.  The first `summed` walks have states of their own, the others' are the
+// transposes that those write.
+hipError_t launch_lin_states(const LinWalks &all, int summed, const char **kname);
 // The outputs (up to kFoldSegs also sf).
 hipError_t launch_lin_walks(const LinWalks &all, const char **kname);
-// Scan alone (T == 0 or nseg segments already summed).
+// Scan alone (T == 0: sf = s0).
 hipError_t launch_lin_scan(const LinWalks &all);
 // out[b,t,g,:] = sum over j < r of part[b,t,g*r+j,:] (contiguous), rounded to dtype; ost: out's
 // element strides (batch, token, head).

@@ -33,8 +33,6 @@
 // accumulators for the whole walk.
 #pragma once
 
-#include <type_traits>
-
 #include "linattn.hpp"
 #include "vecio.hpp"
 
@@ -357,10 +355,10 @@ lin_walk(const LinWalks all)
     const int scol = n0 + wave * 32 + l32;
     auto d_of = [](int x, int r) { return 32 * x + 16 * (r / 8) + 4 * (r / 4 % 2) + r % 4; };     // + 8 half
     f32x16 st[NX];
-    // st = keep st + *sp, whose rows are sr apart (or neighbours, turned).  The loads of two
-    // tiles are in flight together where registers allow.
+    // st = keep st + gain *sp, whose rows are sr apart.  The loads of two tiles are in flight
+    // together where registers allow.
     constexpr int TB = kRoomy<T, DK> ? 2 : 1;
-    auto read_state = [&](const float *sp, int sr, int sc, float keep, auto turned) {
+    auto read_state = [&](const float *sp, int sr, int sc, float keep, float gain) {
 #pragma unroll
         for (int x0 = 0; x0 < NX; x0 += TB) {
             int d0 = 8 * half;
@@ -369,22 +367,14 @@ lin_walk(const LinWalks all)
 #pragma unroll
             for (int x = 0; x < TB; ++x)
 #pragma unroll
-                for (int r = 0; r < 16; r += turned ? 4 : 1) {     // rows past the last read those before
-                    const int d = d0 + d_of(x0 + x, r);
-                    if constexpr (turned) {
-                        const Run<float, 4> w = load_raw<float, 4>(sp + min(d, p.Da - 4) + scol * sc, 4);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[x][r + e] = w.v[e];
-                    } else {
-                        v[x][r] = sp[min(d, p.Da - 1) * sr + scol * sc];
-                    }
-                }
+                for (int r = 0; r < 16; ++r)     // rows past the last read that one
+                    v[x][r] = sp[min(d0 + d_of(x0 + x, r), p.Da - 1) * sr + scol * sc];
 #pragma unroll
             for (int x = 0; x < TB; ++x)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     asm volatile("" : "+v"(v[x][r]));     // a load inside the condition would wait for each
-                    st[x0 + x][r] = d0 + d_of(x0 + x, r) < p.Da ? fmaf(keep, st[x0 + x][r], v[x][r]) : 0.0f;
+                    st[x0 + x][r] = d0 + d_of(x0 + x, r) < p.Da ? fmaf(keep, st[x0 + x][r], gain * v[x][r]) : 0.0f;
                 }
         }
     };
@@ -393,26 +383,16 @@ lin_walk(const LinWalks all)
 #pragma unroll
         for (int r = 0; r < 16; ++r) st[x][r] = 0.0f;
     const bool fold = p.nseg <= kFoldSegs, ends = FULL && fold && p.sf && seg + 1 == p.nseg;
-    if (FULL && scol < p.Dc) {
-        const int64_t cells = (int64_t)p.Da * p.Dc;
-        // The state before the first segment and the local ones up to this; or what the scan made of them.
-        auto read_all = [&](auto turned) {
-            const int last = fold ? seg : seg + 1;
+    const float *s0 = p.s0 ? p.s0 + bi * p.s0b + h * p.s0h : nullptr;
+    auto tokens_of = [&](int g) { return max(0, min(n - g * p.seg_len, p.seg_len)); };
+    if (FULL && scol < p.Dc && (seg > 0 || s0)) {
+        // The state before the first segment; or the local ones up to this, of which the first
+        // holds that state's rest; or what the scan made of them.
+        const bool first = seg == 0;
 #pragma unroll 1
-            for (int g = fold ? 0 : seg; g < last; ++g)
-                read_state(p.ws + (bh * p.nseg + g) * cells, (int)p.wsr, (int)p.wsc,
-                           fold ? lin_pow(p.log_decay[h], max(0, min(n - g * p.seg_len, p.seg_len))) : 0.0f, turned);
-        };
-        if (p.s0 && fold) read_state(p.s0 + bi * p.s0b + h * p.s0h, (int)p.s0r, (int)p.s0c, 0.0f, std::false_type{});
-        // 16-byte reads of transposed states only where registers are left: the second copy made
-        // the loop of the widest bf16 walk spill (244 us became 295 over 65536 tokens x 16 heads),
-        // fp32 gradients gain (101 us became 92 over 8 x 1024 tokens x 8 heads).
-        if constexpr (kWavesPerSimd<T, DK, NW> < 3) {
-            if (p.wsr == 1 && p.Da % 4 == 0) read_all(std::true_type{});
-            else read_all(std::false_type{});
-        } else {
-            read_all(std::false_type{});
-        }
+        for (int g = first || fold ? 0 : seg; g < (first || !fold ? seg + 1 : seg); ++g)
+            read_state(first ? s0 : p.ws + (bh * p.nseg + g) * (int64_t)p.Da * p.Dc, (int)(first ? p.s0r : p.Dc),
+                       (int)(first ? p.s0c : 1), fold && g > 0 ? lin_pow(p.log_decay[h], tokens_of(g)) : 0.0f, 1.0f);
     }
 
     if (!kRoomy<T, DK> && nchunk > 0) fetch(ufirst);
@@ -537,11 +517,13 @@ lin_walk(const LinWalks all)
         __syncthreads();
     }
 
-    float *dp = nullptr;
-    int dr = 0, dc = 0;      // a state's offsets stay below 2^16
+    if (!FULL && seg == 0 && s0 && scol < p.Dc)
+        read_state(s0, (int)p.s0r, (int)p.s0c, 1.0f, lin_pow(p.log_decay[h], tokens_of(0)));
+    float *dp = nullptr, *tp = nullptr;
+    int dr = p.Dc, dc = 1;       // a state's offsets stay below 2^16
     if (!FULL) {
         dp = p.ws + (bh * p.nseg + seg) * (int64_t)p.Da * p.Dc;
-        dr = (int)p.wsr; dc = (int)p.wsc;
+        if (p.wst) tp = p.wst + (bh * p.nseg + seg) * (int64_t)p.Da * p.Dc;
     } else if (ends) {
         dp = p.sf + bi * p.sfb + h * p.sfh;
         dr = (int)p.sfr; dc = (int)p.sfc;
@@ -556,6 +538,16 @@ lin_walk(const LinWalks all)
                 const int d = d0 + d_of(x, r);
                 if (d < p.Da) dp[d * dr + scol * dc] = FULL ? st[x][r] * scale : st[x][r];
             }
+        if (!FULL && tp) {
+#pragma unroll
+            for (int x = 0; x < NX; ++x)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4) {
+                    const int d = d0 + d_of(x, r);
+                    const float f[4] = {st[x][r], st[x][r + 1], st[x][r + 2], st[x][r + 3]};
+                    if (d < p.Da) store_run<float, 4>(tp + scol * p.Da + d, p.Da - d, f);
+                }
+        }
     }
 }
 

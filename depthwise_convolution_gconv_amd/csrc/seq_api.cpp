@@ -144,7 +144,7 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t lin_workspace(const LinShape &s, bool backward, gconv_dtype_t dtype)
 {
     const size_t states = align256(lin_states_bytes(s, backward, dtype));
-    return backward ? 2 * states + 2 * align256(lin_part_bytes(s)) : states;
+    return backward ? 3 * states + 2 * align256(lin_part_bytes(s)) : states;
 }
 
 // What every pass over these heads shares.
@@ -258,7 +258,7 @@ gconv_status_t gconv_linear_attention(const void *q, const void *k, const void *
     p.out = o; p.osb = strides[9]; p.ost = strides[10]; p.osh = strides[11];
     set_s0(p, initial_state, s, false);
     set_sf(p, final_state, s);
-    p.ws = (float *)workspace; p.wsr = s.Dv; p.wsc = 1;
+    p.ws = (float *)workspace;
     p.p_scale = p.inter_scale = scale;
     p.upd_scale = 1.0f;
     p.e0 = 1;
@@ -269,7 +269,7 @@ gconv_status_t gconv_linear_attention(const void *q, const void *k, const void *
         return done(gconv::launch_lin_scan(all), kname);
     }
     hipError_t err = hipSuccess;
-    if (p.nseg > 1) err = gconv::launch_lin_states(all, &kname);
+    if (p.nseg > 1) err = gconv::launch_lin_states(all, 1, &kname);
     if (err == hipSuccess) err = gconv::launch_lin_walks(all, &kname);
     return done(err, kname);
 }
@@ -309,23 +309,24 @@ gconv_status_t gconv_linear_attention_backward(const void *q, const void *k, con
         vdo{d_o, strides + 9, s.H, s.Dv};
     const int32_t rep = (int32_t)(s.H / s.Hk);
     const size_t nstates = align256(lin_states_bytes(s, true, dtype)), npart = align256(lin_part_bytes(s));
-    float *ahead = (float *)workspace, *behind = (float *)((char *)workspace + nstates);
-    char *part = (char *)workspace + 2 * nstates;
+    float *ahead = (float *)workspace, *behind = (float *)((char *)workspace + nstates),
+          *turned = (float *)((char *)workspace + 2 * nstates);
+    char *part = (char *)workspace + 3 * nstates;
     const char *kname = "lin_scan";
     const gconv::LinWalk base = lin_base(s, true, log_decay, lengths, dtype, hip_stream);
     gconv::LinWalks all = {};
     all.count = 3;
     gconv::LinWalk &pv = all.w[0], &pq = all.w[1], &pk = all.w[2];
 
-    // Gradients of later tokens: states of q do^T from the end, which dv reads by row and
-    // dk transposed; their value before the first token is the initial state's gradient.
+    // Gradients of later tokens: states of q do^T from the end, for dv and transposed for dk; their value before the first token is the initial state's gradient.
     pv = base;
     set_a(pv, vk);
     set_b(pv, vq);
     set_c(pv, vdo);
     set_s0(pv, dfinal, s, false);
     set_sf(pv, dinitial, s);
-    pv.ws = behind; pv.wsr = s.Dv; pv.wsc = 1;
+    pv.ws = behind;
+    pv.wst = turned;
     pv.p_scale = pv.upd_scale = scale;
     pv.inter_scale = 1.0f;
     pv.e0 = 0;
@@ -344,7 +345,7 @@ gconv_status_t gconv_linear_attention_backward(const void *q, const void *k, con
     set_b(pq, vv);
     set_c(pq, vk);
     set_s0(pq, initial_state, s, true);
-    pq.ws = ahead; pq.wsr = s.Dk; pq.wsc = 1;
+    pq.ws = ahead;
     pq.p_scale = pq.inter_scale = scale;
     pq.upd_scale = 1.0f;
     pq.e0 = 1;
@@ -355,7 +356,8 @@ gconv_status_t gconv_linear_attention_backward(const void *q, const void *k, con
     set_c(pk, vq);
     set_s0(pk, dfinal, s, true);
     pk.sf = nullptr;
-    pk.wsr = 1; pk.wsc = s.Dv;
+    pk.ws = turned;
+    pk.wst = nullptr;
 
     // A key head that serves several value heads: each writes its share in fp32, then the
     // shares are added and rounded once.
@@ -369,11 +371,7 @@ gconv_status_t gconv_linear_attention_backward(const void *q, const void *k, con
     key_grad(pq, dq, strides + 12, (float *)part);
     key_grad(pk, dk, strides + 15, (float *)(part + npart));
     hipError_t err = hipSuccess;
-    if (base.nseg > 1) {
-        gconv::LinWalks states = all;
-        states.count = 2;    // dk's are dv's
-        err = gconv::launch_lin_states(states, &kname);
-    }
+    if (base.nseg > 1) err = gconv::launch_lin_states(all, 2, &kname);
     if (err == hipSuccess) err = gconv::launch_lin_walks(all, &kname);
     if (rep > 1) {
         auto sum = [&](const void *shares, void *out, const int64_t *st) {
