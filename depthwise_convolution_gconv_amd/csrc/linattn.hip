@@ -61,19 +61,19 @@ lin_scan(const LinWalks all)
     }
 }
 
+// The value heads of a key head added up: workgroups of 256 columns of a token's Hk D.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-lin_group_sum(const float *__restrict__ part, T *__restrict__ out, int64_t sb, int64_t st, int64_t sh, int64_t total,
-              int64_t T_in, int Hk, int r, int D)
+lin_group_sum(const float *__restrict__ part, T *__restrict__ out, int64_t sb, int64_t st, int64_t sh, int T_in, int Hk,
+              int r, int D, int blocks)
 {
-    for (int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x; x < total; x += (int64_t)gridDim.x * kThreads) {
-        const int64_t g = x / D, bt = g / Hk;    // (batch, token, key head), (batch, token)
-        const int d = (int)(x - g * D);
-        const float *src = part + g * r * D + d;
-        float s = src[0];
-        for (int j = 1; j < r; ++j) s += src[(int64_t)j * D];
-        out[bt / T_in * sb + bt % T_in * st + (g - bt * Hk) * sh + d] = from_f32<T>(s);
-    }
+    const int64_t bt = blockIdx.x / blocks;      // (batch, token)
+    const int x = (int)(blockIdx.x % blocks) * kThreads + threadIdx.x, g = x / D, d = x - g * D;
+    if (g >= Hk) return;
+    const float *src = part + (bt * Hk + g) * r * D + d;
+    float s = src[0];
+    for (int j = 1; j < r; ++j) s += src[j * D];
+    out[bt / T_in * sb + bt % T_in * st + g * sh + d] = from_f32<T>(s);
 }
 
 // ---------------------------------------------------------------- single tokens
@@ -169,7 +169,7 @@ static hipError_t run_walks(const LinWalks &all, bool full)
         LinWalks some = {};
         bool first = true;
         for (int j = 0; j < all.count; ++j)
-            if (lin_alike(all.w[j], all.w[i])) {
+            if (lin_alike(all.w[j].Da, all.w[j].Dc, all.w[i].Da, all.w[i].Dc)) {
                 first = first && j >= i;
                 some.w[some.count++] = all.w[j];
             }
@@ -200,20 +200,21 @@ hipError_t launch_lin_walks(const LinWalks &all, const char **kname)
 hipError_t launch_lin_group_sum(const float *part, void *out, const int64_t *ost, int64_t B, int64_t T, int Hk, int r,
                                 int D, int dtype, hipStream_t stream)
 {
-    const int64_t total = B * T * Hk * D;
-    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(total, kThreads), 1 << 16)), block(kThreads);
+    const int blocks = (int)ceil_div((int64_t)Hk * D, kThreads);
+    if (B * T * blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(B * T * blocks)), block(kThreads);
     switch (dtype) {
     case DT_F32:
         hipLaunchKernelGGL((lin_group_sum<float>), grid, block, 0, stream, part, (float *)out, ost[0], ost[1], ost[2],
-                           total, T, Hk, r, D);
+                           (int)T, Hk, r, D, blocks);
         break;
     case DT_F16:
         hipLaunchKernelGGL((lin_group_sum<_Float16>), grid, block, 0, stream, part, (_Float16 *)out, ost[0], ost[1],
-                           ost[2], total, T, Hk, r, D);
+                           ost[2], (int)T, Hk, r, D, blocks);
         break;
     default:
         hipLaunchKernelGGL((lin_group_sum<__bf16>), grid, block, 0, stream, part, (__bf16 *)out, ost[0], ost[1], ost[2],
-                           total, T, Hk, r, D);
+                           (int)T, Hk, r, D, blocks);
         break;
     }
     return hipGetLastError();

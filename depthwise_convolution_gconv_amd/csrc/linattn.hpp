@@ -66,8 +66,18 @@ struct LinWalks {
     int64_t blocks;              // workgroups
 };
 
-// Walks of the same column counts: one kernel and one number of workgroups for each.
-inline bool lin_alike(const LinWalk &p, const LinWalk &q) { return p.Da == q.Da && p.Dc == q.Dc; }
+// The kernel of a walk: columns of a and b it holds (64, 128 or 256) and waves of 32 columns of
+// c.  Two waves where 64 columns are all there are, but for the widest rows: their staging is
+// shared by four.
+inline int lin_wide(int64_t Da) { return Da <= 64 ? 64 : Da <= 128 ? 128 : 256; }
+inline int lin_waves(int64_t Da, int64_t Dc) { return Dc <= 64 && Da <= 128 ? 2 : 4; }
+inline int64_t lin_tiles(int64_t Da, int64_t Dc) { return ceil_div(Dc, 32 * lin_waves(Da, Dc)); }
+
+// Walks that one launch can make: one kernel, and one number of workgroups for each.
+inline bool lin_alike(int64_t Da, int64_t Dc, int64_t Ea, int64_t Ec)
+{
+    return lin_wide(Da) == lin_wide(Ea) && lin_waves(Da, Dc) == lin_waves(Ea, Ec) && lin_tiles(Da, Dc) == lin_tiles(Ea, Ec);
+}
 
 // The walks of all segments, outputs (full) or local states only, for each dtype; all alike.
 hipError_t run_lin_walks_f32(const LinWalks &all, bool full);

@@ -562,14 +562,16 @@ template <typename T, int DK, int NW, bool FULL> hipError_t run_walk_on(LinWalks
     return hipGetLastError();
 }
 
-// The walks of `all` are alike (lin_alike).
+// The walks of `all` are alike.
 template <typename T, bool FULL> hipError_t run_walks(const LinWalks &all)
 {
-    // Two waves where 64 columns are all there are, but for wide rows: their staging is shared by four.
     const LinWalk &p = all.w[0];
-    if (p.Da <= 64) return p.Dc <= 64 ? run_walk_on<T, 64, 2, FULL>(all) : run_walk_on<T, 64, 4, FULL>(all);
-    if (p.Da <= 128) return p.Dc <= 64 ? run_walk_on<T, 128, 2, FULL>(all) : run_walk_on<T, 128, 4, FULL>(all);
-    return run_walk_on<T, 256, 4, FULL>(all);
+    const bool two = lin_waves(p.Da, p.Dc) == 2;
+    switch (lin_wide(p.Da)) {
+    case 64: return two ? run_walk_on<T, 64, 2, FULL>(all) : run_walk_on<T, 64, 4, FULL>(all);
+    case 128: return two ? run_walk_on<T, 128, 2, FULL>(all) : run_walk_on<T, 128, 4, FULL>(all);
+    default: return run_walk_on<T, 256, 4, FULL>(all);
+    }
 }
 
 }  // namespace

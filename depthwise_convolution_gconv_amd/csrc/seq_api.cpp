@@ -114,12 +114,12 @@ void lin_segments(const LinShape &s, bool backward, gconv_dtype_t dtype, int32_t
 {
     const int64_t chunks = std::max<int64_t>(1, gconv::ceil_div(s.T, kChunk)), heads = std::max<int64_t>(1, s.B * s.H);
     auto fit = [&](int64_t walks, int64_t Da, int64_t Dc) {
-        return lin_slots(Da, dtype) / (walks * heads * gconv::ceil_div(Dc, 128));
+        return lin_slots(Da, dtype) / (walks * heads * gconv::lin_tiles(Da, Dc));
     };
-    // The output; or dv, and dq and dk, of one launch where heads are square.
-    int64_t n = !backward         ? fit(1, s.Dk, s.Dv)
-                : s.Dk == s.Dv    ? fit(3, s.Dk, s.Dv)
-                                  : std::min(fit(1, s.Dk, s.Dv), fit(2, s.Dv, s.Dk));
+    // The output; or dv, and dq and dk, in one launch where they can be.
+    int64_t n = !backward                                      ? fit(1, s.Dk, s.Dv)
+                : gconv::lin_alike(s.Dk, s.Dv, s.Dv, s.Dk)     ? fit(3, s.Dk, s.Dv)
+                                                               : std::min(fit(1, s.Dk, s.Dv), fit(2, s.Dv, s.Dk));
     n = std::max<int64_t>(1, std::min<int64_t>({n, chunks / 2, 1024}));
     const int64_t each = gconv::ceil_div(chunks, n);
     *nseg = (int32_t)gconv::ceil_div(chunks, each);
