@@ -175,7 +175,11 @@ def linear_attention(q, k, v, log_decay, scale: Optional[float] = None, initial_
     scale defaults to Dk**-0.5.  initial_state: fp32 [B, H, Dk, Dv].  lengths: int32 [B],
     the tokens of each sequence that exist; the outputs of the others are zero.
     Returns o [B, T, H, Dv], or (o, state) with the fp32 state after each sequence's last
-    token, which linear_attention_step carries on from."""
+    token, which linear_attention_step carries on from.
+
+    Sums and states are fp32; scores, and the state where a query meets it, are rounded to the
+    inputs' precision for their second product.  A non-finite v makes its column NaN in the
+    other tokens of its chunk of 32 too, earlier ones among them."""
     dt, shape, strides, g, n = _attn_args(q, k, v, log_decay, lengths)
     B, T, Hk, H, Dk, Dv = shape
     dev = q.get_device()

@@ -295,9 +295,10 @@ void gconv_autotune_clear(void);
  *     S_t = lam S_(t-1) + k_t v_t^T,   o_t = scale * q_t S_t
  * initial_state: fp32 [B,H,Dk,Dv] = S_(-1), or NULL (zero).  final_state: the same shape,
  * S after lengths[b] tokens, or NULL.  strides = {q: batch, token, head; k; v; o}, 12
- * values.  Tokens are taken in chunks of 64: a non-finite q, k or v of a real token can
- * reach the outputs of its whole chunk.  workspace: gconv_linear_attention_workspace
- * bytes (may be 0), 16-byte aligned. */
+ * values.  Tokens are taken in chunks of 32: a non-finite v of a real token makes its column
+ * of the outputs NaN for the whole chunk (a non-finite q or k reaches its own and later
+ * tokens only), and an infinity in fp16 or fp32 inputs counts as NaN.  workspace:
+ * gconv_linear_attention_workspace bytes (may be 0), 16-byte aligned. */
 gconv_status_t gconv_linear_attention_workspace(const int64_t *shape, gconv_dtype_t dtype, int32_t backward,
                                                 size_t *bytes);
 gconv_status_t gconv_linear_attention(const void *q, const void *k, const void *v, void *o, const int64_t *shape,
