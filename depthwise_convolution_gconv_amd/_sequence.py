@@ -95,36 +95,21 @@ def _whole(name: str, t: Optional[torch.Tensor], dtype, dev: int, shape) -> int:
     return t.data_ptr()
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream     # current_stream() without its Python object
+# The current device and stream without their Python objects, which cost more than the rest of a
+# single-token call's checks.
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-class _On:
-    """The device and stream a call runs on."""
+def _stream(dev: int, stream) -> int:
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
-    __slots__ = ("device", "stream", "handle", "_guard")
 
-    def __init__(self, device: int, stream):
-        self.device = device
-        self.stream = stream
-        self._guard = None
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.device:
-            self._guard = torch.cuda.device(self.device)
-            self._guard.__enter__()
-        self.handle = _raw_stream(self.device) if self.stream is None else self.stream.cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-
-    def made(self, *tensors):
-        """Tensors this call allocated: their memory is in use on the call's stream."""
-        if self.stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
+def _made(stream, *tensors):
+    """Tensors a call allocated: their memory is in use on the stream it was given."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _workspace(need: int, ref: torch.Tensor) -> Optional[torch.Tensor]:
@@ -188,15 +173,18 @@ def linear_attention(q, k, v, log_decay, scale: Optional[float] = None, initial_
     need = _size(0)
     L = _library()
     _check(L.gconv_linear_attention_workspace(sh, dt, 0, ctypes.byref(need)))
-    with _On(dev, stream) as on:
-        o = _like(v)
-        st = q.new_empty((B, H, Dk, Dv), dtype=torch.float32) if return_state else None
-        ws = _workspace(need.value, q)
-        on.made(o, st, ws)
-        _check(L.gconv_linear_attention(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), sh,
-            _array(*strides, *o.stride()[:3]), g,
-            Dk ** -0.5 if scale is None else scale, s0, _ptr(st), n, dt, _ptr(ws), need.value, on.handle))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return linear_attention(q, k, v, log_decay, scale, initial_state, lengths, return_state, stream)
+    o = _like(v)
+    st = q.new_empty((B, H, Dk, Dv), dtype=torch.float32) if return_state else None
+    ws = _workspace(need.value, q)
+    if stream is not None:
+        _made(stream, o, st, ws)
+    _check(L.gconv_linear_attention(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), sh,
+        _array(*strides, *o.stride()[:3]), g,
+        Dk ** -0.5 if scale is None else scale, s0, _ptr(st), n, dt, _ptr(ws), need.value, _stream(dev, stream)))
     return (o, st) if return_state else o
 
 
@@ -215,15 +203,18 @@ def linear_attention_backward(q, k, v, log_decay, do, scale: Optional[float] = N
     need = _size(0)
     L = _library()
     _check(L.gconv_linear_attention_workspace(sh, dt, 1, ctypes.byref(need)))
-    with _On(dev, stream) as on:
-        dq, dk, dv = _like(q), _like(k), _like(v)
-        ds = q.new_empty((B, H, Dk, Dv), dtype=torch.float32) if initial_state is not None else None
-        ws = _workspace(need.value, q)
-        on.made(dq, dk, dv, ds, ws)
-        _check(L.gconv_linear_attention_backward(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), sh,
-            _array(*strides, *dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3]), g, Dk ** -0.5 if scale is None else scale, s0, sf,
-            _ptr(ds), n, dt, _ptr(ws), need.value, on.handle))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return linear_attention_backward(q, k, v, log_decay, do, scale, initial_state, lengths, dstate, stream)
+    dq, dk, dv = _like(q), _like(k), _like(v)
+    ds = q.new_empty((B, H, Dk, Dv), dtype=torch.float32) if initial_state is not None else None
+    ws = _workspace(need.value, q)
+    if stream is not None:
+        _made(stream, dq, dk, dv, ds, ws)
+    _check(L.gconv_linear_attention_backward(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), sh,
+        _array(*strides, *dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3]), g, Dk ** -0.5 if scale is None else scale, s0, sf,
+        _ptr(ds), n, dt, _ptr(ws), need.value, _stream(dev, stream)))
     return dq, dk, dv, ds
 
 
@@ -243,13 +234,16 @@ def linear_attention_step(q, k, v, log_decay, state, scale: Optional[float] = No
     g = _whole("log_decay", log_decay, torch.float32, dev, (H,))
     sp = _whole("state", state, torch.float32, dev, (state.shape[0], H, Dk, Dv))
     sl = _whole("slots", slots, torch.int32, dev, (B,))
-    with _On(dev, stream) as on:
-        o = _like(v)
-        on.made(o)
-        _check(_library().gconv_linear_attention_step(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), sp, _array(B, Hk, H, Dk, Dv, state.shape[0]),
-            _array(*strides, *o.stride()[:2]), g,
-            Dk ** -0.5 if scale is None else scale, sl, dt, on.handle))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return linear_attention_step(q, k, v, log_decay, state, scale, slots, stream)
+    o = _like(v)
+    if stream is not None:
+        _made(stream, o)
+    _check(_library().gconv_linear_attention_step(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), sp, _array(B, Hk, H, Dk, Dv, state.shape[0]),
+        _array(*strides, *o.stride()[:2]), g,
+        Dk ** -0.5 if scale is None else scale, sl, dt, _stream(dev, stream)))
     return o
 
 
@@ -281,30 +275,34 @@ def _norm(x, weight, residual, eps, q8, block, stream):
     C = x.shape[-1]
     rows = x.numel() // C
     dev = x.get_device()
-    with _On(dev, stream) as on:
-        xs = _rows("x", x, x)
-        w = _whole("weight", weight, x.dtype, dev, (C,))
-        if not w:
-            _bad("weight is needed")
-        if residual is not None:
-            rs = _rows("residual", residual, x)
-            h = _like(x)
-        else:
-            rs, h = 0, None
-        L = _library()
-        if not q8:
-            y = _like(x)
-            on.made(y, h)
-            _check(L.gconv_rms_norm(x.data_ptr(), _ptr(residual), w, y.data_ptr(), _ptr(h), rows, C, _array(xs, rs), eps,
-                                    dt, on.handle))
-            return y, h
-        y = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
-        nb = -(-C // block) if block > 0 else 1
-        scales = x.new_empty((*x.shape[:-1], nb), dtype=torch.float32)
-        on.made(y, scales, h)
-        _check(L.gconv_rms_norm_e4m3(x.data_ptr(), _ptr(residual), w, y.data_ptr(), scales.data_ptr(), _ptr(h), rows, C,
-                                     _array(xs, rs), eps, block, dt, on.handle))
-        return y, scales, h
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return _norm(x, weight, residual, eps, q8, block, stream)
+    xs = _rows("x", x, x)
+    w = _whole("weight", weight, x.dtype, dev, (C,))
+    if not w:
+        _bad("weight is needed")
+    if residual is not None:
+        rs = _rows("residual", residual, x)
+        h = _like(x)
+    else:
+        rs, h = 0, None
+    L = _library()
+    if not q8:
+        y = _like(x)
+        if stream is not None:
+            _made(stream, y, h)
+        _check(L.gconv_rms_norm(x.data_ptr(), _ptr(residual), w, y.data_ptr(), _ptr(h), rows, C, _array(xs, rs), eps,
+                                dt, _stream(dev, stream)))
+        return y, h
+    y = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
+    nb = -(-C // block) if block > 0 else 1
+    scales = x.new_empty((*x.shape[:-1], nb), dtype=torch.float32)
+    if stream is not None:
+        _made(stream, y, scales, h)
+    _check(L.gconv_rms_norm_e4m3(x.data_ptr(), _ptr(residual), w, y.data_ptr(), scales.data_ptr(), _ptr(h), rows, C,
+                                 _array(xs, rs), eps, block, dt, _stream(dev, stream)))
+    return y, scales, h
 
 
 def rms_norm(x, weight, residual=None, eps: float = 1e-6, stream=None):
@@ -336,17 +334,20 @@ def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, stream=None):
     L = _library()
     need = _size(0)
     _check(L.gconv_rms_norm_backward_workspace(rows, C, dt, ctypes.byref(need)))
-    with _On(dev, stream) as on:
-        w = _whole("weight", weight, h.dtype, dev, (C,))
-        if not w:
-            _bad("weight is needed")
-        ys, hs = _rows("dy", dy, h), _rows("h", h, h)
-        es = _rows("dh", dh, h) if dh is not None else 0
-        dx, dw = _like(h), _like(weight)
-        ws = _workspace(need.value, h)
-        on.made(dx, dw, ws)
-        _check(L.gconv_rms_norm_backward(dy.data_ptr(), h.data_ptr(), w, _ptr(dh), dx.data_ptr(), dw.data_ptr(), rows,
-                                         C, _array(ys, hs, es), eps, dt, _ptr(ws), need.value, on.handle))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return rms_norm_backward(dy, h, weight, eps, dh, stream)
+    w = _whole("weight", weight, h.dtype, dev, (C,))
+    if not w:
+        _bad("weight is needed")
+    ys, hs = _rows("dy", dy, h), _rows("h", h, h)
+    es = _rows("dh", dh, h) if dh is not None else 0
+    dx, dw = _like(h), _like(weight)
+    ws = _workspace(need.value, h)
+    if stream is not None:
+        _made(stream, dx, dw, ws)
+    _check(L.gconv_rms_norm_backward(dy.data_ptr(), h.data_ptr(), w, _ptr(dh), dx.data_ptr(), dw.data_ptr(), rows,
+                                     C, _array(ys, hs, es), eps, dt, _ptr(ws), need.value, _stream(dev, stream)))
     return dx, dw
 
 
@@ -379,12 +380,15 @@ def dwconv1d_causal(x, weight, bias=None, activation: Optional[str] = None, init
     dev = x.get_device()
     s0 = _whole("initial_state", initial_state, x.dtype, dev, (B, K - 1, C))
     n = _whole("lengths", lengths, torch.int32, dev, (B,))
-    with _On(dev, stream) as on:
-        y = _like(x)
-        st = x.new_empty((B, K - 1, C)) if return_state else None
-        on.made(y, st)
-        _check(_library().gconv_dw1d_causal(x.data_ptr(), w, b, y.data_ptr(), s0, _ptr(st), n, _array(B, T, C, K),
-                                            _array(*x.stride()[:2]), act, dt, on.handle))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return dwconv1d_causal(x, weight, bias, activation, initial_state, lengths, return_state, stream)
+    y = _like(x)
+    st = x.new_empty((B, K - 1, C)) if return_state else None
+    if stream is not None:
+        _made(stream, y, st)
+    _check(_library().gconv_dw1d_causal(x.data_ptr(), w, b, y.data_ptr(), s0, _ptr(st), n, _array(B, T, C, K),
+                                        _array(*x.stride()[:2]), act, dt, _stream(dev, stream)))
     return (y, st) if return_state else y
 
 
@@ -404,15 +408,18 @@ def dwconv1d_causal_backward(x, weight, bias, dy, activation: Optional[str] = No
     sh = _array(B, T, C, K)
     need = _size(0)
     _check(L.gconv_dw1d_causal_backward_workspace(sh, dt, ctypes.byref(need)))
-    with _On(dev, stream) as on:
-        dx, dw = _like(x), _like(weight)
-        db = _like(bias) if bias is not None else None
-        ds = x.new_empty((B, K - 1, C)) if initial_state is not None else None
-        ws = _workspace(need.value, x)
-        on.made(dx, dw, db, ds, ws)
-        _check(L.gconv_dw1d_causal_backward(x.data_ptr(), w, b, dy.data_ptr(), s0, sf, dx.data_ptr(), dw.data_ptr(),
-                                            _ptr(db), _ptr(ds), n, sh, _array(*x.stride()[:2], *dy.stride()[:2]),
-                                            act, dt, _ptr(ws), need.value, on.handle))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return dwconv1d_causal_backward(x, weight, bias, dy, activation, initial_state, lengths, dstate, stream)
+    dx, dw = _like(x), _like(weight)
+    db = _like(bias) if bias is not None else None
+    ds = x.new_empty((B, K - 1, C)) if initial_state is not None else None
+    ws = _workspace(need.value, x)
+    if stream is not None:
+        _made(stream, dx, dw, db, ds, ws)
+    _check(L.gconv_dw1d_causal_backward(x.data_ptr(), w, b, dy.data_ptr(), s0, sf, dx.data_ptr(), dw.data_ptr(),
+                                        _ptr(db), _ptr(ds), n, sh, _array(*x.stride()[:2], *dy.stride()[:2]),
+                                        act, dt, _ptr(ws), need.value, _stream(dev, stream)))
     return dx, dw, db, ds
 
 
@@ -426,9 +433,12 @@ def dwconv1d_causal_step(x, weight, bias, state, activation: Optional[str] = Non
         _bad("state must be [n, K-1, C]")
     sp = _whole("state", state, x.dtype, dev, (state.shape[0], K - 1, C))
     sl = _whole("slots", slots, torch.int32, dev, (B,))
-    with _On(dev, stream) as on:
-        y = _like(x)
-        on.made(y)
-        _check(_library().gconv_dw1d_causal_step(x.data_ptr(), w, b, sp, y.data_ptr(), sl,
-                                                 _array(B, C, K, state.shape[0]), x.stride(0), act, dt, on.handle))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return dwconv1d_causal_step(x, weight, bias, state, activation, slots, stream)
+    y = _like(x)
+    if stream is not None:
+        _made(stream, y)
+    _check(_library().gconv_dw1d_causal_step(x.data_ptr(), w, b, sp, y.data_ptr(), sl,
+                                             _array(B, C, K, state.shape[0]), x.stride(0), act, dt, _stream(dev, stream)))
     return y
