@@ -80,16 +80,21 @@ lin_group_sum(const float *__restrict__ part, T *__restrict__ out, int64_t sb, i
 // ---------------------------------------------------------------- single tokens
 //
 // S <- lam S + k v^T in place, o = scale q S: one pass over the state, which is all the
-// traffic there is (8 Dk Dv bytes a head): 97 us for the 537 MB of 256 sequences x 16 heads of
-// 128 x 128, 5.5 TB/s, more than a copy's 5.1.  One workgroup for each (token, head): lanes
-// run along 4 columns each, thread rows take every RP-th row of the state, and the RP
+// traffic there is (8 Dk Dv bytes a head).  One workgroup for each (token, head): lanes run
+// along 4 columns each, thread rows take every RP-th row of the state, U at a time, and the RP
 // partial sums of o are added in a fixed order through LDS.
-template <typename T, int CG>
-__global__ void __launch_bounds__(kThreads)
+//
+// Many heads: more waves beat more rows in flight (256 sequences x 16 heads of 128 x 128, 537
+// MB: 114 us with 8 rows, 105 with 4, 97 with 2, 5.5 TB/s where a copy takes 5.1).  Up to
+// a head a compute unit, and more than 8 rows a thread: four times the threads and twice the
+// rows in flight (6 heads of 178 x 225: 19 us became 9.7, 16 of 128 x 128: 7.4 became 5.9; 8 of
+// 64 x 64: 4.4 would be 5.4).
+template <typename T, int CG, int NT, int U>
+__global__ void __launch_bounds__(NT)
 lin_step(const LinStep p)
 {
-    constexpr int RP = kThreads / CG;
-    __shared__ float red[RP][CG * 4];
+    constexpr int RP = NT / CG;
+    __shared__ __attribute__((aligned(16))) float red[RP][CG * 4];
     const int tid = threadIdx.x, c0 = tid % CG * 4, r0 = tid / CG;
     const int h = blockIdx.x % p.H, bi = blockIdx.x / p.H;
     const int left = p.Dv - c0;
@@ -106,9 +111,6 @@ lin_step(const LinStep p)
     load_run<T, 4>((const T *)p.v + bi * p.vsb + h * p.vsh + c0, left, v);
     const float lam = expf(p.log_decay[h]);
     float *sp = p.state + (slot * p.H + h) * (int64_t)p.Dk * p.Dv + c0;
-    // Rows in flight for each thread: more waves beat more rows (256 x 16 heads of 128 x 128: 114 us
-    // with 8, 105 with 4, 96 with 2, 97 with 1).
-    constexpr int U = 2;
     for (int d0 = r0; d0 < p.Dk; d0 += RP * U) {
         float s[U][4], qv[U], kv[U];
 #pragma unroll
@@ -130,26 +132,36 @@ lin_step(const LinStep p)
             store_run<float, 4>(sp + (int64_t)d * p.Dv, left, s[x]);
         }
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) red[r0][c0 + e] = o[e];
-    __syncthreads();
+    for (int half = RP / 2; half > 0; half /= 2) {     // rows half .. 2 half - 1 to those before them
+        if (r0 >= half && r0 < 2 * half) *reinterpret_cast<float4 *>(&red[r0][c0]) = float4{o[0], o[1], o[2], o[3]};
+        __syncthreads();
+        if (r0 < half) {
+            const float4 x = *reinterpret_cast<const float4 *>(&red[r0 + half][c0]);
+            o[0] += x.x; o[1] += x.y; o[2] += x.z; o[3] += x.w;
+        }
+    }
     if (r0 == 0 && left > 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            for (int r = 1; r < RP; ++r) o[e] += red[r][c0 + e];
-            o[e] *= p.scale;
-        }
+        for (int e = 0; e < 4; ++e) o[e] *= p.scale;
         store_run<T, 4>(op, left, o);
     }
 }
 
+template <typename T, int CG> hipError_t run_step_on(const LinStep &p)
+{
+    const int64_t heads = (int64_t)p.B * p.H;
+    if (heads > 256 || p.Dk * CG <= 2048)
+        hipLaunchKernelGGL((lin_step<T, CG, 256, 2>), dim3((unsigned)heads), dim3(256), 0, p.stream, p);
+    else
+        hipLaunchKernelGGL((lin_step<T, CG, 1024, 4>), dim3((unsigned)heads), dim3(1024), 0, p.stream, p);
+    return hipGetLastError();
+}
+
 template <typename T> hipError_t run_step(const LinStep &p)
 {
-    const dim3 grid((unsigned)(p.B * p.H)), block(kThreads);
-    if (p.Dv <= 64) hipLaunchKernelGGL((lin_step<T, 16>), grid, block, 0, p.stream, p);
-    else if (p.Dv <= 128) hipLaunchKernelGGL((lin_step<T, 32>), grid, block, 0, p.stream, p);
-    else hipLaunchKernelGGL((lin_step<T, 64>), grid, block, 0, p.stream, p);
-    return hipGetLastError();
+    if (p.Dv <= 64) return run_step_on<T, 16>(p);
+    if (p.Dv <= 128) return run_step_on<T, 32>(p);
+    return run_step_on<T, 64>(p);
 }
 
 }  // namespace
