@@ -183,7 +183,7 @@ static hipError_t run_walks(const LinWalks &all, bool full)
         LinWalks some = {};
         bool first = true;
         for (int j = 0; j < all.count; ++j)
-            if (lin_alike(all.w[j].Da, all.w[j].Dc, all.w[i].Da, all.w[i].Dc)) {
+            if (lin_alike(all.w[j].Da, all.w[j].Dc, all.w[i].Da, all.w[i].Dc, all.w[0].dtype)) {
                 first = first && j >= i;
                 some.w[some.count++] = all.w[j];
             }

@@ -294,10 +294,10 @@ template <typename T, int DK, int NW, bool FULL> struct WalkLds {
 
 // Waves of a SIMD that registers are kept for: two or three workgroups share a compute unit.
 template <typename T, int DK, int NW>
-constexpr int kWavesPerSimd = DK == 256 ? 1 : kParts<T> == 1 && DK / NW <= 32 ? 3 : 2;
+constexpr int kWavesPerSimd = DK == 256 ? (kParts<T> == 3 ? 1 : 2) : kParts<T> == 1 && DK / NW <= 32 ? 3 : 2;
 
 // Kernels that have registers to spare before their loop (the others would spill into it).
-template <typename T, int DK> constexpr bool kRoomy = DK == 64 ? kParts<T> > 1 : (DK == 128) == (kParts<T> == 3);
+template <typename T, int DK> constexpr bool kRoomy = DK == 64 ? kParts<T> > 1 : DK == 128 && kParts<T> == 3;
 
 template <typename T, int DK, int NW, bool FULL>
 __global__ void __launch_bounds__(64 * NW, (kWavesPerSimd<T, DK, NW>))
@@ -580,11 +580,14 @@ template <typename T, int DK, int NW, bool FULL> hipError_t run_walk_on(LinWalks
 template <typename T, bool FULL> hipError_t run_walks(const LinWalks &all)
 {
     const LinWalk &p = all.w[0];
-    const bool two = lin_waves(p.Da, p.Dc) == 2;
+    const bool two = lin_waves(p.Da, p.Dc, p.dtype) == 2;
     switch (lin_wide(p.Da)) {
     case 64: return two ? run_walk_on<T, 64, 2, FULL>(all) : run_walk_on<T, 64, 4, FULL>(all);
     case 128: return two ? run_walk_on<T, 128, 2, FULL>(all) : run_walk_on<T, 128, 4, FULL>(all);
-    default: return run_walk_on<T, 256, 4, FULL>(all);
+    default:
+        if constexpr (kParts<T> < 3)
+            if (lin_waves(p.Da, p.Dc, p.dtype) == 8) return run_walk_on<T, 256, 8, FULL>(all);
+        return run_walk_on<T, 256, 4, FULL>(all);
     }
 }
 

@@ -103,22 +103,23 @@ gconv_status_t check_strides(const int64_t *strides, int n)
 constexpr int64_t kChunk = 64;
 
 // Workgroups that the 256 compute units hold of the kernel for a walk (Da, Dc), by its
-// registers and LDS: one of the widest and of wide fp32 ones, two of wide fp16 ones, else three.
-int64_t lin_slots(int64_t Da, gconv_dtype_t dtype)
+// registers and LDS.
+int64_t lin_slots(int64_t Da, int64_t Dc, gconv_dtype_t dtype)
 {
-    if (Da > 128 || (Da > 64 && dtype == GCONV_F32)) return 256;
-    return Da > 64 && dtype == GCONV_F16 ? 512 : 768;
+    if (Da > 128) return dtype == GCONV_BF16 && gconv::lin_waves(Da, Dc, (int)dtype) == 4 ? 512 : 256;
+    if (Da > 64) return dtype == GCONV_F32 ? 256 : dtype == GCONV_F16 ? 512 : 768;
+    return 768;
 }
 
 void lin_segments(const LinShape &s, bool backward, gconv_dtype_t dtype, int32_t *nseg, int32_t *seg_len)
 {
     const int64_t chunks = std::max<int64_t>(1, gconv::ceil_div(s.T, kChunk)), heads = std::max<int64_t>(1, s.B * s.H);
     auto fit = [&](int64_t walks, int64_t Da, int64_t Dc) {
-        return lin_slots(Da, dtype) / (walks * heads * gconv::lin_tiles(Da, Dc));
+        return lin_slots(Da, Dc, dtype) / (walks * heads * gconv::lin_tiles(Da, Dc, (int)dtype));
     };
     // The output; or dv, and dq and dk, in one launch where they can be.
     int64_t n = !backward                                      ? fit(1, s.Dk, s.Dv)
-                : gconv::lin_alike(s.Dk, s.Dv, s.Dv, s.Dk)     ? fit(3, s.Dk, s.Dv)
+                : gconv::lin_alike(s.Dk, s.Dv, s.Dv, s.Dk, (int)dtype) ? fit(3, s.Dk, s.Dv)
                                                                : std::min(fit(1, s.Dk, s.Dv), fit(2, s.Dv, s.Dk));
     n = std::max<int64_t>(1, std::min<int64_t>({n, chunks / 2, 1024}));
     const int64_t each = gconv::ceil_div(chunks, n);
