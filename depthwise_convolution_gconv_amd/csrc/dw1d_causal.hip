@@ -71,7 +71,7 @@ __device__ __forceinline__ const T *xs_at(const CausalArgs &a, int64_t b, int64_
     return a.s0 ? (const T *)a.s0 + (b * (a.K - 1) + t + a.K - 1) * a.C + c : nullptr;
 }
 
-constexpr int kRun = 16;    // tokens for each thread of causal_run
+constexpr int kRun = 16;    // tokens for each thread of causal_run (2 x 8192 x 6144: 82.3 us a call, 83.3 with 24, 87.5 with 32)
 
 template <typename T, int K>
 __global__ void __launch_bounds__(kThreads)
