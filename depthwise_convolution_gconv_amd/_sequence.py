@@ -162,8 +162,8 @@ def linear_attention(q, k, v, log_decay, scale: Optional[float] = None, initial_
     Returns o [B, T, H, Dv], or (o, state) with the fp32 state after each sequence's last
     token, which linear_attention_step carries on from.
 
-    Sums and states are fp32; scores, and the state where a query meets it, are rounded to the
-    inputs' precision for their second product.  A non-finite v makes its column NaN in the
+    Sums and states are fp32; scores, and the state where a query meets it, enter their second
+    product with 16 bits for 16-bit inputs and 24 for fp32.  A non-finite v makes its column NaN in the
     other tokens of its chunk of 32 too, earlier ones among them."""
     dt, shape, strides, g, n = _attn_args(q, k, v, log_decay, lengths)
     B, T, Hk, H, Dk, Dv = shape
@@ -192,7 +192,7 @@ def linear_attention_backward(q, k, v, log_decay, do, scale: Optional[float] = N
                               lengths=None, dstate=None, stream=None):
     """(dq, dk, dv, dinitial) of linear_attention from the gradients `do` of its output and
     `dstate` (fp32, or None: zero) of its final state.  dinitial is None without an
-    initial_state.  log_decay is a constant: it gets no gradient."""
+    initial_state.  log_decay is a constant: it gets no gradient.  Precision as forward."""
     dt, shape, strides, g, n = _attn_args(q, k, v, log_decay, lengths)
     B, T, Hk, H, Dk, Dv = shape
     dev = q.get_device()

@@ -19,9 +19,9 @@
 // for fp16 (exact), three for fp32 (exact).  Products of two parts below the last bit that
 // the result can show are left out.  The weighted rows lam^(m-j-e0) c_j of the state's
 // update always have three parts (24 bits), so the state is the fp32 sum it would be on a
-// vector unit.  Scores and the state that meets a_i are rounded to as many parts as the
-// inputs have: their error stays at one rounding of the output's own type (2^-9 of a term
-// in bf16, 2^-18 in fp16, 2^-25 in fp32), and both stay fp32 in their accumulators.
+// vector unit.  Scores and the state that meets a_i have two parts in 16 bits and three in
+// fp32: they lose 2^-16 (2^-24) of a term, below what an output of the inputs' type shows, and
+// both stay fp32 in their accumulators.
 //
 // Nothing but the inputs goes through LDS.  Products run transposed (columns of the
 // accumulators are tokens i, rows are j or columns of c): scores and the state leave the
@@ -32,19 +32,17 @@
 // eight rows stand for eight neighbours of a.  A wave keeps the state of its 32 columns in
 // accumulators for the whole walk.
 //
-// What bounds it (bf16, 128 x 128 heads): HBM.  Over 65536 tokens x 16 heads the outputs' walk
-// takes 242 us for 1.07 GB and the local states' 127-135 us for 0.54 GB; with every product
-// left out they take 216 and 116 us.  Per chunk a wave issues 42 matrix instructions (1344
-// cycles) and about 400 vector ones (1600 cycles), which three workgroups on a compute unit
-// overlap.  32 tokens rather than 64: half the registers for what is on its way, so three
-// workgroups instead of two, and no off-diagonal tile of scores (504 -> 486 us, and 447 with
-// the segments that three workgroups call for).  Two parts instead of three in the update took
-// 403 instead of 421 us and left the state with 2.5e-6 of error instead of 1e-7. Two parts for
-// the scores and for the state that meets a_i would bring bf16 outputs from 2.3e-3 of error to
-// the 1.7e-3 of their own rounding, and take 432 instead of 390 us.  fp16 and
-// fp32 pay for their parts (3 and 6 products for one) and are bound by those: 39 us for 5 x
-// 1021 tokens x 12 heads of 96 x 80 in fp16, 62 us for the three walks of 8 x 1024 tokens x 8
-// heads of 64 in fp32.
+// What bounds it (bf16, 128 x 128 heads): HBM, and beside it the products.  65536 tokens x 16
+// heads take 432 us: 1.07 GB for the outputs' walk, 0.54 GB for the local states', and the scan.
+// One part for the scores and the state that meets a_i would take 390 us, with 2.4e-3 of error
+// beside the 1.7e-3 of the outputs' own rounding; the gradients of 4 x 4096 tokens x 16 heads
+// would take 249 us instead of 284.  32 tokens rather than 64: half the registers for what is on
+// its way, so three workgroups on a compute unit instead of two, and no off-diagonal tile of
+// scores (504 -> 486 us, and 447 with the segments that three workgroups call for, all with one
+// part).  Two parts instead of three in the update took 403 instead of 421 us and left the state
+// with 2.5e-6 of error instead of 1e-7.  fp16 and fp32 pay for their parts (3 and 6 products for
+// one) and are bound by those: 39 us for 5 x 1021 tokens x 12 heads of 96 x 80 in fp16, 62 us for
+// the three walks of 8 x 1024 tokens x 8 heads of 64 in fp32.
 #pragma once
 
 #include "linattn.hpp"
@@ -64,6 +62,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 template <typename T> constexpr int kParts = sizeof(T) == 4 ? 3 : 2;
 template <> constexpr int kParts<__bf16> = 1;
 constexpr int kUpdParts = 3;
+// Of scores, and of the state that meets a_i.
+template <typename T> constexpr int kMidParts = sizeof(T) == 4 ? 3 : 2;
 constexpr int kLen = 32;     // tokens in a chunk
 
 // A tile of D columns in LDS, laid out so that the 16-byte reads of 16 rows and the transposing
@@ -303,7 +303,7 @@ template <typename T, int DK, int NW, bool FULL>
 __global__ void __launch_bounds__(64 * NW, (kWavesPerSimd<T, DK, NW>))
 lin_walk(const LinWalks all)
 {
-    constexpr int NP = kParts<T>, L = kLen, NT = 32 * NW, NTH = 64 * NW;
+    constexpr int NP = kParts<T>, NM = kMidParts<T>, L = kLen, NT = 32 * NW, NTH = 64 * NW;
     typedef WalkLds<T, DK, NW, FULL> Lds;
     constexpr int NX = DK / 32, NS = DK / 16, NG = L / 16;          // state tiles, steps along columns, along tokens
     __shared__ __attribute__((aligned(16))) Lds sm;
@@ -464,7 +464,7 @@ lin_walk(const LinWalks all)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) f[e] = st[s / 2][s % 2 * 8 + e];
                     sco = mma<NP - 1>(read_row<DK, NP>(sm.b, row_at(s)), aq, sco);
-                    acc = mma<NP - 1>(split8<NP>(f), aq, acc);
+                    acc = mma<NM - 1>(split8<NM>(f), aq, acc);
                 }
                 const float fi = scale * p.inter_scale * sm.pw[min(l32 + p.e0, L)];
 #pragma unroll
@@ -481,12 +481,12 @@ lin_walk(const LinWalks all)
                         f[e + 3] = sco[8 * g + e + 3] * w.w;
                     }
                     // Scores of later tokens are masked, not only multiplied by zero: they may be infinite.
-                    Part8<NP> pr = split8<NP>(f);
+                    Part8<NM> pr = split8<NM>(f);
                     const u32x4 mask = *reinterpret_cast<const u32x4 *>(&sm.mask[256 * g + 4 * lane]);
 #pragma unroll
-                    for (int q = 0; q < NP; ++q)
+                    for (int q = 0; q < NM; ++q)
                         pr.p[q] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, pr.p[q]) & mask);
-                    acc = mma<NP - 1>(read_col<NT, NP>(sm.c, ccol_at(g)), pr, acc);
+                    acc = mma<NM - 1>(read_col<NT, NP>(sm.c, ccol_at(g)), pr, acc);
                 }
             }
             if (m < L) {

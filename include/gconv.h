@@ -284,7 +284,10 @@ void gconv_autotune_clear(void);
  *  - slots: int32 [B] on the device or NULL (slot b for sequence b): the row of a pool of
  *    n states that sequence b owns, each at most once.  A slot outside [0, n) has no
  *    state: the token's output is zero and nothing is updated.
- *  - Sums and states are fp32; outputs are rounded once to the dtype.
+ *  - Sums and states are fp32; outputs are rounded once to the dtype.  Between its two
+ *    products linear attention over whole prompts, and its gradients, carry a score, and the
+ *    state that meets a query, with 16 bits (2^-16 of the term) for 16-bit tensors and 24 for
+ *    fp32 ones.
  *  - No output may overlap an input or another output.
  * Results do not depend on the launch: no atomics, fixed orders of addition. */
 

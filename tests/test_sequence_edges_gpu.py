@@ -1,0 +1,53 @@
+"""Edges of the sequence operators: precision of scores and states, borders of roundings, slow
+decays, non-finite values, streams and sizes near the largest ones.
+
+u = 2^-24 is the relative error of one fp32 rounding; the other tolerances stand beside their
+tests, counted from the roundings that a result passes.
+"""
+import pytest
+import torch
+
+import depthwise_convolution_gconv_amd as gc
+from test_sequence_gpu import DT, U32, attn_def, attn_inputs, near, rounding
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- precision of scores and states
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_scores_and_states_are_finer_than_the_outputs(dt):
+    # Few positive terms, so that one rounding of a score or a state shows in the output.  Scores, and
+    # the state where a query meets it, have 16 bits (2^-16 of a term), sums fp32; the output is
+    # rounded once, the gradients of k and v meet one state more.
+    B, T, Dk, Dv = 3000, 3, 2, 4
+    gen = torch.Generator().manual_seed(1)
+    pos = lambda *s: 1.0 + torch.rand(*s, generator=gen)  # noqa: E731
+    q, k, v, do = (pos(B, T, 1, d).to(DT[dt]).cuda() for d in (Dk, Dk, Dv, Dv))
+    s0, ds = pos(B, 1, Dk, Dv).cuda(), pos(B, 1, Dk, Dv).cuda()
+    g = torch.full((1,), -0.1).cuda()
+    o, s = gc.linear_attention(q, k, v, g, scale=0.75, initial_state=s0, return_state=True)
+    got = gc.linear_attention_backward(q, k, v, g, do, scale=0.75, initial_state=s0, dstate=ds)
+    leaves = [t.double().cpu().requires_grad_() for t in (q, k, v, s0)]
+    ro, rs = attn_def(*leaves[:3], g.cpu(), 0.75, leaves[3], [T] * B)
+    ref = torch.autograd.grad((ro * do.double().cpu()).sum() + (rs * ds.double().cpu()).sum(), leaves)
+    for name, y, r in zip(("o", "dq", "dk", "dv"), (o, *got), (ro.detach(), *ref)):
+        near(name, y, r, rounding(DT[dt], r) + (1.02 * 2.0 ** -16 + (T + Dv + 24) * U32) * r)
+    near("state", s, rs.detach(), (T + 8) * U32 * rs.detach())
+    near("dinitial", got[3], ref[3], (T + 8) * U32 * ref[3])
+
+
+def test_bf16_error_is_that_of_the_outputs_rounding():
+    # Terms of either sign: errors of 2^-16 of a term stay 2^-16 of the sum, beside a rounding whose
+    # 2-norm is above 2^-10 of it; together less than a tenth more.
+    B, T, H, D = 2, 300, 2, 64
+    q, k, v, g, s0 = attn_inputs(B, T, H, H, D, D, torch.bfloat16, 2, True)
+    do = torch.randn(B, T, H, D, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    o = gc.linear_attention(q, k, v, g, initial_state=s0)
+    got = gc.linear_attention_backward(q, k, v, g, do, initial_state=s0)
+    leaves = [t.double().cpu().requires_grad_() for t in (q, k, v)]
+    ro, _ = attn_def(*leaves, g.cpu(), D ** -0.5, s0.double().cpu(), [T] * B)
+    ref = torch.autograd.grad((ro * do.double().cpu()).sum(), leaves)
+    for name, y, r in zip(("o", "dq", "dk", "dv"), (o, *got), (ro.detach(), *ref)):
+        own = float((r.bfloat16().double() - r).norm())
+        assert float((y.double().cpu() - r).norm()) <= 1.1 * own, name
