@@ -10,7 +10,7 @@
 // loads at any alignment) between the sum of squares and the output, so the kernels move
 // each input and output once and are bound by HBM.  Rows of up to 128 / 512 / 4096 /
 // 16384 columns take 16 / 64 / 256 / 1024 threads (8192 rows of 4096 in bf16 with a residual
-// and an e4m3 output: 43 us, 5.5 TB/s; the gradient of 16384 rows of 2048: 46 us and 5 us for
+// and an e4m3 output: 44 us, 5.3 TB/s; the gradient of 16384 rows of 2048: 46 us and 5 us for
 // the sum of 1024 partial rows, 5.3 TB/s together); longer rows are read again for each
 // pass (rms_norm_long).  Squares and sums are fp32; h is rounded to the dtype before it is
 // squared because it is what the next layer sees as its residual.
@@ -59,7 +59,9 @@ __device__ __forceinline__ float abs_bits_max(uint32_t amax)
 }
 
 // VE values divided by the scale, clamped, as e4m3 (round to nearest even), at any byte alignment.
-template <int VE> __device__ __forceinline__ void store_e4m3(uint8_t *dst, int valid, const float (&y)[VE], float inv)
+// A quotient, not a product with 1 / scale: values on a border between two e4m3 numbers, which
+// rows of few distinct values have many of, would go to the other side.
+template <int VE> __device__ __forceinline__ void store_e4m3(uint8_t *dst, int valid, const float (&y)[VE], float scale)
 {
     uint32_t w[VE / 4];
 #pragma unroll
@@ -67,7 +69,7 @@ template <int VE> __device__ __forceinline__ void store_e4m3(uint8_t *dst, int v
         float f[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float v = y[4 * e + i] * inv;
+            const float v = y[4 * e + i] / scale;
             f[i] = v > kE4m3Max ? kE4m3Max : v < -kE4m3Max ? -kE4m3Max : v;   // NaN stays
         }
         int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
@@ -159,10 +161,10 @@ rms_norm_rows(const RmsArgs a)
 #pragma unroll
                 for (int i = 0; i < TPR / 64; ++i) amax = max(amax, redq[i]);
             }
-            const float s = abs_bits_max(amax) / kE4m3Max, inv = 1.0f / s;
+            const float s = abs_bits_max(amax) / kE4m3Max;
             if (sub == 0) a.scales[row] = s;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) store_e4m3<VE>(qp + (v * TPR + sub) * VE, C - (v * TPR + sub) * VE, f[v], inv);
+            for (int v = 0; v < NV; ++v) store_e4m3<VE>(qp + (v * TPR + sub) * VE, C - (v * TPR + sub) * VE, f[v], s);
         } else {
             // A block of columns is held by block / VE neighbouring lanes (a block wider than the row by all of them).
             const int group = min(a.block / VE, TPR < 64 ? TPR : 64);
@@ -174,9 +176,9 @@ rms_norm_rows(const RmsArgs a)
                 for (int e = 0; e < VE; ++e) am = max(am, __builtin_bit_cast(uint32_t, f[v][e]) & 0x7fffffffu);
                 am = max_lanes(am, group);
                 const int col = (v * TPR + sub) * VE;
-                const float s = abs_bits_max(am) / kE4m3Max, inv = 1.0f / s;
+                const float s = abs_bits_max(am) / kE4m3Max;
                 if (col % a.block == 0 && col < C) a.scales[row * nb + col / a.block] = s;
-                store_e4m3<VE>(qp + col, C - col, f[v], inv);
+                store_e4m3<VE>(qp + col, C - col, f[v], s);
             }
         }
     }
@@ -255,7 +257,7 @@ rms_norm_long(const RmsArgs a)
                 s = abs_bits_max(am) / kE4m3Max;
                 if (col % a.block == 0 && col < a.C) a.scales[row * nb + col / a.block] = s;
             }
-            if (col < a.C) store_e4m3<VE>(qp + col, (int)min(a.C - col, (int64_t)VE), f, 1.0f / s);
+            if (col < a.C) store_e4m3<VE>(qp + col, (int)min(a.C - col, (int64_t)VE), f, s);
         }
     }
 }

@@ -51,3 +51,28 @@ def test_bf16_error_is_that_of_the_outputs_rounding():
     for name, y, r in zip(("o", "dq", "dk", "dv"), (o, *got), (ro.detach(), *ref)):
         own = float((r.bfloat16().double() - r).norm())
         assert float((y.double().cpu() - r).norm()) <= 1.1 * own, name
+
+
+# ---------------------------------------------------------------- e4m3
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("C", [64, 300, 2000, 5000, 20001])
+@pytest.mark.parametrize("block", [0, 32, 64, 256])
+def test_e4m3_is_the_quotient(C, block, dt):
+    # Few distinct values: with 448 in every scale's columns many quotients lie on a border between
+    # two e4m3 numbers.  All values are exact in every dtype and so are the sums of their squares
+    # (below 2^24), so the fp32 norm of the same rows has the same y, and q = e4m3(y / scale) bit for bit.
+    gen = torch.Generator().manual_seed(4)
+    x = torch.zeros(200, C)
+    x[:, :40] = torch.randint(-112, 113, (200, 40), generator=gen).float() * 4
+    x[:, 3], x[:, 33] = 448.0, -448.0
+    w = torch.ones(C)
+    y = gc.rms_norm(x.cuda(), w.cuda())
+    q, s = gc.rms_norm_e4m3(x.to(DT[dt]).cuda(), w.to(DT[dt]).cuda(), block=block)
+    blk = block or C
+    nb = -(-C // blk)
+    top = torch.nn.functional.pad(y.cpu(), (0, nb * blk - C)).view(200, nb, blk).abs().amax(-1)
+    want = top.clamp(min=2.0 ** -100) / 448.0
+    assert torch.equal(s.cpu(), want)
+    want = (y.cpu() / want.repeat_interleave(blk, 1)[:, :C]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    assert torch.equal(q.float().cpu(), want.float())
