@@ -325,7 +325,8 @@ lin_walk(const LinWalks all)
     const int64_t bh = (int64_t)bi * p.H + h;
     const int n = lin_len(p, bi), n0 = dv * NT;
     const int useg = seg * p.seg_len;
-    const int utop = min(useg + p.seg_len, FULL ? p.T : n);   // tokens [useg, utop) of this workgroup
+    // Tokens [useg, utop) of this workgroup; useg + seg_len may pass 2^31.
+    const int top = FULL ? p.T : n, utop = top - useg > p.seg_len ? useg + p.seg_len : top;
     const int ulive = min(n, utop);
     // Outputs go from the first chunk on.  Local states go from the last one back: each chunk
     // then adds its tokens with their weights at the segment's end, the state itself is never

@@ -76,3 +76,22 @@ def test_e4m3_is_the_quotient(C, block, dt):
     assert torch.equal(s.cpu(), want)
     want = (y.cpu() / want.repeat_interleave(blk, 1)[:, :C]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
     assert torch.equal(q.float().cpu(), want.float())
+
+
+# ---------------------------------------------------------------- the longest sequences
+
+def test_last_segment_of_the_longest_sequence():
+    # The largest T, where the last segment's rounded-up end passes 2^31.  All inputs are one value
+    # at stride 0 and the decay is 1/2, so every sum is 2 but near its start, all of it exact.
+    T = 2 ** 31 - 1 - 4096
+    one = torch.ones(1, 1, 1, 1, dtype=torch.bfloat16, device="cuda").expand(1, T, 1, 1)
+    g = torch.full((1,), 0.5, dtype=torch.float64).log().float().cuda()
+    o, s = gc.linear_attention(one, one, one, g, scale=1.0, return_state=True)
+    assert o.flatten()[:3].tolist() == [1.0, 1.5, 1.75]
+    assert abs(float(s) - 2.0) <= 16 * U32
+    assert bool((o.view(-1)[16:] == 2.0).all())
+    del o
+    dq, dk, dv, _ = gc.linear_attention_backward(one, one, one, g, one, scale=1.0)
+    assert dq.flatten()[:3].tolist() == [1.0, 1.5, 1.75] and bool((dq.view(-1)[16:] == 2.0).all())
+    for d in (dk, dv):
+        assert d.flatten()[-3:].tolist() == [1.75, 1.5, 1.0] and bool((d.view(-1)[:-16] == 2.0).all())
