@@ -4,8 +4,10 @@ conv1d that carries its state.
 
 Like the convolution binding: argument checks and marshalling only, on the caller's
 current device and stream, outputs and workspaces from torch.  Every function takes
-`stream` (default: the current stream).  With another stream than the current one, the
-call's outputs and workspace are recorded on it; its inputs are the caller's to keep.
+`stream` (default: the current stream of the tensors' device).  With another one the call
+runs as under torch.cuda.stream(stream): its outputs and workspace are that stream's
+memory, and the outputs may also be used on the caller's current stream, once that waits
+for the other.  That the inputs are ready on `stream`, and kept, is the caller's to see to.
 """
 from __future__ import annotations
 
@@ -101,15 +103,23 @@ _device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _stream(dev: int, stream) -> int:
-    return _raw_stream(dev) if stream is None else stream.cuda_stream
-
-
-def _made(stream, *tensors):
-    """Tensors a call allocated: their memory is in use on the stream it was given."""
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+def _on_stream(stream, ref: torch.Tensor, fn, *args):
+    """fn(*args) as the work of `stream`: what it allocates is the stream's own memory (a block
+    that the current stream has freed may still be in use there), and the current stream's use
+    of its outputs counts too when they are freed."""
+    dev = ref.get_device()
+    if dev < 0:
+        return fn(*args)      # refuses them
+    if stream.device.index != dev:
+        _bad(f"stream is on {stream.device}, the tensors are on device {dev}")
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        out = fn(*args)
+    if here != stream:
+        for t in out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                t.record_stream(here)
+    return out
 
 
 def _workspace(need: int, ref: torch.Tensor) -> Optional[torch.Tensor]:
@@ -165,6 +175,8 @@ def linear_attention(q, k, v, log_decay, scale: Optional[float] = None, initial_
     Sums and states are fp32; scores, and the state where a query meets it, enter their second
     product with 16 bits for 16-bit inputs and 24 for fp32.  A non-finite v makes its column NaN in the
     other tokens of its chunk of 32 too, earlier ones among them."""
+    if stream is not None:
+        return _on_stream(stream, q, linear_attention, q, k, v, log_decay, scale, initial_state, lengths, return_state)
     dt, shape, strides, g, n = _attn_args(q, k, v, log_decay, lengths)
     B, T, Hk, H, Dk, Dv = shape
     dev = q.get_device()
@@ -175,16 +187,14 @@ def linear_attention(q, k, v, log_decay, scale: Optional[float] = None, initial_
     _check(L.gconv_linear_attention_workspace(sh, dt, 0, ctypes.byref(need)))
     if _device() != dev:
         with torch.cuda.device(dev):
-            return linear_attention(q, k, v, log_decay, scale, initial_state, lengths, return_state, stream)
+            return linear_attention(q, k, v, log_decay, scale, initial_state, lengths, return_state)
     o = _like(v)
     st = q.new_empty((B, H, Dk, Dv), dtype=torch.float32) if return_state else None
     ws = _workspace(need.value, q)
-    if stream is not None:
-        _made(stream, o, st, ws)
     _check(L.gconv_linear_attention(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), sh,
         _array(*strides, *o.stride()[:3]), g,
-        Dk ** -0.5 if scale is None else scale, s0, _ptr(st), n, dt, _ptr(ws), need.value, _stream(dev, stream)))
+        Dk ** -0.5 if scale is None else scale, s0, _ptr(st), n, dt, _ptr(ws), need.value, _raw_stream(dev)))
     return (o, st) if return_state else o
 
 
@@ -193,6 +203,8 @@ def linear_attention_backward(q, k, v, log_decay, do, scale: Optional[float] = N
     """(dq, dk, dv, dinitial) of linear_attention from the gradients `do` of its output and
     `dstate` (fp32, or None: zero) of its final state.  dinitial is None without an
     initial_state.  log_decay is a constant: it gets no gradient.  Precision as forward."""
+    if stream is not None:
+        return _on_stream(stream, q, linear_attention_backward, q, k, v, log_decay, do, scale, initial_state, lengths, dstate)
     dt, shape, strides, g, n = _attn_args(q, k, v, log_decay, lengths)
     B, T, Hk, H, Dk, Dv = shape
     dev = q.get_device()
@@ -205,16 +217,14 @@ def linear_attention_backward(q, k, v, log_decay, do, scale: Optional[float] = N
     _check(L.gconv_linear_attention_workspace(sh, dt, 1, ctypes.byref(need)))
     if _device() != dev:
         with torch.cuda.device(dev):
-            return linear_attention_backward(q, k, v, log_decay, do, scale, initial_state, lengths, dstate, stream)
+            return linear_attention_backward(q, k, v, log_decay, do, scale, initial_state, lengths, dstate)
     dq, dk, dv = _like(q), _like(k), _like(v)
     ds = q.new_empty((B, H, Dk, Dv), dtype=torch.float32) if initial_state is not None else None
     ws = _workspace(need.value, q)
-    if stream is not None:
-        _made(stream, dq, dk, dv, ds, ws)
     _check(L.gconv_linear_attention_backward(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), sh,
         _array(*strides, *dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3]), g, Dk ** -0.5 if scale is None else scale, s0, sf,
-        _ptr(ds), n, dt, _ptr(ws), need.value, _stream(dev, stream)))
+        _ptr(ds), n, dt, _ptr(ws), need.value, _raw_stream(dev)))
     return dq, dk, dv, ds
 
 
@@ -223,6 +233,8 @@ def linear_attention_step(q, k, v, log_decay, state, scale: Optional[float] = No
     [n, H, Dk, Dv] is updated in place.  slots: int32 [B], the row of `state` that each
     sequence owns, each row at most once (default: row b); a slot outside [0, n) leaves
     the pool alone and gives a zero output.  Returns o [B, H, Dv]."""
+    if stream is not None:
+        return _on_stream(stream, q, linear_attention_step, q, k, v, log_decay, state, scale, slots)
     dt = _dtype("q", q)
     if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
         _bad("q and k must be [B, Hk, Dk], v [B, H, Dv], state [n, H, Dk, Dv]")
@@ -236,14 +248,12 @@ def linear_attention_step(q, k, v, log_decay, state, scale: Optional[float] = No
     sl = _whole("slots", slots, torch.int32, dev, (B,))
     if _device() != dev:
         with torch.cuda.device(dev):
-            return linear_attention_step(q, k, v, log_decay, state, scale, slots, stream)
+            return linear_attention_step(q, k, v, log_decay, state, scale, slots)
     o = _like(v)
-    if stream is not None:
-        _made(stream, o)
     _check(_library().gconv_linear_attention_step(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), sp, _array(B, Hk, H, Dk, Dv, state.shape[0]),
         _array(*strides, *o.stride()[:2]), g,
-        Dk ** -0.5 if scale is None else scale, sl, dt, _stream(dev, stream)))
+        Dk ** -0.5 if scale is None else scale, sl, dt, _raw_stream(dev)))
     return o
 
 
@@ -268,7 +278,7 @@ def _rows(name: str, t: torch.Tensor, ref: torch.Tensor) -> int:
     return t.shape[-1] if step is None else row
 
 
-def _norm(x, weight, residual, eps, q8, block, stream):
+def _norm(x, weight, residual, eps, q8, block):
     dt = _dtype("x", x)
     if x.dim() < 1 or x.shape[-1] < 1:
         _bad("x must be [..., C] with C >= 1")
@@ -277,7 +287,7 @@ def _norm(x, weight, residual, eps, q8, block, stream):
     dev = x.get_device()
     if _device() != dev:
         with torch.cuda.device(dev):
-            return _norm(x, weight, residual, eps, q8, block, stream)
+            return _norm(x, weight, residual, eps, q8, block)
     xs = _rows("x", x, x)
     w = _whole("weight", weight, x.dtype, dev, (C,))
     if not w:
@@ -290,25 +300,23 @@ def _norm(x, weight, residual, eps, q8, block, stream):
     L = _library()
     if not q8:
         y = _like(x)
-        if stream is not None:
-            _made(stream, y, h)
         _check(L.gconv_rms_norm(x.data_ptr(), _ptr(residual), w, y.data_ptr(), _ptr(h), rows, C, _array(xs, rs), eps,
-                                dt, _stream(dev, stream)))
+                                dt, _raw_stream(dev)))
         return y, h
     y = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
     nb = -(-C // block) if block > 0 else 1
     scales = x.new_empty((*x.shape[:-1], nb), dtype=torch.float32)
-    if stream is not None:
-        _made(stream, y, scales, h)
     _check(L.gconv_rms_norm_e4m3(x.data_ptr(), _ptr(residual), w, y.data_ptr(), scales.data_ptr(), _ptr(h), rows, C,
-                                 _array(xs, rs), eps, block, dt, _stream(dev, stream)))
+                                 _array(xs, rs), eps, block, dt, _raw_stream(dev)))
     return y, scales, h
 
 
 def rms_norm(x, weight, residual=None, eps: float = 1e-6, stream=None):
     """y = weight * h / sqrt(mean(h^2) + eps) over the last axis of x [..., C], where h is x,
     or x + residual rounded to the dtype.  Returns y, or (y, h) with a residual."""
-    y, h = _norm(x, weight, residual, eps, False, 0, stream)
+    if stream is not None:
+        return _on_stream(stream, x, rms_norm, x, weight, residual, eps)
+    y, h = _norm(x, weight, residual, eps, False, 0)
     return y if residual is None else (y, h)
 
 
@@ -317,7 +325,9 @@ def rms_norm_e4m3(x, weight, residual=None, eps: float = 1e-6, block: int = 0, s
     y = q * scale: one scale for a row (block 0, scales [..., 1]) or for each `block`
     columns (32, 64, 128 or 256; scales [..., ceil(C / block)]).
     Returns (q, scales), or (q, scales, h) with a residual."""
-    y, scales, h = _norm(x, weight, residual, eps, True, int(block), stream)
+    if stream is not None:
+        return _on_stream(stream, x, rms_norm_e4m3, x, weight, residual, eps, block)
+    y, scales, h = _norm(x, weight, residual, eps, True, int(block))
     return (y, scales) if residual is None else (y, scales, h)
 
 
@@ -325,6 +335,8 @@ def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, stream=None):
     """(dx, dw) of rms_norm: dx is the gradient of x and of residual alike, from the gradient
     dy of y, the normed rows h (x itself without a residual) and the gradient dh of the h
     output (or None)."""
+    if stream is not None:
+        return _on_stream(stream, h, rms_norm_backward, dy, h, weight, eps, dh)
     dt = _dtype("h", h)
     if h.dim() < 1 or h.shape[-1] < 1:
         _bad("h must be [..., C] with C >= 1")
@@ -336,7 +348,7 @@ def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, stream=None):
     _check(L.gconv_rms_norm_backward_workspace(rows, C, dt, ctypes.byref(need)))
     if _device() != dev:
         with torch.cuda.device(dev):
-            return rms_norm_backward(dy, h, weight, eps, dh, stream)
+            return rms_norm_backward(dy, h, weight, eps, dh)
     w = _whole("weight", weight, h.dtype, dev, (C,))
     if not w:
         _bad("weight is needed")
@@ -344,10 +356,8 @@ def rms_norm_backward(dy, h, weight, eps: float = 1e-6, dh=None, stream=None):
     es = _rows("dh", dh, h) if dh is not None else 0
     dx, dw = _like(h), _like(weight)
     ws = _workspace(need.value, h)
-    if stream is not None:
-        _made(stream, dx, dw, ws)
     _check(L.gconv_rms_norm_backward(dy.data_ptr(), h.data_ptr(), w, _ptr(dh), dx.data_ptr(), dw.data_ptr(), rows,
-                                     C, _array(ys, hs, es), eps, dt, _ptr(ws), need.value, _stream(dev, stream)))
+                                     C, _array(ys, hs, es), eps, dt, _ptr(ws), need.value, _raw_stream(dev)))
     return dx, dw
 
 
@@ -375,6 +385,8 @@ def dwconv1d_causal(x, weight, bias=None, activation: Optional[str] = None, init
     activation: None or "silu".  lengths: int32 [B]; the outputs past them are zero.
     Returns y, or (y, state) with the last K-1 inputs of each sequence, which
     dwconv1d_causal_step carries on from."""
+    if stream is not None:
+        return _on_stream(stream, x, dwconv1d_causal, x, weight, bias, activation, initial_state, lengths, return_state)
     dt, C, K, w, b, act = _conv_args(x, weight, bias, activation, 3)
     B, T, _ = x.shape
     dev = x.get_device()
@@ -382,13 +394,11 @@ def dwconv1d_causal(x, weight, bias=None, activation: Optional[str] = None, init
     n = _whole("lengths", lengths, torch.int32, dev, (B,))
     if _device() != dev:
         with torch.cuda.device(dev):
-            return dwconv1d_causal(x, weight, bias, activation, initial_state, lengths, return_state, stream)
+            return dwconv1d_causal(x, weight, bias, activation, initial_state, lengths, return_state)
     y = _like(x)
     st = x.new_empty((B, K - 1, C)) if return_state else None
-    if stream is not None:
-        _made(stream, y, st)
     _check(_library().gconv_dw1d_causal(x.data_ptr(), w, b, y.data_ptr(), s0, _ptr(st), n, _array(B, T, C, K),
-                                        _array(*x.stride()[:2]), act, dt, _stream(dev, stream)))
+                                        _array(*x.stride()[:2]), act, dt, _raw_stream(dev)))
     return (y, st) if return_state else y
 
 
@@ -397,6 +407,8 @@ def dwconv1d_causal_backward(x, weight, bias, dy, activation: Optional[str] = No
     """(dx, dw, db, dinitial) of dwconv1d_causal from the gradients dy of its output and
     dstate (or None: zero) of its final state.  db is None without a bias, dinitial
     without an initial_state."""
+    if stream is not None:
+        return _on_stream(stream, x, dwconv1d_causal_backward, x, weight, bias, dy, activation, initial_state, lengths, dstate)
     dt, C, K, w, b, act = _conv_args(x, weight, bias, activation, 3)
     B, T, _ = x.shape
     dev = x.get_device()
@@ -410,22 +422,22 @@ def dwconv1d_causal_backward(x, weight, bias, dy, activation: Optional[str] = No
     _check(L.gconv_dw1d_causal_backward_workspace(sh, dt, ctypes.byref(need)))
     if _device() != dev:
         with torch.cuda.device(dev):
-            return dwconv1d_causal_backward(x, weight, bias, dy, activation, initial_state, lengths, dstate, stream)
+            return dwconv1d_causal_backward(x, weight, bias, dy, activation, initial_state, lengths, dstate)
     dx, dw = _like(x), _like(weight)
     db = _like(bias) if bias is not None else None
     ds = x.new_empty((B, K - 1, C)) if initial_state is not None else None
     ws = _workspace(need.value, x)
-    if stream is not None:
-        _made(stream, dx, dw, db, ds, ws)
     _check(L.gconv_dw1d_causal_backward(x.data_ptr(), w, b, dy.data_ptr(), s0, sf, dx.data_ptr(), dw.data_ptr(),
                                         _ptr(db), _ptr(ds), n, sh, _array(*x.stride()[:2], *dy.stride()[:2]),
-                                        act, dt, _ptr(ws), need.value, _stream(dev, stream)))
+                                        act, dt, _ptr(ws), need.value, _raw_stream(dev)))
     return dx, dw, db, ds
 
 
 def dwconv1d_causal_step(x, weight, bias, state, activation: Optional[str] = None, slots=None, stream=None):
     """The next token of each sequence: x [B, C]; state [n, K-1, C] moves up by one row in
     place.  slots as for linear_attention_step.  Returns y [B, C]."""
+    if stream is not None:
+        return _on_stream(stream, x, dwconv1d_causal_step, x, weight, bias, state, activation, slots)
     dt, C, K, w, b, act = _conv_args(x, weight, bias, activation, 2)
     B = x.shape[0]
     dev = x.get_device()
@@ -435,10 +447,8 @@ def dwconv1d_causal_step(x, weight, bias, state, activation: Optional[str] = Non
     sl = _whole("slots", slots, torch.int32, dev, (B,))
     if _device() != dev:
         with torch.cuda.device(dev):
-            return dwconv1d_causal_step(x, weight, bias, state, activation, slots, stream)
+            return dwconv1d_causal_step(x, weight, bias, state, activation, slots)
     y = _like(x)
-    if stream is not None:
-        _made(stream, y)
     _check(_library().gconv_dw1d_causal_step(x.data_ptr(), w, b, sp, y.data_ptr(), sl,
-                                             _array(B, C, K, state.shape[0]), x.stride(0), act, dt, _stream(dev, stream)))
+                                             _array(B, C, K, state.shape[0]), x.stride(0), act, dt, _raw_stream(dev)))
     return y

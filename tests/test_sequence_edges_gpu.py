@@ -95,3 +95,89 @@ def test_last_segment_of_the_longest_sequence():
     assert dq.flatten()[:3].tolist() == [1.0, 1.5, 1.75] and bool((dq.view(-1)[16:] == 2.0).all())
     for d in (dk, dv):
         assert d.flatten()[-3:].tolist() == [1.75, 1.5, 1.0] and bool((d.view(-1)[:-16] == 2.0).all())
+
+
+# ---------------------------------------------------------------- other streams
+
+def stream_calls():
+    """Every entry point as a function of the stream it is given, with its inputs ready."""
+    q, k, v, g, s0 = attn_inputs(1, 500, 2, 4, 64, 64, torch.bfloat16, 5, True)
+    do, r = torch.randn_like(v), torch.randn(2000, 640, device="cuda").bfloat16()
+    x, w = torch.randn(2000, 640, device="cuda").bfloat16(), torch.ones(640, device="cuda", dtype=torch.bfloat16)
+    cx, cw = torch.randn(2, 400, 640, device="cuda").bfloat16(), torch.randn(640, 1, 4, device="cuda").bfloat16()
+    cs = torch.randn(2, 3, 640, device="cuda").bfloat16()
+
+    def fresh(t):
+        t = t.clone()
+        torch.cuda.synchronize()
+        return t
+
+    calls = {
+        "attn": lambda st: gc.linear_attention(q, k, v, g, initial_state=s0, return_state=True, stream=st),
+        "attn_bwd": lambda st: gc.linear_attention_backward(q, k, v, g, do, initial_state=s0, stream=st),
+        "attn_step": lambda st: gc.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], g, fresh(s0), stream=st),
+        "norm": lambda st: gc.rms_norm(x, w, residual=r, stream=st),
+        "norm_e4m3": lambda st: [t.view(torch.uint8) for t in gc.rms_norm_e4m3(x, w, residual=r, block=64, stream=st)],
+        "norm_bwd": lambda st: gc.rms_norm_backward(x, r, w, stream=st),
+        "conv": lambda st: gc.dwconv1d_causal(cx, cw, None, "silu", cs, return_state=True, stream=st),
+        "conv_bwd": lambda st: gc.dwconv1d_causal_backward(cx, cw, None, cx, "silu", cs, stream=st),
+        "conv_step": lambda st: gc.dwconv1d_causal_step(cx[:, 0], cw, None, fresh(cs), "silu", stream=st),
+    }
+    torch.cuda.synchronize()
+    return calls
+
+
+@pytest.mark.parametrize("name", ["attn", "attn_bwd", "norm", "norm_bwd", "conv", "conv_bwd"])
+def test_a_side_stream_leaves_memory_alone_that_the_current_one_still_reads(name):
+    # The current stream has freed blocks of every size the call needs, and reads them late.
+    call = stream_calls()[name]
+    want = [t.clone() for t in call(None) if t is not None]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    sizes = {1 << 20, 12 << 20} | {t.numel() * t.element_size() for t in want}
+    kept = [torch.randint(0, 255, (n,), dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    expect = [t.clone() for t in kept]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    late = [t.clone() for t in kept]      # after the sleep
+    del kept
+    got = call(side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    for a, b in zip(late, expect):
+        assert torch.equal(a, b)
+    for a, b in zip(want, [t for t in got if t is not None]):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", ["attn", "attn_bwd", "norm", "norm_bwd", "conv", "conv_bwd"])
+def test_outputs_of_a_side_stream_are_kept_for_the_current_one(name):
+    # The current stream waits for the side one and reads the outputs late; they are freed before
+    # that, and the side stream makes the next outputs at once.
+    call, side = stream_calls()[name], torch.cuda.Stream()
+    want = [t.clone() for t in call(None) if t is not None]
+    torch.cuda.synchronize()
+    got = [t for t in call(side) if t is not None]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(50_000_000)
+    late = [t.clone() for t in got]
+    del got
+    with torch.cuda.stream(side):
+        junk = [torch.full_like(t, 3.0) for t in want for _ in range(3)]
+    call(side)
+    torch.cuda.synchronize()
+    for a, b in zip(want, late):
+        assert torch.equal(a, b)
+    del junk
+
+
+def test_every_entry_point_takes_a_stream():
+    side = torch.cuda.Stream()
+    for name, call in stream_calls().items():
+        want = call(None)
+        torch.cuda.synchronize()
+        got = call(side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        for a, b in zip(want if isinstance(want, (tuple, list)) else (want,), got if isinstance(got, (tuple, list)) else (got,)):
+            assert (a is None and b is None) or torch.equal(a, b), name
