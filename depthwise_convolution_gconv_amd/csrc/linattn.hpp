@@ -41,7 +41,8 @@ struct LinWalk {
     hipStream_t stream;
 };
 
-__device__ __forceinline__ float lin_pow(float g, int e) { return e == 0 ? 1.0f : (float)exp((double)g * e); }
+__device__ __forceinline__ double lin_pow64(float g, int e) { return e == 0 ? 1.0 : exp((double)g * e); }
+__device__ __forceinline__ float lin_pow(float g, int e) { return (float)lin_pow64(g, e); }
 
 // Length of sequence b.
 __device__ __forceinline__ int lin_len(const LinWalk &p, int b)

@@ -280,6 +280,14 @@ template <typename TO> __device__ __forceinline__ void store_tile(TO *o, int hal
     }
 }
 
+// A value that all lanes of a wave have, in scalar registers.
+__device__ __forceinline__ double wave_value(double x)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 template <typename T, int DK, int NW, bool FULL> struct WalkLds {
     static constexpr int NP = kParts<T>;
     static constexpr int tiles = 2 * NP * ((FULL ? 2 : 1) * Tile<DK>::size + Tile<32 * NW>::size) + (FULL ? 0 : 16);
@@ -290,6 +298,7 @@ template <typename T, int DK, int NW, bool FULL> struct WalkLds {
     uint32_t mask[FULL ? 8 * 64 : 4];   // halves of ones for the pairs of them with j <= i, [r / 8][lane][r / 2 % 4]
     float upd[kLen];                    // upd_scale lam^(m-j-e0)
     float pw[kLen + 1];                 // lam^0 .. lam^kLen
+    double fade;                        // lam^kLen
 };
 
 // Waves of a SIMD that registers are kept for: two or three workgroups share a compute unit.
@@ -361,7 +370,11 @@ lin_walk(const LinWalks all)
         u32x4 *z = reinterpret_cast<u32x4 *>(&sm);
         for (int e = tid; e < Lds::tiles / 16; e += NTH) z[e] = u32x4{0, 0, 0, 0};
     }
-    if (tid <= L) sm.pw[tid] = lin_pow(p.log_decay[h], tid);
+    if (tid <= L) {
+        const double power = lin_pow64(p.log_decay[h], tid);
+        sm.pw[tid] = (float)power;
+        if (tid == L) sm.fade = power;
+    }
 
     if (kRoomy<T, DK> && nchunk > 0) fetch(ufirst);
 
@@ -433,12 +446,15 @@ lin_walk(const LinWalks all)
     auto ccol_at = [&](int g) { return ccol0 + 4 * g * Tile<NT>::group; };
 
     // Outputs: the state is scale times its registers, so that it need not be scaled for every
-    // chunk's decay.  Local states: scale is the weight of the next chunk's last token.
-    float scale = 1.0f;
+    // chunk's decay.  Local states: scale is the weight of the next chunk's last token.  In 64
+    // bits (one for the wave): every chunk multiplies it by the same power, whose rounding to fp32
+    // would add up to 2^-25 a chunk (918 u after 65536 tokens with a log decay of -4e-8).
+    double scale64 = 1.0;
     for (int k = 0; k < nchunk; ++k) {
         const int u0 = ufirst + k * du;
         const int m = max(0, min(ulive - u0, L));
-        const float faded = scale * sm.pw[m];
+        const double faded64 = wave_value(scale64 * (m == L ? sm.fade : (double)sm.pw[m]));
+        const float scale = (float)scale64, faded = (float)faded64;
         const bool settle = FULL && !(faded >= 0x1p-10f && faded <= 0x1p10f);   // registers take the scale
         // The previous chunk's readers are done (barrier at the loop's end).
         if constexpr (FULL) sa.stage(sm.a, shift_ab);
@@ -528,9 +544,10 @@ lin_walk(const LinWalks all)
                     st[x] = mma<2>(read_col<DK, NP>(sm.b, bcol_at(g, x)), wc, st[x]);
             }
         }
-        scale = settle ? 1.0f : faded;
+        scale64 = settle ? 1.0 : faded64;
         __syncthreads();
     }
+    const float scale = (float)scale64;
 
     if (!FULL && seg == 0 && s0 && scol < p.Dc)
         read_state(s0, (int)p.s0r, (int)p.s0c, 1.0f, lin_pow(p.log_decay[h], tokens_of(0)));

@@ -181,3 +181,28 @@ def test_every_entry_point_takes_a_stream():
         torch.cuda.synchronize()
         for a, b in zip(want if isinstance(want, (tuple, list)) else (want,), got if isinstance(got, (tuple, list)) else (got,)):
             assert (a is None and b is None) or torch.equal(a, b), name
+
+
+# ---------------------------------------------------------------- slow decays
+
+@pytest.mark.parametrize("H,segments", [(768, 1), (96, 8), (85, 9)])
+@pytest.mark.parametrize("decay", [-1e-6, -3e-7, -4e-8, 3e-7])
+def test_a_state_fades_over_many_tokens(H, segments, decay):
+    # Keys of zero leave the initial state to fade: lam^T S_0, and lam^(t+1) S_0 as outputs, with no
+    # sum in them.  A segment rounds its state's scale and its product (2 u), a join of two segments
+    # the power, the product and the sum (3 u), an output the two powers, the product of the scales,
+    # the state's parts, and its own value (8 u).
+    T = 65536
+    shape = (1, T, H, H, 1, 1)
+    assert gc.linear_attention_workspace(shape, torch.float32) in ((0,) if segments == 1 else
+                                                                   (4 * H * segments, -(-4 * H * segments // 256) * 256))
+    one, zero = (torch.full((1, 1, 1, 1), x, device="cuda").expand(1, T, H, 1) for x in (1.0, 0.0))
+    g = torch.full((H,), decay).cuda()
+    s0 = 1.0 + torch.rand(1, H, 1, 1, generator=torch.Generator().manual_seed(6)).cuda()
+    o, s = gc.linear_attention(one, zero, zero, g, scale=1.0, initial_state=s0, return_state=True)
+    gd, joins = g.double(), min(segments, 8)
+    want = s0.double() * torch.exp(gd * T).view(1, H, 1, 1)
+    assert float(((s - want).abs() / want).max()) <= (4 + 3 * joins) * U32
+    t = torch.arange(1, T + 1, device="cuda", dtype=torch.float64).view(1, T, 1, 1)
+    want = s0.double().view(1, 1, H, 1) * torch.exp(gd.view(1, 1, H, 1) * t)
+    assert float(((o - want).abs() / want).max()) <= (12 + 3 * joins) * U32
