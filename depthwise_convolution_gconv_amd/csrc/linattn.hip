@@ -13,14 +13,16 @@ constexpr int kThreads = 256;
 
 // States before each segment but the first from the segments' own sums, in place:
 //     R_1 = local_0,  R_(g+1) = lam^(tokens of g) R_g + local_g
-// (local_0 holds what is left of s0).  Two neighbouring elements for each thread, 8
-// segments' loads in flight: 20 us for 47 segments of 16 heads of 128 x 128, 100 MB, 5 TB/s.
+// (local_0 holds what is left of s0).  Powers and the running state are fp64, rounded where a
+// state leaves: a slowly fading state passes up to 1024 powers of one sign of rounding (fp32: 176
+// half steps after 512 segments).  Two neighbouring elements for each thread, 8 segments' loads
+// in flight: 20 us for 47 segments of 16 heads of 128 x 128, 100 MB, 5 TB/s.
 constexpr int kMaxSeg = 1024;
 constexpr int kScan = 2;
 __global__ void __launch_bounds__(kThreads)
 lin_scan(const LinWalks all)
 {
-    __shared__ float lam[kMaxSeg];
+    __shared__ double lam[kMaxSeg];
     const int tid = threadIdx.x;
     // Every walk's states have as many elements.
     const int64_t cells = (int64_t)all.w[0].Da * all.w[0].Dc, tiles = (cells + kScan * kThreads - 1) / (kScan * kThreads);
@@ -29,12 +31,12 @@ lin_scan(const LinWalks all)
     const int h = (int)(bh % p.H), bi = (int)(bh / p.H);
     const int n = lin_len(p, bi);
     for (int g = tid; g < p.nseg; g += kThreads)
-        lam[g] = lin_pow(p.log_decay[h], max(0, min(n - g * p.seg_len, p.seg_len)));
+        lam[g] = lin_pow64(p.log_decay[h], max(0, min(n - g * p.seg_len, p.seg_len)));
     __syncthreads();
     const int64_t x = ((blockIdx.x % all.blocks % tiles) * kThreads + tid) * kScan;
     const int left = (int)min(cells - x, (int64_t)kScan);
     if (left <= 0) return;
-    float r[kScan];
+    double r[kScan];
 #pragma unroll
     for (int e = 0; e < kScan; ++e) {
         const int64_t d = (x + e) / p.Dc, c = (x + e) % p.Dc;
@@ -48,16 +50,17 @@ lin_scan(const LinWalks all)
 #pragma unroll
         for (int g = 0; g < 8; ++g)
             if (g0 + g < p.nseg) {
-                if (g0 + g > 0) store_run<float, kScan>(w + (g0 + g) * cells, left, r);
+                const float before[kScan] = {(float)r[0], (float)r[1]};
+                if (g0 + g > 0) store_run<float, kScan>(w + (g0 + g) * cells, left, before);
 #pragma unroll
-                for (int e = 0; e < kScan; ++e) r[e] = fmaf(lam[g0 + g], r[e], loc[g][e]);
+                for (int e = 0; e < kScan; ++e) r[e] = fma(lam[g0 + g], r[e], (double)loc[g][e]);
             }
     }
     if (p.sf) {
 #pragma unroll
         for (int e = 0; e < kScan; ++e) {
             const int64_t d = (x + e) / p.Dc, c = (x + e) % p.Dc;
-            if (e < left) p.sf[bi * p.sfb + h * p.sfh + d * p.sfr + c * p.sfc] = r[e];
+            if (e < left) p.sf[bi * p.sfb + h * p.sfh + d * p.sfr + c * p.sfc] = (float)r[e];
         }
     }
 }

@@ -185,7 +185,7 @@ def test_every_entry_point_takes_a_stream():
 
 # ---------------------------------------------------------------- slow decays
 
-@pytest.mark.parametrize("H,segments", [(768, 1), (96, 8), (85, 9)])
+@pytest.mark.parametrize("H,segments", [(768, 1), (96, 8), (85, 9), (1, 512)])
 @pytest.mark.parametrize("decay", [-1e-6, -3e-7, -4e-8, 3e-7])
 def test_a_state_fades_over_many_tokens(H, segments, decay):
     # Keys of zero leave the initial state to fade: lam^T S_0, and lam^(t+1) S_0 as outputs, with no
