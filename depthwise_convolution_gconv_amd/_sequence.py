@@ -173,8 +173,8 @@ def linear_attention(q, k, v, log_decay, scale: Optional[float] = None, initial_
     token, which linear_attention_step carries on from.
 
     Sums and states are fp32; scores, and the state where a query meets it, enter their second
-    product with 16 bits for 16-bit inputs and 24 for fp32.  A non-finite v makes its column NaN in the
-    other tokens of its chunk of 32 too, earlier ones among them."""
+    product with 16 bits for 16-bit inputs and 24 for fp32.
+    A value that is not finite reaches its own and later tokens only; an infinity counts as NaN."""
     if stream is not None:
         return _on_stream(stream, q, linear_attention, q, k, v, log_decay, scale, initial_state, lengths, return_state)
     dt, shape, strides, g, n = _attn_args(q, k, v, log_decay, lengths)

@@ -174,8 +174,8 @@ template <typename T> __device__ __forceinline__ void shift_tail(Raw8<T> &r, int
     }
 }
 
-// They go to their parts' tiles.
-template <typename T, int D> __device__ __forceinline__ void stage8(__bf16 *t, int at, const Raw8<T> &v)
+// Their parts, and those to their tiles.
+template <typename T> __device__ __forceinline__ Part8<kParts<T>> parts8(const Raw8<T> &v)
 {
     constexpr int NP = kParts<T>;
     Part8<NP> r;
@@ -188,9 +188,26 @@ template <typename T, int D> __device__ __forceinline__ void stage8(__bf16 *t, i
         for (int e = 0; e < 8; ++e) f[e] = to_f32(x.v[e]);
         r = split8<NP>(f);
     }
+    return r;
+}
+template <int D, int NP> __device__ __forceinline__ void put8(__bf16 *t, int at, const Part8<NP> &r)
+{
 #pragma unroll
     for (int q = 0; q < NP; ++q) *reinterpret_cast<bf16x8 *>(t + q * Tile<D>::size + at) = r.p[q];
 }
+
+// x plus zero times every value of a run: NaN if one is not finite.
+__device__ __forceinline__ float taint(bf16x8 v, float x)
+{
+    const bf16x2 zero = {(__bf16)0.0f, (__bf16)0.0f};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const bf16x2 two = {v[i], v[i + 1]};
+        x = __builtin_amdgcn_fdot2_f32_bf16(two, zero, x, false);
+    }
+    return x;
+}
+constexpr int kNoToken = 0x7fffffff;
 
 // A thread's share of a tile of kLen tokens by D columns: NR runs of 8 of one column block,
 // every STEP tokens.  Blocks past the last column are neither read nor staged.
@@ -237,8 +254,13 @@ template <typename T, int D, int NTH> struct Share {
         }
         p += chunk;
     }
-    // shift: row ends inside a load have to be moved (not for narrow rows).
-    __device__ __forceinline__ void stage(__bf16 *t, bool shift)
+    // shift: row ends inside a load have to be moved (not for narrow rows).  bad: for c, whose
+    // values that are not finite a product would take to all tokens (0 x NaN where a score is
+    // masked).  They become zeros, and each column keeps the first of its tokens, counted from the
+    // chunk's first u0 on, that had one: bad[0] tells whether any has, bad[1 + column] is that
+    // token.  Outputs from there on become NaN after the walk (in it, a test a chunk took 14 of 442
+    // us over 65536 tokens x 16 heads in bf16; finding the values takes 5).
+    __device__ __forceinline__ void stage(__bf16 *t, bool shift, int *bad = nullptr, int u0 = 0)
     {
         if (left <= 0) return;
         const int d = threadIdx.x % (D / 8) * 8;
@@ -246,8 +268,31 @@ template <typename T, int D, int NTH> struct Share {
 #pragma unroll
             for (int i = 0; i < NR; ++i) shift_tail<T>(r[i], left);
         }
+        float tainted = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NR; ++i) stage8<T, D>(t, Tile<D>::at(j + i * STEP, d), r[i]);
+        for (int i = 0; i < NR; ++i) {
+            const Part8<kParts<T>> x = parts8<T>(r[i]);
+            put8<D>(t, Tile<D>::at(j + i * STEP, d), x);
+            if (bad) tainted = taint(x.p[0], tainted);
+        }
+        if (bad && tainted != tainted) drop_bad(t, bad, u0);
+    }
+    __device__ __forceinline__ void drop_bad(__bf16 *t, int *bad, int u0)
+    {
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));     // addresses are made here, not kept for the whole walk
+        const int d = tid % (D / 8) * 8;
+        bad[0] = 1;
+#pragma unroll 1
+        for (int row = tid / (D / 8); row < kLen; row += STEP)
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+                __bf16 *p = t + Tile<D>::at(row, d) + e;     // in the same block of columns
+                const __bf16 x = *p;
+                if ((__builtin_bit_cast(uint16_t, x) & 0x7fff) < 0x7f80) continue;
+                atomicMin(&bad[1 + d + e], u0 + row);
+                for (int q = 0; q < kParts<T>; ++q) p[q * Tile<D>::size] = (__bf16)0.0f;
+            }
     }
 };
 
@@ -299,6 +344,7 @@ template <typename T, int DK, int NW, bool FULL> struct WalkLds {
     float upd[kLen];                    // upd_scale lam^(m-j-e0)
     float pw[kLen + 1];                 // lam^0 .. lam^kLen
     double fade;                        // lam^kLen
+    int bad[FULL ? 1 + 32 * NW : 1];    // see drop_bad
 };
 
 // Waves of a SIMD that registers are kept for: two or three workgroups share a compute unit.
@@ -369,6 +415,10 @@ lin_walk(const LinWalks all)
     {   // columns past the last stay zero
         u32x4 *z = reinterpret_cast<u32x4 *>(&sm);
         for (int e = tid; e < Lds::tiles / 16; e += NTH) z[e] = u32x4{0, 0, 0, 0};
+    }
+    if constexpr (FULL) {
+        if (tid < NT) sm.bad[1 + tid] = kNoToken;
+        if (tid == 0) sm.bad[0] = 0;
     }
     if (tid <= L) {
         const double power = lin_pow64(p.log_decay[h], tid);
@@ -459,7 +509,7 @@ lin_walk(const LinWalks all)
         // The previous chunk's readers are done (barrier at the loop's end).
         if constexpr (FULL) sa.stage(sm.a, shift_ab);
         sb.stage(sm.b, shift_ab);
-        sc.stage(sm.c, shift_c);
+        sc.stage(sm.c, shift_c, FULL ? sm.bad : nullptr, u0);
         if (tid < L)
             sm.upd[tid] = p.upd_scale * sm.pw[max(m - tid - p.e0, 0)] * (!FULL ? scale : settle ? 1.0f : 1.0f / faded);
         __syncthreads();
@@ -548,6 +598,16 @@ lin_walk(const LinWalks all)
         __syncthreads();
     }
     const float scale = (float)scale64;
+    if (FULL && sm.bad[0]) {     // behind the loop's last barrier, which orders these stores after its own
+#pragma unroll 1
+        for (int col = 0; col < min(NT, p.Dc - n0); ++col)
+#pragma unroll 1
+            for (int64_t u = (int64_t)sm.bad[1 + col] + tid; u < ulive; u += NTH) {
+                const int64_t at = bi * p.osb + (int64_t)lin_token(p, (int)u, n) * p.ost + h * p.osh + n0 + col;
+                if (sizeof(T) == 4 || p.out_f32) ((float *)p.out)[at] = __builtin_nanf("");
+                else ((T *)p.out)[at] = from_f32<T>(__builtin_nanf(""));
+            }
+    }
 
     if (!FULL && seg == 0 && s0 && scol < p.Dc)
         read_state(s0, (int)p.s0r, (int)p.s0c, 1.0f, lin_pow(p.log_decay[h], tokens_of(0)));
@@ -561,6 +621,12 @@ lin_walk(const LinWalks all)
         dr = (int)p.sfr; dc = (int)p.sfc;
     }
     if (dp && scol < p.Dc) {
+        if (FULL && sm.bad[0] && sm.bad[1 + wave * 32 + l32] != kNoToken) {
+#pragma unroll
+            for (int x = 0; x < NX; ++x)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) st[x][r] = __builtin_nanf("");
+        }
         int d0 = 8 * half;
         asm volatile("" : "+v"(d0));
 #pragma unroll

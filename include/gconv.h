@@ -298,9 +298,9 @@ void gconv_autotune_clear(void);
  *     S_t = lam S_(t-1) + k_t v_t^T,   o_t = scale * q_t S_t
  * initial_state: fp32 [B,H,Dk,Dv] = S_(-1), or NULL (zero).  final_state: the same shape,
  * S after lengths[b] tokens, or NULL.  strides = {q: batch, token, head; k; v; o}, 12
- * values.  Tokens are taken in chunks of 32: a non-finite v of a real token makes its column
- * of the outputs NaN for the whole chunk (a non-finite q or k reaches its own and later
- * tokens only), and an infinity in fp16 or fp32 inputs counts as NaN.  workspace:
+ * values.  A value of a real token that is not finite reaches its own and
+ * later tokens only: a v its column of their outputs, a q its token, a k all that follow;
+ * an infinity counts as NaN, and so does an fp32 value from 2^128 (1 - 2^-9) on.  workspace:
  * gconv_linear_attention_workspace bytes (may be 0), 16-byte aligned. */
 gconv_status_t gconv_linear_attention_workspace(const int64_t *shape, gconv_dtype_t dtype, int32_t backward,
                                                 size_t *bytes);
@@ -313,7 +313,9 @@ gconv_status_t gconv_linear_attention(const void *q, const void *k, const void *
 /* Its gradients: dq, dk [B,T,Hk,Dk] (the value heads of a key head added), dv [B,T,H,Dv]
  * and, if dinitial is not NULL, the gradient of initial_state (fp32), from the gradients
  * d_o of o and dfinal (fp32, or NULL: zero) of final_state.  strides = {q, k, v, d_o, dq,
- * dk, dv: batch, token, head}, 21 values.  log_decay is a constant: it has no gradient. */
+ * dk, dv: batch, token, head}, 21 values.  log_decay is a constant: it has no gradient.
+ * Values that are not finite reach the tokens that the formulas name: of k and v later ones
+ * (in dq), of q and d_o earlier ones (in dk and dv), and of each its own. */
 gconv_status_t gconv_linear_attention_backward(const void *q, const void *k, const void *v, const void *d_o,
                                                void *dq, void *dk, void *dv, const int64_t *shape,
                                                const int64_t *strides, const float *log_decay, float scale,

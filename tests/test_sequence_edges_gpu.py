@@ -206,3 +206,56 @@ def test_a_state_fades_over_many_tokens(H, segments, decay):
     t = torch.arange(1, T + 1, device="cuda", dtype=torch.float64).view(1, T, 1, 1)
     want = s0.double().view(1, 1, H, 1) * torch.exp(gd.view(1, 1, H, 1) * t)
     assert float(((o - want).abs() / want).max()) <= (12 + 3 * joins) * U32
+
+
+# ---------------------------------------------------------------- values that are not finite
+
+# Where a value of an input that is not finite shows: in the outputs' rows before its token, its
+# own, and later ones; in its own column or in all.  What the rows do not name stays bit for bit.
+REACH = {
+    ("q", "o"): ("own", "all"), ("k", "o"): ("own later", "all"), ("v", "o"): ("own later", "col"),
+    ("q", "dk"): ("before own", "col"), ("q", "dv"): ("before own", "all"),
+    ("k", "dq"): ("own later", "col"), ("k", "dv"): ("own", "all"),
+    ("v", "dq"): ("own later", "all"), ("v", "dk"): ("own", "all"),
+    ("do", "dq"): ("own", "all"), ("do", "dk"): ("before own", "all"), ("do", "dv"): ("before own", "col"),
+}
+
+
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("T,token,D", [(100, 50, 64), (100, 63, 33), (700, 130, 128), (2600, 2111, 40)])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_values_that_are_not_finite_reach_no_token_they_must_not(dt, T, token, D, value):
+    q, k, v, g, s0 = attn_inputs(1, T, 1, 1, D, D, DT[dt], 7, True, decay="-0.01")
+    do = torch.randn(1, T, 1, D, generator=torch.Generator().manual_seed(8)).to(DT[dt]).cuda()
+    ins = {"q": q, "k": k, "v": v, "do": do}
+
+    def run():
+        o, s = gc.linear_attention(q, k, v, g, initial_state=s0, return_state=True)
+        dq, dk, dv, ds = gc.linear_attention_backward(q, k, v, g, do, initial_state=s0)
+        return {"o": o, "dq": dq, "dk": dk, "dv": dv}, s, ds
+
+    clean, clean_s, clean_ds = run()
+    col = D - 2
+    for name, t in ins.items():
+        kept = t[0, token, 0, col].clone()
+        t[0, token, 0, col] = float(value)
+        got, s, ds = run()
+        t[0, token, 0, col] = kept
+        for out, y in got.items():
+            rows, cols = REACH.get((name, out), ("", ""))
+            hit = torch.zeros(T, D, dtype=torch.bool, device="cuda")
+            c = slice(col, col + 1) if cols == "col" else slice(0, D)
+            for part, r in (("before", slice(0, token)), ("own", slice(token, token + 1)), ("later", slice(token + 1, T))):
+                if part in rows:
+                    hit[r, c] = True
+            y, ref = y[0, :, 0], clean[out][0, :, 0]
+            assert torch.equal(y[~hit], ref[~hit]), (name, out)
+            assert not torch.isfinite(y[hit]).any(), (name, out)
+        # The state: a row of it for k, a column for v; the initial state's gradient likewise for q and do.
+        for y, ref, row, column in ((s[0, 0], clean_s[0, 0], "k", "v"), (ds[0, 0], clean_ds[0, 0], "q", "do")):
+            hit = torch.zeros(D, D, dtype=torch.bool, device="cuda")
+            if name == row:
+                hit[col] = True
+            if name == column:
+                hit[:, col] = True
+            assert torch.equal(y[~hit], ref[~hit]) and not torch.isfinite(y[hit]).any(), name
