@@ -98,9 +98,10 @@ def _whole(name: str, t: Optional[torch.Tensor], dtype, dev: int, shape) -> int:
 
 
 # The current device and stream without their Python objects, which cost more than the rest of a
-# single-token call's checks.
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# single-token call's checks.  Builds of torch without a GPU lack them, and have no tensor that a
+# call would get as far with.
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _on_stream(stream, ref: torch.Tensor, fn, *args):
