@@ -36,6 +36,12 @@ struct Dw1dArgs {
 
 enum { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2 };
 
+// Whether HIP takes a launch: fewer than 2^31 workgroups and fewer than 2^32 threads.
+inline bool grid_fits(int64_t blocks, int threads)
+{
+    return blocks < int64_t(1) << 31 && blocks <= ((int64_t(1) << 32) - 1) / threads;
+}
+
 // Storage <-> fp32.  Widening is exact for every storage type; narrowing
 // rounds to nearest, ties to even (v_cvt_f16_f32 / v_cvt_pk_bf16_f32).
 __device__ __forceinline__ float to_f32(float v) { return v; }

@@ -17,7 +17,6 @@ constexpr int kThreads = 256;
 // state leaves: a slowly fading state passes up to 1024 powers of one sign of rounding (fp32: 176
 // half steps after 512 segments).  Two neighbouring elements for each thread, 8 segments' loads
 // in flight: 20 us for 47 segments of 16 heads of 128 x 128, 100 MB, 5 TB/s.
-constexpr int kMaxSeg = 1024;
 constexpr int kScan = 2;
 __global__ void __launch_bounds__(kThreads)
 lin_scan(const LinWalks all)
@@ -69,9 +68,9 @@ lin_scan(const LinWalks all)
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 lin_group_sum(const float *__restrict__ part, T *__restrict__ out, int64_t sb, int64_t st, int64_t sh, int T_in, int Hk,
-              int r, int D, int blocks)
+              int r, int D, int blocks, int64_t bt0)
 {
-    const int64_t bt = blockIdx.x / blocks;      // (batch, token)
+    const int64_t bt = bt0 + blockIdx.x / blocks;      // (batch, token)
     const int x = (int)(blockIdx.x % blocks) * kThreads + threadIdx.x, g = x / D, d = x - g * D;
     if (g >= Hk) return;
     const float *src = part + (bt * Hk + g) * r * D + d;
@@ -169,12 +168,18 @@ template <typename T> hipError_t run_step(const LinStep &p)
 
 }  // namespace
 
+static int64_t scan_blocks(int64_t heads, int64_t cells) { return heads * ceil_div(cells, kScan * kThreads); }
+
+bool lin_scan_fits(int64_t count, int64_t heads, int64_t cells)
+{
+    return grid_fits(count * scan_blocks(heads, cells), kThreads);
+}
+
 hipError_t launch_lin_scan(const LinWalks &walks)
 {
     LinWalks all = walks;
     const LinWalk &p = all.w[0];
-    all.blocks = (int64_t)p.B * p.H * ceil_div((int64_t)p.Da * p.Dc, kScan * kThreads);
-    if (all.count * all.blocks >= (int64_t(1) << 31) || p.nseg > kMaxSeg) return hipErrorInvalidValue;
+    all.blocks = scan_blocks((int64_t)p.B * p.H, (int64_t)p.Da * p.Dc);
     hipLaunchKernelGGL(lin_scan, dim3((unsigned)(all.count * all.blocks)), dim3(kThreads), 0, p.stream, all);
     return hipGetLastError();
 }
@@ -214,27 +219,29 @@ hipError_t launch_lin_walks(const LinWalks &all, const char **kname)
     return run_walks(all, true);
 }
 
+template <typename T>
+static hipError_t run_group_sum(const float *part, T *out, const int64_t *ost, int64_t B, int64_t T_in, int Hk, int r, int D,
+                                hipStream_t stream)
+{
+    const int blocks = (int)ceil_div((int64_t)Hk * D, kThreads);
+    const int64_t most = ((int64_t(1) << 32) - 1) / kThreads / blocks;      // tokens of a launch
+    for (int64_t bt0 = 0; bt0 < B * T_in; bt0 += most) {
+        hipLaunchKernelGGL((lin_group_sum<T>), dim3((unsigned)(std::min(most, B * T_in - bt0) * blocks)), dim3(kThreads), 0,
+                           stream, part, out, ost[0], ost[1], ost[2], (int)T_in, Hk, r, D, blocks, bt0);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+}
+
 hipError_t launch_lin_group_sum(const float *part, void *out, const int64_t *ost, int64_t B, int64_t T, int Hk, int r,
                                 int D, int dtype, hipStream_t stream)
 {
-    const int blocks = (int)ceil_div((int64_t)Hk * D, kThreads);
-    if (B * T * blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)(B * T * blocks)), block(kThreads);
     switch (dtype) {
-    case DT_F32:
-        hipLaunchKernelGGL((lin_group_sum<float>), grid, block, 0, stream, part, (float *)out, ost[0], ost[1], ost[2],
-                           (int)T, Hk, r, D, blocks);
-        break;
-    case DT_F16:
-        hipLaunchKernelGGL((lin_group_sum<_Float16>), grid, block, 0, stream, part, (_Float16 *)out, ost[0], ost[1],
-                           ost[2], (int)T, Hk, r, D, blocks);
-        break;
-    default:
-        hipLaunchKernelGGL((lin_group_sum<__bf16>), grid, block, 0, stream, part, (__bf16 *)out, ost[0], ost[1], ost[2],
-                           (int)T, Hk, r, D, blocks);
-        break;
+    case DT_F32: return run_group_sum(part, (float *)out, ost, B, T, Hk, r, D, stream);
+    case DT_F16: return run_group_sum(part, (_Float16 *)out, ost, B, T, Hk, r, D, stream);
+    default: return run_group_sum(part, (__bf16 *)out, ost, B, T, Hk, r, D, stream);
     }
-    return hipGetLastError();
 }
 
 hipError_t launch_lin_step(const LinStep &p, const char **kname)

@@ -96,6 +96,7 @@ hipError_t run_lin_walks_bf16(const LinWalks &all, bool full);
 // Up to this many segments, each walk adds up the local states before its own, and the last
 // one writes sf: a mean of half as many reads as there are segments, and no scan.
 constexpr int kFoldSegs = 8;
+constexpr int kMaxSeg = 1024;    // segments of a sequence at most
 
 // The segment states (nseg > 1): local sums into ws, the first with what is left of s0, then
 // past kFoldSegs the scan that turns them into the states before each segment but the first
@@ -104,10 +105,11 @@ constexpr int kFoldSegs = 8;
 hipError_t launch_lin_states(const LinWalks &all, int summed, const char **kname);
 // The outputs (up to kFoldSegs also sf).
 hipError_t launch_lin_walks(const LinWalks &all, const char **kname);
-// Scan alone (T == 0: sf = s0).
+// Scan alone (T == 0: sf = s0), and whether a launch takes it.
 hipError_t launch_lin_scan(const LinWalks &all);
+bool lin_scan_fits(int64_t count, int64_t heads, int64_t cells);
 // out[b,t,g,:] = sum over j < r of part[b,t,g*r+j,:] (contiguous), rounded to dtype; ost: out's
-// element strides (batch, token, head).
+// element strides (batch, token, head).  In as many launches as it takes.
 hipError_t launch_lin_group_sum(const float *part, void *out, const int64_t *ost, int64_t B, int64_t T, int Hk, int r,
                                 int D, int dtype, hipStream_t stream);
 

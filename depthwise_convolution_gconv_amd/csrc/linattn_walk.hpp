@@ -654,9 +654,7 @@ template <typename T, int DK, int NW, bool FULL> hipError_t run_walk_on(LinWalks
     const LinWalk &p = all.w[0];
     all.ndv = (int32_t)ceil_div(p.Dc, 32 * NW);
     all.blocks = (int64_t)all.count * p.B * p.H * p.nseg * all.ndv;
-    const int64_t grid = 8 * ceil_div(all.blocks, 8);
-    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((lin_walk<T, DK, NW, FULL>), dim3((unsigned)grid), dim3(64 * NW), 0, p.stream, all);
+    hipLaunchKernelGGL((lin_walk<T, DK, NW, FULL>), dim3((unsigned)(8 * ceil_div(all.blocks, 8))), dim3(64 * NW), 0, p.stream, all);
     return hipGetLastError();
 }
 

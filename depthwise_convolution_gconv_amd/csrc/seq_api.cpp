@@ -121,10 +121,31 @@ void lin_segments(const LinShape &s, bool backward, gconv_dtype_t dtype, int32_t
     int64_t n = !backward                                      ? fit(1, s.Dk, s.Dv)
                 : gconv::lin_alike(s.Dk, s.Dv, s.Dv, s.Dk, (int)dtype) ? fit(3, s.Dk, s.Dv)
                                                                : std::min(fit(1, s.Dk, s.Dv), fit(2, s.Dv, s.Dk));
-    n = std::max<int64_t>(1, std::min<int64_t>({n, chunks / 2, 1024}));
+    n = std::max<int64_t>(1, std::min<int64_t>({n, chunks / 2, gconv::kMaxSeg}));
     const int64_t each = gconv::ceil_div(chunks, n);
     *nseg = (int32_t)gconv::ceil_div(chunks, each);
     *seg_len = (int32_t)(each * kChunk);
+}
+
+// Every launch of a call, before the first is made.  (The local states' launches are no larger
+// than the outputs', and the sum over value heads goes in pieces.)
+gconv_status_t lin_grids(const LinShape &s, bool backward, gconv_dtype_t dtype)
+{
+    int32_t nseg, len;
+    lin_segments(s, backward, dtype, &nseg, &len);
+    auto walks = [&](int64_t count, int64_t Da, int64_t Dc) {
+        const int64_t blocks = count * s.B * s.H * nseg * gconv::lin_tiles(Da, Dc, (int)dtype);
+        return gconv::grid_fits(8 * gconv::ceil_div(blocks, 8), 64 * gconv::lin_waves(Da, Dc, (int)dtype));
+    };
+    const bool alike = gconv::lin_alike(s.Dk, s.Dv, s.Dv, s.Dk, (int)dtype);
+    const bool fits = s.T == 0   ? gconv::lin_scan_fits(1, s.B * s.H, s.Dk * s.Dv)
+                      : !backward ? walks(1, s.Dk, s.Dv)
+                      : alike     ? walks(3, s.Dk, s.Dv)
+                                  : walks(1, s.Dk, s.Dv) && walks(2, s.Dv, s.Dk);
+    if (!fits || (nseg > gconv::kFoldSegs && !gconv::lin_scan_fits(backward ? 3 : 1, s.B * s.H, s.Dk * s.Dv)))
+        return fail(GCONV_ERR_UNSUPPORTED, "linear attention: %lld heads need more threads than a launch takes",
+                    (long long)(s.B * s.H));
+    return GCONV_OK;
 }
 
 // One set of segment states.
@@ -216,8 +237,8 @@ gconv_status_t gconv_linear_attention_workspace(const int64_t *shape, gconv_dtyp
     if (!bytes) return fail(GCONV_ERR_INVALID_ARG, "NULL bytes");
     if (bad_dtype(dtype)) return fail(GCONV_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
     LinShape s;
-    const gconv_status_t st = lin_shape(shape, &s);
-    if (st != GCONV_OK) return st;
+    gconv_status_t st = lin_shape(shape, &s);
+    if (st != GCONV_OK || (st = lin_grids(s, backward != 0, dtype)) != GCONV_OK) return st;
     *bytes = lin_workspace(s, backward != 0, dtype);
     return GCONV_OK;
 }
@@ -231,7 +252,9 @@ gconv_status_t gconv_linear_attention(const void *q, const void *k, const void *
     if (bad_dtype(dtype)) return fail(GCONV_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
     LinShape s;
     gconv_status_t st = lin_shape(shape, &s);
-    if (st != GCONV_OK || (st = check_strides(strides, 12)) != GCONV_OK) return st;
+    if (st != GCONV_OK || (st = check_strides(strides, 12)) != GCONV_OK ||
+        (st = lin_grids(s, false, dtype)) != GCONV_OK)
+        return st;
     if (!log_decay) return fail(GCONV_ERR_INVALID_ARG, "NULL log_decay");
     if (s.B > 0 && s.T > 0 && (!q || !k || !v || !o)) return fail(GCONV_ERR_INVALID_ARG, "NULL q, k, v or o");
     const size_t need = lin_workspace(s, false, dtype), es = elem(dtype), ns = 4 * (size_t)(s.B * s.H * s.Dk * s.Dv);
@@ -286,7 +309,9 @@ gconv_status_t gconv_linear_attention_backward(const void *q, const void *k, con
     if (bad_dtype(dtype)) return fail(GCONV_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
     LinShape s;
     gconv_status_t st = lin_shape(shape, &s);
-    if (st != GCONV_OK || (st = check_strides(strides, 21)) != GCONV_OK) return st;
+    if (st != GCONV_OK || (st = check_strides(strides, 21)) != GCONV_OK ||
+        (st = lin_grids(s, true, dtype)) != GCONV_OK)
+        return st;
     if (!log_decay) return fail(GCONV_ERR_INVALID_ARG, "NULL log_decay");
     if (s.B > 0 && s.T > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv))
         return fail(GCONV_ERR_INVALID_ARG, "NULL q, k, v, d_o, dq, dk or dv");

@@ -80,7 +80,15 @@ def test_e4m3_is_the_quotient(C, block, dt):
 
 # ---------------------------------------------------------------- the longest sequences
 
-def test_last_segment_of_the_longest_sequence():
+@pytest.fixture
+def much_memory():
+    """Gives tens of GB back to the device after the test."""
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
+def test_last_segment_of_the_longest_sequence(much_memory):
     # The largest T, where the last segment's rounded-up end passes 2^31.  All inputs are one value
     # at stride 0 and the decay is 1/2, so every sum is 2 but near its start, all of it exact.
     T = 2 ** 31 - 1 - 4096
@@ -259,3 +267,16 @@ def test_values_that_are_not_finite_reach_no_token_they_must_not(dt, T, token, D
             if name == column:
                 hit[:, col] = True
             assert torch.equal(y[~hit], ref[~hit]) and not torch.isfinite(y[hit]).any(), name
+
+
+def test_shares_of_value_heads_past_a_launch(much_memory):
+    # 2^24 tokens of 256 columns are 2^32 threads for the sum over two value heads: two launches.
+    # All inputs are one value at stride 0 and the decay is 1/2, so a head's share is 2 but near an end.
+    T, D = 2 ** 24, 256
+    one = lambda h, d: torch.ones(1, 1, 1, 1, dtype=torch.bfloat16, device="cuda").expand(1, T, h, d)  # noqa: E731
+    g = torch.full((2,), 0.5, dtype=torch.float64).log().float().cuda()
+    dense = torch.ones(1, 1, 1, D, dtype=torch.bfloat16, device="cuda").expand(1, T, 1, D)
+    dq, dk, dv, _ = gc.linear_attention_backward(dense, dense, one(2, 1), g, one(2, 1), scale=1.0)
+    assert bool((dq[0, 16:] == 4.0).all()) and bool((dk[0, :-16] == 4.0).all())
+    assert bool((dq[0, 0] == 2.0).all()) and bool((dk[0, -1] == 2.0).all())
+    assert bool((dv[0, :-16] == 2.0 * D).all())
