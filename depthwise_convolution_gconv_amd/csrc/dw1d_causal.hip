@@ -526,18 +526,34 @@ causal_step(const CausalStepArgs a, int cblocks)
     store_run<T, VE>(yp, left, z);
 }
 
+// The grid of a call: workgroups along channels and along tokens; cx (up to 4 taps): channel runs
+// of a workgroup.
+struct Plan {
+    int64_t cblocks, tblocks, blocks;
+    int cx;
+};
+Plan plan_fwd(const CausalArgs &a)
+{
+    Plan p = {};
+    if (a.K <= 4) {
+        const int64_t runs = ceil_div(a.C, a.dtype == DT_F32 ? 4 : 8);
+        for (p.cx = 8; p.cx < kThreads && p.cx < runs;) p.cx *= 2;
+        p.cblocks = ceil_div(runs, p.cx);
+        p.tblocks = ceil_div(a.T, (int64_t)(kThreads / p.cx) * kRun);
+    } else {
+        p.cblocks = ceil_div(a.C, kCT);
+        p.tblocks = ceil_div(a.T, kTT);
+    }
+    p.tblocks = std::max<int64_t>(1, p.tblocks);
+    p.blocks = a.B * p.cblocks * p.tblocks;
+    return p;
+}
+
 template <typename T, int K> hipError_t run_short(const CausalArgs &a)
 {
-    constexpr int VE = 16 / sizeof(T);
-    const int64_t runs = ceil_div(a.C, VE);
-    int cx = 8;
-    while (cx < kThreads && cx < runs) cx *= 2;
-    const int64_t cblocks = ceil_div(runs, cx);
-    const int64_t tblocks = std::max<int64_t>(1, ceil_div(a.T, (int64_t)(kThreads / cx) * kRun));
-    const int64_t blocks = a.B * cblocks * tblocks;
-    if (blocks > kGridMax) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((causal_run<T, K>), dim3((unsigned)blocks), dim3(kThreads), 0, a.stream, a, cx, (int)cblocks,
-                       (int)tblocks);
+    const Plan p = plan_fwd(a);
+    hipLaunchKernelGGL((causal_run<T, K>), dim3((unsigned)p.blocks), dim3(kThreads), 0, a.stream, a, p.cx, (int)p.cblocks,
+                       (int)p.tblocks);
     return hipGetLastError();
 }
 
@@ -552,49 +568,56 @@ template <typename T> hipError_t run_fwd(const CausalArgs &a, const char **kname
     default: break;
     }
     *kname = "causal_tile";
-    const int64_t cblocks = ceil_div(a.C, kCT), tblocks = std::max<int64_t>(1, ceil_div(a.T, kTT));
-    const int64_t blocks = a.B * cblocks * tblocks;
-    if (blocks > kGridMax) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((causal_tile<T>), dim3((unsigned)blocks), dim3(kThreads),
-                       (unsigned)((kTT + 2 * a.K - 1) * kCT * sizeof(float)), a.stream, a, (int)cblocks, (int)tblocks);
+    const Plan p = plan_fwd(a);
+    hipLaunchKernelGGL((causal_tile<T>), dim3((unsigned)p.blocks), dim3(kThreads),
+                       (unsigned)((kTT + 2 * a.K - 1) * kCT * sizeof(float)), a.stream, a, (int)p.cblocks, (int)p.tblocks);
     return hipGetLastError();
 }
 
-template <typename T, int NT> hipError_t run_bwd_tile(const CausalArgs &a, int64_t blocks, int64_t cblocks, int64_t tblocks)
+template <typename T, int NT> hipError_t run_bwd_tile(const CausalArgs &a, const Plan &p)
 {
-    hipLaunchKernelGGL((causal_bwd_tile<T, NT>), dim3((unsigned)(8 * ceil_div(blocks, 8))), dim3(kThreads), 0, a.stream, a,
-                       (int)cblocks, (int)tblocks, blocks);
+    hipLaunchKernelGGL((causal_bwd_tile<T, NT>), dim3((unsigned)(8 * ceil_div(p.blocks, 8))), dim3(kThreads), 0, a.stream,
+                       a, (int)p.cblocks, (int)p.tblocks, p.blocks);
     return hipGetLastError();
 }
 
 // Tiles along the sequence: its tokens and, for the state's gradient, the K-1 before them.
 int64_t bwd_tblocks(int64_t T, int64_t K) { return ceil_div(T + K - 1, kTT); }
 
+Plan plan_bwd(const CausalArgs &a)
+{
+    Plan p = {};
+    p.cblocks = ceil_div(a.C, kBT);
+    p.tblocks = a.s0 ? bwd_tblocks(a.T, a.K) : ceil_div(a.T, kTT);
+    p.blocks = a.B * p.tblocks * p.cblocks;
+    return p;
+}
+int64_t reduce_blocks(const CausalArgs &a) { return ceil_div((a.K + 1) * a.C, 64); }
+
 template <typename T> hipError_t run_bwd(const CausalArgs &a, const char **kname)
 {
     *kname = "causal_bwd_tile";
-    const int64_t cblocks = ceil_div(a.C, kBT), tblocks = a.s0 ? bwd_tblocks(a.T, a.K) : ceil_div(a.T, kTT);
-    const int64_t tiles = a.B * tblocks, blocks = tiles * cblocks;
-    if (blocks > kGridMax - 8) return hipErrorInvalidValue;
+    const Plan p = plan_bwd(a);
     hipError_t err = hipSuccess;
-    if (blocks > 0) {
-        if (a.K <= 4) err = run_bwd_tile<T, 1>(a, blocks, cblocks, tblocks);
-        else if (a.K <= 8) err = run_bwd_tile<T, 2>(a, blocks, cblocks, tblocks);
-        else if (a.K <= 16) err = run_bwd_tile<T, 4>(a, blocks, cblocks, tblocks);
-        else if (a.K <= 32) err = run_bwd_tile<T, 8>(a, blocks, cblocks, tblocks);
-        else err = run_bwd_tile<T, 16>(a, blocks, cblocks, tblocks);
+    if (p.blocks > 0) {
+        if (a.K <= 4) err = run_bwd_tile<T, 1>(a, p);
+        else if (a.K <= 8) err = run_bwd_tile<T, 2>(a, p);
+        else if (a.K <= 16) err = run_bwd_tile<T, 4>(a, p);
+        else if (a.K <= 32) err = run_bwd_tile<T, 8>(a, p);
+        else err = run_bwd_tile<T, 16>(a, p);
     }
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL((causal_bwd_reduce<T>), dim3((unsigned)ceil_div((a.K + 1) * a.C, 64)), dim3(1024), 0, a.stream,
-                       a.ws, (T *)a.dw, (T *)a.db, tiles, a.C, (int)a.K);
+    hipLaunchKernelGGL((causal_bwd_reduce<T>), dim3((unsigned)reduce_blocks(a)), dim3(1024), 0, a.stream, a.ws, (T *)a.dw,
+                       (T *)a.db, a.B * p.tblocks, a.C, (int)a.K);
     return hipGetLastError();
 }
 
+int64_t step_cblocks(const CausalStepArgs &a) { return ceil_div(a.C, kThreads * 4); }
+
 template <typename T> hipError_t run_step(const CausalStepArgs &a)
 {
-    const int64_t cblocks = ceil_div(a.C, kThreads * 4), blocks = a.B * cblocks;
-    if (blocks > kGridMax) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks), block(kThreads);
+    const int64_t cblocks = step_cblocks(a);
+    const dim3 grid((unsigned)(a.B * cblocks)), block(kThreads);
     switch (a.K) {
     case 2: hipLaunchKernelGGL((causal_step<T, 2>), grid, block, 0, a.stream, a, (int)cblocks); break;
     case 3: hipLaunchKernelGGL((causal_step<T, 3>), grid, block, 0, a.stream, a, (int)cblocks); break;
@@ -605,6 +628,13 @@ template <typename T> hipError_t run_step(const CausalStepArgs &a)
 }
 
 }  // namespace
+
+bool causal_fits(const CausalArgs &a) { return grid_fits(plan_fwd(a).blocks, kThreads); }
+bool causal_bwd_fits(const CausalArgs &a)
+{
+    return grid_fits(8 * ceil_div(plan_bwd(a).blocks, 8), kThreads) && grid_fits(reduce_blocks(a), 1024);
+}
+bool causal_step_fits(const CausalStepArgs &a) { return grid_fits(a.B * step_cblocks(a), kThreads); }
 
 hipError_t launch_causal(const CausalArgs &a, const char **kname)
 {

@@ -446,7 +446,30 @@ rms_bwd_reduce(const float *__restrict__ ws, T *__restrict__ dw, int64_t C, int 
     if (slice == 0 && c < C) dw[c] = from_f32<T>(s);
 }
 
-template <typename T, int TPR, int NV> hipError_t run_rows(const RmsArgs &a)
+// A launch of more than 2^32 - 1 threads would silently lose some: rows go in pieces that fit.
+// one(piece) launches the rows of `piece`.
+int64_t rows_of_launch(int rows_each, int threads) { return ((int64_t(1) << 32) - 1) / threads * rows_each; }
+
+template <typename T, typename F> hipError_t in_pieces(const RmsArgs &a, int64_t most, F one)
+{
+    const int64_t nb = a.block ? ceil_div(a.C, a.block) : 1;
+    for (int64_t r = 0; r < a.rows; r += most) {
+        RmsArgs p = a;
+        p.rows = std::min(most, a.rows - r);
+        p.x = (const T *)a.x + r * a.xs;
+        if (a.residual) {
+            p.residual = (const T *)a.residual + r * a.rs;
+            p.h = (T *)a.h + r * a.C;
+        }
+        p.y = (char *)a.y + r * a.C * (a.scales ? 1 : (int64_t)sizeof(T));
+        if (a.scales) p.scales = a.scales + r * nb;
+        const hipError_t err = one(p);
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+}
+
+template <typename T, int TPR, int NV> hipError_t run_some_rows(const RmsArgs &a)
 {
     constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
     const dim3 grid((unsigned)ceil_div(a.rows, RPW)), block(TPR < 256 ? 256 : TPR);
@@ -458,6 +481,12 @@ template <typename T, int TPR, int NV> hipError_t run_rows(const RmsArgs &a)
         else hipLaunchKernelGGL((rms_norm_rows<T, TPR, NV, false, false>), grid, block, 0, a.stream, a);
     }
     return hipGetLastError();
+}
+
+template <typename T, int TPR, int NV> hipError_t run_rows(const RmsArgs &a)
+{
+    constexpr int NT = TPR < 256 ? 256 : TPR;
+    return in_pieces<T>(a, rows_of_launch(NT / TPR, NT), run_some_rows<T, TPR, NV>);
 }
 
 template <typename T> hipError_t run_norm(const RmsArgs &a, const char **kname)
@@ -472,17 +501,21 @@ template <typename T> hipError_t run_norm(const RmsArgs &a, const char **kname)
     if (a.C <= 8192) return run_rows<T, 1024, X>(a);
     if (a.C <= 16384) return run_rows<T, 1024, 2 * X>(a);
     *kname = "rms_norm_long";
-    const dim3 grid((unsigned)a.rows), block(1024);
-    if (a.scales) hipLaunchKernelGGL((rms_norm_long<T, true>), grid, block, 0, a.stream, a);
-    else hipLaunchKernelGGL((rms_norm_long<T, false>), grid, block, 0, a.stream, a);
-    return hipGetLastError();
+    return in_pieces<T>(a, rows_of_launch(1, 1024), [](const RmsArgs &p) {
+        const dim3 grid((unsigned)p.rows), block(1024);
+        if (p.scales) hipLaunchKernelGGL((rms_norm_long<T, true>), grid, block, 0, p.stream, p);
+        else hipLaunchKernelGGL((rms_norm_long<T, false>), grid, block, 0, p.stream, p);
+        return hipGetLastError();
+    });
 }
 
 // Rows of partial weight gradients a call makes.
 int bwd_groups(int64_t rows, int64_t C)
 {
     const int64_t rpw = C <= 128 ? 16 : C <= 512 ? 4 : 1;
-    return (int)std::min<int64_t>(ceil_div(rows, rpw), kBwdGroups);
+    // Past 16384 columns a launch has a thread for each of a group's columns: fewer groups from 2^22 columns on.
+    const int64_t most = ((int64_t(1) << 32) - 1) / (256 * ceil_div(C, 256));
+    return (int)std::min<int64_t>({ceil_div(rows, rpw), kBwdGroups, most});
 }
 
 template <typename T, int TPR, int NV> hipError_t run_bwd_rows(const RmsBwdArgs &a, int groups)
@@ -507,8 +540,17 @@ template <typename T> hipError_t run_bwd(const RmsBwdArgs &a, const char **kname
         else {
             *kname = "rms_bwd_long";
             float *rs = a.ws + (int64_t)groups * a.C;
-            hipLaunchKernelGGL((rms_bwd_long<T>), dim3((unsigned)a.rows), dim3(1024), 0, a.stream, a, rs);
-            if ((err = hipGetLastError()) != hipSuccess) return err;
+            const int64_t most = rows_of_launch(1, 1024);
+            for (int64_t r = 0; r < a.rows; r += most) {
+                RmsBwdArgs p = a;
+                p.dy = (const T *)a.dy + r * a.dys;
+                p.h = (const T *)a.h + r * a.hs;
+                if (a.dh) p.dh = (const T *)a.dh + r * a.dhs;
+                p.dx = (T *)a.dx + r * a.C;
+                hipLaunchKernelGGL((rms_bwd_long<T>), dim3((unsigned)std::min(most, a.rows - r)), dim3(1024), 0, a.stream,
+                                   p, rs + r);
+                if ((err = hipGetLastError()) != hipSuccess) return err;
+            }
             hipLaunchKernelGGL((rms_bwd_long_dw<T>), dim3((unsigned)(ceil_div(a.C, 256) * groups)), dim3(256), 0,
                                a.stream, a, rs, groups);
             err = hipGetLastError();

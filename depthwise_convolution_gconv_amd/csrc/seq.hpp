@@ -43,8 +43,11 @@ struct CausalArgs {
     int dtype;
     hipStream_t stream;
 };
+// (fits: whether the launches of a call take it)
+bool causal_fits(const CausalArgs &a);
 hipError_t launch_causal(const CausalArgs &a, const char **kname);
 size_t causal_bwd_workspace(int64_t B, int64_t T, int64_t C, int64_t K);
+bool causal_bwd_fits(const CausalArgs &a);
 hipError_t launch_causal_bwd(const CausalArgs &a, const char **kname);
 
 struct CausalStepArgs {
@@ -56,6 +59,7 @@ struct CausalStepArgs {
     int dtype;
     hipStream_t stream;
 };
+bool causal_step_fits(const CausalStepArgs &a);
 hipError_t launch_causal_step(const CausalStepArgs &a, const char **kname);
 
 // The thread's error text and last kernel name, held by api.cpp.
@@ -63,7 +67,6 @@ void set_last_error(const char *text);
 void set_last_kernel(const char *name);
 
 constexpr int kCausalMaxK = 64;
-// Largest number of rows a launch's grid takes.
-constexpr int64_t kGridMax = (int64_t(1) << 31) - 1;
+constexpr int64_t kNormMaxRows = (int64_t(1) << 31) - 1;
 
 }  // namespace gconv

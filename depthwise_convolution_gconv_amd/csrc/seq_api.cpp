@@ -460,7 +460,7 @@ static gconv_status_t norm_check(int64_t rows, int64_t C, const int64_t *strides
     if (bad_dtype(dtype)) return fail(GCONV_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
     if (rows < 0 || C < 1) return fail(GCONV_ERR_INVALID_ARG, "RMS norm: rows >= 0 and C >= 1 are needed");
     if (!(eps >= 0.0f)) return fail(GCONV_ERR_INVALID_ARG, "RMS norm: eps must be >= 0");
-    if (C > int64_t(1) << 24 || rows > gconv::kGridMax)
+    if (C > int64_t(1) << 24 || rows > gconv::kNormMaxRows)
         return fail(GCONV_ERR_UNSUPPORTED, "RMS norm: at most 2^24 columns and 2^31 - 1 rows");
     return ns ? check_strides(strides, ns) : GCONV_OK;
 }
@@ -553,6 +553,8 @@ gconv_status_t gconv_rms_norm_backward(const void *dy, const void *h, const void
 
 // ---------------------------------------------------------------- causal depthwise conv1d
 
+static const char kTooManyThreads[] = "causal conv1d: the call needs more threads than a launch takes";
+
 static gconv_status_t causal_shape(int64_t B, int64_t T, int64_t C, int64_t K, gconv_act_t act, gconv_dtype_t dtype)
 {
     if (bad_dtype(dtype)) return fail(GCONV_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
@@ -597,6 +599,7 @@ gconv_status_t gconv_dw1d_causal(const void *x, const void *w, const void *bias,
     a.B = B; a.T = T; a.C = C; a.K = K; a.xsb = strides[0]; a.xst = strides[1];
     a.silu = activation == GCONV_ACT_SILU;
     a.dtype = (int)dtype; a.stream = (hipStream_t)hip_stream;
+    if (!gconv::causal_fits(a)) return fail(GCONV_ERR_UNSUPPORTED, kTooManyThreads);
     const char *kname = "";
     const hipError_t err = gconv::launch_causal(a, &kname);
     return done(err, kname);
@@ -650,6 +653,7 @@ gconv_status_t gconv_dw1d_causal_backward(const void *x, const void *w, const vo
     a.B = B; a.T = T; a.C = C; a.K = K; a.xsb = strides[0]; a.xst = strides[1]; a.dysb = strides[2]; a.dyst = strides[3];
     a.silu = activation == GCONV_ACT_SILU;
     a.dtype = (int)dtype; a.stream = (hipStream_t)hip_stream;
+    if (!gconv::causal_bwd_fits(a)) return fail(GCONV_ERR_UNSUPPORTED, kTooManyThreads);
     const char *kname = "";
     const hipError_t err = gconv::launch_causal_bwd(a, &kname);
     return done(err, kname);
@@ -687,6 +691,7 @@ gconv_status_t gconv_dw1d_causal_step(const void *x, const void *w, const void *
     a.x = x; a.w = w; a.bias = bias; a.y = y; a.state = state; a.slots = slots;
     a.B = B; a.C = C; a.K = K; a.n = n; a.xsb = x_stride; a.silu = activation == GCONV_ACT_SILU;
     a.dtype = (int)dtype; a.stream = (hipStream_t)hip_stream;
+    if (!gconv::causal_step_fits(a)) return fail(GCONV_ERR_UNSUPPORTED, kTooManyThreads);
     const char *kname = "";
     const hipError_t err = gconv::launch_causal_step(a, &kname);
     return done(err, kname);

@@ -80,3 +80,22 @@ def test_attention_refuses_more_threads_than_a_launch_takes():
     assert attn((1 << 23, 0, 1, 1, 256, 256), 2, FAR[6]) == UNSUPPORTED
     # One head less than 2^32 threads need is taken.
     assert L.gconv_linear_attention_workspace(arr((1 << 23) - 8, 1, 1, 1, 256, 256), 2, 0, ctypes.byref(n)) == 0
+
+
+def test_conv_refuses_more_threads_than_a_launch_takes():
+    L = S._library()
+
+    def conv(B, T, C, K, dtype=1):
+        return L.gconv_dw1d_causal(FAR[0], FAR[1], 0, FAR[2], 0, 0, 0, arr(B, T, C, K), arr(T * C, C), 0, dtype, None)
+
+    def bwd(B, T, C, K):
+        return L.gconv_dw1d_causal_backward(FAR[0], FAR[1], 0, FAR[2], 0, 0, FAR[3], FAR[4], 0, 0, 0, arr(B, T, C, K),
+                                            arr(T * C, C, T * C, C), 0, 1, FAR[5], 1 << 50, None)
+
+    def step(B, C, K):
+        return L.gconv_dw1d_causal_step(FAR[0], FAR[1], 0, FAR[2], FAR[3], FAR[4], arr(B, C, K, 5), C, 0, 1, None)
+
+    for call in (lambda: conv(1 << 24, 1, 1, 4), lambda: conv(1 << 24, 1, 1, 9), lambda: conv(1 << 12, 1 << 18, 64, 5),
+                 lambda: bwd(1 << 24, 1, 1, 4), lambda: bwd(1, 1, 1 << 23, 64), lambda: step(1 << 24, 1, 4),
+                 lambda: step(1 << 23, 1025, 4)):
+        assert call() == UNSUPPORTED and "threads" in gc.gconv_last_error()

@@ -280,3 +280,44 @@ def test_shares_of_value_heads_past_a_launch(much_memory):
     assert bool((dq[0, 16:] == 4.0).all()) and bool((dk[0, :-16] == 4.0).all())
     assert bool((dq[0, 0] == 2.0).all()) and bool((dk[0, -1] == 2.0).all())
     assert bool((dv[0, :-16] == 2.0 * D).all())
+
+
+def test_norm_of_more_rows_than_a_launch_takes(much_memory):
+    # 16 rows of one column share a workgroup: 2^28 rows are 2^32 threads.  A row of one value has
+    # itself as its norm: y is its sign, h twice the value, and the scale of 448 is |y| / 448.
+    rows = 2 ** 28 + 5
+    x = torch.ones(rows, 1, dtype=torch.float16, device="cuda")
+    x[::3] = -1.5
+    x[-1] = 0.0
+    w = torch.ones(1, dtype=torch.float16, device="cuda")
+    y, h = gc.rms_norm(x, w, residual=x)
+    assert torch.equal(y, x.sign()) and torch.equal(h, 2 * x)
+    del y, h
+    q, s, h = gc.rms_norm_e4m3(x, w, residual=x)
+    assert torch.equal(h, 2 * x)
+    del h
+    sign = x.sign()
+    assert torch.equal(q.to(torch.float16), 448.0 * sign)
+    # The root and the quotient are one rounding each, eps 1e-6 / 8 of a value of 2 at most.
+    assert bool(((s[:-1] * 448.0 - 1.0).abs() <= 1.3e-7 + 6 * U32).all()) and float(s[-1]) == float(torch.tensor(2.0 ** -100) / 448.0)
+
+
+def test_norm_gradient_of_more_rows_and_columns_than_a_launch_takes(much_memory):
+    # Rows past 16384 columns take 1024 threads each: 2^22 rows are 2^32 threads (dx of 137 GB, from
+    # one row at stride 0).
+    rows, C = 2 ** 22 + 3, 16385
+    w = torch.ones(C, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator().manual_seed(9)
+    dy, h = (torch.randn(1, C, generator=gen).bfloat16().cuda() for _ in range(2))
+    first, _ = gc.rms_norm_backward(dy, h, w)
+    if torch.cuda.mem_get_info()[0] > 160 << 30:
+        dx, _ = gc.rms_norm_backward(dy.expand(rows, C), h.expand(rows, C), w)
+        for r in range(0, rows, 1 << 19):
+            assert bool((dx[r:r + (1 << 19)] == first).all()), r
+        del dx
+        torch.cuda.empty_cache()
+    # 2^22 columns in 1024 rows of partial sums are 2^32 threads.
+    rows, C = 1024, 2 ** 22
+    one = torch.ones(1, 1, dtype=torch.bfloat16, device="cuda").expand(1, C).contiguous()
+    dx, dw = gc.rms_norm_backward(one.expand(rows, C), one.expand(rows, C), one[0])
+    assert bool((dw == 1024.0).all()) and bool((dx.abs() <= 2e-6).all())
