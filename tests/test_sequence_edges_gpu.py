@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import depthwise_convolution_gconv_amd as gc
-from test_sequence_gpu import DT, U32, attn_def, attn_inputs, near, rounding
+from test_sequence_gpu import DT, U32, attn_def, attn_inputs, bounds, near, near_norm, rounding
 
 pytestmark = pytest.mark.gpu
 
@@ -321,3 +321,138 @@ def test_norm_gradient_of_more_rows_and_columns_than_a_launch_takes(much_memory)
     one = torch.ones(1, 1, dtype=torch.bfloat16, device="cuda").expand(1, C).contiguous()
     dx, dw = gc.rms_norm_backward(one.expand(rows, C), one.expand(rows, C), one[0])
     assert bool((dw == 1024.0).all()) and bool((dx.abs() <= 2e-6).all())
+
+
+# ---------------------------------------------------------------- joined segments
+
+def grads_def(leaves, g, scale, n, do, ds):
+    o, s = attn_def(*leaves[:3], g, scale, leaves[3], n)
+    return [o.detach(), s.detach(), *torch.autograd.grad((o * do).sum() + (s * ds).sum(), leaves)]
+
+
+SEGMENTS = [  # B, T, H, Dk, Dv, lengths, segments: to eight the walks add the states up, past that a scan does
+    (1, 300, 1, 32, 32, None, 2),
+    (1, 1000, 1, 64, 64, None, 8),
+    (1, 1000, 2, 48, 96, [997], 8),
+    (1, 1100, 1, 64, 64, None, 9),
+    (2, 1150, 1, 40, 128, [1150, 500], 9),      # one ends segments before the last
+    (1, 2500, 1, 33, 20, [2449], 20),
+]
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("case", SEGMENTS, ids=lambda c: "x".join(map(str, c[:5])) + f"-{c[6]}")
+def test_segments_with_a_visible_carry(case, dt):
+    # A decay of -1e-3 leaves nine tenths of a state after a segment of 128 tokens.  Tolerances as in
+    # test_sequence_gpu.py.
+    B, T, H, Dk, Dv, lengths, segments = case
+    q, k, v, g, s0 = attn_inputs(B, T, H, H, Dk, Dv, DT[dt], 31, True, decay="-0.001")
+    n = lengths if lengths is not None else [T] * B
+    ln = torch.tensor(lengths, dtype=torch.int32).cuda() if lengths is not None else None
+    gen = torch.Generator().manual_seed(32)
+    do, ds = torch.randn(B, T, H, Dv, generator=gen).to(DT[dt]).cuda(), torch.randn(B, H, Dk, Dv, generator=gen).cuda()
+    one = -(-4 * B * H * segments * Dk * Dv // 256) * 256
+    shape = (B, T, H, H, Dk, Dv)
+    assert gc.linear_attention_workspace(shape, DT[dt]) == one
+    assert gc.linear_attention_workspace(shape, DT[dt], backward=True) == 3 * one
+    o, s = gc.linear_attention(q, k, v, g, initial_state=s0, lengths=ln, return_state=True)
+    got = gc.linear_attention_backward(q, k, v, g, do, initial_state=s0, lengths=ln, dstate=ds)
+    torch.cuda.synchronize()
+    ref, mag = (grads_def([fn(t).requires_grad_() for t in (q, k, v, s0)], g.cpu(), Dk ** -0.5, n, fn(do), fn(ds))
+                for fn in (lambda t: t.double().cpu(), lambda t: t.double().cpu().abs()))
+    f, fa, fs = bounds(DT[dt], T, max(Dk, Dv) + 1)
+    for name, y, r, m in zip(("o", "state", "dq", "dk", "dv", "dinitial"), (o, s, *got), ref, mag):
+        if y.dtype == torch.float32:
+            near(name, y, r, fs * m + (rounding(DT[dt], r) if dt == "f32" else 0.0))
+            near_norm(name, y, r, 1e-6)
+        else:
+            near(name, y, r, rounding(DT[dt], r) + fa * m)
+            near_norm(name, y, r, 2 * f)
+
+
+# ---------------------------------------------------------------- lengths, strides, threads
+
+def test_lengths_outside_their_range():
+    # Below 0 as 0, above T as T.
+    lengths, meant = (torch.tensor(x, dtype=torch.int32).cuda() for x in ([-5, 40, 1000, -2 ** 31, 2 ** 31 - 1],
+                                                                       [0, 40, 70, 0, 70]))
+    q, k, v, g, s0 = attn_inputs(5, 70, 1, 2, 40, 24, torch.bfloat16, 33, True)
+    x, w, c0 = torch.randn(5, 70, 48, device="cuda"), torch.randn(48, 1, 4, device="cuda"), torch.randn(5, 3, 48, device="cuda")
+    x9, w9, c9 = x, torch.randn(48, 1, 9, device="cuda"), torch.randn(5, 8, 48, device="cuda")
+
+    def run(ln):
+        return [*gc.linear_attention(q, k, v, g, initial_state=s0, lengths=ln, return_state=True),
+                *gc.linear_attention_backward(q, k, v, g, v, initial_state=s0, lengths=ln),
+                *gc.dwconv1d_causal(x, w, None, "silu", c0, ln, return_state=True),
+                *gc.dwconv1d_causal_backward(x, w, w[:, 0, 0].contiguous(), x, "silu", c0, ln, c0),
+                *gc.dwconv1d_causal(x9, w9, None, None, c9, ln, return_state=True),
+                *gc.dwconv1d_causal_backward(x9, w9, w[:, 0, 0].contiguous(), x9, None, c9, ln, c9)]
+
+    for i, (a, b) in enumerate(zip(run(lengths), run(meant))):
+        assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_strided_gradients_of_outputs(dt):
+    # Views of wider tensors against their copies, bit for bit: the same arithmetic on the same values.
+    gen = torch.Generator().manual_seed(34)
+    rnd = lambda *s: torch.randn(*s, generator=gen).to(DT[dt]).cuda()  # noqa: E731
+    q, k, v, g, s0 = attn_inputs(2, 90, 2, 4, 40, 37, DT[dt], 35, True)
+    for do in (rnd(2, 90, 4, 40)[..., 1:38], rnd(2, 4, 90, 37).transpose(1, 2), rnd(2, 1, 4, 37).expand(2, 90, 4, 37)):
+        a = gc.linear_attention_backward(q, k, v, g, do, initial_state=s0)
+        b = gc.linear_attention_backward(q, k, v, g, do.contiguous(), initial_state=s0)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    for K in (3, 9):
+        x, w, b0 = rnd(2, 90, 48), rnd(48, 1, K), rnd(48)
+        for dy in (rnd(2, 90, 53)[..., 2:50], rnd(90, 2, 48).transpose(0, 1), rnd(2, 1, 48).expand(2, 90, 48)):
+            a = gc.dwconv1d_causal_backward(x, w, b0, dy, "silu")[:3]
+            b = gc.dwconv1d_causal_backward(x, w, b0, dy.contiguous(), "silu")[:3]
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    for C in (37, 600, 3000, 9000, 17000):
+        dy, h, dh = (rnd(6, C + 5)[:, i:i + C] for i in (1, 2, 3))
+        w = rnd(C)
+        a = gc.rms_norm_backward(dy, h, w, dh=dh)
+        b = gc.rms_norm_backward(dy.contiguous(), h.contiguous(), w, dh=dh.contiguous())
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_two_host_threads():
+    # Each on a stream of its own, with calls that are refused in between: results and error texts
+    # are the thread's own.
+    import threading
+
+    sizes, out, errors = (96, 160), {}, []
+
+    def inputs(i):
+        q, k, v, g, s0 = attn_inputs(1, 300 + 50 * i, 1, 2, 64, 64, torch.bfloat16, 36 + i, True)
+        x = torch.randn(500, sizes[i], generator=torch.Generator().manual_seed(38 + i)).bfloat16().cuda()
+        return q, k, v, g, s0, x, torch.ones(sizes[i], device="cuda", dtype=torch.bfloat16)
+
+    def run(q, k, v, g, s0, x, w):
+        return [*gc.linear_attention(q, k, v, g, initial_state=s0, return_state=True),
+                *gc.linear_attention_backward(q, k, v, g, v, initial_state=s0),
+                *gc.rms_norm(x, w, residual=x), *gc.rms_norm_backward(x, x, w)]
+
+    ins = [inputs(i) for i in range(2)]
+    want = [run(*ins[i]) for i in range(2)]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    out[i] = run(*ins[i])
+                    with pytest.raises(gc.GconvError, match=f"{i + 17} columns a scale"):
+                        gc.rms_norm_e4m3(ins[i][5], ins[i][6], block=i + 17)
+                torch.cuda.current_stream().synchronize()
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(out[i], want[i]))
