@@ -93,6 +93,11 @@ hipError_t run_lin_walks_f32(const LinWalks &all, bool full);
 hipError_t run_lin_walks_f16(const LinWalks &all, bool full);
 hipError_t run_lin_walks_bf16(const LinWalks &all, bool full);
 
+// Workgroups of a walk (Da, Dc) for outputs that a compute unit holds at once.
+int lin_held_f32(int64_t Da, int64_t Dc);
+int lin_held_f16(int64_t Da, int64_t Dc);
+int lin_held_bf16(int64_t Da, int64_t Dc);
+
 // Up to this many segments, each walk adds up the local states before its own, and the last
 // one writes sf: a mean of half as many reads as there are segments, and no scan.
 constexpr int kFoldSegs = 8;

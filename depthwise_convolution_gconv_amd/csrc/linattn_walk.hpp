@@ -658,19 +658,39 @@ template <typename T, int DK, int NW, bool FULL> hipError_t run_walk_on(LinWalks
     return hipGetLastError();
 }
 
+// f of the kernel for a walk (Da, Dc).
+template <int DK_, int NW_> struct Kernel {
+    static constexpr int DK = DK_, NW = NW_;
+};
+template <typename T, typename F> auto on_kernel(int64_t Da, int64_t Dc, int dtype, F f)
+{
+    const int waves = lin_waves(Da, Dc, dtype);
+    switch (lin_wide(Da)) {
+    case 64: return waves == 2 ? f(Kernel<64, 2>{}) : f(Kernel<64, 4>{});
+    case 128: return waves == 2 ? f(Kernel<128, 2>{}) : f(Kernel<128, 4>{});
+    default:
+        if constexpr (kParts<T> < 3)
+            if (waves == 8) return f(Kernel<256, 8>{});
+        return f(Kernel<256, 4>{});
+    }
+}
+
 // The walks of `all` are alike.
 template <typename T, bool FULL> hipError_t run_walks(const LinWalks &all)
 {
     const LinWalk &p = all.w[0];
-    const bool two = lin_waves(p.Da, p.Dc, p.dtype) == 2;
-    switch (lin_wide(p.Da)) {
-    case 64: return two ? run_walk_on<T, 64, 2, FULL>(all) : run_walk_on<T, 64, 4, FULL>(all);
-    case 128: return two ? run_walk_on<T, 128, 2, FULL>(all) : run_walk_on<T, 128, 4, FULL>(all);
-    default:
-        if constexpr (kParts<T> < 3)
-            if (lin_waves(p.Da, p.Dc, p.dtype) == 8) return run_walk_on<T, 256, 8, FULL>(all);
-        return run_walk_on<T, 256, 4, FULL>(all);
-    }
+    return on_kernel<T>(p.Da, p.Dc, p.dtype, [&](auto k) { return run_walk_on<T, decltype(k)::DK, decltype(k)::NW, FULL>(all); });
+}
+
+// Workgroups of the outputs' kernel that a compute unit holds: by the registers it is built for
+// and by its LDS.
+template <typename T> int held_walks(int64_t Da, int64_t Dc, int dtype)
+{
+    return on_kernel<T>(Da, Dc, dtype, [](auto k) {
+        constexpr int DK = decltype(k)::DK, NW = decltype(k)::NW;
+        constexpr int regs = 4 * kWavesPerSimd<T, DK, NW> / NW, lds = 160 * 1024 / (int)sizeof(WalkLds<T, DK, NW, true>);
+        return regs < lds ? regs : lds;
+    });
 }
 
 }  // namespace

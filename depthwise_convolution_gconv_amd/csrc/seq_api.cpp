@@ -95,20 +95,25 @@ gconv_status_t check_strides(const int64_t *strides, int n)
     return GCONV_OK;
 }
 
-// Segments of a sequence: as many workgroups as the compute units hold at once, counted for
-// each launch of a call, while a segment keeps at least 2 chunks of 64 tokens (a cut sequence
-// reads two of its three inputs again, and every segment sets up its tables and reads a state).
-// Measured with 16 heads of 128 over 65536 tokens in bf16: 508 us with 16 segments, 398 with
-// 47, 453 with 64.
+// Segments of a sequence: as many workgroups as the 256 compute units hold at once of the
+// outputs' kernel, counted for each launch of a call, while a segment keeps at least 2 chunks of
+// 64 tokens (a cut sequence reads two of its three inputs again, and every segment sets up its
+// tables and reads a state).  16 heads over 32768 tokens with as many workgroups as are held, and
+// with a half more or less: fp16, 64 x 64 (1024): 138 us, 178 with 1536, 161 with 768; fp16, 64 x
+// 128 (512): 236, 259 with 768, 321 with 256; fp32, 64 x 128 (512): 351, 396, 431; fp32, 128 x 64
+// (512): 384, 455, 639; fp32, 64 x 64 (768): 230, 260 with 1024, 293 with 512; bf16, 128 x 128
+// (768): 233, 272 with 1024, 238 with 512; bf16, 64 x 64 (1536): 107, 96 with 1024, 105 with 768.
+// At least 64, 128 and 192 tokens in a segment: 16 heads of 128 over 2048 tokens in bf16 48, 44
+// and 63 us, 8 heads of 64 over 1024, gradients, 31, 29 and 36; 12 heads of 96 x 80 over 5 x 1021
+// in fp16 70, 68 and 68; few heads over few tokens gain from 64 (4 heads of 128 over 2 x 700: 32,
+// 38 and 44 us).
 constexpr int64_t kChunk = 64;
 
-// Workgroups that the 256 compute units hold of the kernel for a walk (Da, Dc), by its
-// registers and LDS.
 int64_t lin_slots(int64_t Da, int64_t Dc, gconv_dtype_t dtype)
 {
-    if (Da > 128) return dtype == GCONV_BF16 && gconv::lin_waves(Da, Dc, (int)dtype) == 4 ? 512 : 256;
-    if (Da > 64) return dtype == GCONV_F32 ? 256 : dtype == GCONV_F16 ? 512 : 768;
-    return 768;
+    return 256 * (dtype == GCONV_F32   ? gconv::lin_held_f32(Da, Dc)
+                  : dtype == GCONV_F16 ? gconv::lin_held_f16(Da, Dc)
+                                       : gconv::lin_held_bf16(Da, Dc));
 }
 
 void lin_segments(const LinShape &s, bool backward, gconv_dtype_t dtype, int32_t *nseg, int32_t *seg_len)
