@@ -203,7 +203,9 @@ def linear_attention_backward(q, k, v, log_decay, do, scale: Optional[float] = N
                               lengths=None, dstate=None, stream=None):
     """(dq, dk, dv, dinitial) of linear_attention from the gradients `do` of its output and
     `dstate` (fp32, or None: zero) of its final state.  dinitial is None without an
-    initial_state.  log_decay is a constant: it gets no gradient.  Precision as forward."""
+    initial_state.  log_decay is a constant: it gets no gradient.  Precision as forward; a value
+    that is not finite reaches the tokens that the formulas name (of q and do: its own and
+    earlier ones)."""
     if stream is not None:
         return _on_stream(stream, q, linear_attention_backward, q, k, v, log_decay, do, scale, initial_state, lengths, dstate)
     dt, shape, strides, g, n = _attn_args(q, k, v, log_decay, lengths)

@@ -16,9 +16,9 @@
 // causal_bwd_tile<T, NT>: one tile of the gradients, 32 channels x 64 tokens: z is computed
 //   again, dz = dy act'(z) goes to LDS with the K-1 rows behind the tile, then dx is the
 //   correlation of dz with the reversed taps and dw, db are the tile's sums, which a second
-//   kernel adds over the tiles in a fixed order.  Bound by vector instructions: 27 us for
-//   8 x 1024 x 512 in fp32 with 31 taps (about 1500 a wave, 950 of them the products; 50 MB
-//   take 10 us).  64 channels a tile, two workgroups a compute unit, took 41 us.
+//   kernel adds over the tiles in a fixed order.  Bound by vector instructions: 32 us by kernel
+//   trace, and 4 for the sum, for 8 x 1024 x 512 in fp32 with 31 taps (about 1500 a wave, 950 of
+//   them the products; 50 MB take 8 us).  64 channels a tile, two workgroups a compute unit, took 41 us.
 // causal_step<T, KS>: one token; the state moves up by one row in place.
 #include <algorithm>
 

@@ -87,9 +87,9 @@ lin_group_sum(const float *__restrict__ part, T *__restrict__ out, int64_t sb, i
 // partial sums of o are added in a fixed order through LDS.
 //
 // Many heads: more waves beat more rows in flight (256 sequences x 16 heads of 128 x 128, 537
-// MB: 114 us with 8 rows, 105 with 4, 97 with 2, 5.5 TB/s where a copy takes 5.1).  Up to
-// a head a compute unit, and more than 8 rows a thread: four times the threads and twice the
-// rows in flight (6 heads of 178 x 225: 19 us became 9.7, 16 of 128 x 128: 7.4 became 5.9; 8 of
+// MB: 114 us with 8 rows, 105 with 4, 97 with 2, 5.6 TB/s where a streaming copy reaches 6.5).
+// Up to a head a compute unit, and more than 8 rows a thread: four times the threads and twice
+// the rows in flight (6 heads of 178 x 225: 19 us became 9.7, 16 of 128 x 128: 7.4 became 5.9; 8 of
 // 64 x 64: 4.4 would be 5.4).
 template <typename T, int CG, int NT, int U>
 __global__ void __launch_bounds__(NT)

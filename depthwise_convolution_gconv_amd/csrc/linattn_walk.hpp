@@ -33,15 +33,16 @@
 // accumulators for the whole walk.
 //
 // What bounds it (bf16, 128 x 128 heads): HBM, and beside it the products.  65536 tokens x 16
-// heads take 432 us: 1.07 GB for the outputs' walk, 0.54 GB for the local states', and the scan.
-// One part for the scores and the state that meets a_i would take 390 us, with 2.4e-3 of error
-// beside the 1.7e-3 of the outputs' own rounding; the gradients of 4 x 4096 tokens x 16 heads
-// would take 249 us instead of 284.  32 tokens rather than 64: half the registers for what is on
+// heads take 442 us: 1.07 GB for the outputs' walk, 0.54 GB for the local states', and the scan.
+// One part for the scores and the state that meets a_i took 390 us where two took 432, with
+// 2.4e-3 of error beside the 1.7e-3 of the outputs' own rounding, and 249 instead of 284 us for
+// the gradients of 4 x 4096 tokens x 16 heads; the scale in 64 bits and the search for values that
+// are not finite took the rest.  32 tokens rather than 64: half the registers for what is on
 // its way, so three workgroups on a compute unit instead of two, and no off-diagonal tile of
 // scores (504 -> 486 us, and 447 with the segments that three workgroups call for, all with one
 // part).  Two parts instead of three in the update took 403 instead of 421 us and left the state
 // with 2.5e-6 of error instead of 1e-7.  fp16 and fp32 pay for their parts (3 and 6 products for
-// one) and are bound by those: 39 us for 5 x 1021 tokens x 12 heads of 96 x 80 in fp16, 62 us for
+// one) and are bound by those: 40 us for 5 x 1021 tokens x 12 heads of 96 x 80 in fp16, 67 us for
 // the three walks of 8 x 1024 tokens x 8 heads of 64 in fp32.
 #pragma once
 
