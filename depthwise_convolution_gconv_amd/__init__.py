@@ -34,6 +34,12 @@ from ._binding import (  # noqa: F401
     lib,
     lib_path,
 )
+from ._block import (  # noqa: F401
+    gated_recurrence,
+    gated_recurrence_backward,
+    gated_recurrence_step,
+    gated_recurrence_workspace,
+)
 from ._sequence import (  # noqa: F401
     dwconv1d_causal,
     dwconv1d_causal_backward,

@@ -33,6 +33,8 @@ EXPORTS = ("gconv_out_shape", "gconv_select_route", "gconv_fwd", "gconv_fwd_rout
            "gconv_linear_attention_step", "gconv_rms_norm", "gconv_rms_norm_e4m3",
            "gconv_rms_norm_backward_workspace", "gconv_rms_norm_backward", "gconv_dw1d_causal",
            "gconv_dw1d_causal_backward_workspace", "gconv_dw1d_causal_backward", "gconv_dw1d_causal_step",
+           "gconv_gated_recurrence_workspace", "gconv_gated_recurrence", "gconv_gated_recurrence_backward",
+           "gconv_gated_recurrence_step",
            "gconv_last_kernel", "gconv_status_string", "gconv_last_error")
 
 _i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p

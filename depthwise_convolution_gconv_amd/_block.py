@@ -1,0 +1,144 @@
+"""Operators of a recurrent mixing block in libgconv.so: the gated linear recurrence.
+
+Argument checks and marshalling only, in the manner of the other sequence operators: the
+caller's current device and stream, or `stream`; outputs and workspaces from torch.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from ._binding import DTYPES, _check, _i32, _i64, _i64p, _vp, lib
+from ._sequence import (_array, _bad, _device, _dtype, _like, _on_stream, _ptr, _raw_stream, _size, _view, _whole,
+                        _workspace)
+
+_fns = None
+
+
+def _library():
+    """The entry points with their argument types set."""
+    global _fns
+    if _fns is None:
+        L = lib()
+        sizep = ctypes.POINTER(_size)
+        for name, args in {
+            "gconv_gated_recurrence_workspace": [_i64p, _i32, _i32, sizep],
+            "gconv_gated_recurrence": [_vp] * 5 + [_i64p, _i64p] + [_vp] * 3 + [_i32, _vp, _size, _vp],
+            "gconv_gated_recurrence_backward": [_vp] * 10 + [_i64p, _i64p] + [_vp] * 4 + [_i32, _vp, _size, _vp],
+            "gconv_gated_recurrence_step": [_vp] * 6 + [_i64p, _i64p, _vp, _i32, _vp],
+        }.items():
+            fn = getattr(L, name)
+            fn.argtypes = args
+            fn.restype = _i32
+        _fns = L
+    return _fns
+
+
+# ---------------------------------------------------------------- gated recurrence
+
+def _gated_args(x, r, i, log_decay, lengths, dims):
+    dt = _dtype("x", x)
+    if x.dim() != dims:
+        _bad("x, r and i must be [B, T, C]" if dims == 3 else "x, r and i must be [B, C]")
+    dtype, dev, shape = x.dtype, x.get_device(), x.shape
+    st = (*_view("x", x, dtype, dev, shape)[:-1], *_view("r", r, dtype, dev, shape)[:-1],
+          *_view("i", i, dtype, dev, shape)[:-1])
+    g = _whole("log_decay", log_decay, torch.float32, dev, (shape[-1],))
+    if not g and shape[-1]:
+        _bad("log_decay is needed")
+    return dt, dev, st, g, _whole("lengths", lengths, torch.int32, dev, (shape[0],))
+
+
+def gated_recurrence_workspace(shape, dtype: torch.dtype, backward: bool = False) -> int:
+    """Workspace bytes of gated_recurrence (or its backward) for shape (B, T, C)."""
+    n = _size(0)
+    _check(_library().gconv_gated_recurrence_workspace(_array(*shape), DTYPES[dtype], int(backward), ctypes.byref(n)))
+    return n.value
+
+
+def gated_recurrence(x, r, i, log_decay, initial_state=None, lengths=None, return_state: bool = False, stream=None):
+    """Gated linear recurrence over whole prompts, each channel by itself.
+
+        a_t = exp(log_decay * sigmoid(r_t)),   h_t = a_t h_(t-1) + sqrt(1 - a_t^2) sigmoid(i_t) x_t
+
+    x and the logits r, i of its gates [B, T, C], any strides but contiguous channels; log_decay
+    fp32 [C], finite and <= 0.  initial_state: fp32 [B, C].  lengths: int32 [B], the tokens of each
+    sequence that exist; the outputs of the others are zero.  Returns h [B, T, C], or (h, state)
+    with the fp32 state after each sequence's last token, which gated_recurrence_step carries on
+    from.
+
+    Gates, sums and states are fp32.  A value that is not finite reaches its own and later tokens
+    of its channel only; an infinity may count as NaN in later ones."""
+    if stream is not None:
+        return _on_stream(stream, x, gated_recurrence, x, r, i, log_decay, initial_state, lengths, return_state)
+    dt, dev, strides, g, n = _gated_args(x, r, i, log_decay, lengths, 3)
+    B, T, C = x.shape
+    s0 = _whole("initial_state", initial_state, torch.float32, dev, (B, C))
+    sh = _array(B, T, C)
+    need = _size(0)
+    L = _library()
+    _check(L.gconv_gated_recurrence_workspace(sh, dt, 0, ctypes.byref(need)))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return gated_recurrence(x, r, i, log_decay, initial_state, lengths, return_state)
+    h = _like(x)
+    st = x.new_empty((B, C), dtype=torch.float32) if return_state else None
+    ws = _workspace(need.value, x)
+    _check(L.gconv_gated_recurrence(x.data_ptr(), r.data_ptr(), i.data_ptr(), g, h.data_ptr(), sh, _array(*strides), s0,
+                                    _ptr(st), n, dt, _ptr(ws), need.value, _raw_stream(dev)))
+    return (h, st) if return_state else h
+
+
+def gated_recurrence_backward(x, r, i, log_decay, h, dh, initial_state=None, lengths=None, dstate=None, stream=None):
+    """(dx, dr, di, dlog_decay, dinitial) of gated_recurrence from its output h, the gradient dh of
+    that and dstate (fp32 [B, C], or None: zero) of its final state.  The states before each token
+    are taken from h as it was rounded.  dlog_decay is fp32 [C]; dinitial is None without an
+    initial_state.  Where 1 - a^2 is zero (log_decay zero, or a gate that underflows) the root is
+    taken to have no derivative."""
+    if stream is not None:
+        return _on_stream(stream, x, gated_recurrence_backward, x, r, i, log_decay, h, dh, initial_state, lengths, dstate)
+    dt, dev, strides, g, n = _gated_args(x, r, i, log_decay, lengths, 3)
+    B, T, C = x.shape
+    strides += (*_view("h", h, x.dtype, dev, x.shape)[:2], *_view("dh", dh, x.dtype, dev, x.shape)[:2])
+    s0 = _whole("initial_state", initial_state, torch.float32, dev, (B, C))
+    sf = _whole("dstate", dstate, torch.float32, dev, (B, C))
+    sh = _array(B, T, C)
+    need = _size(0)
+    L = _library()
+    _check(L.gconv_gated_recurrence_workspace(sh, dt, 1, ctypes.byref(need)))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return gated_recurrence_backward(x, r, i, log_decay, h, dh, initial_state, lengths, dstate)
+    dx, dr, di = _like(x), _like(r), _like(i)
+    dg = torch.empty_like(log_decay)
+    ds = x.new_empty((B, C), dtype=torch.float32) if initial_state is not None else None
+    ws = _workspace(need.value, x)
+    _check(L.gconv_gated_recurrence_backward(
+        x.data_ptr(), r.data_ptr(), i.data_ptr(), g, h.data_ptr(), dh.data_ptr(), dx.data_ptr(), dr.data_ptr(),
+        di.data_ptr(), dg.data_ptr(), sh, _array(*strides), s0, sf, _ptr(ds), n, dt, _ptr(ws), need.value,
+        _raw_stream(dev)))
+    return dx, dr, di, dg, ds
+
+
+def gated_recurrence_step(x, r, i, log_decay, state, slots=None, stream=None):
+    """The next token of each sequence: x, r, i [B, C]; state fp32 [n, C] is updated in place.
+    slots: int32 [B], the row of `state` that each sequence owns, each row at most once (default:
+    row b); a slot outside [0, n) leaves the pool alone and gives a zero output.  Returns h [B, C]."""
+    if stream is not None:
+        return _on_stream(stream, x, gated_recurrence_step, x, r, i, log_decay, state, slots)
+    dt, dev, strides, g, _ = _gated_args(x, r, i, log_decay, None, 2)
+    B, C = x.shape
+    if state.dim() != 2:
+        _bad("state must be [n, C]")
+    sp = _whole("state", state, torch.float32, dev, (state.shape[0], C))
+    sl = _whole("slots", slots, torch.int32, dev, (B,))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return gated_recurrence_step(x, r, i, log_decay, state, slots)
+    h = _like(x)
+    _check(_library().gconv_gated_recurrence_step(x.data_ptr(), r.data_ptr(), i.data_ptr(), g, sp, h.data_ptr(),
+                                                  _array(B, C, state.shape[0]), _array(*strides), sl, dt,
+                                                  _raw_stream(dev)))
+    return h

@@ -1,0 +1,55 @@
+// block.hpp -- host-validated calls of the recurrent block's operators: gated linear
+// recurrence, group norm with an activation, product in 8-bit integers.
+#pragma once
+
+#include "common.hpp"
+
+namespace gconv {
+
+// h_t = a_t h_(t-1) + sqrt(1 - a_t^2) sigmoid(i_t) x_t,  a_t = exp(log_decay sigmoid(r_t)).
+struct GatedArgs {
+    const void *x, *r, *i;               // [B][T][C], channels contiguous
+    const float *log_decay;              // [C]
+    const float *s0;                     // [B][C] or nullptr
+    const int32_t *lengths;              // [B] or nullptr: T
+    void *h;                             // forward: written; backward: read, [B][T][C] contiguous
+    float *sf;                           // final state or nullptr; backward: its gradient
+    const void *dh;                      // backward from here on
+    const float *dsf;                    // gradient of the final state or nullptr
+    void *dx, *dr, *di;                  // contiguous
+    float *ds0;                          // or nullptr
+    float *dlog;                         // [C]
+    int64_t B, T, C;
+    int64_t xsb, xst, rsb, rst, isb, ist, hsb, hst, dsb, dst;   // element strides: batch, token
+    float *ws;
+    int dtype;
+    hipStream_t stream;
+};
+// How a call is laid out over workgroups.
+struct GatedPlan {
+    int32_t lanes;                       // lanes that share a row, two channels each
+    int32_t waves;                       // of a workgroup
+    int32_t nseg;                        // segments of a sequence
+    int64_t seg_len;                     // tokens of a segment
+};
+GatedPlan gated_plan(int64_t B, int64_t T, int64_t C, int dtype, bool backward);
+size_t gated_workspace(const GatedPlan &g, int64_t B, int64_t C, bool backward);
+// Whether the launches and 32-bit offsets of a call take it.
+bool gated_fits(const GatedArgs &a, const GatedPlan &g, bool backward);
+hipError_t launch_gated(const GatedArgs &a, const GatedPlan &g, const char **kname);
+hipError_t launch_gated_bwd(const GatedArgs &a, const GatedPlan &g, const char **kname);
+
+struct GatedStepArgs {
+    const void *x, *r, *i;
+    const float *log_decay;
+    float *state;
+    void *h;
+    const int32_t *slots;
+    int64_t B, C, n, xs, rs, is;
+    int dtype;
+    hipStream_t stream;
+};
+bool gated_step_fits(const GatedStepArgs &a);
+hipError_t launch_gated_step(const GatedStepArgs &a, const char **kname);
+
+}  // namespace gconv

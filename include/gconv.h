@@ -389,6 +389,39 @@ gconv_status_t gconv_dw1d_causal_step(const void *x, const void *w, const void *
                                       const int32_t *slots, const int64_t *shape, int64_t x_stride,
                                       gconv_act_t activation, gconv_dtype_t dtype, void *hip_stream);
 
+/* Gated linear recurrence, each channel by itself.  shape = {B, T, C}: x and the logits r, i of
+ * its gates [B,T,C] (strides = {x batch, x token; r; i}, 6 values), h [B,T,C].  log_decay: fp32 [C]
+ * on the device, finite and <= 0.
+ *     a_t = exp(log_decay sigmoid(r_t)),   h_t = a_t h_(t-1) + sqrt(1 - a_t^2) sigmoid(i_t) x_t
+ * initial_state: fp32 [B,C] = h_(-1), or NULL (zero).  final_state: fp32 [B,C], or NULL: h after
+ * lengths[b] tokens, before its rounding.  A value of a real token that is not finite reaches its
+ * own and later tokens of its channel only; an infinity may count as NaN in later ones.  Token
+ * strides over about 2^20 elements are GCONV_ERR_UNSUPPORTED.  workspace:
+ * gconv_gated_recurrence_workspace bytes (may be 0), 16-byte aligned. */
+gconv_status_t gconv_gated_recurrence_workspace(const int64_t *shape, gconv_dtype_t dtype, int32_t backward,
+                                                size_t *bytes);
+gconv_status_t gconv_gated_recurrence(const void *x, const void *r, const void *i, const float *log_decay, void *h,
+                                      const int64_t *shape, const int64_t *strides, const float *initial_state,
+                                      float *final_state, const int32_t *lengths, gconv_dtype_t dtype,
+                                      void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/* Its gradients: dx, dr, di [B,T,C], dlog_decay [C] (fp32) and, if not NULL, dinitial [B,C] (fp32;
+ * only with initial_state) from h as the forward call wrote it, the gradient dh of h and dfinal
+ * (fp32 [B,C], or NULL: zero) of final_state.  strides = {x, r, i, h, dh: batch, token}, 10 values.
+ * Where 1 - a^2 is zero the root counts as having no derivative. */
+gconv_status_t gconv_gated_recurrence_backward(const void *x, const void *r, const void *i, const float *log_decay,
+                                               const void *h, const void *dh, void *dx, void *dr, void *di,
+                                               float *dlog_decay, const int64_t *shape, const int64_t *strides,
+                                               const float *initial_state, const float *dfinal, float *dinitial,
+                                               const int32_t *lengths, gconv_dtype_t dtype, void *workspace,
+                                               size_t workspace_bytes, void *hip_stream);
+
+/* One token for each sequence: shape = {B, C, n}; x, r, i [B,C] (strides: their rows), state fp32
+ * [n,C] updated in place, h [B,C]. */
+gconv_status_t gconv_gated_recurrence_step(const void *x, const void *r, const void *i, const float *log_decay,
+                                           float *state, void *h, const int64_t *shape, const int64_t *strides,
+                                           const int32_t *slots, gconv_dtype_t dtype, void *hip_stream);
+
 /* Name of the kernel the last successful gconv_fwd / gconv_fwd_route / gconv_fwd_ex /
  * gconv_dw1d_bwd_data / gconv_dw1d_bwd_filter call on this host thread launched
  * (the first of two for the filter gradient; "" before the first call or after
