@@ -23,73 +23,71 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// Two neighbouring channels as they are stored.
-template <typename T> struct Two {
-    typedef uint32_t raw;
-    typedef uint32_t mem __attribute__((aligned(2)));
-    typedef uint16_t one;
-};
-template <> struct Two<float> {
-    typedef uint2 raw;
-    typedef uint32_t mem __attribute__((ext_vector_type(2), aligned(4)));
-    typedef uint32_t one;
-};
+// A lane's channels: 8 bytes of a row.
+typedef uint32_t lane_mem __attribute__((ext_vector_type(2), aligned(2)));
+template <typename T> constexpr int lane_channels() { return 8 / (int)sizeof(T); }
 
-__device__ __forceinline__ uint32_t alone(uint32_t v, uint32_t) { return v; }
-__device__ __forceinline__ uint2 alone(uint32_t v, uint2) { return make_uint2(v, 0); }
-__device__ __forceinline__ uint32_t second(uint32_t w) { return w >> 16; }
-__device__ __forceinline__ uint2 second(uint2 w) { return make_uint2(w.y, 0); }
-
-// What a stripe of channels is: whole; the one that C ends in (a pair past the end is read from the
-// last pair that exists, its only channel from the second of that); the one channel of C = 1.
-enum { kWhole = 0, kEdge = 1, kSingle = 2 };
+// What a stripe of channels is: whole; the one that C ends in (a lane that reaches past the end
+// reads the last 8 bytes of the row and shifts them down); all of a row shorter than 8 bytes.
+enum { kWhole = 0, kEdge = 1, kShort = 2 };
 
 struct Cols {
     uint32_t at;           // byte offset that is read
     uint32_t to;           // and that is written
-    bool has_lo, has_hi;   // which of the two exist
+    int shift;             // bits by which what is read lies too high
+    int have;              // channels of the lane that exist
 };
 
 template <typename T, int MODE>
-__device__ __forceinline__ typename Two<T>::raw load2(const char *base, uint32_t row, const Cols &c)
+__device__ __forceinline__ uint2 load_lane(const char *base, uint32_t row, const Cols &c)
 {
-    typedef typename Two<T>::raw raw;
-    if constexpr (MODE == kSingle)
-        return alone(*reinterpret_cast<const typename Two<T>::one *>(base + (row + c.at)), raw{});
-    else
-        return __builtin_bit_cast(raw, *reinterpret_cast<const typename Two<T>::mem *>(base + (row + c.at)));
+    if constexpr (MODE == kShort) {
+        uint64_t w = 0;
+        for (int k = 0; k < c.have; ++k) {
+            if constexpr (sizeof(T) == 2)
+                w |= (uint64_t) * reinterpret_cast<const uint16_t *>(base + (row + c.at + 2 * k)) << 16 * k;
+            else
+                w |= (uint64_t) * reinterpret_cast<const uint32_t *>(base + (row + c.at + 4 * k)) << 32 * k;
+        }
+        return __builtin_bit_cast(uint2, w);
+    } else {
+        return __builtin_bit_cast(uint2, *reinterpret_cast<const lane_mem *>(base + (row + c.at)));
+    }
 }
 
-template <typename T> __device__ __forceinline__ void split2(uint32_t w, float (&f)[2])
+template <typename T, int MODE, int V>
+__device__ __forceinline__ void values(uint2 w, const Cols &c, float (&f)[V])
 {
-    f[0] = to_f32(__builtin_bit_cast(T, (uint16_t)w));
-    f[1] = to_f32(__builtin_bit_cast(T, (uint16_t)(w >> 16)));
-}
-template <> __device__ __forceinline__ void split2<__bf16>(uint32_t w, float (&f)[2])
-{
-    f[0] = __builtin_bit_cast(float, w << 16);
-    f[1] = __builtin_bit_cast(float, w & 0xffff0000u);
-}
-template <typename T> __device__ __forceinline__ void split2(uint2 w, float (&f)[2])
-{
-    f[0] = __builtin_bit_cast(float, w.x);
-    f[1] = __builtin_bit_cast(float, w.y);
-}
-template <typename T, int MODE, typename RAW> __device__ __forceinline__ void values(RAW w, const Cols &c, float (&f)[2])
-{
-    split2<T>(MODE == kEdge && !c.has_hi ? second(w) : w, f);
+    if constexpr (MODE == kEdge) w = __builtin_bit_cast(uint2, __builtin_bit_cast(uint64_t, w) >> c.shift);
+    if constexpr (sizeof(T) == 4) {
+        f[0] = __builtin_bit_cast(float, w.x);
+        f[1] = __builtin_bit_cast(float, w.y);
+    } else if constexpr (__is_same(T, __bf16)) {
+        f[0] = __builtin_bit_cast(float, w.x << 16);
+        f[1] = __builtin_bit_cast(float, w.x & 0xffff0000u);
+        f[2] = __builtin_bit_cast(float, w.y << 16);
+        f[3] = __builtin_bit_cast(float, w.y & 0xffff0000u);
+    } else {
+        typedef T quad __attribute__((ext_vector_type(4)));
+        const quad q = __builtin_bit_cast(quad, w);
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] = to_f32(q[k]);
+    }
 }
 
-template <typename T, int MODE>
-__device__ __forceinline__ void store2(char *base, uint32_t row, const Cols &c, float lo, float hi)
+template <typename T, int MODE, int V>
+__device__ __forceinline__ void store_lane(char *base, uint32_t row, const Cols &c, const float (&f)[V])
 {
     if constexpr (MODE != kWhole) {
-        if (c.has_lo) *reinterpret_cast<T *>(base + (row + c.to)) = from_f32<T>(lo);
-        if (c.has_hi) *reinterpret_cast<T *>(base + (row + c.to + (uint32_t)sizeof(T))) = from_f32<T>(hi);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (k < c.have) *reinterpret_cast<T *>(base + (row + c.to + k * (uint32_t)sizeof(T))) = from_f32<T>(f[k]);
     } else {
-        typedef T pair __attribute__((ext_vector_type(2)));
-        const pair v = {from_f32<T>(lo), from_f32<T>(hi)};
-        *reinterpret_cast<typename Two<T>::mem *>(base + (row + c.to)) = __builtin_bit_cast(typename Two<T>::mem, v);
+        typedef T vec __attribute__((ext_vector_type(V)));
+        vec v;
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = from_f32<T>(f[k]);
+        *reinterpret_cast<lane_mem *>(base + (row + c.to)) = __builtin_bit_cast(lane_mem, v);
     }
 }
 
@@ -114,8 +112,7 @@ __device__ __forceinline__ void decay(float l, float &a, float &m)
 }
 
 // Tokens of a lane's run: what fits in registers with the next tile's loads beside it.
-template <typename T> constexpr int run_len() { return sizeof(T) == 4 ? 4 : 8; }
-template <typename T> constexpr int run_len_bwd() { return sizeof(T) == 4 ? 2 : 4; }
+constexpr int kRun = 4, kRunBwd = 2;
 
 // A run's map joined with the one before it.
 __device__ __forceinline__ void join_maps(float &A, float &E, float Ab, float Eb)
@@ -126,22 +123,49 @@ __device__ __forceinline__ void join_maps(float &A, float &E, float Ab, float Eb
 
 // Maps of the runs of a wave (64 / LR of them, LR lanes each) -> the map before each run, and in
 // its last run's lanes that of the wave.
-template <int LR>
-__device__ __forceinline__ void scan_wave(int lane, float (&A)[2], float (&E)[2], float (&Ab)[2], float (&Eb)[2])
+template <int LR, int V>
+__device__ __forceinline__ void scan_wave(int lane, float (&A)[V], float (&E)[V], float (&Ab)[V], float (&Eb)[V])
 {
 #pragma unroll
     for (int d = LR; d < 64; d *= 2)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < V; ++k) {
             const float pa = __shfl_up(A[k], d), pe = __shfl_up(E[k], d);
             if (lane >= d) join_maps(A[k], E[k], pa, pe);
         }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < V; ++k) {
         const float pa = __shfl_up(A[k], LR), pe = __shfl_up(E[k], LR);
         Ab[k] = lane >= LR ? pa : 1.0f;
         Eb[k] = lane >= LR ? pe : 0.0f;
     }
+}
+
+// Maps of the waves of a tile, two channels in 16 bytes.
+template <int NW, int LR, int V> struct Maps { float4 m[V / 2][NW][LR]; };
+
+template <int NW, int LR, int V>
+__device__ __forceinline__ void put_maps(Maps<NW, LR, V> &to, int wave, int at, const float (&A)[V], const float (&E)[V])
+{
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) to.m[k][wave][at] = make_float4(A[2 * k], E[2 * k], A[2 * k + 1], E[2 * k + 1]);
+}
+
+// The state after the tile, and (h) that before the wave.
+template <int NW, int LR, int V>
+__device__ __forceinline__ void through_waves(const Maps<NW, LR, V> &maps, int wave, int at, float (&carry)[V], float (&h)[V])
+{
+    asm volatile("" : "+s"(wave));      // compared here, not once for all tiles in 2 NW scalar registers
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            const float4 m = maps.m[k / 2][w][at];
+            h[k] = w == wave ? carry[k] : h[k];
+            h[k + 1] = w == wave ? carry[k + 1] : h[k + 1];
+            carry[k] = fmaf(m.x, carry[k], m.y);
+            carry[k + 1] = fmaf(m.z, carry[k + 1], m.w);
+        }
 }
 
 struct Walk {
@@ -180,12 +204,14 @@ __device__ __forceinline__ int64_t live_tokens(const Walk &p, int64_t b)
 template <typename T, int LR>
 __device__ __forceinline__ Cols columns(const Walk &p, int ct, int lane, int64_t &c)
 {
-    c = (int64_t)ct * 2 * LR + 2 * (lane % LR);
+    constexpr int V = lane_channels<T>();
+    c = ((int64_t)ct * LR + lane % LR) * V;
+    const int64_t read = max((int64_t)0, min(c, p.C - V));
     Cols k;
-    k.has_lo = c < p.C;
-    k.has_hi = c + 1 < p.C;
+    k.have = (int)max((int64_t)0, min((int64_t)V, p.C - c));
     k.to = (uint32_t)(c * sizeof(T));
-    k.at = (uint32_t)(max((int64_t)0, min(c, p.C - 2)) * sizeof(T));
+    k.at = (uint32_t)(read * sizeof(T));
+    k.shift = 8 * (int)sizeof(T) * (int)min(c - read, (int64_t)(V - 1));
     return k;
 }
 
@@ -209,19 +235,20 @@ __device__ __forceinline__ float fold(const Walk &p, int64_t b, int seg, int64_t
 
 // ---------------------------------------------------------------- forward
 
-template <typename T, int L> struct RawIn { typename Two<T>::raw x[L], r[L], i[L]; };
+struct RawIn { uint2 x[kRun], r[kRun], i[kRun]; };
 
-template <typename T, int MODE, int L>
+// step: byte offsets of the lane's run in x, r and i.
+template <typename T, int MODE>
 __device__ __forceinline__ void load_in(const Walk &p, const char *const (&base)[3], int64_t t0, int64_t live, int run, int TS,
-                                        const uint32_t (&step)[3], const Cols &col, RawIn<T, L> &raw)
+                                        const uint32_t (&step)[3], const Cols &col, RawIn &raw)
 {
     const char *x = base[0] + t0 * p.xst, *r = base[1] + t0 * p.rst, *i = base[2] + t0 * p.ist;
     if (t0 + TS <= live) {
 #pragma unroll
-        for (int l = 0; l < L; ++l) {
-            raw.x[l] = load2<T, MODE>(x, step[0], col);
-            raw.r[l] = load2<T, MODE>(r, step[1], col);
-            raw.i[l] = load2<T, MODE>(i, step[2], col);
+        for (int l = 0; l < kRun; ++l) {
+            raw.x[l] = load_lane<T, MODE>(x, step[0], col);
+            raw.r[l] = load_lane<T, MODE>(r, step[1], col);
+            raw.i[l] = load_lane<T, MODE>(i, step[2], col);
             x += fresh(p.xst);
             r += fresh(p.rst);
             i += fresh(p.ist);
@@ -229,134 +256,136 @@ __device__ __forceinline__ void load_in(const Walk &p, const char *const (&base)
     } else {        // rows past the end are read from the last one
         const int last = (int)(live - 1 - t0);
 #pragma unroll
-        for (int l = 0; l < L; ++l) {
-            const uint32_t row = (uint32_t)min(run * L + l, last);
-            raw.x[l] = load2<T, MODE>(x, row * (uint32_t)p.xst, col);
-            raw.r[l] = load2<T, MODE>(r, row * (uint32_t)p.rst, col);
-            raw.i[l] = load2<T, MODE>(i, row * (uint32_t)p.ist, col);
+        for (int l = 0; l < kRun; ++l) {
+            const uint32_t row = (uint32_t)min(run * kRun + l, last);
+            raw.x[l] = load_lane<T, MODE>(x, row * (uint32_t)p.xst, col);
+            raw.r[l] = load_lane<T, MODE>(r, row * (uint32_t)p.rst, col);
+            raw.i[l] = load_lane<T, MODE>(i, row * (uint32_t)p.ist, col);
         }
     }
 }
 
-template <typename T, int MODE, int L>
-__device__ __forceinline__ void gates(const RawIn<T, L> &raw, const Cols &col, const float (&ld)[2], int live_rows, float (&a)[L][2], float (&u)[L][2])
+template <typename T, int MODE, int V>
+__device__ __forceinline__ void gates(const RawIn &raw, const Cols &col, const float (&ld)[V], int rows, float (&a)[kRun][V],
+                                      float (&u)[kRun][V])
 {
 #pragma unroll
-    for (int l = 0; l < L; ++l) {
-        float x[2], r[2], i[2];
+    for (int l = 0; l < kRun; ++l) {
+        float x[V], r[V], i[V];
         values<T, MODE>(raw.x[l], col, x);
         values<T, MODE>(raw.r[l], col, r);
         values<T, MODE>(raw.i[l], col, i);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < V; ++k) {
             float m;
             decay(ld[k] * sigmoid(r[k]), a[l][k], m);
             u[l][k] = __builtin_amdgcn_sqrtf(m) * (x[k] * sigmoid(i[k]));
         }
         __builtin_amdgcn_sched_barrier(0);      // one token after the other: temporaries of all at once do not fit
     }
-    if (live_rows < L)      // tokens that do not exist leave the state alone, whatever was read
+    if (rows < kRun)        // tokens that do not exist leave the state alone, whatever was read
 #pragma unroll
-        for (int l = 0; l < L; ++l)
+        for (int l = 0; l < kRun; ++l)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                a[l][k] = l < live_rows ? a[l][k] : 1.0f;
-                u[l][k] = l < live_rows ? u[l][k] : 0.0f;
+            for (int k = 0; k < V; ++k) {
+                a[l][k] = l < rows ? a[l][k] : 1.0f;
+                u[l][k] = l < rows ? u[l][k] : 0.0f;
             }
 }
 
 template <typename T, int LR, int NW, int MODE>
-__device__ __forceinline__ void walk_body(const Walk &p, int ct, int seg, int64_t b, float4 (*agg)[NW][LR])
+__device__ __forceinline__ void walk_body(const Walk &p, int ct, int seg, int64_t b, Maps<NW, LR, lane_channels<T>()> *maps)
 {
-    constexpr int RW = 64 / LR, L = run_len<T>(), TS = NW * RW * L;
+    constexpr int V = lane_channels<T>(), RW = 64 / LR, TS = NW * RW * kRun;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int run = wave * RW + lane / LR;
     int64_t c;
     const Cols col = columns<T, LR>(p, ct, lane, c);
     const int64_t n = live_tokens(p, b), begin = seg * p.seg_len, end = min(begin + p.seg_len, p.T), live = min(end, n);
     const char *const base[3] = {p.x + b * p.xsb, p.r + b * p.rsb, p.i + b * p.isb};
-    const uint32_t step[3] = {(uint32_t)(run * L * p.xst), (uint32_t)(run * L * p.rst), (uint32_t)(run * L * p.ist)};
-    const uint32_t hrow = (uint32_t)(p.C * sizeof(T));
+    const uint32_t step[3] = {(uint32_t)(run * kRun * p.xst), (uint32_t)(run * kRun * p.rst), (uint32_t)(run * kRun * p.ist)};
+    const uint32_t hrow = (uint32_t)(p.C * sizeof(T)), first = (uint32_t)(run * kRun) * hrow;
     char *const out = p.h + b * p.T * (int64_t)hrow;
 
-    RawIn<T, L> raw;
-    if (begin < live) load_in<T, MODE, L>(p, base, begin, live, run, TS, step, col, raw);
-    float ld[2], carry[2];
+    RawIn raw;
+    if (begin < live) load_in<T, MODE>(p, base, begin, live, run, TS, step, col, raw);
+    float ld[V], carry[V];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < V; ++k) {
         const int64_t ck = min(c + k, p.C - 1);
         ld[k] = p.log_decay[ck] * kLog2e;
         carry[k] = fold(p, b, seg, ck, p.s0 ? p.s0[b * p.C + ck] : 0.0f);
     }
     int buf = 0;
     for (int64_t t0 = begin; t0 < live; t0 += TS, buf ^= 1) {
-        RawIn<T, L> next;
-        if (t0 + TS < live) load_in<T, MODE, L>(p, base, t0 + TS, live, run, TS, step, col, next);
+        RawIn next;
+        if (t0 + TS < live) load_in<T, MODE>(p, base, t0 + TS, live, run, TS, step, col, next);
         const bool full = t0 + TS <= live;
-        const int rows = full ? L : (int)min((int64_t)L, max((int64_t)0, live - t0 - run * L));
-        float a[L][2], u[L][2];
-        gates<T, MODE, L>(raw, col, ld, rows, a, u);
-        float A[2] = {1.0f, 1.0f}, E[2] = {0.0f, 0.0f}, Ab[2], Eb[2];
+        const int rows = full ? kRun : (int)min((int64_t)kRun, max((int64_t)0, live - t0 - run * kRun));
+        float a[kRun][V], u[kRun][V], A[V], E[V], Ab[V], Eb[V], h[V];
+        gates<T, MODE>(raw, col, ld, rows, a, u);
 #pragma unroll
-        for (int l = 0; l < L; ++l)
+        for (int k = 0; k < V; ++k) {
+            A[k] = a[0][k];
+            E[k] = u[0][k];
+        }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+        for (int l = 1; l < kRun; ++l)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
                 A[k] *= a[l][k];
                 E[k] = fmaf(a[l][k], E[k], u[l][k]);
             }
         scan_wave<LR>(lane, A, E, Ab, Eb);
-        if (lane >= 64 - LR) agg[buf][wave][lane - (64 - LR)] = make_float4(A[0], E[0], A[1], E[1]);
+        if (lane >= 64 - LR) put_maps(maps[buf], wave, lane - (64 - LR), A, E);
         __syncthreads();
-        float h[2] = {carry[0], carry[1]};
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float4 m = agg[buf][w][lane % LR];
-            h[0] = w == wave ? carry[0] : h[0];
-            h[1] = w == wave ? carry[1] : h[1];
-            carry[0] = fmaf(m.x, carry[0], m.y);
-            carry[1] = fmaf(m.z, carry[1], m.w);
-        }
+        for (int k = 0; k < V; ++k) h[k] = carry[k];
+        through_waves(maps[buf], wave, lane % LR, carry, h);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) h[k] = fmaf(Ab[k], h[k], Eb[k]);
+        for (int k = 0; k < V; ++k) h[k] = fmaf(Ab[k], h[k], Eb[k]);
         char *o = out + t0 * (int64_t)hrow;
-        const uint32_t first = (uint32_t)(run * L) * hrow;
         if (full) {
 #pragma unroll
-            for (int l = 0; l < L; ++l) {
+            for (int l = 0; l < kRun; ++l) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) h[k] = fmaf(a[l][k], h[k], u[l][k]);
-                store2<T, MODE>(o, first, col, h[0], h[1]);
+                for (int k = 0; k < V; ++k) h[k] = fmaf(a[l][k], h[k], u[l][k]);
+                store_lane<T, MODE>(o, first, col, h);
                 o += fresh(hrow);
             }
         } else {
 #pragma unroll
-            for (int l = 0; l < L; ++l) {
+            for (int l = 0; l < kRun; ++l) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) h[k] = fmaf(a[l][k], h[k], u[l][k]);
-                if (l < rows) store2<T, MODE>(o, first, col, h[0], h[1]);
+                for (int k = 0; k < V; ++k) h[k] = fmaf(a[l][k], h[k], u[l][k]);
+                if (l < rows) store_lane<T, MODE>(o, first, col, h);
                 o += fresh(hrow);
             }
         }
         raw = next;
     }
-    for (int64_t t = max(begin, n) + run; t < end; t += NW * RW)
-        store2<T, MODE>(out + t * (int64_t)hrow, 0, col, 0.0f, 0.0f);
+    const float zero[V] = {};
+    for (int64_t t = max(begin, n) + run; t < end; t += NW * RW) store_lane<T, MODE>(out + t * (int64_t)hrow, 0, col, zero);
     if (p.sf && seg == p.nseg - 1 && threadIdx.x < LR)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (c + k < p.C) p.sf[b * p.C + c + k] = carry[k];
+        for (int k = 0; k < V; ++k)
+            if (k < col.have) p.sf[b * p.C + c + k] = carry[k];
 }
 
-template <typename T, int LR, int NW, bool SINGLE>
+// Whole, last and only stripe of a row.
+#define GATED_BODY(body, ...)                                                             \
+    if constexpr (SHORT) body<__VA_ARGS__, kShort>(p, ct, seg, b, maps);                  \
+    else if ((int64_t)(ct + 1) * LR * lane_channels<T>() <= p.C) body<__VA_ARGS__, kWhole>(p, ct, seg, b, maps); \
+    else body<__VA_ARGS__, kEdge>(p, ct, seg, b, maps)
+
+template <typename T, int LR, int NW, bool SHORT>
 __global__ __launch_bounds__(64 * NW) void gated_walk(const Walk p)
 {
-    __shared__ float4 agg[2][NW][LR];
+    __shared__ Maps<NW, LR, lane_channels<T>()> maps[2];
     int ct, seg;
     int64_t b;
     if (!place(p, p.nseg, ct, seg, b)) return;
-    if constexpr (SINGLE) walk_body<T, LR, NW, kSingle>(p, ct, seg, b, agg);
-    else if ((int64_t)(ct + 1) * 2 * LR <= p.C) walk_body<T, LR, NW, kWhole>(p, ct, seg, b, agg);
-    else walk_body<T, LR, NW, kEdge>(p, ct, seg, b, agg);
+    GATED_BODY(walk_body, T, LR, NW);
 }
 
 // ---------------------------------------------------------------- (A, E) of segments
@@ -364,9 +393,9 @@ __global__ __launch_bounds__(64 * NW) void gated_walk(const Walk p)
 // Each run of lanes takes a stretch of the segment of its own; no joins until its end.  Forward:
 // maps of h.  Backward (from the sequence's end): maps of c_t = a_t (dh_t + c_(t+1)).
 template <typename T, int LR, int NW, bool BWD, int MODE>
-__device__ __forceinline__ void states_body(const Walk &p, int ct, int seg, int64_t b, float4 (*agg)[LR])
+__device__ __forceinline__ void states_body(const Walk &p, int ct, int seg, int64_t b, Maps<NW, LR, lane_channels<T>()> &maps)
 {
-    constexpr int RW = 64 / LR, L = 8;
+    constexpr int V = lane_channels<T>(), RW = 64 / LR, L = 4;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int run = wave * RW + lane / LR;
     int64_t c;
@@ -374,26 +403,30 @@ __device__ __forceinline__ void states_body(const Walk &p, int ct, int seg, int6
     const int64_t n = live_tokens(p, b), stretch = p.seg_len / (NW * RW);
     // Positions count from the start of the walk: token q forward, n - 1 - q backward.
     const int64_t first = seg * p.seg_len + run * stretch, past = min(first + stretch, n);
-    float ld[2], A[2] = {1.0f, 1.0f}, E[2] = {0.0f, 0.0f};
+    float ld[V], A[V], E[V], Ab[V], Eb[V];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) ld[k] = p.log_decay[min(c + k, p.C - 1)] * kLog2e;
+    for (int k = 0; k < V; ++k) {
+        ld[k] = p.log_decay[min(c + k, p.C - 1)] * kLog2e;
+        A[k] = 1.0f;
+        E[k] = 0.0f;
+    }
     for (int64_t q = first; q < past; q += L) {
-        typename Two<T>::raw r[L], x[L], i[L];
+        uint2 r[L], x[L], i[L];
 #pragma unroll
         for (int l = 0; l < L; ++l) {
             const int64_t at = min(q + l, past - 1), t = BWD ? n - 1 - at : at;
-            r[l] = load2<T, MODE>(p.r + b * p.rsb + t * p.rst, 0, col);
-            x[l] = BWD ? load2<T, MODE>(p.dh + b * p.dsb + t * p.dst, 0, col) : load2<T, MODE>(p.x + b * p.xsb + t * p.xst, 0, col);
-            if constexpr (!BWD) i[l] = load2<T, MODE>(p.i + b * p.isb + t * p.ist, 0, col);
+            r[l] = load_lane<T, MODE>(p.r + b * p.rsb + t * p.rst, 0, col);
+            x[l] = BWD ? load_lane<T, MODE>(p.dh + b * p.dsb + t * p.dst, 0, col) : load_lane<T, MODE>(p.x + b * p.xsb + t * p.xst, 0, col);
+            if constexpr (!BWD) i[l] = load_lane<T, MODE>(p.i + b * p.isb + t * p.ist, 0, col);
         }
 #pragma unroll
         for (int l = 0; l < L; ++l) {
-            float rf[2], xf[2], jf[2];
+            float rf[V], xf[V], jf[V];
             values<T, MODE>(r[l], col, rf);
             values<T, MODE>(x[l], col, xf);
             if constexpr (!BWD) values<T, MODE>(i[l], col, jf);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < V; ++k) {
                 float a, m, u;
                 const float s = ld[k] * sigmoid(rf[k]);
                 if constexpr (BWD) {
@@ -410,34 +443,38 @@ __device__ __forceinline__ void states_body(const Walk &p, int ct, int seg, int6
             }
         }
     }
-    float Ab[2], Eb[2];
     scan_wave<LR>(lane, A, E, Ab, Eb);
-    if (lane >= 64 - LR) agg[wave][lane - (64 - LR)] = make_float4(A[0], E[0], A[1], E[1]);
+    if (lane >= 64 - LR) put_maps(maps, wave, lane - (64 - LR), A, E);
     __syncthreads();
     if (threadIdx.x >= LR) return;
-    float4 m = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-    for (int w = 0; w < NW; ++w) {
-        const float4 v = agg[w][lane];
-        m.y = fmaf(v.x, m.y, v.y);
-        m.x *= v.x;
-        m.w = fmaf(v.z, m.w, v.w);
-        m.z *= v.z;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        A[k] = 1.0f;
+        E[k] = 0.0f;
     }
+    for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            const float4 v = maps.m[k / 2][w][lane];
+            E[k] = fmaf(v.x, E[k], v.y);
+            A[k] *= v.x;
+            E[k + 1] = fmaf(v.z, E[k + 1], v.w);
+            A[k + 1] *= v.z;
+        }
     float2 *const o = reinterpret_cast<float2 *>(p.maps) + (b * p.nseg + seg) * p.C + c;
-    if (col.has_lo) o[0] = make_float2(m.x, m.y);
-    if (col.has_hi) o[1] = make_float2(m.z, m.w);
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+        if (k < col.have) o[k] = make_float2(A[k], E[k]);
 }
 
-template <typename T, int LR, int NW, bool BWD, bool SINGLE>
+template <typename T, int LR, int NW, bool BWD, bool SHORT>
 __global__ __launch_bounds__(64 * NW) void gated_states(const Walk p)
 {
-    __shared__ float4 agg[NW][LR];
+    __shared__ Maps<NW, LR, lane_channels<T>()> maps;
     int ct, seg;
     int64_t b;
     if (!place(p, p.nseg - 1, ct, seg, b)) return;     // nothing follows the last segment
-    if constexpr (SINGLE) states_body<T, LR, NW, BWD, kSingle>(p, ct, seg, b, agg);
-    else if ((int64_t)(ct + 1) * 2 * LR <= p.C) states_body<T, LR, NW, BWD, kWhole>(p, ct, seg, b, agg);
-    else states_body<T, LR, NW, BWD, kEdge>(p, ct, seg, b, agg);
+    GATED_BODY(states_body, T, LR, NW, BWD);
 }
 
 // ---------------------------------------------------------------- backward
@@ -447,28 +484,25 @@ __global__ __launch_bounds__(64 * NW) void gated_states(const Walk p)
 //     dr = dla log_decay r'(1 - r'),  dlog_decay = sum of dla r'      (s = sqrt(1 - a^2))
 // so each gradient is G times a factor of the token alone.  Where s is 0 (r' underflows, or a
 // log_decay of 0) the root has no derivative, and its term is left out.
-template <typename T, int L> struct RawBwd { typename Two<T>::raw x[L], r[L], i[L], h[L], d[L]; };
+struct RawBwd { uint2 x[kRunBwd], r[kRunBwd], i[kRunBwd], h[kRunBwd], d[kRunBwd]; };
 
-// Row l of a lane: token t0 - l (tokens fall), its h one token before.
-template <typename T, int MODE, int L>
-__device__ __forceinline__ void load_bwd(const Walk &p, const char *const (&base)[5], int64_t t0, int run, int TS, const Cols &col,
-                                         RawBwd<T, L> &raw)
+// Row l of a lane: token t0 - run kRunBwd - l (tokens fall), its h one token before.
+// step: byte offsets of the lane's oldest token from the tile's.
+template <typename T, int MODE>
+__device__ __forceinline__ void load_bwd(const Walk &p, const char *const (&base)[5], int64_t t0, int run, int TS,
+                                         const uint32_t (&step)[5], const Cols &col, RawBwd &raw)
 {
-    // t0: the newest token of the tile; the oldest is t0 - TS + 1.
     const int64_t low = t0 - TS + 1;
     if (low >= 1) {
-        const uint32_t up = (uint32_t)(TS - L - run * L);      // the lane's oldest token, from low
-        const uint32_t ox = up * (uint32_t)p.xst, orr = up * (uint32_t)p.rst, oi = up * (uint32_t)p.ist, oh = up * (uint32_t)p.hst,
-                       od = up * (uint32_t)p.dst;
         const char *x = base[0] + low * p.xst, *r = base[1] + low * p.rst, *i = base[2] + low * p.ist,
                    *h = base[3] + (low - 1) * p.hst, *d = base[4] + low * p.dst;
 #pragma unroll
-        for (int l = L - 1; l >= 0; --l) {
-            raw.r[l] = load2<T, MODE>(r, orr, col);
-            raw.d[l] = load2<T, MODE>(d, od, col);
-            raw.x[l] = load2<T, MODE>(x, ox, col);
-            raw.i[l] = load2<T, MODE>(i, oi, col);
-            raw.h[l] = load2<T, MODE>(h, oh, col);
+        for (int l = kRunBwd - 1; l >= 0; --l) {
+            raw.r[l] = load_lane<T, MODE>(r, step[1], col);
+            raw.d[l] = load_lane<T, MODE>(d, step[4], col);
+            raw.x[l] = load_lane<T, MODE>(x, step[0], col);
+            raw.i[l] = load_lane<T, MODE>(i, step[2], col);
+            raw.h[l] = load_lane<T, MODE>(h, step[3], col);
             x += fresh(p.xst);
             r += fresh(p.rst);
             i += fresh(p.ist);
@@ -477,21 +511,21 @@ __device__ __forceinline__ void load_bwd(const Walk &p, const char *const (&base
         }
     } else {        // tokens before the first are read from it
 #pragma unroll
-        for (int l = 0; l < L; ++l) {
-            const int64_t t = max((int64_t)0, t0 - run * L - l);
-            raw.r[l] = load2<T, MODE>(base[1] + t * p.rst, 0, col);
-            raw.d[l] = load2<T, MODE>(base[4] + t * p.dst, 0, col);
-            raw.x[l] = load2<T, MODE>(base[0] + t * p.xst, 0, col);
-            raw.i[l] = load2<T, MODE>(base[2] + t * p.ist, 0, col);
-            raw.h[l] = load2<T, MODE>(base[3] + max((int64_t)0, t - 1) * p.hst, 0, col);
+        for (int l = 0; l < kRunBwd; ++l) {
+            const int64_t t = max((int64_t)0, t0 - run * kRunBwd - l);
+            raw.r[l] = load_lane<T, MODE>(base[1] + t * p.rst, 0, col);
+            raw.d[l] = load_lane<T, MODE>(base[4] + t * p.dst, 0, col);
+            raw.x[l] = load_lane<T, MODE>(base[0] + t * p.xst, 0, col);
+            raw.i[l] = load_lane<T, MODE>(base[2] + t * p.ist, 0, col);
+            raw.h[l] = load_lane<T, MODE>(base[3] + max((int64_t)0, t - 1) * p.hst, 0, col);
         }
     }
 }
 
 template <typename T, int LR, int NW, int MODE>
-__device__ __forceinline__ void bwd_body(const Walk &p, int ct, int seg, int64_t b, float4 (*agg)[NW][LR])
+__device__ __forceinline__ void bwd_body(const Walk &p, int ct, int seg, int64_t b, Maps<NW, LR, lane_channels<T>()> *maps)
 {
-    constexpr int RW = 64 / LR, L = run_len_bwd<T>(), TS = NW * RW * L;
+    constexpr int V = lane_channels<T>(), RW = 64 / LR, L = kRunBwd, TS = NW * RW * L;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int run = wave * RW + lane / LR;
     int64_t c;
@@ -499,30 +533,33 @@ __device__ __forceinline__ void bwd_body(const Walk &p, int ct, int seg, int64_t
     // Segments count from the sequence's end.
     const int64_t n = live_tokens(p, b), top = n - 1 - seg * p.seg_len, bottom = max((int64_t)0, n - (seg + 1) * p.seg_len);
     const char *const base[5] = {p.x + b * p.xsb, p.r + b * p.rsb, p.i + b * p.isb, p.h_in + b * p.hsb, p.dh + b * p.dsb};
-    const uint32_t orow = (uint32_t)(p.C * sizeof(T));
+    const int up = TS - L - run * L;
+    const uint32_t step[5] = {(uint32_t)(up * p.xst), (uint32_t)(up * p.rst), (uint32_t)(up * p.ist), (uint32_t)(up * p.hst),
+                              (uint32_t)(up * p.dst)};
+    const uint32_t orow = (uint32_t)(p.C * sizeof(T)), oldest = (uint32_t)up * orow;
     const int64_t ob = b * p.T * (int64_t)orow;
 
-    RawBwd<T, L> raw;
-    if (top >= bottom) load_bwd<T, MODE, L>(p, base, top, run, TS, col, raw);
-    float ld[2], carry[2], before[2], share[2] = {0.0f, 0.0f};
+    RawBwd raw;
+    if (top >= bottom) load_bwd<T, MODE>(p, base, top, run, TS, step, col, raw);
+    float ld[V], carry[V], before[V], share[V];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < V; ++k) {
         const int64_t ck = min(c + k, p.C - 1);
         ld[k] = p.log_decay[ck];
         carry[k] = fold(p, b, seg, ck, p.sf ? p.sf[b * p.C + ck] : 0.0f);
         before[k] = p.s0 ? p.s0[b * p.C + ck] : 0.0f;
+        share[k] = 0.0f;
     }
     int buf = 0;
     for (int64_t t0 = top; t0 >= bottom; t0 -= TS, buf ^= 1) {
-        RawBwd<T, L> next;
-        if (t0 - TS >= bottom) load_bwd<T, MODE, L>(p, base, t0 - TS, run, TS, col, next);
+        RawBwd next;
+        if (t0 - TS >= bottom) load_bwd<T, MODE>(p, base, t0 - TS, run, TS, step, col, next);
         const bool full = t0 - TS + 1 >= bottom;
         const int rows = full ? L : (int)min((int64_t)L, max((int64_t)0, t0 - run * L - bottom + 1));
-        float a[L][2], g[L][2], fx[L][2], fi[L][2], fr[L][2], fd[L][2];
-        float A[2] = {1.0f, 1.0f}, E[2] = {0.0f, 0.0f}, Ab[2], Eb[2];
+        float a[L][V], g[L][V], fx[L][V], fi[L][V], fr[L][V], fd[L][V], A[V], E[V], Ab[V], Eb[V], cc[V];
 #pragma unroll
         for (int l = 0; l < L; ++l) {
-            float x[2], r[2], i[2], h[2];
+            float x[V], r[V], i[V], h[V];
             values<T, MODE>(raw.x[l], col, x);
             values<T, MODE>(raw.r[l], col, r);
             values<T, MODE>(raw.i[l], col, i);
@@ -530,7 +567,7 @@ __device__ __forceinline__ void bwd_body(const Walk &p, int ct, int seg, int64_t
             values<T, MODE>(raw.d[l], col, g[l]);
             const bool start = t0 - run * L - l == 0;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < V; ++k) {
                 const float sr = sigmoid(r[k]), si = sigmoid(i[k]), la = ld[k] * sr;
                 float m;
                 decay(kLog2e * la, a[l][k], m);
@@ -549,91 +586,92 @@ __device__ __forceinline__ void bwd_body(const Walk &p, int ct, int seg, int64_t
 #pragma unroll
             for (int l = 0; l < L; ++l)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < V; ++k) {
                     a[l][k] = l < rows ? a[l][k] : 1.0f;
                     g[l][k] = l < rows ? g[l][k] : 0.0f;
-                    fd[l][k] = l < rows ? fd[l][k] : 0.0f;
                 }
 #pragma unroll
-        for (int l = 0; l < L; ++l)
+        for (int k = 0; k < V; ++k) {
+            A[k] = a[0][k];
+            E[k] = a[0][k] * g[0][k];
+        }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+        for (int l = 1; l < L; ++l)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
                 A[k] *= a[l][k];
                 E[k] = a[l][k] * (g[l][k] + E[k]);
             }
         scan_wave<LR>(lane, A, E, Ab, Eb);
-        if (lane >= 64 - LR) agg[buf][wave][lane - (64 - LR)] = make_float4(A[0], E[0], A[1], E[1]);
+        if (lane >= 64 - LR) put_maps(maps[buf], wave, lane - (64 - LR), A, E);
         __syncthreads();
-        float cc[2] = {carry[0], carry[1]};
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float4 m = agg[buf][w][lane % LR];
-            cc[0] = w == wave ? carry[0] : cc[0];
-            cc[1] = w == wave ? carry[1] : cc[1];
-            carry[0] = fmaf(m.x, carry[0], m.y);
-            carry[1] = fmaf(m.z, carry[1], m.w);
-        }
+        for (int k = 0; k < V; ++k) cc[k] = carry[k];
+        through_waves(maps[buf], wave, lane % LR, carry, cc);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) cc[k] = fmaf(Ab[k], cc[k], Eb[k]);
+        for (int k = 0; k < V; ++k) cc[k] = fmaf(Ab[k], cc[k], Eb[k]);
+        // The tile's oldest token is t0 - TS + 1, which a tile that is not full may have below 0.
+        const int64_t at = ob + (t0 - TS + 1) * (int64_t)orow;
 #pragma unroll
         for (int l = 0; l < L; ++l) {
-            float G[2];
+            float ox[V], oi[V], orr[V];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                G[k] = g[l][k] + cc[k];
-                cc[k] = a[l][k] * G[k];
-                // A token that does not exist adds nothing, whatever G is.
-                share[k] = l < rows ? fmaf(G[k], fd[l][k], share[k]) : share[k];
+            for (int k = 0; k < V; ++k) {
+                const float G = g[l][k] + cc[k];
+                cc[k] = a[l][k] * G;
+                ox[k] = G * fx[l][k];
+                oi[k] = G * fi[l][k];
+                orr[k] = G * fr[l][k];
+                // A token that does not exist adds nothing, whatever its factors are.
+                share[k] = l < rows ? fmaf(G, fd[l][k], share[k]) : share[k];
             }
             if (full || l < rows) {
-                const int64_t at = ob + (t0 - run * L - l) * (int64_t)orow;
-                store2<T, MODE>(p.dx + at, 0, col, G[0] * fx[l][0], G[1] * fx[l][1]);
-                store2<T, MODE>(p.dr + at, 0, col, G[0] * fr[l][0], G[1] * fr[l][1]);
-                store2<T, MODE>(p.di + at, 0, col, G[0] * fi[l][0], G[1] * fi[l][1]);
+                const int64_t o = at + (L - 1 - l) * (int64_t)orow;
+                store_lane<T, MODE>(p.dx + o, oldest, col, ox);
+                store_lane<T, MODE>(p.dr + o, oldest, col, orr);
+                store_lane<T, MODE>(p.di + o, oldest, col, oi);
             }
         }
         raw = next;
     }
     // Tokens that do not exist: this segment's part of [n, T).
+    const float zero[V] = {};
     for (int64_t t = n + (int64_t)seg * NW * RW + run; t < p.T; t += (int64_t)p.nseg * NW * RW) {
-        const int64_t at = ob + t * (int64_t)orow;
-        store2<T, MODE>(p.dx + at, 0, col, 0.0f, 0.0f);
-        store2<T, MODE>(p.dr + at, 0, col, 0.0f, 0.0f);
-        store2<T, MODE>(p.di + at, 0, col, 0.0f, 0.0f);
+        const int64_t o = ob + t * (int64_t)orow;
+        store_lane<T, MODE>(p.dx + o, 0, col, zero);
+        store_lane<T, MODE>(p.dr + o, 0, col, zero);
+        store_lane<T, MODE>(p.di + o, 0, col, zero);
     }
     if (p.h && seg == p.nseg - 1 && threadIdx.x < LR)      // p.h: the first state's gradient, fp32
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (c + k < p.C) reinterpret_cast<float *>(p.h)[b * p.C + c + k] = carry[k];
+        for (int k = 0; k < V; ++k)
+            if (k < col.have) reinterpret_cast<float *>(p.h)[b * p.C + c + k] = carry[k];
     // Shares of log_decay's gradient: over the runs of a wave, then over the waves.
 #pragma unroll
-    for (int d = LR; d < 64; d *= 2)
+    for (int dist = LR; dist < 64; dist *= 2)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) share[k] += __shfl_xor(share[k], d);
+        for (int k = 0; k < V; ++k) share[k] += __shfl_xor(share[k], dist);
     __syncthreads();
-    if (lane < LR) agg[0][wave][lane] = make_float4(share[0], share[1], 0.0f, 0.0f);
+    if (lane < LR) put_maps(maps[0], wave, lane, share, share);
     __syncthreads();
     if (threadIdx.x >= LR) return;
-    float sum[2] = {0.0f, 0.0f};
-    for (int w = 0; w < NW; ++w) {
-        sum[0] += agg[0][w][lane].x;
-        sum[1] += agg[0][w][lane].y;
-    }
     float *const o = p.part + (b * p.nseg + seg) * p.C + c;
-    if (col.has_lo) o[0] = sum[0];
-    if (col.has_hi) o[1] = sum[1];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        float sum = 0.0f;
+        for (int w = 0; w < NW; ++w) sum += k % 2 ? maps[0].m[k / 2][w][lane].z : maps[0].m[k / 2][w][lane].x;
+        if (k < col.have) o[k] = sum;
+    }
 }
 
-template <typename T, int LR, int NW, bool SINGLE>
+template <typename T, int LR, int NW, bool SHORT>
 __global__ __launch_bounds__(64 * NW) void gated_bwd_walk(const Walk p)
 {
-    __shared__ float4 agg[2][NW][LR];
+    __shared__ Maps<NW, LR, lane_channels<T>()> maps[2];
     int ct, seg;
     int64_t b;
     if (!place(p, p.nseg, ct, seg, b)) return;
-    if constexpr (SINGLE) bwd_body<T, LR, NW, kSingle>(p, ct, seg, b, agg);
-    else if ((int64_t)(ct + 1) * 2 * LR <= p.C) bwd_body<T, LR, NW, kWhole>(p, ct, seg, b, agg);
-    else bwd_body<T, LR, NW, kEdge>(p, ct, seg, b, agg);
+    GATED_BODY(bwd_body, T, LR, NW);
 }
 
 // Sum over sequences and segments, in order: 16 rows at a time, then those 16.
@@ -676,11 +714,11 @@ __global__ __launch_bounds__(256) void gated_step(const T *__restrict__ x, const
     h[b * C + c] = from_f32<T>(v);
 }
 
-int tile_steps(const GatedPlan &g, int dtype, bool backward)
+// Channels of a stripe, and tokens of a tile.
+int stripe(const GatedPlan &g, int dtype) { return g.lanes * (dtype == DT_F32 ? 2 : 4); }
+int tile_steps(const GatedPlan &g, bool backward)
 {
-    const int run = dtype == DT_F32 ? (backward ? run_len_bwd<float>() : run_len<float>())
-                                    : (backward ? run_len_bwd<__bf16>() : run_len<__bf16>());
-    return g.waves * (64 / g.lanes) * run;
+    return g.waves * (64 / g.lanes) * (backward ? kRunBwd : kRun);
 }
 
 Walk make_walk(const GatedArgs &a, const GatedPlan &g)
@@ -688,7 +726,7 @@ Walk make_walk(const GatedArgs &a, const GatedPlan &g)
     const int64_t es = a.dtype == DT_F32 ? 4 : 2;
     Walk p = {};
     p.B = a.B; p.T = a.T; p.C = a.C; p.seg_len = g.seg_len; p.nseg = g.nseg;
-    p.tiles = (int32_t)ceil_div(a.C, 2 * g.lanes);
+    p.tiles = (int32_t)ceil_div(a.C, stripe(g, a.dtype));
     p.blocks = a.B * g.nseg * p.tiles;
     p.x = (const char *)a.x; p.r = (const char *)a.r; p.i = (const char *)a.i;
     p.log_decay = a.log_decay; p.s0 = a.s0; p.lengths = a.lengths;
@@ -712,14 +750,12 @@ template <typename F> hipError_t with_type(int dtype, F &&f)
 
 template <int N> struct Int { static constexpr int value = N; };
 
-// The kernels that exist: (lanes, waves, one channel).
-template <typename F> hipError_t with_shape(const GatedPlan &g, int64_t C, F &&f)
+// The kernels that exist: (lanes, waves, rows shorter than a lane's 8 bytes).
+template <typename F> hipError_t with_shape(const GatedPlan &g, int64_t C, int dtype, F &&f)
 {
-    constexpr Int<0> more{};
-    if (C == 1) return f(Int<16>{}, Int<4>{}, Int<1>{});
-    if (g.lanes == 16)
-        return g.waves == 16 ? f(Int<16>{}, Int<16>{}, more) : g.waves == 8 ? f(Int<16>{}, Int<8>{}, more) : f(Int<16>{}, Int<4>{}, more);
-    return g.waves == 16 ? f(Int<8>{}, Int<16>{}, more) : g.waves == 8 ? f(Int<8>{}, Int<8>{}, more) : f(Int<8>{}, Int<4>{}, more);
+    constexpr Int<0> whole{};
+    if (C < (dtype == DT_F32 ? 2 : 4)) return f(Int<16>{}, Int<4>{}, Int<1>{});
+    return g.waves == 8 ? f(Int<32>{}, Int<8>{}, whole) : f(Int<32>{}, Int<4>{}, whole);
 }
 
 template <bool BWD> hipError_t launch_states(Walk p, const GatedPlan &g, int dtype, hipStream_t stream)
@@ -727,7 +763,7 @@ template <bool BWD> hipError_t launch_states(Walk p, const GatedPlan &g, int dty
     p.blocks = p.B * (g.nseg - 1) * p.tiles;
     const dim3 grid((unsigned)(8 * ceil_div(p.blocks, 8)));
     return with_type(dtype, [&](auto t) {
-        return with_shape(g, p.C, [&](auto lanes, auto waves, auto one) {
+        return with_shape(g, p.C, dtype, [&](auto lanes, auto waves, auto one) {
             gated_states<decltype(t), lanes.value, waves.value, BWD, one.value><<<grid, 64 * waves.value, 0, stream>>>(p);
             return hipGetLastError();
         });
@@ -738,10 +774,11 @@ template <bool BWD> hipError_t launch_states(Walk p, const GatedPlan &g, int dty
 
 GatedPlan gated_plan(int64_t B, int64_t T, int64_t C, int dtype, bool backward)
 {
-    GatedPlan g = {16, C == 1 ? 4 : 8, 1, std::max<int64_t>(T, 1)};
-    const int64_t stripes = std::max<int64_t>(1, B * ceil_div(C, 32));
-    const int64_t ts = tile_steps(g, dtype, backward), tiles = ceil_div(std::max<int64_t>(T, 1), ts);
-    g.nseg = (int32_t)std::max<int64_t>(1, std::min<int64_t>({512 / stripes, tiles / 2, 256}));
+    GatedPlan g = {32, backward || T <= 256 ? 4 : 8, 1, std::max<int64_t>(T, 1)};
+    if (C < (dtype == DT_F32 ? 2 : 4)) g = {16, 4, 1, g.seg_len};
+    const int64_t stripes = std::max<int64_t>(1, B * ceil_div(C, stripe(g, dtype)));
+    const int64_t ts = tile_steps(g, backward), tiles = ceil_div(std::max<int64_t>(T, 1), ts);
+    g.nseg = stripes >= 192 ? 1 : (int32_t)std::max<int64_t>(1, std::min<int64_t>({512 / stripes, tiles / 2, 256}));
     const int64_t each = ceil_div(tiles, (int64_t)g.nseg);
     g.nseg = (int32_t)ceil_div(tiles, each);
     g.seg_len = each * ts;
@@ -755,10 +792,10 @@ size_t gated_workspace(const GatedPlan &g, int64_t B, int64_t C, bool backward)
 
 bool gated_fits(const GatedArgs &a, const GatedPlan &g, bool backward)
 {
-    const int64_t es = a.dtype == DT_F32 ? 4 : 2, ts = tile_steps(g, a.dtype, backward), top = (int64_t(1) << 31) - 1;
+    const int64_t es = a.dtype == DT_F32 ? 4 : 2, ts = tile_steps(g, backward), top = (int64_t(1) << 31) - 1;
     for (int64_t st : {a.xst, a.rst, a.ist, a.C, backward ? a.hst : 0, backward ? a.dst : 0})
         if (ts * es > top / std::max<int64_t>(st, 1)) return false;
-    return grid_fits(8 * ceil_div(a.B * g.nseg * ceil_div(a.C, 2 * g.lanes), 8), 64 * g.waves);
+    return grid_fits(8 * ceil_div(a.B * g.nseg * ceil_div(a.C, stripe(g, a.dtype)), 8), 64 * g.waves);
 }
 
 hipError_t launch_gated(const GatedArgs &a, const GatedPlan &g, const char **kname)
@@ -773,7 +810,7 @@ hipError_t launch_gated(const GatedArgs &a, const GatedPlan &g, const char **kna
     }
     const dim3 grid((unsigned)(8 * ceil_div(p.blocks, 8)));
     return with_type(a.dtype, [&](auto t) {
-        return with_shape(g, a.C, [&](auto lanes, auto waves, auto one) {
+        return with_shape(g, a.C, a.dtype, [&](auto lanes, auto waves, auto one) {
             gated_walk<decltype(t), lanes.value, waves.value, one.value><<<grid, 64 * waves.value, 0, a.stream>>>(p);
             return hipGetLastError();
         });
@@ -797,7 +834,7 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const GatedPlan &g, const char *
         }
         const dim3 grid((unsigned)(8 * ceil_div(p.blocks, 8)));
         const hipError_t err = with_type(a.dtype, [&](auto t) {
-            return with_shape(g, a.C, [&](auto lanes, auto waves, auto one) {
+            return with_shape(g, a.C, a.dtype, [&](auto lanes, auto waves, auto one) {
                 gated_bwd_walk<decltype(t), lanes.value, waves.value, one.value><<<grid, 64 * waves.value, 0, a.stream>>>(p);
                 return hipGetLastError();
             });
