@@ -39,6 +39,9 @@ from ._block import (  # noqa: F401
     gated_recurrence_backward,
     gated_recurrence_step,
     gated_recurrence_workspace,
+    group_norm,
+    group_norm_backward,
+    group_norm_workspace,
 )
 from ._sequence import (  # noqa: F401
     dwconv1d_causal,

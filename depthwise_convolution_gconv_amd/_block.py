@@ -1,4 +1,5 @@
-"""Operators of a recurrent mixing block in libgconv.so: the gated linear recurrence.
+"""Operators of a recurrent mixing block in libgconv.so: the gated linear recurrence, and group
+norm with an activation over channels-last tensors.
 
 Argument checks and marshalling only, in the manner of the other sequence operators: the
 caller's current device and stream, or `stream`; outputs and workspaces from torch.
@@ -11,8 +12,8 @@ from typing import Optional
 import torch
 
 from ._binding import DTYPES, _check, _i32, _i64, _i64p, _vp, lib
-from ._sequence import (_array, _bad, _device, _dtype, _like, _on_stream, _ptr, _raw_stream, _size, _view, _whole,
-                        _workspace)
+from ._sequence import (ACTIVATIONS, _array, _bad, _device, _dtype, _f32, _like, _on_stream, _ptr, _raw_stream, _size,
+                        _view, _whole, _workspace)
 
 _fns = None
 
@@ -28,6 +29,9 @@ def _library():
             "gconv_gated_recurrence": [_vp] * 5 + [_i64p, _i64p] + [_vp] * 3 + [_i32, _vp, _size, _vp],
             "gconv_gated_recurrence_backward": [_vp] * 10 + [_i64p, _i64p] + [_vp] * 4 + [_i32, _vp, _size, _vp],
             "gconv_gated_recurrence_step": [_vp] * 6 + [_i64p, _i64p, _vp, _i32, _vp],
+            "gconv_group_norm_workspace": [_i64p, _i32, _i32, sizep],
+            "gconv_group_norm": [_vp] * 5 + [_i64p, _i64p, _vp, _f32, _i32, _i32, _vp, _size, _vp],
+            "gconv_group_norm_backward": [_vp] * 8 + [_i64p, _i64p, _vp, _i32, _i32, _vp, _size, _vp],
         }.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -142,3 +146,101 @@ def gated_recurrence_step(x, r, i, log_decay, state, slots=None, stream=None):
                                                   _array(B, C, state.shape[0]), _array(*strides), sl, dt,
                                                   _raw_stream(dev)))
     return h
+
+
+# ---------------------------------------------------------------- group norm
+
+def _positions(name: str, t: torch.Tensor, ref: torch.Tensor):
+    """Strides of a [N, ..., C] tensor's samples and positions, whose axes must lie at one stride."""
+    st = _view(name, t, ref.dtype, ref.get_device(), ref.shape)
+    if t.dim() == 2:
+        return st[0], 0
+    if t.dim() == 3:
+        return st[0], st[1]
+    step = None          # from the last position axis on: each longer axis goes on where the shorter ones end
+    for n, s in reversed(list(zip(t.shape[1:-1], st[1:-1]))):
+        if n == 1:
+            continue
+        if step is None:
+            first = step = s
+        elif s != step and t.numel():
+            _bad(f"{name}: its positions must lie at one stride")
+        step = s * n
+    return st[0], 0 if step is None else first
+
+
+def _norm_args(x, groups, weight, bias, activation, lengths):
+    dt = _dtype("x", x)
+    if x.dim() < 2 or x.shape[-1] < 1:
+        _bad("x must be [N, ..., C] with C >= 1")
+    if activation not in ACTIVATIONS:
+        _bad(f"unknown activation {activation!r}")
+    dev, N, C = x.get_device(), x.shape[0], x.shape[-1]
+    P = 1
+    for n in x.shape[1:-1]:
+        P *= n
+    w = _whole("weight", weight, x.dtype, dev, (C,))
+    if not w:
+        _bad("weight is needed")
+    return (dt, dev, (N, P, C, int(groups)), _positions("x", x, x), w, _whole("bias", bias, x.dtype, dev, (C,)),
+            ACTIVATIONS[activation], _whole("lengths", lengths, torch.int32, dev, (N,)))
+
+
+def group_norm_workspace(shape, dtype: torch.dtype, backward: bool = False) -> int:
+    """Workspace bytes of group_norm (or its backward) for shape (N, P, C, G), P positions a sample."""
+    n = _size(0)
+    _check(_library().gconv_group_norm_workspace(_array(*shape), DTYPES[dtype], int(backward), ctypes.byref(n)))
+    return n.value
+
+
+def group_norm(x, groups: int, weight, bias=None, eps: float = 1e-5, activation: Optional[str] = None, lengths=None,
+               return_stats: bool = False, stream=None):
+    """Group norm with an activation over channels-last x [N, ..., C]: y = act(weight * (x - mean) /
+    sqrt(var + eps) + bias), mean and (biased) variance over a sample's positions and the C / groups
+    channels of a group.  x [N, C] is normed row by row (a token's heads, say).
+
+    x may be a view whose positions lie at one stride, with contiguous channels.  activation: None
+    or "silu".  lengths: int32 [N], the positions of each sample that exist, in order; the outputs
+    of the others are zero.  Returns y, or (y, stats) with stats fp32 [N, groups, 2], the mean and
+    1 / sqrt(var + eps), which group_norm_backward takes.  A sample without positions has mean 0
+    and variance 0."""
+    if stream is not None:
+        return _on_stream(stream, x, group_norm, x, groups, weight, bias, eps, activation, lengths, return_stats)
+    dt, dev, shape, strides, w, b, act, n = _norm_args(x, groups, weight, bias, activation, lengths)
+    sh = _array(*shape)
+    need = _size(0)
+    L = _library()
+    _check(L.gconv_group_norm_workspace(sh, dt, 0, ctypes.byref(need)))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return group_norm(x, groups, weight, bias, eps, activation, lengths, return_stats)
+    y = _like(x)
+    stats = x.new_empty((shape[0], shape[3], 2), dtype=torch.float32) if return_stats else None
+    ws = _workspace(need.value, x)
+    _check(L.gconv_group_norm(x.data_ptr(), w, b, y.data_ptr(), _ptr(stats), sh, _array(*strides), n, eps, act, dt,
+                              _ptr(ws), need.value, _raw_stream(dev)))
+    return (y, stats) if return_stats else y
+
+
+def group_norm_backward(dy, x, groups: int, weight, bias, stats, activation: Optional[str] = None, lengths=None,
+                        stream=None):
+    """(dx, dw, db) of group_norm from the gradient dy of its output and the stats that it returned.
+    db is None without a bias."""
+    if stream is not None:
+        return _on_stream(stream, x, group_norm_backward, dy, x, groups, weight, bias, stats, activation, lengths)
+    dt, dev, shape, strides, w, b, act, n = _norm_args(x, groups, weight, bias, activation, lengths)
+    ds = _positions("dy", dy, x)
+    sh = _array(*shape)
+    need = _size(0)
+    L = _library()
+    _check(L.gconv_group_norm_workspace(sh, dt, 1, ctypes.byref(need)))
+    st = _whole("stats", stats, torch.float32, dev, (shape[0], shape[3], 2))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return group_norm_backward(dy, x, groups, weight, bias, stats, activation, lengths)
+    dx, dw = _like(x), _like(weight)
+    db = _like(bias) if bias is not None else None
+    ws = _workspace(need.value, x)
+    _check(L.gconv_group_norm_backward(dy.data_ptr(), x.data_ptr(), w, b, st, dx.data_ptr(), dw.data_ptr(), _ptr(db), sh,
+                                       _array(*ds, *strides), n, act, dt, _ptr(ws), need.value, _raw_stream(dev)))
+    return dx, dw, db

@@ -52,4 +52,36 @@ struct GatedStepArgs {
 bool gated_step_fits(const GatedStepArgs &a);
 hipError_t launch_gated_step(const GatedStepArgs &a, const char **kname);
 
+// y = act(weight (x - mean) rstd + bias) with the statistics of a sample's group.
+struct GroupNormArgs {
+    const void *x;                       // [N][P][C], channels contiguous
+    const void *weight, *bias;           // [C]; bias may be nullptr
+    void *y;                             // [N][P][C] contiguous; backward: dx
+    const void *dy;                      // backward: [N][P][C], channels contiguous
+    void *dw, *db;                       // backward: [C]; db may be nullptr
+    const float *stats;                  // backward: (mean, rstd) [N][G][2]
+    float *stats_out;                    // forward: the same, or nullptr
+    const int32_t *lengths;              // [N] or nullptr: P
+    void *ws;
+    int64_t N, P, C, G;
+    int64_t xsb, xst, dsb, dst;          // element strides: sample, position
+    float eps;
+    int32_t silu;
+    int dtype;
+    hipStream_t stream;
+};
+// How a call is laid out: threads of a workgroup, channels of a vector (V), groups and vectors
+// of a row of its slab, positions of a thread (K), chunks of a sample's positions, parts of a
+// group too wide for one workgroup, samples that a gradients' workgroup takes one after the other.
+struct GroupNormPlan {
+    int32_t threads, V, kg, cols, K, chunks, chunk_rows, parts;
+    int64_t range;
+};
+GroupNormPlan gn_plan(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, bool backward);
+size_t gn_chunk_bytes(const GroupNormPlan &g, int64_t N, int64_t G);
+size_t gn_workspace(const GroupNormPlan &g, int64_t N, int64_t C, int64_t G, bool backward);
+bool gn_fits(const GroupNormArgs &a, const GroupNormPlan &g);
+hipError_t launch_group_norm(const GroupNormArgs &a, const GroupNormPlan &g, const char **kname);
+hipError_t launch_group_norm_bwd(const GroupNormArgs &a, const GroupNormPlan &g, const char **kname);
+
 }  // namespace gconv

@@ -1,5 +1,5 @@
 // block_api.cpp -- C entry points of the recurrent block's operators (gated linear
-// recurrence): validation, plans and launches.  Host code only.
+// recurrence, group norm): validation, plans and launches.  Host code only.
 #include <hip/hip_runtime.h>
 
 #include "block.hpp"
@@ -39,6 +39,31 @@ gconv_status_t gated_check(const gconv::GatedArgs &a, const gconv::GatedPlan &g,
 {
     if (!gconv::gated_fits(a, g, backward))
         return fail(GCONV_ERR_UNSUPPORTED, "gated recurrence: the sizes or token strides exceed what a launch takes");
+    return GCONV_OK;
+}
+
+// ---------------------------------------------------------------- group norm
+
+gconv_status_t gn_shape(const int64_t *shape, gconv_act_t act, gconv_dtype_t dtype)
+{
+    if (bad_dtype(dtype)) return fail(GCONV_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (act != GCONV_ACT_NONE && act != GCONV_ACT_SILU)
+        return fail(GCONV_ERR_INVALID_ARG, "unknown activation %d", (int)act);
+    if (!shape) return fail(GCONV_ERR_INVALID_ARG, "NULL shape");
+    const int64_t N = shape[0], P = shape[1], C = shape[2], G = shape[3];
+    if (N < 0 || P < 0 || C < 1 || G < 1)
+        return fail(GCONV_ERR_INVALID_ARG, "group norm: N, P >= 0 and C, G >= 1 are needed");
+    if (C % G != 0)
+        return fail(GCONV_ERR_SHAPE, "group norm: %lld channels do not divide into %lld groups", (long long)C, (long long)G);
+    if (C > int64_t(1) << 20 || N > kMax || P > kMax - 65536 || (double)N * (double)P * (double)C >= kCells / 8)
+        return fail(GCONV_ERR_UNSUPPORTED, "group norm: at most 2^20 channels, 2^31 - 1 samples and positions");
+    return GCONV_OK;
+}
+
+gconv_status_t gn_check(const gconv::GroupNormArgs &a, const gconv::GroupNormPlan &g)
+{
+    if (!gconv::gn_fits(a, g))
+        return fail(GCONV_ERR_UNSUPPORTED, "group norm: the sizes or position strides exceed what a launch takes");
     return GCONV_OK;
 }
 
@@ -190,6 +215,96 @@ gconv_status_t gconv_gated_recurrence_step(const void *x, const void *r, const v
         return fail(GCONV_ERR_UNSUPPORTED, "gated recurrence step: the call needs more threads than a launch takes");
     const char *kname = "";
     const hipError_t err = gconv::launch_gated_step(a, &kname);
+    return done(err, kname);
+}
+
+// ---------------------------------------------------------------- group norm
+
+gconv_status_t gconv_group_norm_workspace(const int64_t *shape, gconv_dtype_t dtype, int32_t backward, size_t *bytes)
+{
+    gconv::set_last_error("");
+    if (!bytes) return fail(GCONV_ERR_INVALID_ARG, "NULL bytes");
+    const gconv_status_t st = gn_shape(shape, GCONV_ACT_NONE, dtype);
+    if (st != GCONV_OK) return st;
+    const gconv::GroupNormPlan g = gconv::gn_plan(shape[0], shape[1], shape[2], shape[3], (int)dtype, backward != 0);
+    *bytes = gconv::gn_workspace(g, shape[0], shape[2], shape[3], backward != 0);
+    return GCONV_OK;
+}
+
+gconv_status_t gconv_group_norm(const void *x, const void *weight, const void *bias, void *y, float *stats, const int64_t *shape,
+                                const int64_t *strides, const int32_t *lengths, float eps, gconv_act_t activation,
+                                gconv_dtype_t dtype, void *workspace, size_t workspace_bytes, void *hip_stream)
+{
+    gconv::set_last_error("");
+    gconv_status_t st = gn_shape(shape, activation, dtype);
+    if (st != GCONV_OK) return st;
+    const int64_t N = shape[0], P = shape[1], C = shape[2], G = shape[3];
+    if ((st = reach(strides, 2, N, P)) != GCONV_OK) return st;
+    if (!(eps >= 0.0f)) return fail(GCONV_ERR_INVALID_ARG, "group norm: eps must be >= 0");
+    if (!weight) return fail(GCONV_ERR_INVALID_ARG, "NULL weight");
+    if (N > 0 && P > 0 && (!x || !y)) return fail(GCONV_ERR_INVALID_ARG, "NULL x or y");
+    const gconv::GroupNormPlan g = gconv::gn_plan(N, P, C, G, (int)dtype, false);
+    const size_t need = gconv::gn_workspace(g, N, C, G, false), es = elem(dtype);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != GCONV_OK) return st;
+    const Range ranges[] = {
+        {"y", y, es * (size_t)(N * P * C), true},
+        {"stats", stats, 8 * (size_t)(N * G), true},
+        {"workspace", workspace, need, true},
+        {"x", x, extent(N, strides[0], P, strides[1], 1, 0, C, es), false},
+        {"weight", weight, es * (size_t)C, false},
+        {"bias", bias, es * (size_t)C, false},
+        {"lengths", lengths, 4 * (size_t)N, false},
+    };
+    if ((st = check_ranges(ranges, sizeof(ranges) / sizeof(ranges[0]))) != GCONV_OK) return st;
+    gconv::GroupNormArgs a = {};
+    a.x = x; a.weight = weight; a.bias = bias; a.y = y; a.stats_out = stats; a.lengths = lengths; a.ws = workspace;
+    a.N = N; a.P = P; a.C = C; a.G = G; a.xsb = strides[0]; a.xst = strides[1];
+    a.eps = eps; a.silu = activation == GCONV_ACT_SILU; a.dtype = (int)dtype; a.stream = (hipStream_t)hip_stream;
+    if ((st = gn_check(a, g)) != GCONV_OK) return st;
+    if (N == 0 || (P == 0 && !stats)) return done(hipSuccess, "");
+    const char *kname = "";
+    const hipError_t err = gconv::launch_group_norm(a, g, &kname);
+    return done(err, kname);
+}
+
+gconv_status_t gconv_group_norm_backward(const void *dy, const void *x, const void *weight, const void *bias, const float *stats,
+                                         void *dx, void *dw, void *db, const int64_t *shape, const int64_t *strides,
+                                         const int32_t *lengths, gconv_act_t activation, gconv_dtype_t dtype, void *workspace,
+                                         size_t workspace_bytes, void *hip_stream)
+{
+    gconv::set_last_error("");
+    gconv_status_t st = gn_shape(shape, activation, dtype);
+    if (st != GCONV_OK) return st;
+    const int64_t N = shape[0], P = shape[1], C = shape[2], G = shape[3];
+    if ((st = reach(strides, 4, N, P)) != GCONV_OK) return st;
+    if (!weight || !dw) return fail(GCONV_ERR_INVALID_ARG, "NULL weight or dw");
+    if ((bias != nullptr) != (db != nullptr)) return fail(GCONV_ERR_INVALID_ARG, "group norm: db goes with a bias");
+    if (N > 0 && !stats) return fail(GCONV_ERR_INVALID_ARG, "NULL stats");
+    if (N > 0 && P > 0 && (!x || !dy || !dx)) return fail(GCONV_ERR_INVALID_ARG, "NULL x, dy or dx");
+    const gconv::GroupNormPlan g = gconv::gn_plan(N, P, C, G, (int)dtype, true);
+    const size_t need = gconv::gn_workspace(g, N, C, G, true), es = elem(dtype);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != GCONV_OK) return st;
+    const Range ranges[] = {
+        {"dx", dx, es * (size_t)(N * P * C), true},
+        {"dw", dw, es * (size_t)C, true},
+        {"db", db, es * (size_t)C, true},
+        {"workspace", workspace, need, true},
+        {"dy", dy, extent(N, strides[0], P, strides[1], 1, 0, C, es), false},
+        {"x", x, extent(N, strides[2], P, strides[3], 1, 0, C, es), false},
+        {"stats", stats, 8 * (size_t)(N * G), false},
+        {"weight", weight, es * (size_t)C, false},
+        {"bias", bias, es * (size_t)C, false},
+        {"lengths", lengths, 4 * (size_t)N, false},
+    };
+    if ((st = check_ranges(ranges, sizeof(ranges) / sizeof(ranges[0]))) != GCONV_OK) return st;
+    gconv::GroupNormArgs a = {};
+    a.x = x; a.dy = dy; a.weight = weight; a.bias = bias; a.stats = stats; a.y = dx; a.dw = dw; a.db = db; a.lengths = lengths;
+    a.ws = workspace;
+    a.N = N; a.P = P; a.C = C; a.G = G; a.dsb = strides[0]; a.dst = strides[1]; a.xsb = strides[2]; a.xst = strides[3];
+    a.silu = activation == GCONV_ACT_SILU; a.dtype = (int)dtype; a.stream = (hipStream_t)hip_stream;
+    if ((st = gn_check(a, g)) != GCONV_OK) return st;
+    const char *kname = "";
+    const hipError_t err = gconv::launch_group_norm_bwd(a, g, &kname);
     return done(err, kname);
 }
 

@@ -1,0 +1,652 @@
+// group_norm.hip -- group norm with an activation over channels-last tensors [N][P][C]:
+//     y = act(w (x - mean) rstd + b),   mean and rstd = 1 / sqrt(var + eps) of a sample's group
+// (its positions that exist times C / G channels), and its gradients.
+//
+// A workgroup takes a slab: the positions of one sample (or a chunk of them) times a bundle of
+// whole groups.  A thread keeps one vector of V channels, all of one group, for every R-th
+// position in registers.  Where a sample's bundle fits (up to 256 KB of registers) everything
+// happens in one launch, x is read once and y written once; else one launch takes the statistics
+// of chunks and a second one joins them and reads x again, which the last-level cache holds for
+// tensors up to its 256 MB.
+//
+// Statistics: a thread's sum, and its squares about its own mean; joined exactly,
+//     M2 = sum over threads of M2_t + n_t (mean_t - mean)^2,
+// so an offset much larger than the spread costs nothing.  The order of addition is fixed.
+//
+// Gradients: with xhat = (x - mean) rstd, dz = dy act'(w xhat + b), m = positions times channels,
+//     dx = rstd (w dz - S1 / m - xhat S2 / m),  S1 = sum of w dz,  S2 = sum of w dz xhat,
+//     dw = sum of dz xhat,  db = sum of dz  over samples and positions.
+// dw and db leave each workgroup as fp32 partial sums; a last launch adds them in order.
+//
+// Bound by HBM; with silu two quarter-rate instructions an element, four in gradients.
+#include <algorithm>
+
+#include "block.hpp"
+
+namespace gconv {
+namespace {
+
+template <int BYTES> struct Words;
+template <> struct Words<2> { typedef uint16_t type; };
+template <> struct Words<4> { typedef uint32_t type __attribute__((aligned(2))); };
+template <> struct Words<8> { typedef uint32_t type __attribute__((ext_vector_type(2), aligned(2))); };
+template <> struct Words<16> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2))); };
+template <typename T, int V> struct Vec { T v[V]; };
+
+template <typename T, int V> __device__ __forceinline__ Vec<T, V> load_vec(const char *p)
+{
+    typedef typename Words<V * sizeof(T)>::type W;
+    return __builtin_bit_cast(Vec<T, V>, *reinterpret_cast<const W *>(p));
+}
+template <typename T, int V> __device__ __forceinline__ void store_vec(char *p, const float (&f)[V])
+{
+    typedef typename Words<V * sizeof(T)>::type W;
+    Vec<T, V> r;
+#pragma unroll
+    for (int k = 0; k < V; ++k) r.v[k] = from_f32<T>(f[k]);
+    *reinterpret_cast<W *>(p) = __builtin_bit_cast(W, r);
+}
+
+__device__ __forceinline__ float sigmoid(float z)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * z));
+}
+
+// One position after the other: the temporaries of all at once would not fit beside the data.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// What a second pass over the registers computes it computes again: kept from the first, the fp32
+// values of 16-bit data would take twice their registers.
+template <typename T, int V, int K> __device__ __forceinline__ void forget(Vec<T, V> (&raw)[K])
+{
+    typedef typename Words<V * sizeof(T)>::type W;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        if constexpr (sizeof(W) > 4) {
+            W w = __builtin_bit_cast(W, raw[j]);
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(W) / 4; ++i) {
+                uint32_t u = w[i];
+                asm volatile("" : "+v"(u));
+                w[i] = u;
+            }
+            raw[j] = __builtin_bit_cast(Vec<T, V>, w);
+        } else {
+            uint32_t u = (uint32_t)__builtin_bit_cast(W, raw[j]);
+            asm volatile("" : "+v"(u));
+            raw[j] = __builtin_bit_cast(Vec<T, V>, (W)u);
+        }
+    }
+}
+
+struct Norm {
+    const char *x, *dy, *w, *b;          // b may be nullptr
+    char *y;                             // or dx
+    const float *stats;                  // backward: (mean, rstd) [N][G][2]
+    float *stats_out;                    // forward: the same, or nullptr
+    float2 *chunk;                       // of chunks: (mean, M2), or (S1, S2) [N][G][chunks * parts]
+    float *part;                         // (dw, db) [rows][2][C]
+    const int32_t *lengths;
+    int64_t N, P, C, blocks, rows, range;   // rows of `part`, samples of each
+    int64_t xsb, xst, dsb, dst;          // bytes
+    int32_t G, cg, kg, bundles, cols, R, parts, chunks, chunk_rows;
+    float eps;
+    int32_t silu;
+};
+
+constexpr int kMaxThreads = 1024;
+
+// What a workgroup is to do with its slab.
+enum { kWholeSample = 0, kChunkStats = 1, kChunkApply = 2 };
+
+struct Slab {
+    int64_t n;             // sample (backward: the first of a range)
+    int32_t chunk, bundle, part;
+    int32_t first;         // position
+    int32_t rows;          // positions that the chunk has
+    int32_t c0;            // channel of the slab
+    int32_t cols;          // vectors of a row
+    int32_t groups;
+};
+
+__device__ __forceinline__ bool find_slab(const Norm &p, Slab &s)
+{
+    // Neighbouring bundles, which may share lines, on one XCD.
+    const int64_t per = (p.blocks + 7) / 8, id = (int64_t)(blockIdx.x % 8) * per + blockIdx.x / 8;
+    if (blockIdx.x / 8 >= per || id >= p.blocks) return false;
+    const int64_t rest = id / p.bundles;
+    const int at = (int)(id - rest * p.bundles);
+    s.part = at % p.parts;
+    s.bundle = at / p.parts;
+    s.n = rest / p.chunks;
+    s.chunk = (int)(rest - s.n * p.chunks);
+    s.first = s.chunk * p.chunk_rows;
+    s.rows = (int)min((int64_t)p.chunk_rows, p.P - s.first);
+    return true;
+}
+
+template <int V> __device__ __forceinline__ void slab_columns(const Norm &p, Slab &s)
+{
+    s.groups = min(p.kg, p.G - s.bundle * p.kg);
+    s.c0 = s.bundle * p.kg * p.cg + s.part * p.cols * V;
+    s.cols = p.parts > 1 ? min(p.cols, p.cg / V - s.part * p.cols) : s.groups * (p.cg / V);
+}
+
+__device__ __forceinline__ int live_rows(const Norm &p, int64_t n, const Slab &s)
+{
+    int64_t live = p.P;
+    if (p.lengths) live = max((int64_t)0, min(p.P, (int64_t)p.lengths[n]));
+    return (int)max((int64_t)0, min((int64_t)s.rows, live - s.first));
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int d = 32; d; d /= 2) v += __shfl_xor(v, d);
+    return v;
+}
+
+// Threads of a group, in the order in which a wave takes them: lane, lane + 64, ...
+struct Members {
+    int r, j, dr, dj, width, R;
+    __device__ Members(int lane, int width, int R) : width(width), R(R)
+    {
+        r = lane / width; j = lane - r * width;
+        dr = 64 / width; dj = 64 - dr * width;
+    }
+    __device__ bool on() const { return r < R; }
+    __device__ void next()
+    {
+        r += dr; j += dj;
+        if (j >= width) { j -= width; ++r; }
+    }
+};
+
+// Elements of a thread that starts at row r of `live` rows, R apart.
+__device__ __forceinline__ float count_of(int r, int live, int R, int V) { return r < live ? (float)(V * ((live - 1 - r) / R + 1)) : 0.0f; }
+
+// Sums of two values over the threads of each group: written to out[group] by its wave.
+template <int V>
+__device__ __forceinline__ void group_sums(const Norm &p, const Slab &s, int tid, float a, float b, float2 *mine, float2 *out)
+{
+    mine[tid] = make_float2(a, b);
+    __syncthreads();
+    const int lane = tid % 64, width = p.parts > 1 ? s.cols : p.cg / V;
+    for (int g = tid / 64; g < s.groups; g += blockDim.x / 64) {
+        float sa = 0.0f, sb = 0.0f;
+        for (Members m(lane, width, p.R); m.on(); m.next()) {
+            const float2 v = mine[m.r * p.cols + g * width + m.j];
+            sa += v.x;
+            sb += v.y;
+        }
+        sa = wave_sum(sa);
+        sb = wave_sum(sb);
+        if (lane == 0) out[g] = make_float2(sa, sb);
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- forward
+
+template <typename T, int V, int K, int WHAT>
+__global__ __launch_bounds__(kMaxThreads) void gn_forward(const Norm p)
+{
+    __shared__ float2 mine[kMaxThreads];
+    __shared__ float2 out[kMaxThreads];
+    Slab s;
+    if (!find_slab(p, s)) return;
+    slab_columns<V>(p, s);
+    const int tid = threadIdx.x, lane = tid % 64, r0 = tid / p.cols, col = tid - r0 * p.cols;
+    const int live = live_rows(p, s.n, s), width = p.parts > 1 ? s.cols : p.cg / V;
+    const bool on = r0 < p.R && col < s.cols;
+    const int64_t c = s.c0 + (int64_t)col * V;
+    const char *const x = p.x + s.n * p.xsb + s.first * p.xst + s.c0 * (int64_t)sizeof(T);
+    const uint32_t from = (uint32_t)r0 * (uint32_t)p.xst + (uint32_t)(col * V * sizeof(T));
+    Vec<T, V> raw[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+        if (on && r0 + j * p.R < live) raw[j] = load_vec<T, V>(x + j * (p.R * p.xst) + from);
+
+    if constexpr (WHAT != kChunkApply) {
+        float sum = 0.0f, m2 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if (on && r0 + j * p.R < live)
+#pragma unroll
+                for (int k = 0; k < V; ++k) sum += to_f32(raw[j].v[k]);
+        forget<T, V, K>(raw);
+        const float own = on ? sum / fmaxf(count_of(r0, live, p.R, V), 1.0f) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if (on && r0 + j * p.R < live)
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float d = to_f32(raw[j].v[k]) - own;
+                    m2 = fmaf(d, d, m2);
+                }
+        keep_order();
+        mine[tid] = make_float2(sum, m2);
+        forget<T, V, K>(raw);
+        __syncthreads();
+        const float total = (float)live * (width * V);
+        for (int g = tid / 64; g < s.groups; g += blockDim.x / 64) {
+            float a = 0.0f, q = 0.0f;
+            for (Members m(lane, width, p.R); m.on(); m.next()) a += mine[m.r * p.cols + g * width + m.j].x;
+            const float mean = wave_sum(a) / fmaxf(total, 1.0f);
+            for (Members m(lane, width, p.R); m.on(); m.next()) {
+                const float2 v = mine[m.r * p.cols + g * width + m.j];
+                const float n = count_of(m.r, live, p.R, V);
+                if (n > 0.0f) {
+                    const float d = v.x / n - mean;
+                    q += fmaf(n * d, d, v.y);
+                }
+            }
+            q = wave_sum(q);
+            const int64_t at = s.n * p.G + s.bundle * p.kg + g;
+            if constexpr (WHAT == kChunkStats) {
+                if (lane == 0) p.chunk[at * (p.chunks * p.parts) + s.chunk * p.parts + s.part] = make_float2(mean, q);
+            } else if (lane == 0) {
+                const float2 v = make_float2(mean, 1.0f / sqrtf(q / fmaxf(total, 1.0f) + p.eps));
+                out[g] = v;
+                if (p.stats_out) reinterpret_cast<float2 *>(p.stats_out)[at] = v;
+            }
+        }
+        if constexpr (WHAT == kChunkStats) return;
+    } else {
+        // Statistics of the chunks, joined as those of threads are.
+        int64_t all = p.P;
+        if (p.lengths) all = max((int64_t)0, min(p.P, (int64_t)p.lengths[s.n]));
+        const int slots = p.chunks * p.parts;
+        const float total = fmaxf((float)all * p.cg, 1.0f);
+        auto size = [&](int i) {        // elements of slot i
+            const int ch = i / p.parts, pt = i - ch * p.parts;
+            const int64_t first = (int64_t)ch * p.chunk_rows;
+            const int64_t r = max((int64_t)0, min(min((int64_t)p.chunk_rows, p.P - first), all - first));
+            return (float)r * (p.parts > 1 ? min(p.cols * V, p.cg - pt * p.cols * V) : p.cg);
+        };
+        for (int g = tid / 64; g < s.groups; g += blockDim.x / 64) {
+            const int64_t at = s.n * p.G + s.bundle * p.kg + g;
+            const float2 *const mine_of = p.chunk + at * slots;
+            float a = 0.0f, q = 0.0f;
+            for (int i = lane; i < slots; i += 64) a = fmaf(size(i), mine_of[i].x, a);
+            const float mean = wave_sum(a) / total;
+            for (int i = lane; i < slots; i += 64) {
+                const float2 v = mine_of[i];
+                const float d = v.x - mean;
+                q += fmaf(size(i) * d, d, v.y);
+            }
+            q = wave_sum(q);
+            if (lane == 0) {
+                const float2 v = make_float2(mean, 1.0f / sqrtf(q / total + p.eps));
+                out[g] = v;
+                if (p.stats_out && s.chunk == 0 && s.part == 0) reinterpret_cast<float2 *>(p.stats_out)[at] = v;
+            }
+        }
+        forget<T, V, K>(raw);
+    }
+    __syncthreads();
+    if (!on) return;
+    const float2 st = out[p.parts > 1 ? 0 : col / width];
+    const Vec<T, V> w = load_vec<T, V>(p.w + c * (int64_t)sizeof(T));
+    Vec<T, V> b = {};
+    if (p.b) b = load_vec<T, V>(p.b + c * (int64_t)sizeof(T));
+    char *const y = p.y + ((s.n * p.P + s.first) * p.C + s.c0) * (int64_t)sizeof(T);
+    const int64_t row = p.C * (int64_t)sizeof(T);
+    const uint32_t to = (uint32_t)r0 * (uint32_t)row + (uint32_t)(col * V * sizeof(T));
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const int r = r0 + j * p.R;
+        if (r >= s.rows) continue;
+        float f[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float z = fmaf((to_f32(raw[j].v[k]) - st.x) * st.y, to_f32(w.v[k]), to_f32(b.v[k]));
+            f[k] = r < live ? (p.silu ? z * sigmoid(z) : z) : 0.0f;
+        }
+        store_vec<T, V>(y + j * (p.R * row) + to, f);
+        keep_order();
+    }
+}
+
+// ---------------------------------------------------------------- backward
+
+template <typename T, int V>
+__device__ __forceinline__ void slopes(const Vec<T, V> &x, const Vec<T, V> &dy, const float (&w)[V], const float (&b)[V], float2 st,
+                                       int silu, float (&hat)[V], float (&dz)[V])
+{
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        hat[k] = (to_f32(x.v[k]) - st.x) * st.y;
+        dz[k] = to_f32(dy.v[k]);
+        if (silu) {
+            const float z = fmaf(hat[k], w[k], b[k]), sg = sigmoid(z);
+            dz[k] *= fmaf(z * sg, 1.0f - sg, sg);
+        }
+    }
+}
+
+// Sums of each column's values over the rows of threads: col_sums[0..cols V) of `out`, for the
+// thread's own V values.
+template <int V>
+__device__ __forceinline__ void column_sums(const Norm &p, const Slab &s, int tid, int r0, int col, const float (&v)[V], float *mine,
+                                            float *out)
+{
+    const int W = s.cols * V, step = p.cols * V;
+    __syncthreads();
+    if (r0 < p.R && col < s.cols)
+#pragma unroll
+        for (int k = 0; k < V; ++k) mine[r0 * step + col * V + k] = v[k];
+    __syncthreads();
+    // The rows in `parts` interleaved shares, then the shares.
+    const int parts = min(p.R, max(1, (int)blockDim.x / W));
+    for (int u = tid; u < W * parts; u += blockDim.x) {
+        const int part = u / W, c = u - part * W;
+        float a = 0.0f;
+        for (int r = part; r < p.R; r += parts) a += mine[r * step + c];
+        mine[part * step + c] = a;      // this thread's own first row
+    }
+    __syncthreads();
+    for (int c = tid; c < W; c += blockDim.x) {
+        float a = 0.0f;
+        for (int r = 0; r < parts; ++r) a += mine[r * step + c];
+        out[c] = a;
+    }
+}
+
+template <typename T, int V, int K, int WHAT>
+__global__ __launch_bounds__(kMaxThreads) void gn_backward(const Norm p)
+{
+    __shared__ float2 mine[kMaxThreads];
+    __shared__ float2 out[kMaxThreads];
+    __shared__ float cells[WHAT == kChunkApply ? 1 : kMaxThreads * V];
+    Slab s;
+    if (!find_slab(p, s)) return;
+    slab_columns<V>(p, s);
+    const int tid = threadIdx.x, lane = tid % 64, r0 = tid / p.cols, col = tid - r0 * p.cols;
+    const int width = p.parts > 1 ? s.cols : p.cg / V;
+    const bool on = r0 < p.R && col < s.cols;
+    const int64_t c = s.c0 + (int64_t)col * V, row = p.C * (int64_t)sizeof(T);
+    const int g = on ? (p.parts > 1 ? 0 : col / width) : 0;
+    const uint32_t at0 = (uint32_t)(col * V * sizeof(T)), xat = (uint32_t)r0 * (uint32_t)p.xst + at0,
+                   dat = (uint32_t)r0 * (uint32_t)p.dst + at0, to = (uint32_t)r0 * (uint32_t)row + at0;
+    float w[V] = {}, b[V] = {}, dw[V] = {}, db[V] = {};
+    if (on) {
+        const Vec<T, V> wr = load_vec<T, V>(p.w + c * (int64_t)sizeof(T));
+        Vec<T, V> br = {};
+        if (p.b) br = load_vec<T, V>(p.b + c * (int64_t)sizeof(T));
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            w[k] = to_f32(wr.v[k]);
+            b[k] = to_f32(br.v[k]);
+        }
+    }
+    // Whole samples: a range of them, their dw and db added up on the way.
+    const int64_t from = WHAT == kWholeSample ? s.n * p.range : s.n, past = WHAT == kWholeSample ? min(from + p.range, p.N) : s.n + 1;
+    for (int64_t n = from; n < past; ++n) {
+        const int live = live_rows(p, n, s);
+        const char *const x = p.x + n * p.xsb + s.first * p.xst + s.c0 * (int64_t)sizeof(T);
+        const char *const dy = p.dy + n * p.dsb + s.first * p.dst + s.c0 * (int64_t)sizeof(T);
+        Vec<T, V> xr[K], dr[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if (on && r0 + j * p.R < live) {
+                xr[j] = load_vec<T, V>(x + j * (p.R * p.xst) + xat);
+                dr[j] = load_vec<T, V>(dy + j * (p.R * p.dst) + dat);
+            }
+        const int64_t at = n * p.G + s.bundle * p.kg;
+        const float2 st = reinterpret_cast<const float2 *>(p.stats)[at + g];
+        if constexpr (WHAT != kChunkApply) {
+            float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (on && r0 + j * p.R < live) {
+                    float hat[V], dz[V];
+                    slopes<T, V>(xr[j], dr[j], w, b, st, p.silu, hat, dz);
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        const float t = w[k] * dz[k];
+                        s1 += t;
+                        s2 = fmaf(t, hat[k], s2);
+                        dw[k] = fmaf(dz[k], hat[k], dw[k]);
+                        db[k] += dz[k];
+                    }
+                    keep_order();
+                }
+            group_sums<V>(p, s, tid, s1, s2, mine, out);
+            forget<T, V, K>(xr);
+            forget<T, V, K>(dr);
+            if constexpr (WHAT == kChunkStats) {
+                if (tid < s.groups) p.chunk[(at + tid) * (p.chunks * p.parts) + s.chunk * p.parts + s.part] = out[tid];
+            }
+        } else {
+            const int slots = p.chunks * p.parts;
+            for (int k = tid / 64; k < s.groups; k += blockDim.x / 64) {
+                float s1 = 0.0f, s2 = 0.0f;
+                for (int i = lane; i < slots; i += 64) {
+                    const float2 v = p.chunk[(at + k) * slots + i];
+                    s1 += v.x;
+                    s2 += v.y;
+                }
+                s1 = wave_sum(s1);
+                s2 = wave_sum(s2);
+                if (lane == 0) out[k] = make_float2(s1, s2);
+            }
+            forget<T, V, K>(xr);
+            forget<T, V, K>(dr);
+            __syncthreads();
+        }
+        if constexpr (WHAT != kChunkStats) {
+            int64_t all = p.P;
+            if (p.lengths) all = max((int64_t)0, min(p.P, (int64_t)p.lengths[n]));
+            const float inv = 1.0f / fmaxf((float)all * p.cg, 1.0f);
+            const float m1 = out[g].x * inv, m2 = out[g].y * inv;
+            char *const dx = p.y + ((n * p.P + s.first) * p.C + s.c0) * (int64_t)sizeof(T);
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                const int r = r0 + j * p.R;
+                if (!on || r >= s.rows) continue;
+                float hat[V], dz[V], f[V];
+                slopes<T, V>(xr[j], dr[j], w, b, st, p.silu, hat, dz);
+#pragma unroll
+                for (int k = 0; k < V; ++k) f[k] = r < live ? st.y * (fmaf(w[k], dz[k], -m1) - hat[k] * m2) : 0.0f;
+                store_vec<T, V>(dx + j * (p.R * row) + to, f);
+                keep_order();
+            }
+            if constexpr (WHAT == kWholeSample) __syncthreads();      // `out` is read before the next sample's
+        }
+    }
+    if constexpr (WHAT != kChunkApply) {
+        const int64_t line = WHAT == kWholeSample ? s.n : s.n * p.chunks + s.chunk;
+        float *const o = p.part + line * 2 * p.C + s.c0;
+        column_sums<V>(p, s, tid, r0, col, dw, cells, o);
+        column_sums<V>(p, s, tid, r0, col, db, cells, o + p.C);
+    }
+}
+
+// Partial sums [rows][2][C] -> dw [C], db [C] (or nullptr), in order: 16 rows at a time, then those 16.
+template <typename T>
+__global__ __launch_bounds__(256) void gn_param_sum(const float *__restrict__ part, T *__restrict__ dw, T *__restrict__ db, int64_t rows,
+                                                    int64_t C)
+{
+    __shared__ float s[16][17];
+    const int col = threadIdx.x % 16, row = threadIdx.x / 16;
+    const int64_t c = (int64_t)blockIdx.x * 16 + col;
+    float v = 0.0f;
+    if (c < 2 * C)
+        for (int64_t r = row; r < rows; r += 16) v += part[r * 2 * C + c];
+    s[row][col] = v;
+    __syncthreads();
+    if (row == 0 && c < 2 * C) {
+        for (int r = 1; r < 16; ++r) v += s[r][col];
+        if (c < C) dw[c] = from_f32<T>(v);
+        else if (db) db[c - C] = from_f32<T>(v);
+    }
+}
+
+// ---------------------------------------------------------------- plans and launches
+
+template <int N> struct Int { static constexpr int value = N; };
+
+template <typename F> hipError_t with_vec(int dtype, int V, F &&f)
+{
+    auto by = [&](auto t) {
+        if constexpr (sizeof(t) == 2)
+            if (V == 8) return f(t, Int<8>{});
+        return V == 4 ? f(t, Int<4>{}) : V == 2 ? f(t, Int<2>{}) : f(t, Int<1>{});
+    };
+    return dtype == DT_F32 ? by(float{}) : dtype == DT_F16 ? by(_Float16{}) : by(__bf16{});
+}
+template <typename F> hipError_t with_rows(int K, F &&f)
+{
+    return K <= 1 ? f(Int<1>{}) : K <= 4 ? f(Int<4>{}) : K <= 8 ? f(Int<8>{}) : f(Int<16>{});
+}
+
+template <int WHAT> hipError_t run_forward(const Norm &p, int dtype, int V, int threads, int K, hipStream_t stream)
+{
+    const dim3 grid((unsigned)(8 * ceil_div(p.blocks, 8)));
+    return with_vec(dtype, V, [&](auto t, auto v) {
+        return with_rows(K, [&](auto k) {
+            if constexpr (WHAT != kWholeSample && k.value == 16) return hipErrorInvalidValue;     // no plan has it
+            else {
+                gn_forward<decltype(t), v.value, k.value, WHAT><<<grid, threads, 0, stream>>>(p);
+                return hipGetLastError();
+            }
+        });
+    });
+}
+
+template <int WHAT> hipError_t run_backward(const Norm &p, int dtype, int V, int threads, int K, hipStream_t stream)
+{
+    const dim3 grid((unsigned)(8 * ceil_div(p.blocks, 8)));
+    return with_vec(dtype, V, [&](auto t, auto v) {
+        return with_rows(K, [&](auto k) {
+            if constexpr (k.value == 16) return hipErrorInvalidValue;        // no plan has it
+            else {
+                gn_backward<decltype(t), v.value, k.value, WHAT><<<grid, threads, 0, stream>>>(p);
+                return hipGetLastError();
+            }
+        });
+    });
+}
+
+Norm make_norm(const GroupNormArgs &a, const GroupNormPlan &g)
+{
+    const int64_t es = a.dtype == DT_F32 ? 4 : 2;
+    Norm p = {};
+    p.x = (const char *)a.x; p.dy = (const char *)a.dy; p.w = (const char *)a.weight; p.b = (const char *)a.bias; p.y = (char *)a.y;
+    p.stats = a.stats; p.stats_out = a.stats_out; p.lengths = a.lengths;
+    p.N = a.N; p.P = a.P; p.C = a.C; p.G = (int32_t)a.G; p.cg = (int32_t)(a.C / a.G);
+    p.xsb = a.xsb * es; p.xst = a.P > 1 ? a.xst * es : 0; p.dsb = a.dsb * es; p.dst = a.P > 1 ? a.dst * es : 0;
+    p.kg = g.kg; p.cols = g.cols; p.R = g.threads / g.cols; p.parts = g.parts; p.chunks = g.chunks; p.chunk_rows = g.chunk_rows;
+    p.bundles = (int32_t)ceil_div(a.G, g.kg) * g.parts;
+    p.range = g.range;
+    p.blocks = ceil_div(a.N, g.range) * g.chunks * p.bundles;
+    p.rows = ceil_div(a.N, g.range) * g.chunks;
+    p.eps = a.eps; p.silu = a.silu;
+    p.chunk = (float2 *)a.ws;
+    p.part = (float *)((char *)a.ws + gn_chunk_bytes(g, a.N, a.G));
+    return p;
+}
+
+}  // namespace
+
+size_t gn_chunk_bytes(const GroupNormPlan &g, int64_t N, int64_t G)
+{
+    const int64_t slots = (int64_t)g.chunks * g.parts;
+    return slots > 1 ? (sizeof(float2) * (size_t)(N * G * slots) + 255) & ~(size_t)255 : 0;
+}
+
+GroupNormPlan gn_plan(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, bool backward)
+{
+    const int es = dtype == DT_F32 ? 4 : 2;
+    const int64_t cg = C / G;
+    GroupNormPlan g = {};
+    g.V = 16 / es;
+    while (cg % g.V) g.V /= 2;
+    const int64_t cgv = cg / g.V;
+    const int most = backward ? 8 : 16;      // vectors of a thread, of each tensor
+    g.parts = (int32_t)ceil_div(cgv, kMaxThreads);
+    g.range = 1;
+    g.chunks = 1;
+    g.chunk_rows = (int32_t)P;
+    if (g.parts == 1) {
+        // Rows of a line (128 bytes) at least, and a wave's worth of vectors.
+        for (int64_t bytes : {int64_t(128), int64_t(64), cg * es}) {
+            int64_t kg = std::min(G, std::max(ceil_div(bytes, cg * es), ceil_div(64, cgv * std::max<int64_t>(P, 1))));
+            kg = std::max<int64_t>(1, std::min(kg, kMaxThreads / cgv));
+            const int64_t cols = kg * cgv;
+            for (int want : {backward ? 4 : 8, most})
+                for (int t = 64; t <= kMaxThreads; t *= 2) {
+                    if (t < cols || (want == most && t < kMaxThreads)) continue;
+                    const int64_t R = t / cols, K = ceil_div(std::max<int64_t>(P, 1), R);
+                    if (K > want) continue;
+                    g.kg = (int32_t)kg; g.cols = (int32_t)cols; g.threads = t; g.K = (int32_t)K;
+                    if (backward) {     // samples of a workgroup: enough workgroups, few partial sums
+                        const int64_t bundles = ceil_div(G, kg), held = 256 * (2048 / t);
+                        g.range = std::max<int64_t>(1, ceil_div(N * bundles, held));
+                    }
+                    return g;
+                }
+        }
+    }
+    // Chunks of positions: rows as wide as 64 lanes take.
+    g.kg = g.parts > 1 ? 1 : (int32_t)std::max<int64_t>(1, std::min(G, 64 / cgv));
+    g.cols = (int32_t)(g.parts > 1 ? ceil_div(cgv, g.parts) : g.kg * cgv);
+    g.threads = (int32_t)std::max<int64_t>(512, 64 * ceil_div(g.cols, 64));
+    if (g.threads > 512) g.threads = kMaxThreads;
+    g.K = backward ? 4 : 8;
+    const int64_t R = g.threads / g.cols;
+    g.chunk_rows = (int32_t)std::min<int64_t>(R * g.K, std::max<int64_t>(P, 1));
+    g.chunks = (int32_t)ceil_div(std::max<int64_t>(P, 1), g.chunk_rows);
+    return g;
+}
+
+size_t gn_workspace(const GroupNormPlan &g, int64_t N, int64_t C, int64_t G, bool backward)
+{
+    return gn_chunk_bytes(g, N, G) + (backward ? sizeof(float) * 2 * (size_t)(ceil_div(N, g.range) * g.chunks * C) : 0);
+}
+
+bool gn_fits(const GroupNormArgs &a, const GroupNormPlan &g)
+{
+    // A thread's first position lies within 2^31 bytes of its workgroup's.
+    const int64_t es = a.dtype == DT_F32 ? 4 : 2, top = ((int64_t(1) << 31) - 1) / es / 2, R = g.threads / g.cols;
+    for (int64_t st : {a.P > 1 ? a.xst : 0, a.P > 1 ? a.dst : 0, a.C})
+        if (st > top / R) return false;
+    return grid_fits(8 * ceil_div(ceil_div(a.N, g.range) * g.chunks * ceil_div(a.G, g.kg) * g.parts, 8), g.threads);
+}
+
+hipError_t launch_group_norm(const GroupNormArgs &a, const GroupNormPlan &g, const char **kname)
+{
+    const Norm p = make_norm(a, g);
+    if (g.chunks * g.parts == 1) {
+        *kname = "gn_forward";
+        return run_forward<kWholeSample>(p, a.dtype, g.V, g.threads, g.K, a.stream);
+    }
+    *kname = "gn_forward_chunks";
+    const hipError_t err = run_forward<kChunkStats>(p, a.dtype, g.V, g.threads, g.K, a.stream);
+    return err != hipSuccess ? err : run_forward<kChunkApply>(p, a.dtype, g.V, g.threads, g.K, a.stream);
+}
+
+hipError_t launch_group_norm_bwd(const GroupNormArgs &a, const GroupNormPlan &g, const char **kname)
+{
+    const Norm p = make_norm(a, g);
+    *kname = g.chunks * g.parts == 1 ? "gn_backward" : "gn_backward_chunks";
+    if (p.blocks > 0) {
+        hipError_t err;
+        if (g.chunks * g.parts == 1) {
+            err = run_backward<kWholeSample>(p, a.dtype, g.V, g.threads, g.K, a.stream);
+        } else {
+            err = run_backward<kChunkStats>(p, a.dtype, g.V, g.threads, g.K, a.stream);
+            if (err == hipSuccess) err = run_backward<kChunkApply>(p, a.dtype, g.V, g.threads, g.K, a.stream);
+        }
+        if (err != hipSuccess) return err;
+    }
+    const unsigned grid = (unsigned)ceil_div(2 * a.C, 16);
+    return with_vec(a.dtype, 1, [&](auto t, auto) {
+        typedef decltype(t) E;
+        gn_param_sum<E><<<grid, 256, 0, a.stream>>>(p.part, (E *)a.dw, (E *)a.db, p.rows, a.C);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace gconv

@@ -422,6 +422,28 @@ gconv_status_t gconv_gated_recurrence_step(const void *x, const void *r, const v
                                            float *state, void *h, const int64_t *shape, const int64_t *strides,
                                            const int32_t *slots, gconv_dtype_t dtype, void *hip_stream);
 
+/* Group norm with an activation over channels-last tensors.  shape = {N, P, C, G}: x, y [N,P,C]
+ * (strides = {x sample, x position}), P positions a sample (1: a row is normed by itself), G groups of
+ * C / G channels, weight [C], bias [C] or NULL:
+ *     y = act(weight (x - mean) / sqrt(var + eps) + bias)
+ * mean and var (biased) over the positions that exist (lengths: int32 [N], or NULL: P) and the channels
+ * of a group.  stats: fp32 [N,G,2] = (mean, 1 / sqrt(var + eps)), or NULL.  A sample without positions
+ * has mean 0 and variance 0.  A value that is not finite reaches its sample's group only.  C at most
+ * 2^20.  workspace: gconv_group_norm_workspace bytes (may be 0), 16-byte aligned. */
+gconv_status_t gconv_group_norm_workspace(const int64_t *shape, gconv_dtype_t dtype, int32_t backward, size_t *bytes);
+gconv_status_t gconv_group_norm(const void *x, const void *weight, const void *bias, void *y, float *stats,
+                                const int64_t *shape, const int64_t *strides, const int32_t *lengths, float eps,
+                                gconv_act_t activation, gconv_dtype_t dtype, void *workspace,
+                                size_t workspace_bytes, void *hip_stream);
+
+/* Its gradients: dx [N,P,C], dw [C] and db [C] (with a bias, else NULL) from the gradient dy of y and the
+ * stats of the forward call.  strides = {dy sample, dy position, x sample, x position}. */
+gconv_status_t gconv_group_norm_backward(const void *dy, const void *x, const void *weight, const void *bias,
+                                         const float *stats, void *dx, void *dw, void *db, const int64_t *shape,
+                                         const int64_t *strides, const int32_t *lengths, gconv_act_t activation,
+                                         gconv_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                         void *hip_stream);
+
 /* Name of the kernel the last successful gconv_fwd / gconv_fwd_route / gconv_fwd_ex /
  * gconv_dw1d_bwd_data / gconv_dw1d_bwd_filter call on this host thread launched
  * (the first of two for the filter gradient; "" before the first call or after
