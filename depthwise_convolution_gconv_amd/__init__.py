@@ -42,6 +42,8 @@ from ._block import (  # noqa: F401
     group_norm,
     group_norm_backward,
     group_norm_workspace,
+    matmul_int8,
+    quantize_int8,
 )
 from ._sequence import (  # noqa: F401
     dwconv1d_causal,

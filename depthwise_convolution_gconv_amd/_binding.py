@@ -36,6 +36,7 @@ EXPORTS = ("gconv_out_shape", "gconv_select_route", "gconv_fwd", "gconv_fwd_rout
            "gconv_gated_recurrence_workspace", "gconv_gated_recurrence", "gconv_gated_recurrence_backward",
            "gconv_gated_recurrence_step",
            "gconv_group_norm_workspace", "gconv_group_norm", "gconv_group_norm_backward",
+           "gconv_quantize_int8", "gconv_matmul_int8",
            "gconv_last_kernel", "gconv_status_string", "gconv_last_error")
 
 _i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p

@@ -1,5 +1,5 @@
-"""Operators of a recurrent mixing block in libgconv.so: the gated linear recurrence, and group
-norm with an activation over channels-last tensors.
+"""Operators of a recurrent mixing block in libgconv.so: the gated linear recurrence, group
+norm with an activation over channels-last tensors, and the product in 8-bit integers.
 
 Argument checks and marshalling only, in the manner of the other sequence operators: the
 caller's current device and stream, or `stream`; outputs and workspaces from torch.
@@ -12,8 +12,8 @@ from typing import Optional
 import torch
 
 from ._binding import DTYPES, _check, _i32, _i64, _i64p, _vp, lib
-from ._sequence import (ACTIVATIONS, _array, _bad, _device, _dtype, _f32, _like, _on_stream, _ptr, _raw_stream, _size,
-                        _view, _whole, _workspace)
+from ._sequence import (ACTIVATIONS, _array, _bad, _device, _dtype, _f32, _like, _on_stream, _ptr, _raw_stream, _rows,
+                        _size, _view, _whole, _workspace)
 
 _fns = None
 
@@ -32,6 +32,8 @@ def _library():
             "gconv_group_norm_workspace": [_i64p, _i32, _i32, sizep],
             "gconv_group_norm": [_vp] * 5 + [_i64p, _i64p, _vp, _f32, _i32, _i32, _vp, _size, _vp],
             "gconv_group_norm_backward": [_vp] * 8 + [_i64p, _i64p, _vp, _i32, _i32, _vp, _size, _vp],
+            "gconv_quantize_int8": [_vp] * 3 + [_i64, _i64, _i64, _i32, _vp],
+            "gconv_matmul_int8": [_vp] * 6 + [_i64p, _i32, _vp],
         }.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -244,3 +246,60 @@ def group_norm_backward(dy, x, groups: int, weight, bias, stats, activation: Opt
     _check(L.gconv_group_norm_backward(dy.data_ptr(), x.data_ptr(), w, b, st, dx.data_ptr(), dw.data_ptr(), _ptr(db), sh,
                                        _array(*ds, *strides), n, act, dt, _ptr(ws), need.value, _raw_stream(dev)))
     return dx, dw, db
+
+
+# ---------------------------------------------------------------- product in 8-bit integers
+
+def quantize_int8(x, stream=None):
+    """Rows of x [..., K] as 8-bit integers: (q int8 [..., K], scales fp32 [..., 1]) with
+    scale = max(max|row|, 2^-100) / 127 and q = x / scale, each quotient fp32's own, rounded to
+    the nearest integer (ties to even); x is about q * scale.  x's rows may lie at any one stride.
+    A value that is not finite makes its row's scale that, and q without meaning."""
+    if stream is not None:
+        return _on_stream(stream, x, quantize_int8, x)
+    dt = _dtype("x", x)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        _bad("x must be [..., K] with K >= 1")
+    K, dev = x.shape[-1], x.get_device()
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return quantize_int8(x)
+    xs = _rows("x", x, x)
+    q = x.new_empty(x.shape, dtype=torch.int8)
+    scales = x.new_empty((*x.shape[:-1], 1), dtype=torch.float32)
+    _check(_library().gconv_quantize_int8(x.data_ptr(), q.data_ptr(), scales.data_ptr(), x.numel() // K, K, xs, dt,
+                                          _raw_stream(dev)))
+    return q, scales
+
+
+def matmul_int8(q, scales, weight, weight_scales, bias=None, dtype: torch.dtype = torch.bfloat16, stream=None):
+    """y[..., n] = (sum_k q[..., k] * weight[n, k]) * scales * weight_scales[n] + bias[n] in `dtype`
+    (float32, float16 or bfloat16).
+
+    q int8 [..., K] and scales fp32 [..., 1] as quantize_int8 gives them; weight int8 [N, K],
+    weight_scales fp32 [N] or [N, 1] (quantize_int8 of the weights gives both); bias [N] in `dtype`.  All
+    contiguous, K at most 131071.  The sum is exact; it, the products with the scales (the token's
+    first) and the addition of the bias are rounded to fp32, and the result to the dtype."""
+    if stream is not None:
+        return _on_stream(stream, q, matmul_int8, q, scales, weight, weight_scales, bias, dtype)
+    dt = DTYPES.get(dtype)
+    if dt is None:
+        _bad(f"unsupported output dtype {dtype}")
+    if q.dtype is not torch.int8 or not q.is_cuda:
+        _bad("q must be an int8 GPU tensor")
+    if q.dim() < 1 or weight.dim() != 2 or q.shape[-1] < 1:
+        _bad("q must be [..., K] and weight [N, K] with K >= 1")
+    K, N, dev = q.shape[-1], weight.shape[0], q.get_device()
+    qp = _whole("q", q, torch.int8, dev, q.shape)
+    sp = _whole("scales", scales, torch.float32, dev, (*q.shape[:-1], 1))
+    w = _whole("weight", weight, torch.int8, dev, (N, K))
+    ws = _whole("weight_scales", weight_scales.view(N) if weight_scales.dim() == 2 and weight_scales.numel() == N
+                and weight_scales.is_contiguous() else weight_scales, torch.float32, dev, (N,))
+    b = _whole("bias", bias, dtype, dev, (N,))
+    if _device() != dev:
+        with torch.cuda.device(dev):
+            return matmul_int8(q, scales, weight, weight_scales, bias, dtype)
+    y = q.new_empty((*q.shape[:-1], N), dtype=dtype)
+    _check(_library().gconv_matmul_int8(qp, sp, w, ws, b, y.data_ptr(), _array(q.numel() // K, N, K), dt,
+                                        _raw_stream(dev)))
+    return y

@@ -84,4 +84,30 @@ bool gn_fits(const GroupNormArgs &a, const GroupNormPlan &g);
 hipError_t launch_group_norm(const GroupNormArgs &a, const GroupNormPlan &g, const char **kname);
 hipError_t launch_group_norm_bwd(const GroupNormArgs &a, const GroupNormPlan &g, const char **kname);
 
+// q = rint(x / scale), scale = max|row| / 127.
+struct QuantizeArgs {
+    const void *x;                       // [M][K], row stride xs
+    int8_t *q;                           // [M][K]
+    float *scales;                       // [M]
+    int64_t M, K, xs;
+    int dtype;
+    hipStream_t stream;
+};
+bool quantize_fits(int64_t M, int64_t K, int dtype);
+hipError_t launch_quantize(const QuantizeArgs &a, const char **kname);
+
+// y = (q w^T) qs ws + bias
+struct MatmulInt8Args {
+    const int8_t *q, *w;                 // [M][K], [N][K]
+    const float *qs, *ws;                // [M], [N]
+    const void *bias;                    // [N] in the dtype, or nullptr
+    void *y;                             // [M][N]
+    int64_t M, N, K;
+    int dtype;                           // of y and bias
+    hipStream_t stream;
+};
+constexpr int64_t kInt8MaxK = 131071;    // 2^7 2^7 K stays below 2^31
+bool matmul_int8_fits(int64_t M, int64_t N);
+hipError_t launch_matmul_int8(const MatmulInt8Args &a, const char **kname);
+
 }  // namespace gconv

@@ -1,5 +1,5 @@
 // block_api.cpp -- C entry points of the recurrent block's operators (gated linear
-// recurrence, group norm): validation, plans and launches.  Host code only.
+// recurrence, group norm, product in 8-bit integers): validation, plans and launches.  Host code only.
 #include <hip/hip_runtime.h>
 
 #include "block.hpp"
@@ -305,6 +305,71 @@ gconv_status_t gconv_group_norm_backward(const void *dy, const void *x, const vo
     if ((st = gn_check(a, g)) != GCONV_OK) return st;
     const char *kname = "";
     const hipError_t err = gconv::launch_group_norm_bwd(a, g, &kname);
+    return done(err, kname);
+}
+
+// ---------------------------------------------------------------- product in 8-bit integers
+
+static gconv_status_t int8_shape(int64_t M, int64_t N, int64_t K, gconv_dtype_t dtype)
+{
+    if (bad_dtype(dtype)) return fail(GCONV_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (M < 0 || N < 1 || K < 1) return fail(GCONV_ERR_INVALID_ARG, "int8 product: M >= 0 and N, K >= 1 are needed");
+    if (M > kMax - 65536 || N > kMax - 65536)
+        return fail(GCONV_ERR_UNSUPPORTED, "int8 product: sizes exceed the library's index range");
+    return GCONV_OK;
+}
+
+gconv_status_t gconv_quantize_int8(const void *x, int8_t *q, float *scales, int64_t rows, int64_t K, int64_t x_stride,
+                                   gconv_dtype_t dtype, void *hip_stream)
+{
+    gconv::set_last_error("");
+    gconv_status_t st = int8_shape(rows, 1, K, dtype);
+    if (st != GCONV_OK || (st = check_strides(&x_stride, 1)) != GCONV_OK) return st;
+    if (K > int64_t(1) << 30 || (double)rows * (double)(K > x_stride ? K : x_stride) >= kCells / 8)
+        return fail(GCONV_ERR_UNSUPPORTED, "int8 rows: sizes exceed the library's index range");
+    if (rows == 0) return done(hipSuccess, "");
+    if (!x || !q || !scales) return fail(GCONV_ERR_INVALID_ARG, "NULL x, q or scales");
+    const Range ranges[] = {
+        {"q", q, (size_t)(rows * K), true},
+        {"scales", scales, 4 * (size_t)rows, true},
+        {"x", x, extent(rows, x_stride, 1, 0, 1, 0, K, elem(dtype)), false},
+    };
+    if ((st = check_ranges(ranges, sizeof(ranges) / sizeof(ranges[0]))) != GCONV_OK) return st;
+    if (!gconv::quantize_fits(rows, K, (int)dtype))
+        return fail(GCONV_ERR_UNSUPPORTED, "int8 rows: the call needs more threads than a launch takes");
+    const gconv::QuantizeArgs a = {x, q, scales, rows, K, x_stride, (int)dtype, (hipStream_t)hip_stream};
+    const char *kname = "";
+    const hipError_t err = gconv::launch_quantize(a, &kname);
+    return done(err, kname);
+}
+
+gconv_status_t gconv_matmul_int8(const int8_t *q, const float *scales, const int8_t *w, const float *w_scales, const void *bias,
+                                 void *y, const int64_t *shape, gconv_dtype_t dtype, void *hip_stream)
+{
+    gconv::set_last_error("");
+    if (!shape) return fail(GCONV_ERR_INVALID_ARG, "NULL shape");
+    const int64_t M = shape[0], N = shape[1], K = shape[2];
+    gconv_status_t st = int8_shape(M, N, K, dtype);
+    if (st != GCONV_OK) return st;
+    if (K > gconv::kInt8MaxK)
+        return fail(GCONV_ERR_UNSUPPORTED, "int8 product: K = %lld, sums of at most %lld products stay in 32 bits", (long long)K,
+                    (long long)gconv::kInt8MaxK);
+    if (M == 0) return done(hipSuccess, "");
+    if (!q || !scales || !w || !w_scales || !y) return fail(GCONV_ERR_INVALID_ARG, "NULL q, scales, w, w_scales or y");
+    const Range ranges[] = {
+        {"y", y, elem(dtype) * (size_t)(M * N), true},
+        {"q", q, (size_t)(M * K), false},
+        {"scales", scales, 4 * (size_t)M, false},
+        {"w", w, (size_t)(N * K), false},
+        {"w_scales", w_scales, 4 * (size_t)N, false},
+        {"bias", bias, elem(dtype) * (size_t)N, false},
+    };
+    if ((st = check_ranges(ranges, sizeof(ranges) / sizeof(ranges[0]))) != GCONV_OK) return st;
+    if (!gconv::matmul_int8_fits(M, N))
+        return fail(GCONV_ERR_UNSUPPORTED, "int8 product: the call needs more threads than a launch takes");
+    const gconv::MatmulInt8Args a = {q, w, scales, w_scales, bias, y, M, N, K, (int)dtype, (hipStream_t)hip_stream};
+    const char *kname = "";
+    const hipError_t err = gconv::launch_matmul_int8(a, &kname);
     return done(err, kname);
 }
 

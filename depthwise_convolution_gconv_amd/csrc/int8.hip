@@ -1,0 +1,395 @@
+// int8.hip -- product in 8-bit integers with a scale for each token and each output channel, and
+// the tokens' quantiser:
+//     scale_m = max(max|x_m|, 2^-100) / 127,   q = rint(x / scale_m)
+//     y[m][n] = (sum over k of q[m][k] w[n][k]) scale_m wscale_n + bias_n
+// The sum is exact in int32 (K <= 131071); it is rounded to fp32 once, as are the products with
+// the two scales and the bias's addition, and the result to the dtype.
+//
+// Two kernels, by the number of tokens:
+//   mm_tile  tiles of tokens x channels on the matrix cores (v_mfma_i32_32x32x32_i8), both operands
+//            staged 128 bytes of K at a time by loads that go straight to LDS, the next stage's in
+//            flight over the whole of this one's products;
+//   mm_rows  up to 64 tokens: bound by the weights' one read.  A workgroup takes 16 channels, its
+//            waves share K, every wave has all its weights' loads in flight at once
+//            (v_mfma_i32_16x16x64_i8).
+#include <algorithm>
+
+#include "block.hpp"
+#include "vecio.hpp"
+
+namespace gconv {
+namespace {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t any16 __attribute__((ext_vector_type(4), aligned(1)));
+
+// ---------------------------------------------------------------- quantiser
+
+constexpr float kTopFloor = 7.888609052210118e-31f;     // 2^-100
+
+// Largest magnitude as bits: NaN is above infinity, so that it is kept.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu; }
+
+template <typename T, int V> __device__ __forceinline__ uint32_t top_of(const Run<T, V> &r, uint32_t top)
+{
+#pragma unroll
+    for (int k = 0; k < V; ++k) top = max(top, magnitude(to_f32(r.v[k])));
+    return top;
+}
+
+template <typename T, int V> __device__ __forceinline__ void store_q(int8_t *dst, int valid, const Run<T, V> &r, float scale)
+{
+    uint32_t w[V / 4] = {};
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const float v = rintf(to_f32(r.v[k]) / scale);
+        w[k / 4] |= ((uint32_t)(int32_t)v & 0xffu) << 8 * (k % 4);
+    }
+    if (valid >= V) {
+        if constexpr (V == 8) {
+            typedef uint32_t two __attribute__((ext_vector_type(2), aligned(1)));
+            *reinterpret_cast<two *>(dst) = two{w[0], w[1]};
+        } else {
+            typedef uint32_t one __attribute__((aligned(1)));
+            *reinterpret_cast<one *>(dst) = w[0];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (k < valid) dst[k] = (int8_t)(w[k / 4] >> 8 * (k % 4));
+    }
+}
+
+// TPR threads take a row, 256 / TPR rows a workgroup.  NV vectors of a thread stay in registers;
+// what a longer row has beyond them is read a second time.
+template <typename T, int TPR, int NV>
+__global__ __launch_bounds__(256) void int8_rows(const T *__restrict__ x, int8_t *__restrict__ q, float *__restrict__ scales,
+                                                 int64_t M, int64_t K, int64_t xs)
+{
+    constexpr int V = 16 / sizeof(T);
+    __shared__ uint32_t tops[4];
+    const int t = threadIdx.x % TPR;
+    const int64_t m = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+    const bool on = m < M;
+    const T *const row = x + (on ? m : M - 1) * xs;
+    Run<T, V> keep[NV];
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t at = ((int64_t)j * TPR + t) * V, left = K - at;
+        if (left > 0) {
+            keep[j] = load_raw<T, V>(row + at, left < V ? (int)left : V);
+            top = top_of<T, V>(keep[j], top);
+        }
+    }
+    for (int64_t at = ((int64_t)NV * TPR + t) * V; at < K; at += TPR * V)
+        top = top_of<T, V>(load_raw<T, V>(row + at, K - at < V ? (int)(K - at) : V), top);
+#pragma unroll
+    for (int d = 32; d; d /= 2) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    if constexpr (TPR == 256) {
+        if (threadIdx.x % 64 == 0) tops[threadIdx.x / 64] = top;
+        __syncthreads();
+        top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+    }
+    const float high = __builtin_bit_cast(float, top), scale = (high < kTopFloor ? kTopFloor : high) / 127.0f;
+    if (!on) return;
+    if (t == 0) scales[m] = scale;
+    int8_t *const out = q + m * K;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t at = ((int64_t)j * TPR + t) * V, left = K - at;
+        if (left > 0) store_q<T, V>(out + at, left < V ? (int)left : V, keep[j], scale);
+    }
+    for (int64_t at = ((int64_t)NV * TPR + t) * V; at < K; at += TPR * V) {
+        const int valid = K - at < V ? (int)(K - at) : V;
+        store_q<T, V>(out + at, valid, load_raw<T, V>(row + at, valid), scale);
+    }
+}
+
+// ---------------------------------------------------------------- product
+
+struct Mm {
+    const int8_t *q, *w;
+    const float *qs, *ws;
+    const void *bias;                    // [N] in the output's dtype, or nullptr
+    void *y;
+    int32_t M, N, K;
+    int32_t mt, nt;                      // tiles
+};
+
+template <typename T> __device__ __forceinline__ float bias_of(const Mm &p, int n)
+{
+    return p.bias ? to_f32(static_cast<const T *>(p.bias)[n]) : 0.0f;
+}
+
+// 16 bytes of a row from byte k on; those past K are zero.  Rows of any alignment.
+__device__ __forceinline__ uint4 load16(const int8_t *row, int k, int K)
+{
+    if (k + 16 <= K) return __builtin_bit_cast(uint4, *reinterpret_cast<const any16 *>(row + k));
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (k + i < K) w[i / 4] |= (uint32_t)(uint8_t)row[k + i] << 8 * (i % 4);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr int kStage = 128;              // bytes of K in a stage
+constexpr uint32_t kNowhere = 0x80000000u;
+
+// Tile BM x BN, waves WM x WN of it.  ALIGNED: K a multiple of 16 and rows on 16 bytes; else
+// the stages go through registers.
+//
+// LDS holds a stage's rows one after the other, 8 pieces of 16 bytes each, piece c of row r at place
+// c ^ (r & 7): a wave reads one piece of 32 rows at a time, and any 8 rows next to each other then
+// lie in different banks.
+template <typename T, int BM, int BN, int WM, int WN, bool ALIGNED>
+__global__ __launch_bounds__(64 * WM *WN) void mm_tile(const Mm p)
+{
+    constexpr int NWAVES = WM * WN, UA = BM * 8 / 64 / NWAVES, UB = BN * 8 / 64 / NWAVES;   // loads of a wave
+    constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
+    __shared__ uint4 a0[BM * 8], a1[BM * 8], b0[BN * 8], b1[BN * 8];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l32 = lane % 32, hf = lane / 32;
+    const int wm = wave / WN, wn = wave % WN;
+    // Each XCD takes tiles next to each other; within it, runs of 8 tiles of tokens for each channel tile share weights.
+    const int64_t tiles = (int64_t)p.mt * p.nt, per = (tiles + 7) / 8, id = (int64_t)(blockIdx.x % 8) * per + blockIdx.x / 8;
+    if (blockIdx.x / 8 >= per || id >= tiles) return;
+    const int band = (int)(id / (8 * (int64_t)p.nt)), rows_of_band = min(8, p.mt - band * 8);
+    const int in_band = (int)(id - (int64_t)band * 8 * p.nt);
+    const int m0 = (band * 8 + in_band % rows_of_band) * BM, n0 = in_band / rows_of_band * BN;
+    const int rows = min(BM, p.M - m0), cols = min(BN, p.N - n0);
+    const int8_t *const A = p.q + (int64_t)m0 * p.K, *const B = p.w + (int64_t)n0 * p.K;
+
+    i32x16 acc[FM][FN] = {};
+    const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(A), (short)0, rows * p.K, 0x00020000);
+    const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(B), (short)0, cols * p.K, 0x00020000);
+    const int piece = (lane % 8) ^ (lane / 8);      // of the row that this lane's 16 bytes go to
+    uint4 held[ALIGNED ? 1 : UA + UB];
+
+    // Stage k0: straight to LDS, or into registers.
+    auto fetch = [&](uint4 *as, uint4 *bs, int k0) {
+        const int k = 16 * piece;
+        if constexpr (ALIGNED) {
+            const bool in = k0 + k < p.K;
+#pragma unroll
+            for (int i = 0; i < UA; ++i) {
+                const int r = (wave * UA + i) * 8;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (__attribute__((address_space(3))) void *)(as + r * 8), 16,
+                                                         in ? (uint32_t)((r + lane / 8) * p.K + k) : kNowhere, k0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < UB; ++i) {
+                const int r = (wave * UB + i) * 8;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (__attribute__((address_space(3))) void *)(bs + r * 8), 16,
+                                                         in ? (uint32_t)((r + lane / 8) * p.K + k) : kNowhere, k0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < UA; ++i)
+                held[i] = load16(A + (int64_t)min((wave * UA + i) * 8 + lane / 8, rows - 1) * p.K, k0 + k, p.K);
+#pragma unroll
+            for (int i = 0; i < UB; ++i)
+                held[UA + i] = load16(B + (int64_t)min((wave * UB + i) * 8 + lane / 8, cols - 1) * p.K, k0 + k, p.K);
+        }
+    };
+    auto settle = [&](uint4 *as, uint4 *bs) {
+        if constexpr (ALIGNED) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < UA; ++i) as[(wave * UA + i) * 64 + lane] = held[i];
+#pragma unroll
+            for (int i = 0; i < UB; ++i) bs[(wave * UB + i) * 64 + lane] = held[UA + i];
+        }
+        __syncthreads();
+    };
+    auto products = [&](const uint4 *as, const uint4 *bs) {
+#pragma unroll
+        for (int kk = 0; kk < kStage / 32; ++kk) {
+            uint4 a[FM], b[FN];
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int r = (wm * FM + i) * 32 + l32;
+                a[i] = as[r * 8 + ((2 * kk + hf) ^ (r & 7))];
+            }
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const int r = (wn * FN + j) * 32 + l32;
+                b[j] = bs[r * 8 + ((2 * kk + hf) ^ (r & 7))];
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a[i]), __builtin_bit_cast(i32x4, b[j]),
+                                                                      acc[i][j], 0, 0, 0);
+        }
+    };
+
+    // Stages in pairs, one buffer each; one past K holds zeros.
+    fetch(a0, b0, 0);
+    settle(a0, b0);
+    for (int k0 = 0; k0 < p.K; k0 += 2 * kStage) {
+        fetch(a1, b1, k0 + kStage);
+        products(a0, b0);
+        settle(a1, b1);
+        if (k0 + 2 * kStage < p.K) fetch(a0, b0, k0 + 2 * kStage);
+        products(a1, b1);
+        settle(a0, b0);
+    }
+
+    // Lane: column l32 of each 32 x 32 block, rows 8 (r / 4) + 4 hf + r % 4.
+    T *const y = static_cast<T *>(p.y);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const int n = n0 + (wn * FN + j) * 32 + l32;
+        if (n >= p.N) continue;
+        const float ws = p.ws[n], bias = bias_of<T>(p, n);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int m = m0 + (wm * FM + i) * 32 + 8 * (r / 4) + 4 * hf + r % 4;
+                if (m < p.M) y[(int64_t)m * p.N + n] = from_f32<T>((float)acc[i][j][r] * p.qs[m] * ws + bias);
+            }
+    }
+}
+
+// MB blocks of 16 tokens, NW waves that share K.
+template <typename T, int MB, int NW>
+__global__ __launch_bounds__(64 * NW) void mm_rows(const Mm p)
+{
+    constexpr int UNROLL = MB == 4 ? 4 : 8;
+    __shared__ i32x4 sums[NW][MB][64];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), r = lane % 16, g = lane / 16;
+    const int n0 = blockIdx.x * 16;
+    const int8_t *const w = p.w + (int64_t)min(n0 + r, p.N - 1) * p.K;
+    const int8_t *q[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) q[b] = p.q + (int64_t)min(16 * b + r, p.M - 1) * p.K;
+    const int steps = (p.K + 63) / 64, each = (steps + NW - 1) / NW, from = wave * each, to = min(from + each, steps);
+    i32x4 acc[MB] = {};
+    int s = from;
+    for (; s + UNROLL <= to && (s + UNROLL) * 64 <= p.K; s += UNROLL) {
+        uint4 wv[UNROLL], qv[UNROLL][MB];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            wv[u] = __builtin_bit_cast(uint4, *reinterpret_cast<const any16 *>(w + (s + u) * 64 + 16 * g));
+#pragma unroll
+            for (int b = 0; b < MB; ++b) qv[u][b] = __builtin_bit_cast(uint4, *reinterpret_cast<const any16 *>(q[b] + (s + u) * 64 + 16 * g));
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+                acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wv[u]), __builtin_bit_cast(i32x4, qv[u][b]), acc[b],
+                                                               0, 0, 0);
+    }
+    for (; s < to; ++s) {
+        const uint4 wv = load16(w, s * 64 + 16 * g, p.K);
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+            acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wv),
+                                                           __builtin_bit_cast(i32x4, load16(q[b], s * 64 + 16 * g, p.K)), acc[b], 0, 0, 0);
+    }
+#pragma unroll
+    for (int b = 0; b < MB; ++b) sums[wave][b][lane] = acc[b];
+    __syncthreads();
+    // Lane: token r, channels 4 g + i.
+    for (int b = wave; b < MB; b += NW) {
+        i32x4 v = sums[0][b][lane];
+#pragma unroll
+        for (int k = 1; k < NW; ++k) v += sums[k][b][lane];
+        const int m = 16 * b + r;
+        if (m >= p.M) continue;
+        const float qs = p.qs[m];
+        T *const y = static_cast<T *>(p.y) + (int64_t)m * p.N;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = n0 + 4 * g + i;
+            if (n < p.N) y[n] = from_f32<T>((float)v[i] * qs * p.ws[n] + bias_of<T>(p, n));
+        }
+    }
+}
+
+template <int N> struct Int { static constexpr int value = N; };
+
+template <typename F> hipError_t with_type(int dtype, F &&f)
+{
+    if (dtype == DT_F32) return f(float{});
+    if (dtype == DT_F16) return f(_Float16{});
+    return f(__bf16{});
+}
+
+}  // namespace
+
+bool quantize_fits(int64_t M, int64_t K, int dtype) { return grid_fits(M, 256); }
+
+hipError_t launch_quantize(const QuantizeArgs &a, const char **kname)
+{
+    *kname = "int8_rows";
+    const int64_t V = a.dtype == DT_F32 ? 4 : 8;
+    return with_type(a.dtype, [&](auto t) {
+        typedef decltype(t) E;
+        auto run = [&](auto tpr, auto nv) {
+            constexpr int R = 256 / tpr.value;
+            int8_rows<E, tpr.value, nv.value><<<(unsigned)ceil_div(a.M, R), 256, 0, a.stream>>>((const E *)a.x, a.q, a.scales, a.M, a.K, a.xs);
+            return hipGetLastError();
+        };
+        const int64_t vecs = ceil_div(a.K, V);
+        if (vecs <= 128) return run(Int<64>{}, Int<2>{});
+        return vecs <= 512 ? run(Int<256>{}, Int<2>{}) : run(Int<256>{}, Int<8>{});
+    });
+}
+
+namespace {
+
+template <int BM, int BN, int WM, int WN, bool ALIGNED> hipError_t run_tile(Mm p, int dtype, hipStream_t stream)
+{
+    p.mt = (int32_t)ceil_div(p.M, BM);
+    p.nt = (int32_t)ceil_div(p.N, BN);
+    const unsigned grid = (unsigned)(8 * ceil_div((int64_t)p.mt * p.nt, 8));
+    return with_type(dtype, [&](auto t) {
+        mm_tile<decltype(t), BM, BN, WM, WN, ALIGNED><<<grid, 64 * WM * WN, 0, stream>>>(p);
+        return hipGetLastError();
+    });
+}
+
+template <int MB, int NW> hipError_t run_rows(const Mm &p, int dtype, hipStream_t stream)
+{
+    return with_type(dtype, [&](auto t) {
+        mm_rows<decltype(t), MB, NW><<<(unsigned)ceil_div(p.N, 16), 64 * NW, 0, stream>>>(p);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace
+
+bool matmul_int8_fits(int64_t M, int64_t N)
+{
+    return grid_fits(8 * ceil_div(ceil_div(M, 64) * ceil_div(N, 64), 8), 256) && grid_fits(ceil_div(N, 16), 1024);
+}
+
+hipError_t launch_matmul_int8(const MatmulInt8Args &a, const char **kname)
+{
+    Mm p = {};
+    p.q = a.q; p.w = a.w; p.qs = a.qs; p.ws = a.ws; p.bias = a.bias; p.y = a.y;
+    p.M = (int32_t)a.M; p.N = (int32_t)a.N; p.K = (int32_t)a.K;
+    if (a.M <= 64) {
+        *kname = "mm_rows";
+        const bool few = ceil_div(a.N, 16) < 512;
+        if (a.M <= 16) return few ? run_rows<1, 16>(p, a.dtype, a.stream) : run_rows<1, 4>(p, a.dtype, a.stream);
+        if (a.M <= 32) return few ? run_rows<2, 8>(p, a.dtype, a.stream) : run_rows<2, 4>(p, a.dtype, a.stream);
+        return few ? run_rows<4, 8>(p, a.dtype, a.stream) : run_rows<4, 4>(p, a.dtype, a.stream);
+    }
+    *kname = "mm_tile";
+    const bool aligned = a.K % 16 == 0 && (uintptr_t)a.q % 16 == 0 && (uintptr_t)a.w % 16 == 0;
+    auto tiles = [&](int64_t bm, int64_t bn) { return ceil_div(a.M, bm) * ceil_div(a.N, bn); };
+    if (!aligned)
+        return tiles(128, 128) >= 256 ? run_tile<128, 128, 2, 2, false>(p, a.dtype, a.stream)
+                                      : run_tile<64, 64, 2, 2, false>(p, a.dtype, a.stream);
+    if (tiles(256, 256) >= 224) return run_tile<256, 256, 2, 4, true>(p, a.dtype, a.stream);
+    return tiles(128, 128) >= 224 ? run_tile<128, 128, 2, 2, true>(p, a.dtype, a.stream) : run_tile<64, 64, 2, 2, true>(p, a.dtype, a.stream);
+}
+
+}  // namespace gconv

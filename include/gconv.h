@@ -444,6 +444,22 @@ gconv_status_t gconv_group_norm_backward(const void *dy, const void *x, const vo
                                          gconv_dtype_t dtype, void *workspace, size_t workspace_bytes,
                                          void *hip_stream);
 
+/* Rows as 8-bit integers: x [rows, K] (row stride x_stride) -> q [rows, K] and scales [rows] (fp32),
+ *     scale = max(max|x|, 2^-100) / 127,   q = x / scale, the quotient in fp32, rounded to the nearest
+ * integer, ties to even.  A value that is not finite makes its row's scale that, and q without meaning. */
+gconv_status_t gconv_quantize_int8(const void *x, int8_t *q, float *scales, int64_t rows, int64_t K,
+                                   int64_t x_stride, gconv_dtype_t dtype, void *hip_stream);
+
+/* Product in 8-bit integers with a scale for each token and each output channel.  shape = {M, N, K}: q
+ * [M,K] and w [N,K] int8, scales [M] and w_scales [N] fp32, bias [N] or NULL and y [M,N] of the dtype,
+ * all contiguous:
+ *     y[m][n] = (sum over k of q[m][k] w[n][k]) scales[m] w_scales[n] + bias[n]
+ * The sum is exact in 32-bit integers (K at most 131071); it and each step after it are rounded to fp32,
+ * and the result to the dtype. */
+gconv_status_t gconv_matmul_int8(const int8_t *q, const float *scales, const int8_t *w, const float *w_scales,
+                                 const void *bias, void *y, const int64_t *shape, gconv_dtype_t dtype,
+                                 void *hip_stream);
+
 /* Name of the kernel the last successful gconv_fwd / gconv_fwd_route / gconv_fwd_ex /
  * gconv_dw1d_bwd_data / gconv_dw1d_bwd_filter call on this host thread launched
  * (the first of two for the filter gradient; "" before the first call or after
