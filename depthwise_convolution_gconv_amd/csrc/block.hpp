@@ -72,9 +72,10 @@ struct GroupNormArgs {
 };
 // How a call is laid out: threads of a workgroup, channels of a vector (V), groups and vectors
 // of a row of its slab, positions of a thread (K), chunks of a sample's positions, parts of a
-// group too wide for one workgroup, samples that a gradients' workgroup takes one after the other.
+// group too wide for one workgroup, samples that a gradients' workgroup takes one after the other;
+// whole: a workgroup holds all positions of its sample, and one launch does.
 struct GroupNormPlan {
-    int32_t threads, V, kg, cols, K, chunks, chunk_rows, parts;
+    int32_t whole, threads, V, kg, cols, K, chunks, chunk_rows, parts;
     int64_t range;
 };
 GroupNormPlan gn_plan(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, bool backward);

@@ -96,9 +96,6 @@ struct Norm {
 
 constexpr int kMaxThreads = 1024;
 
-// What a workgroup is to do with its slab.
-enum { kWholeSample = 0, kChunkStats = 1, kChunkApply = 2 };
-
 struct Slab {
     int64_t n;             // sample (backward: the first of a range)
     int32_t chunk, bundle, part;
@@ -109,11 +106,8 @@ struct Slab {
     int32_t groups;
 };
 
-__device__ __forceinline__ bool find_slab(const Norm &p, Slab &s)
+__device__ __forceinline__ void slab_of(const Norm &p, int64_t id, Slab &s)
 {
-    // Neighbouring bundles, which may share lines, on one XCD.
-    const int64_t per = (p.blocks + 7) / 8, id = (int64_t)(blockIdx.x % 8) * per + blockIdx.x / 8;
-    if (blockIdx.x / 8 >= per || id >= p.blocks) return false;
     const int64_t rest = id / p.bundles;
     const int at = (int)(id - rest * p.bundles);
     s.part = at % p.parts;
@@ -122,6 +116,14 @@ __device__ __forceinline__ bool find_slab(const Norm &p, Slab &s)
     s.chunk = (int)(rest - s.n * p.chunks);
     s.first = s.chunk * p.chunk_rows;
     s.rows = (int)min((int64_t)p.chunk_rows, p.P - s.first);
+}
+
+// A workgroup's slab: neighbouring bundles, which may share lines, on one XCD.
+__device__ __forceinline__ bool find_slab(const Norm &p, Slab &s)
+{
+    const int64_t per = (p.blocks + 7) / 8, id = (int64_t)(blockIdx.x % 8) * per + blockIdx.x / 8;
+    if (blockIdx.x / 8 >= per || id >= p.blocks) return false;
+    slab_of(p, id, s);
     return true;
 }
 
@@ -188,7 +190,88 @@ __device__ __forceinline__ void group_sums(const Norm &p, const Slab &s, int tid
 
 // ---------------------------------------------------------------- forward
 
-template <typename T, int V, int K, int WHAT>
+// Statistics of each group from its threads' sums and squares about their own means, of `live` rows:
+// done(group, mean, M2) in one lane.
+template <int V, typename F>
+__device__ __forceinline__ void join_threads(const Norm &p, const Slab &s, int tid, int live, float2 own, float2 *mine, F &&done)
+{
+    mine[tid] = own;
+    __syncthreads();
+    const int lane = tid % 64, width = p.parts > 1 ? s.cols : p.cg / V;
+    const float total = fmaxf((float)live * (width * V), 1.0f);
+    for (int g = tid / 64; g < s.groups; g += blockDim.x / 64) {
+        float a = 0.0f, q = 0.0f;
+        for (Members m(lane, width, p.R); m.on(); m.next()) a += mine[m.r * p.cols + g * width + m.j].x;
+        const float mean = wave_sum(a) / total;
+        for (Members m(lane, width, p.R); m.on(); m.next()) {
+            const float2 v = mine[m.r * p.cols + g * width + m.j];
+            const float n = count_of(m.r, live, p.R, V);
+            if (n > 0.0f) {
+                const float d = v.x / n - mean;
+                q += fmaf(n * d, d, v.y);
+            }
+        }
+        q = wave_sum(q);
+        if (lane == 0) done(g, mean, q);
+    }
+}
+
+// Sum, and squares about its own mean, of what a thread holds: rows r0, r0 + R, ... below `live`.
+template <typename T, int V, int K>
+__device__ __forceinline__ float2 own_stats(Vec<T, V> (&raw)[K], bool on, int r0, int R, int live)
+{
+    float sum = 0.0f, m2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+        if (on && r0 + j * R < live)
+#pragma unroll
+            for (int k = 0; k < V; ++k) sum += to_f32(raw[j].v[k]);
+    forget<T, V, K>(raw);
+    const float own = on ? sum / fmaxf(count_of(r0, live, R, V), 1.0f) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        if (on && r0 + j * R < live)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float d = to_f32(raw[j].v[k]) - own;
+                m2 = fmaf(d, d, m2);
+            }
+        keep_order();
+    }
+    forget<T, V, K>(raw);
+    return make_float2(sum, m2);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void normed(const Norm &p, const Vec<T, V> &x, float2 st, const Vec<T, V> &w, const Vec<T, V> &b, bool live,
+                                       char *to)
+{
+    float f[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = fmaf(to_f32(x.v[k]) - st.x, st.y * to_f32(w.v[k]), to_f32(b.v[k]));
+    if (p.silu)     // one branch for all: the channels' exponentials overlap
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] *= sigmoid(f[k]);
+    if (!live)
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] = 0.0f;
+    store_vec<T, V>(to, f);
+}
+
+// Positions of a tile: K for each thread.  A chunk is a row of tiles, the next one's loads under way
+// while one is worked on.
+template <typename T, int V, int K>
+__device__ __forceinline__ void load_tile(const char *base, int64_t st, uint32_t from, bool on, int r0, int R, int first, int live,
+                                          Vec<T, V> (&raw)[K])
+{
+    const char *const x = base + first * st;
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+        if (on && first + r0 + j * R < live) raw[j] = load_vec<T, V>(x + j * (R * st) + from);
+}
+
+// The whole sample in registers.
+template <typename T, int V, int K>
 __global__ __launch_bounds__(kMaxThreads) void gn_forward(const Norm p)
 {
     __shared__ float2 mine[kMaxThreads];
@@ -196,133 +279,156 @@ __global__ __launch_bounds__(kMaxThreads) void gn_forward(const Norm p)
     Slab s;
     if (!find_slab(p, s)) return;
     slab_columns<V>(p, s);
-    const int tid = threadIdx.x, lane = tid % 64, r0 = tid / p.cols, col = tid - r0 * p.cols;
-    const int live = live_rows(p, s.n, s), width = p.parts > 1 ? s.cols : p.cg / V;
+    const int tid = threadIdx.x, r0 = tid / p.cols, col = tid - r0 * p.cols;
+    const int live = live_rows(p, s.n, s), width = p.cg / V;
+    const bool on = r0 < p.R && col < s.cols;
+    const uint32_t here = (uint32_t)(col * V * sizeof(T));
+    Vec<T, V> raw[K];
+    load_tile<T, V, K>(p.x + s.n * p.xsb + s.c0 * (int64_t)sizeof(T), p.xst, (uint32_t)r0 * (uint32_t)p.xst + here, on, r0, p.R, 0, live,
+                       raw);
+    const float total = fmaxf((float)live * p.cg, 1.0f);
+    join_threads<V>(p, s, tid, live, own_stats<T, V, K>(raw, on, r0, p.R, live), mine, [&](int g, float mean, float q) {
+        const float2 v = make_float2(mean, 1.0f / sqrtf(q / total + p.eps));
+        out[g] = v;
+        if (p.stats_out) reinterpret_cast<float2 *>(p.stats_out)[s.n * p.G + s.bundle * p.kg + g] = v;
+    });
+    __syncthreads();
+    if (!on) return;
+    const int64_t c = s.c0 + (int64_t)col * V, row = p.C * (int64_t)sizeof(T);
+    const float2 st = out[col / width];
+    const Vec<T, V> w = load_vec<T, V>(p.w + c * (int64_t)sizeof(T));
+    Vec<T, V> b = {};
+    if (p.b) b = load_vec<T, V>(p.b + c * (int64_t)sizeof(T));
+    char *const y = p.y + (s.n * p.P * p.C + s.c0) * (int64_t)sizeof(T);
+    const uint32_t to = (uint32_t)r0 * (uint32_t)row + here;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const int r = r0 + j * p.R;
+        if (r < s.rows) normed<T, V>(p, raw[j], st, w, b, r < live, y + j * (p.R * row) + to);
+        keep_order();
+    }
+}
+
+constexpr int kTile = 4, kTileBwd = 2;
+
+template <typename T, int V>
+__global__ __launch_bounds__(kMaxThreads) void gn_chunk_stats(const Norm p)
+{
+    constexpr int K = kTile;
+    __shared__ float2 mine[kMaxThreads];
+    Slab s;
+    if (!find_slab(p, s)) return;
+    slab_columns<V>(p, s);
+    const int tid = threadIdx.x, r0 = tid / p.cols, col = tid - r0 * p.cols, live = live_rows(p, s.n, s);
+    const bool on = r0 < p.R && col < s.cols;
+    const char *const x = p.x + s.n * p.xsb + s.first * p.xst + s.c0 * (int64_t)sizeof(T);
+    const uint32_t from = (uint32_t)r0 * (uint32_t)p.xst + (uint32_t)(col * V * sizeof(T));
+    Vec<T, V> raw[K], next[K];
+    load_tile<T, V, K>(x, p.xst, from, on, r0, p.R, 0, live, raw);
+    float n = 0.0f, mean = 0.0f, m2 = 0.0f;
+    for (int first = 0; first < live; first += p.R * K) {
+        load_tile<T, V, K>(x, p.xst, from, on, r0, p.R, first + p.R * K, live, next);
+        const float2 own = own_stats<T, V, K>(raw, on, r0, p.R, min(live - first, p.R * K));
+        const float nb = on ? count_of(r0, min(live - first, p.R * K), p.R, V) : 0.0f;
+        if (nb > 0.0f) {
+            const float d = own.x / nb - mean, all = n + nb, part = nb / all;
+            mean = fmaf(d, part, mean);
+            m2 += fmaf(d * d, n * part, own.y);
+            n = all;
+        }
+#pragma unroll
+        for (int j = 0; j < K; ++j) raw[j] = next[j];
+    }
+    join_threads<V>(p, s, tid, live, make_float2(mean * n, m2), mine, [&](int g, float all, float q) {
+        p.chunk[(s.n * p.G + s.bundle * p.kg + g) * (p.chunks * p.parts) + s.chunk * p.parts + s.part] = make_float2(all, q);
+    });
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(kMaxThreads) void gn_chunk_apply(const Norm p)
+{
+    constexpr int K = kTile;
+    __shared__ float2 out[kMaxThreads];
+    Slab s;
+    if (!find_slab(p, s)) return;
+    slab_columns<V>(p, s);
+    const int tid = threadIdx.x, lane = tid % 64, r0 = tid / p.cols, col = tid - r0 * p.cols, live = live_rows(p, s.n, s);
     const bool on = r0 < p.R && col < s.cols;
     const int64_t c = s.c0 + (int64_t)col * V;
     const char *const x = p.x + s.n * p.xsb + s.first * p.xst + s.c0 * (int64_t)sizeof(T);
     const uint32_t from = (uint32_t)r0 * (uint32_t)p.xst + (uint32_t)(col * V * sizeof(T));
-    Vec<T, V> raw[K];
-#pragma unroll
-    for (int j = 0; j < K; ++j)
-        if (on && r0 + j * p.R < live) raw[j] = load_vec<T, V>(x + j * (p.R * p.xst) + from);
-
-    if constexpr (WHAT != kChunkApply) {
-        float sum = 0.0f, m2 = 0.0f;
-#pragma unroll
-        for (int j = 0; j < K; ++j)
-            if (on && r0 + j * p.R < live)
-#pragma unroll
-                for (int k = 0; k < V; ++k) sum += to_f32(raw[j].v[k]);
-        forget<T, V, K>(raw);
-        const float own = on ? sum / fmaxf(count_of(r0, live, p.R, V), 1.0f) : 0.0f;
-#pragma unroll
-        for (int j = 0; j < K; ++j)
-            if (on && r0 + j * p.R < live)
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float d = to_f32(raw[j].v[k]) - own;
-                    m2 = fmaf(d, d, m2);
-                }
-        keep_order();
-        mine[tid] = make_float2(sum, m2);
-        forget<T, V, K>(raw);
-        __syncthreads();
-        const float total = (float)live * (width * V);
-        for (int g = tid / 64; g < s.groups; g += blockDim.x / 64) {
-            float a = 0.0f, q = 0.0f;
-            for (Members m(lane, width, p.R); m.on(); m.next()) a += mine[m.r * p.cols + g * width + m.j].x;
-            const float mean = wave_sum(a) / fmaxf(total, 1.0f);
-            for (Members m(lane, width, p.R); m.on(); m.next()) {
-                const float2 v = mine[m.r * p.cols + g * width + m.j];
-                const float n = count_of(m.r, live, p.R, V);
-                if (n > 0.0f) {
-                    const float d = v.x / n - mean;
-                    q += fmaf(n * d, d, v.y);
-                }
-            }
-            q = wave_sum(q);
-            const int64_t at = s.n * p.G + s.bundle * p.kg + g;
-            if constexpr (WHAT == kChunkStats) {
-                if (lane == 0) p.chunk[at * (p.chunks * p.parts) + s.chunk * p.parts + s.part] = make_float2(mean, q);
-            } else if (lane == 0) {
-                const float2 v = make_float2(mean, 1.0f / sqrtf(q / fmaxf(total, 1.0f) + p.eps));
-                out[g] = v;
-                if (p.stats_out) reinterpret_cast<float2 *>(p.stats_out)[at] = v;
-            }
+    Vec<T, V> raw[K], next[K], w = {}, b = {};
+    load_tile<T, V, K>(x, p.xst, from, on, r0, p.R, 0, live, raw);
+    if (on) {
+        w = load_vec<T, V>(p.w + c * (int64_t)sizeof(T));
+        if (p.b) b = load_vec<T, V>(p.b + c * (int64_t)sizeof(T));
+    }
+    // Statistics of the chunks, joined as those of threads are.
+    int64_t all = p.P;
+    if (p.lengths) all = max((int64_t)0, min(p.P, (int64_t)p.lengths[s.n]));
+    const int slots = p.chunks * p.parts;
+    const float total = fmaxf((float)all * p.cg, 1.0f);
+    auto size = [&](int i) {        // elements of slot i
+        const int ch = i / p.parts, pt = i - ch * p.parts;
+        const int64_t first = (int64_t)ch * p.chunk_rows;
+        const int64_t r = max((int64_t)0, min(min((int64_t)p.chunk_rows, p.P - first), all - first));
+        return (float)r * (p.parts > 1 ? min(p.cols * V, p.cg - pt * p.cols * V) : p.cg);
+    };
+    for (int g = tid / 64; g < s.groups; g += blockDim.x / 64) {
+        const int64_t at = s.n * p.G + s.bundle * p.kg + g;
+        const float2 *const of = p.chunk + at * slots;
+        float a = 0.0f, q = 0.0f;
+        for (int i = lane; i < slots; i += 64) a = fmaf(size(i), of[i].x, a);
+        const float mean = wave_sum(a) / total;
+        for (int i = lane; i < slots; i += 64) {
+            const float2 v = of[i];
+            const float d = v.x - mean;
+            q += fmaf(size(i) * d, d, v.y);
         }
-        if constexpr (WHAT == kChunkStats) return;
-    } else {
-        // Statistics of the chunks, joined as those of threads are.
-        int64_t all = p.P;
-        if (p.lengths) all = max((int64_t)0, min(p.P, (int64_t)p.lengths[s.n]));
-        const int slots = p.chunks * p.parts;
-        const float total = fmaxf((float)all * p.cg, 1.0f);
-        auto size = [&](int i) {        // elements of slot i
-            const int ch = i / p.parts, pt = i - ch * p.parts;
-            const int64_t first = (int64_t)ch * p.chunk_rows;
-            const int64_t r = max((int64_t)0, min(min((int64_t)p.chunk_rows, p.P - first), all - first));
-            return (float)r * (p.parts > 1 ? min(p.cols * V, p.cg - pt * p.cols * V) : p.cg);
-        };
-        for (int g = tid / 64; g < s.groups; g += blockDim.x / 64) {
-            const int64_t at = s.n * p.G + s.bundle * p.kg + g;
-            const float2 *const mine_of = p.chunk + at * slots;
-            float a = 0.0f, q = 0.0f;
-            for (int i = lane; i < slots; i += 64) a = fmaf(size(i), mine_of[i].x, a);
-            const float mean = wave_sum(a) / total;
-            for (int i = lane; i < slots; i += 64) {
-                const float2 v = mine_of[i];
-                const float d = v.x - mean;
-                q += fmaf(size(i) * d, d, v.y);
-            }
-            q = wave_sum(q);
-            if (lane == 0) {
-                const float2 v = make_float2(mean, 1.0f / sqrtf(q / total + p.eps));
-                out[g] = v;
-                if (p.stats_out && s.chunk == 0 && s.part == 0) reinterpret_cast<float2 *>(p.stats_out)[at] = v;
-            }
+        q = wave_sum(q);
+        if (lane == 0) {
+            const float2 v = make_float2(mean, 1.0f / sqrtf(q / total + p.eps));
+            out[g] = v;
+            if (p.stats_out && s.chunk == 0 && s.part == 0) reinterpret_cast<float2 *>(p.stats_out)[at] = v;
         }
-        forget<T, V, K>(raw);
     }
     __syncthreads();
     if (!on) return;
-    const float2 st = out[p.parts > 1 ? 0 : col / width];
-    const Vec<T, V> w = load_vec<T, V>(p.w + c * (int64_t)sizeof(T));
-    Vec<T, V> b = {};
-    if (p.b) b = load_vec<T, V>(p.b + c * (int64_t)sizeof(T));
-    char *const y = p.y + ((s.n * p.P + s.first) * p.C + s.c0) * (int64_t)sizeof(T);
+    const float2 st = out[p.parts > 1 ? 0 : col / (p.cg / V)];
     const int64_t row = p.C * (int64_t)sizeof(T);
+    char *const y = p.y + (s.n * p.P + s.first) * row + s.c0 * (int64_t)sizeof(T);
     const uint32_t to = (uint32_t)r0 * (uint32_t)row + (uint32_t)(col * V * sizeof(T));
+    for (int first = 0; first < s.rows; first += p.R * K) {
+        load_tile<T, V, K>(x, p.xst, from, true, r0, p.R, first + p.R * K, live, next);
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-        const int r = r0 + j * p.R;
-        if (r >= s.rows) continue;
-        float f[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const float z = fmaf((to_f32(raw[j].v[k]) - st.x) * st.y, to_f32(w.v[k]), to_f32(b.v[k]));
-            f[k] = r < live ? (p.silu ? z * sigmoid(z) : z) : 0.0f;
+        for (int j = 0; j < K; ++j) {
+            const int r = first + r0 + j * p.R;
+            if (r < s.rows) normed<T, V>(p, raw[j], st, w, b, r < live, y + first * row + j * (p.R * row) + to);
+            keep_order();
         }
-        store_vec<T, V>(y + j * (p.R * row) + to, f);
-        keep_order();
+#pragma unroll
+        for (int j = 0; j < K; ++j) raw[j] = next[j];
     }
 }
 
 // ---------------------------------------------------------------- backward
 
+// d = x - mean and dz = dy act'(z), z = a d + b with a = w rstd.
 template <typename T, int V>
-__device__ __forceinline__ void slopes(const Vec<T, V> &x, const Vec<T, V> &dy, const float (&w)[V], const float (&b)[V], float2 st,
-                                       int silu, float (&hat)[V], float (&dz)[V])
+__device__ __forceinline__ void slopes(const Vec<T, V> &x, const Vec<T, V> &dy, const float (&a)[V], const float (&b)[V], float mean,
+                                       int silu, float (&d)[V], float (&dz)[V])
 {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        hat[k] = (to_f32(x.v[k]) - st.x) * st.y;
+        d[k] = to_f32(x.v[k]) - mean;
         dz[k] = to_f32(dy.v[k]);
-        if (silu) {
-            const float z = fmaf(hat[k], w[k], b[k]), sg = sigmoid(z);
+    }
+    if (silu)       // one branch for all: the channels' exponentials overlap
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float z = fmaf(d[k], a[k], b[k]), sg = sigmoid(z);
             dz[k] *= fmaf(z * sg, 1.0f - sg, sg);
         }
-    }
 }
 
 // Sums of each column's values over the rows of threads: col_sums[0..cols V) of `out`, for the
@@ -353,131 +459,264 @@ __device__ __forceinline__ void column_sums(const Norm &p, const Slab &s, int ti
     }
 }
 
-template <typename T, int V, int K, int WHAT>
+// A thread's weights and biases.
+template <typename T, int V>
+__device__ __forceinline__ void load_affine(const Norm &p, bool on, int64_t c, float (&w)[V], float (&b)[V])
+{
+    Vec<T, V> wr = {}, br = {};
+    if (on) {
+        wr = load_vec<T, V>(p.w + c * (int64_t)sizeof(T));
+        if (p.b) br = load_vec<T, V>(p.b + c * (int64_t)sizeof(T));
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        w[k] = to_f32(wr.v[k]);
+        b[k] = to_f32(br.v[k]);
+    }
+}
+
+// What a thread's vector adds to its sums of dz d and of dz.  (dw, db, and S1, S2 of its group all
+// follow from those.)
+template <typename T, int V>
+__device__ __forceinline__ void add_sums(const Norm &p, const Vec<T, V> &x, const Vec<T, V> &dy, const float (&a)[V], const float (&b)[V],
+                                         float mean, float (&sd)[V], float (&sz)[V])
+{
+    float d[V], dz[V];
+    slopes<T, V>(x, dy, a, b, mean, p.silu, d, dz);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        sd[k] = fmaf(dz[k], d[k], sd[k]);
+        sz[k] += dz[k];
+    }
+}
+
+// dx = a dz - rstd S1 / m - d rstd^2 S2 / m: c1 = rstd S1 / m, c2 = rstd^2 S2 / m.
+template <typename T, int V>
+__device__ __forceinline__ void input_slope(const Norm &p, const Vec<T, V> &x, const Vec<T, V> &dy, const float (&a)[V], const float (&b)[V],
+                                            float mean, float c1, float c2, bool live, char *to)
+{
+    float d[V], dz[V], f[V];
+    slopes<T, V>(x, dy, a, b, mean, p.silu, d, dz);
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = live ? fmaf(a[k], dz[k], -fmaf(d[k], c2, c1)) : 0.0f;
+    store_vec<T, V>(to, f);
+}
+
+__device__ __forceinline__ float per_element(const Norm &p, int64_t n)
+{
+    int64_t all = p.P;
+    if (p.lengths) all = max((int64_t)0, min(p.P, (int64_t)p.lengths[n]));
+    return 1.0f / fmaxf((float)all * p.cg, 1.0f);
+}
+
+// Whole samples in registers: a range of them, their dw and db added up on the way.
+template <typename T, int V, int K>
 __global__ __launch_bounds__(kMaxThreads) void gn_backward(const Norm p)
 {
     __shared__ float2 mine[kMaxThreads];
     __shared__ float2 out[kMaxThreads];
-    __shared__ float cells[WHAT == kChunkApply ? 1 : kMaxThreads * V];
+    __shared__ float cells[kMaxThreads * V * (K > 1 ? 2 : 1)];
     Slab s;
     if (!find_slab(p, s)) return;
     slab_columns<V>(p, s);
-    const int tid = threadIdx.x, lane = tid % 64, r0 = tid / p.cols, col = tid - r0 * p.cols;
-    const int width = p.parts > 1 ? s.cols : p.cg / V;
+    const int tid = threadIdx.x, r0 = tid / p.cols, col = tid - r0 * p.cols;
     const bool on = r0 < p.R && col < s.cols;
     const int64_t c = s.c0 + (int64_t)col * V, row = p.C * (int64_t)sizeof(T);
-    const int g = on ? (p.parts > 1 ? 0 : col / width) : 0;
+    const int g = on ? col / (p.cg / V) : 0;
     const uint32_t at0 = (uint32_t)(col * V * sizeof(T)), xat = (uint32_t)r0 * (uint32_t)p.xst + at0,
                    dat = (uint32_t)r0 * (uint32_t)p.dst + at0, to = (uint32_t)r0 * (uint32_t)row + at0;
-    float w[V] = {}, b[V] = {}, dw[V] = {}, db[V] = {};
-    if (on) {
-        const Vec<T, V> wr = load_vec<T, V>(p.w + c * (int64_t)sizeof(T));
-        Vec<T, V> br = {};
-        if (p.b) br = load_vec<T, V>(p.b + c * (int64_t)sizeof(T));
+    // Sums over samples: with more than one position a thread in LDS, its registers hold the sample.
+    float b[V], dw[V] = {}, db[V] = {};
+    if constexpr (K > 1)
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            w[k] = to_f32(wr.v[k]);
-            b[k] = to_f32(br.v[k]);
-        }
-    }
-    // Whole samples: a range of them, their dw and db added up on the way.
-    const int64_t from = WHAT == kWholeSample ? s.n * p.range : s.n, past = WHAT == kWholeSample ? min(from + p.range, p.N) : s.n + 1;
+        for (int k = 0; k < 2 * V; ++k) cells[k * kMaxThreads + tid] = 0.0f;
+    const int64_t from = s.n * p.range, past = min(from + p.range, p.N);
     for (int64_t n = from; n < past; ++n) {
         const int live = live_rows(p, n, s);
-        const char *const x = p.x + n * p.xsb + s.first * p.xst + s.c0 * (int64_t)sizeof(T);
-        const char *const dy = p.dy + n * p.dsb + s.first * p.dst + s.c0 * (int64_t)sizeof(T);
         Vec<T, V> xr[K], dr[K];
+        load_tile<T, V, K>(p.x + n * p.xsb + s.c0 * (int64_t)sizeof(T), p.xst, xat, on, r0, p.R, 0, live, xr);
+        load_tile<T, V, K>(p.dy + n * p.dsb + s.c0 * (int64_t)sizeof(T), p.dst, dat, on, r0, p.R, 0, live, dr);
+        const float2 st = reinterpret_cast<const float2 *>(p.stats)[n * p.G + s.bundle * p.kg + g];
+        float a[V], sd[V] = {}, sz[V] = {}, s1 = 0.0f, s2 = 0.0f;
+        load_affine<T, V>(p, on, c, a, b);
 #pragma unroll
-        for (int j = 0; j < K; ++j)
-            if (on && r0 + j * p.R < live) {
-                xr[j] = load_vec<T, V>(x + j * (p.R * p.xst) + xat);
-                dr[j] = load_vec<T, V>(dy + j * (p.R * p.dst) + dat);
-            }
-        const int64_t at = n * p.G + s.bundle * p.kg;
-        const float2 st = reinterpret_cast<const float2 *>(p.stats)[at + g];
-        if constexpr (WHAT != kChunkApply) {
-            float s1 = 0.0f, s2 = 0.0f;
+        for (int k = 0; k < V; ++k) a[k] *= st.y;
 #pragma unroll
-            for (int j = 0; j < K; ++j)
-                if (on && r0 + j * p.R < live) {
-                    float hat[V], dz[V];
-                    slopes<T, V>(xr[j], dr[j], w, b, st, p.silu, hat, dz);
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const float t = w[k] * dz[k];
-                        s1 += t;
-                        s2 = fmaf(t, hat[k], s2);
-                        dw[k] = fmaf(dz[k], hat[k], dw[k]);
-                        db[k] += dz[k];
-                    }
-                    keep_order();
-                }
-            group_sums<V>(p, s, tid, s1, s2, mine, out);
-            forget<T, V, K>(xr);
-            forget<T, V, K>(dr);
-            if constexpr (WHAT == kChunkStats) {
-                if (tid < s.groups) p.chunk[(at + tid) * (p.chunks * p.parts) + s.chunk * p.parts + s.part] = out[tid];
-            }
-        } else {
-            const int slots = p.chunks * p.parts;
-            for (int k = tid / 64; k < s.groups; k += blockDim.x / 64) {
-                float s1 = 0.0f, s2 = 0.0f;
-                for (int i = lane; i < slots; i += 64) {
-                    const float2 v = p.chunk[(at + k) * slots + i];
-                    s1 += v.x;
-                    s2 += v.y;
-                }
-                s1 = wave_sum(s1);
-                s2 = wave_sum(s2);
-                if (lane == 0) out[k] = make_float2(s1, s2);
-            }
-            forget<T, V, K>(xr);
-            forget<T, V, K>(dr);
-            __syncthreads();
+        for (int j = 0; j < K; ++j) {
+            if (on && r0 + j * p.R < live) add_sums<T, V>(p, xr[j], dr[j], a, b, st.x, sd, sz);
+            keep_order();
         }
-        if constexpr (WHAT != kChunkStats) {
-            int64_t all = p.P;
-            if (p.lengths) all = max((int64_t)0, min(p.P, (int64_t)p.lengths[n]));
-            const float inv = 1.0f / fmaxf((float)all * p.cg, 1.0f);
-            const float m1 = out[g].x * inv, m2 = out[g].y * inv;
-            char *const dx = p.y + ((n * p.P + s.first) * p.C + s.c0) * (int64_t)sizeof(T);
 #pragma unroll
-            for (int j = 0; j < K; ++j) {
-                const int r = r0 + j * p.R;
-                if (!on || r >= s.rows) continue;
-                float hat[V], dz[V], f[V];
-                slopes<T, V>(xr[j], dr[j], w, b, st, p.silu, hat, dz);
-#pragma unroll
-                for (int k = 0; k < V; ++k) f[k] = r < live ? st.y * (fmaf(w[k], dz[k], -m1) - hat[k] * m2) : 0.0f;
-                store_vec<T, V>(dx + j * (p.R * row) + to, f);
-                keep_order();
+        for (int k = 0; k < V; ++k) {
+            if constexpr (K > 1) {
+                cells[k * kMaxThreads + tid] = fmaf(sd[k], st.y, cells[k * kMaxThreads + tid]);
+                cells[(V + k) * kMaxThreads + tid] += sz[k];
+            } else {
+                dw[k] = fmaf(sd[k], st.y, dw[k]);
+                db[k] += sz[k];
             }
-            if constexpr (WHAT == kWholeSample) __syncthreads();      // `out` is read before the next sample's
+            s1 = fmaf(a[k], sz[k], s1);      // rstd S1
+            s2 = fmaf(a[k], sd[k], s2);
+        }
+        group_sums<V>(p, s, tid, s1, s2, mine, out);
+        forget<T, V, K>(xr);
+        forget<T, V, K>(dr);
+        const float inv = per_element(p, n), c1 = out[g].x * inv, c2 = out[g].y * inv * st.y * st.y;
+        char *const dx = p.y + (n * p.P * p.C + s.c0) * (int64_t)sizeof(T);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int r = r0 + j * p.R;
+            if (on && r < s.rows) input_slope<T, V>(p, xr[j], dr[j], a, b, st.x, c1, c2, r < live, dx + j * (p.R * row) + to);
+            keep_order();
+        }
+        __syncthreads();      // `out` is read before the next sample's
+    }
+    if constexpr (K > 1)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            dw[k] = cells[k * kMaxThreads + tid];
+            db[k] = cells[(V + k) * kMaxThreads + tid];
+        }
+    float *const o = p.part + s.n * 2 * p.C + s.c0;
+    column_sums<V>(p, s, tid, r0, col, dw, cells, o);
+    column_sums<V>(p, s, tid, r0, col, db, cells, o + p.C);
+}
+
+// Chunks: S1, S2 and the partial dw, db first, then dx.
+template <typename T, int V>
+__global__ __launch_bounds__(kMaxThreads) void gn_chunk_sums(const Norm p)
+{
+    constexpr int K = kTileBwd;
+    __shared__ float2 mine[kMaxThreads];
+    __shared__ float2 out[kMaxThreads];
+    __shared__ float cells[kMaxThreads * V];
+    Slab s;
+    if (!find_slab(p, s)) return;
+    slab_columns<V>(p, s);
+    const int tid = threadIdx.x, r0 = tid / p.cols, col = tid - r0 * p.cols, live = live_rows(p, s.n, s);
+    const bool on = r0 < p.R && col < s.cols;
+    const int64_t c = s.c0 + (int64_t)col * V, at = s.n * p.G + s.bundle * p.kg;
+    const uint32_t at0 = (uint32_t)(col * V * sizeof(T)), xat = (uint32_t)r0 * (uint32_t)p.xst + at0, dat = (uint32_t)r0 * (uint32_t)p.dst + at0;
+    const char *const x = p.x + s.n * p.xsb + s.first * p.xst + s.c0 * (int64_t)sizeof(T);
+    const char *const dy = p.dy + s.n * p.dsb + s.first * p.dst + s.c0 * (int64_t)sizeof(T);
+    Vec<T, V> xr[K], dr[K], xn[K], dn[K];
+    load_tile<T, V, K>(x, p.xst, xat, on, r0, p.R, 0, live, xr);
+    load_tile<T, V, K>(dy, p.dst, dat, on, r0, p.R, 0, live, dr);
+    float a[V], b[V], sd[V] = {}, sz[V] = {}, s1 = 0.0f, s2 = 0.0f;
+    load_affine<T, V>(p, on, c, a, b);
+    const float2 st = reinterpret_cast<const float2 *>(p.stats)[at + (on && p.parts == 1 ? col / (p.cg / V) : 0)];
+#pragma unroll
+    for (int k = 0; k < V; ++k) a[k] *= st.y;
+    for (int first = 0; first < live; first += p.R * K) {
+        load_tile<T, V, K>(x, p.xst, xat, on, r0, p.R, first + p.R * K, live, xn);
+        load_tile<T, V, K>(dy, p.dst, dat, on, r0, p.R, first + p.R * K, live, dn);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            if (on && first + r0 + j * p.R < live) add_sums<T, V>(p, xr[j], dr[j], a, b, st.x, sd, sz);
+            keep_order();
+        }
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            xr[j] = xn[j];
+            dr[j] = dn[j];
         }
     }
-    if constexpr (WHAT != kChunkApply) {
-        const int64_t line = WHAT == kWholeSample ? s.n : s.n * p.chunks + s.chunk;
-        float *const o = p.part + line * 2 * p.C + s.c0;
-        column_sums<V>(p, s, tid, r0, col, dw, cells, o);
-        column_sums<V>(p, s, tid, r0, col, db, cells, o + p.C);
+    load_affine<T, V>(p, on, c, a, b);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        sd[k] *= st.y;
+        s1 = fmaf(a[k], sz[k], s1);
+        s2 = fmaf(a[k], sd[k], s2);
+    }
+    group_sums<V>(p, s, tid, s1, s2, mine, out);
+    for (int g = tid; g < s.groups; g += blockDim.x) p.chunk[(at + g) * (p.chunks * p.parts) + s.chunk * p.parts + s.part] = out[g];
+    float *const o = p.part + (s.n * p.chunks + s.chunk) * 2 * p.C + s.c0;
+    column_sums<V>(p, s, tid, r0, col, sd, cells, o);
+    column_sums<V>(p, s, tid, r0, col, sz, cells, o + p.C);
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(kMaxThreads) void gn_chunk_slopes(const Norm p)
+{
+    constexpr int K = kTileBwd;
+    __shared__ float2 out[kMaxThreads];
+    Slab s;
+    if (!find_slab(p, s)) return;
+    slab_columns<V>(p, s);
+    const int tid = threadIdx.x, lane = tid % 64, r0 = tid / p.cols, col = tid - r0 * p.cols, live = live_rows(p, s.n, s);
+    const bool on = r0 < p.R && col < s.cols;
+    const int64_t c = s.c0 + (int64_t)col * V, at = s.n * p.G + s.bundle * p.kg, row = p.C * (int64_t)sizeof(T);
+    const uint32_t at0 = (uint32_t)(col * V * sizeof(T)), xat = (uint32_t)r0 * (uint32_t)p.xst + at0,
+                   dat = (uint32_t)r0 * (uint32_t)p.dst + at0, to = (uint32_t)r0 * (uint32_t)row + at0;
+    const char *const x = p.x + s.n * p.xsb + s.first * p.xst + s.c0 * (int64_t)sizeof(T);
+    const char *const dy = p.dy + s.n * p.dsb + s.first * p.dst + s.c0 * (int64_t)sizeof(T);
+    Vec<T, V> xr[K], dr[K], xn[K], dn[K];
+    load_tile<T, V, K>(x, p.xst, xat, on, r0, p.R, 0, live, xr);
+    load_tile<T, V, K>(dy, p.dst, dat, on, r0, p.R, 0, live, dr);
+    float a[V], b[V];
+    load_affine<T, V>(p, on, c, a, b);
+    const int slots = p.chunks * p.parts;
+    for (int k = tid / 64; k < s.groups; k += blockDim.x / 64) {
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int i = lane; i < slots; i += 64) {
+            const float2 v = p.chunk[(at + k) * slots + i];
+            s1 += v.x;
+            s2 += v.y;
+        }
+        s1 = wave_sum(s1);
+        s2 = wave_sum(s2);
+        if (lane == 0) out[k] = make_float2(s1, s2);
+    }
+    __syncthreads();
+    if (!on) return;
+    const int g = p.parts > 1 ? 0 : col / (p.cg / V);
+    const float2 st = reinterpret_cast<const float2 *>(p.stats)[at + g];
+    const float inv = per_element(p, s.n) * st.y, c1 = out[g].x * inv, c2 = out[g].y * inv * st.y;
+#pragma unroll
+    for (int k = 0; k < V; ++k) a[k] *= st.y;
+    char *const dx = p.y + (s.n * p.P + s.first) * row + s.c0 * (int64_t)sizeof(T);
+    for (int first = 0; first < s.rows; first += p.R * K) {
+        load_tile<T, V, K>(x, p.xst, xat, true, r0, p.R, first + p.R * K, live, xn);
+        load_tile<T, V, K>(dy, p.dst, dat, true, r0, p.R, first + p.R * K, live, dn);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int r = first + r0 + j * p.R;
+            if (r < s.rows) input_slope<T, V>(p, xr[j], dr[j], a, b, st.x, c1, c2, r < live, dx + first * row + j * (p.R * row) + to);
+            keep_order();
+        }
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            xr[j] = xn[j];
+            dr[j] = dn[j];
+        }
     }
 }
 
-// Partial sums [rows][2][C] -> dw [C], db [C] (or nullptr), in order: 16 rows at a time, then those 16.
+// Partial sums [rows][2][C] -> dw [C], db [C] (or nullptr), in order: 64 rows at a time, eight of a
+// thread's loads at once, then those 64.
 template <typename T>
-__global__ __launch_bounds__(256) void gn_param_sum(const float *__restrict__ part, T *__restrict__ dw, T *__restrict__ db, int64_t rows,
-                                                    int64_t C)
+__global__ __launch_bounds__(1024) void gn_param_sum(const float *__restrict__ part, T *__restrict__ dw, T *__restrict__ db, int64_t rows,
+                                                     int64_t C)
 {
-    __shared__ float s[16][17];
+    __shared__ float s[64][17];
     const int col = threadIdx.x % 16, row = threadIdx.x / 16;
     const int64_t c = (int64_t)blockIdx.x * 16 + col;
     float v = 0.0f;
-    if (c < 2 * C)
-        for (int64_t r = row; r < rows; r += 16) v += part[r * 2 * C + c];
+    if (c < 2 * C) {
+        int64_t r = row;
+        for (; r + 7 * 64 < rows; r += 8 * 64) {
+            float a[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = part[(r + 64 * i) * 2 * C + c];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v += a[i];
+        }
+        for (; r < rows; r += 64) v += part[r * 2 * C + c];
+    }
     s[row][col] = v;
     __syncthreads();
     if (row == 0 && c < 2 * C) {
-        for (int r = 1; r < 16; ++r) v += s[r][col];
+        for (int r = 1; r < 64; ++r) v += s[r][col];
         if (c < C) dw[c] = from_f32<T>(v);
         else if (db) db[c - C] = from_f32<T>(v);
     }
@@ -496,36 +735,21 @@ template <typename F> hipError_t with_vec(int dtype, int V, F &&f)
     };
     return dtype == DT_F32 ? by(float{}) : dtype == DT_F16 ? by(_Float16{}) : by(__bf16{});
 }
-template <typename F> hipError_t with_rows(int K, F &&f)
+template <typename F> void with_rows(int K, F &&f)
 {
-    return K <= 1 ? f(Int<1>{}) : K <= 4 ? f(Int<4>{}) : K <= 8 ? f(Int<8>{}) : f(Int<16>{});
+    if (K <= 1) f(Int<1>{});
+    else if (K <= 4) f(Int<4>{});
+    else if (K <= 8) f(Int<8>{});
+    else f(Int<16>{});
 }
 
-template <int WHAT> hipError_t run_forward(const Norm &p, int dtype, int V, int threads, int K, hipStream_t stream)
+// f(kernel type, vector) of a call; the kernels of whole samples also by K.
+template <typename F> hipError_t launch_with(const Norm &p, const GroupNormArgs &a, const GroupNormPlan &g, F &&f)
 {
     const dim3 grid((unsigned)(8 * ceil_div(p.blocks, 8)));
-    return with_vec(dtype, V, [&](auto t, auto v) {
-        return with_rows(K, [&](auto k) {
-            if constexpr (WHAT != kWholeSample && k.value == 16) return hipErrorInvalidValue;     // no plan has it
-            else {
-                gn_forward<decltype(t), v.value, k.value, WHAT><<<grid, threads, 0, stream>>>(p);
-                return hipGetLastError();
-            }
-        });
-    });
-}
-
-template <int WHAT> hipError_t run_backward(const Norm &p, int dtype, int V, int threads, int K, hipStream_t stream)
-{
-    const dim3 grid((unsigned)(8 * ceil_div(p.blocks, 8)));
-    return with_vec(dtype, V, [&](auto t, auto v) {
-        return with_rows(K, [&](auto k) {
-            if constexpr (k.value == 16) return hipErrorInvalidValue;        // no plan has it
-            else {
-                gn_backward<decltype(t), v.value, k.value, WHAT><<<grid, threads, 0, stream>>>(p);
-                return hipGetLastError();
-            }
-        });
+    return with_vec(a.dtype, g.V, [&](auto t, auto v) {
+        f(t, v, grid);
+        return hipGetLastError();
     });
 }
 
@@ -552,8 +776,7 @@ Norm make_norm(const GroupNormArgs &a, const GroupNormPlan &g)
 
 size_t gn_chunk_bytes(const GroupNormPlan &g, int64_t N, int64_t G)
 {
-    const int64_t slots = (int64_t)g.chunks * g.parts;
-    return slots > 1 ? (sizeof(float2) * (size_t)(N * G * slots) + 255) & ~(size_t)255 : 0;
+    return g.whole ? 0 : (sizeof(float2) * (size_t)(N * G * g.chunks * g.parts) + 255) & ~(size_t)255;
 }
 
 GroupNormPlan gn_plan(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, bool backward)
@@ -580,7 +803,7 @@ GroupNormPlan gn_plan(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, boo
                     if (t < cols || (want == most && t < kMaxThreads)) continue;
                     const int64_t R = t / cols, K = ceil_div(std::max<int64_t>(P, 1), R);
                     if (K > want) continue;
-                    g.kg = (int32_t)kg; g.cols = (int32_t)cols; g.threads = t; g.K = (int32_t)K;
+                    g.whole = 1; g.kg = (int32_t)kg; g.cols = (int32_t)cols; g.threads = t; g.K = (int32_t)K;
                     if (backward) {     // samples of a workgroup: enough workgroups, few partial sums
                         const int64_t bundles = ceil_div(G, kg), held = 256 * (2048 / t);
                         g.range = std::max<int64_t>(1, ceil_div(N * bundles, held));
@@ -594,9 +817,10 @@ GroupNormPlan gn_plan(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, boo
     g.cols = (int32_t)(g.parts > 1 ? ceil_div(cgv, g.parts) : g.kg * cgv);
     g.threads = (int32_t)std::max<int64_t>(512, 64 * ceil_div(g.cols, 64));
     if (g.threads > 512) g.threads = kMaxThreads;
-    g.K = backward ? 4 : 8;
-    const int64_t R = g.threads / g.cols;
-    g.chunk_rows = (int32_t)std::min<int64_t>(R * g.K, std::max<int64_t>(P, 1));
+    g.K = backward ? kTileBwd : kTile;
+    const int64_t tile = g.threads / g.cols * g.K, tiles = ceil_div(std::max<int64_t>(P, 1), tile);
+    const int64_t bundles = ceil_div(G, g.kg) * g.parts, want = std::max<int64_t>(1, 512 / std::max<int64_t>(1, N * bundles));
+    g.chunk_rows = (int32_t)(tile * ceil_div(tiles, want));
     g.chunks = (int32_t)ceil_div(std::max<int64_t>(P, 1), g.chunk_rows);
     return g;
 }
@@ -618,33 +842,50 @@ bool gn_fits(const GroupNormArgs &a, const GroupNormPlan &g)
 hipError_t launch_group_norm(const GroupNormArgs &a, const GroupNormPlan &g, const char **kname)
 {
     const Norm p = make_norm(a, g);
-    if (g.chunks * g.parts == 1) {
+    if (g.whole) {
         *kname = "gn_forward";
-        return run_forward<kWholeSample>(p, a.dtype, g.V, g.threads, g.K, a.stream);
+        return launch_with(p, a, g, [&](auto t, auto v, dim3 grid) {
+            with_rows(g.K, [&](auto k) {
+                gn_forward<decltype(t), v.value, k.value><<<grid, g.threads, 0, a.stream>>>(p);
+            });
+        });
     }
-    *kname = "gn_forward_chunks";
-    const hipError_t err = run_forward<kChunkStats>(p, a.dtype, g.V, g.threads, g.K, a.stream);
-    return err != hipSuccess ? err : run_forward<kChunkApply>(p, a.dtype, g.V, g.threads, g.K, a.stream);
+    *kname = "gn_chunk_apply";
+    const hipError_t err = launch_with(p, a, g, [&](auto t, auto v, dim3 grid) {
+        gn_chunk_stats<decltype(t), v.value><<<grid, g.threads, 0, a.stream>>>(p);
+    });
+    return err != hipSuccess ? err : launch_with(p, a, g, [&](auto t, auto v, dim3 grid) {
+        gn_chunk_apply<decltype(t), v.value><<<grid, g.threads, 0, a.stream>>>(p);
+    });
 }
 
 hipError_t launch_group_norm_bwd(const GroupNormArgs &a, const GroupNormPlan &g, const char **kname)
 {
     const Norm p = make_norm(a, g);
-    *kname = g.chunks * g.parts == 1 ? "gn_backward" : "gn_backward_chunks";
+    *kname = g.whole ? "gn_backward" : "gn_chunk_slopes";
     if (p.blocks > 0) {
         hipError_t err;
-        if (g.chunks * g.parts == 1) {
-            err = run_backward<kWholeSample>(p, a.dtype, g.V, g.threads, g.K, a.stream);
+        if (g.whole) {
+            err = launch_with(p, a, g, [&](auto t, auto v, dim3 grid) {
+                with_rows(g.K, [&](auto k) {
+                    if constexpr (k.value <= 8) gn_backward<decltype(t), v.value, k.value><<<grid, g.threads, 0, a.stream>>>(p);
+                });
+            });
         } else {
-            err = run_backward<kChunkStats>(p, a.dtype, g.V, g.threads, g.K, a.stream);
-            if (err == hipSuccess) err = run_backward<kChunkApply>(p, a.dtype, g.V, g.threads, g.K, a.stream);
+            err = launch_with(p, a, g, [&](auto t, auto v, dim3 grid) {
+                gn_chunk_sums<decltype(t), v.value><<<grid, g.threads, 0, a.stream>>>(p);
+            });
+            if (err == hipSuccess)
+                err = launch_with(p, a, g, [&](auto t, auto v, dim3 grid) {
+                    gn_chunk_slopes<decltype(t), v.value><<<grid, g.threads, 0, a.stream>>>(p);
+                });
         }
         if (err != hipSuccess) return err;
     }
     const unsigned grid = (unsigned)ceil_div(2 * a.C, 16);
     return with_vec(a.dtype, 1, [&](auto t, auto) {
         typedef decltype(t) E;
-        gn_param_sum<E><<<grid, 256, 0, a.stream>>>(p.part, (E *)a.dw, (E *)a.db, p.rows, a.C);
+        gn_param_sum<E><<<grid, 1024, 0, a.stream>>>(p.part, (E *)a.dw, (E *)a.db, p.rows, a.C);
         return hipGetLastError();
     });
 }

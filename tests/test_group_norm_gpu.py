@@ -93,6 +93,8 @@ CASES = [  # N, P, C, G, silu, bias, lengths, layout
     (2, 3, 5000, 1, True, True, None, "plain"),        # a group wider than a workgroup
     (1, 70, 2062, 2, True, True, [33], "plain"),
     (300, 2, 64, 4, True, True, None, "plain"),
+    (1100, 3, 1030, 1, True, True, None, "plain"),    # too wide, and enough samples for one chunk each
+    (40, 17000, 3, 1, False, True, None, "plain"),
 ]
 
 
