@@ -134,24 +134,30 @@ __device__ __forceinline__ uint4 load16(const int8_t *row, int k, int K)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr int kStage = 128;              // bytes of K in a stage
+constexpr int kStage = 64;               // bytes of K in a stage
+constexpr int kStages = 4;               // stages in LDS: one being read, three on their way
 constexpr uint32_t kNowhere = 0x80000000u;
 
 // Tile BM x BN, waves WM x WN of it.  ALIGNED: K a multiple of 16 and rows on 16 bytes; else
 // the stages go through registers.
 //
-// LDS holds a stage's rows one after the other, 8 pieces of 16 bytes each, piece c of row r at place
-// c ^ (r & 7): a wave reads one piece of 32 rows at a time, and any 8 rows next to each other then
-// lie in different banks.
+// What bounds it is how early a stage is asked for: a tile of 256 x 256 takes 64 KB for each 2048
+// cycles of products, and the first of an XCD's workgroups to touch a line waits some 4000 for it.
+// So stages are short and three are on their way: 2 stages of 128 bytes took 250 us for 8192 x 6144
+// x 4096, 4 of 64 bytes MEASURED_TILE.
+//
+// LDS holds a stage's rows one after the other, 4 pieces of 16 bytes each, piece c of row r at place
+// c ^ (r / 4 & 3): a wave reads one piece of 32 rows at a time, and any 16 rows next to each other
+// then lie in different banks.
 template <typename T, int BM, int BN, int WM, int WN, bool ALIGNED>
-__global__ __launch_bounds__(64 * WM *WN) void mm_tile(const Mm p)
+__global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mm_tile(const Mm p)
 {
-    constexpr int NWAVES = WM * WN, UA = BM * 8 / 64 / NWAVES, UB = BN * 8 / 64 / NWAVES;   // loads of a wave
+    constexpr int NWAVES = WM * WN, UA = BM * 4 / 64 / NWAVES, UB = BN * 4 / 64 / NWAVES;   // loads of a wave
     constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
-    __shared__ uint4 a0[BM * 8], a1[BM * 8], b0[BN * 8], b1[BN * 8];
+    __shared__ uint4 s0[(BM + BN) * 4], s1[(BM + BN) * 4], s2[(BM + BN) * 4], s3[(BM + BN) * 4];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l32 = lane % 32, hf = lane / 32;
     const int wm = wave / WN, wn = wave % WN;
-    // Each XCD takes tiles next to each other; within it, runs of 8 tiles of tokens for each channel tile share weights.
+    // Each XCD takes tiles next to each other: bands of 8 tiles of tokens, channel tile after channel tile.
     const int64_t tiles = (int64_t)p.mt * p.nt, per = (tiles + 7) / 8, id = (int64_t)(blockIdx.x % 8) * per + blockIdx.x / 8;
     if (blockIdx.x / 8 >= per || id >= tiles) return;
     const int band = (int)(id / (8 * (int64_t)p.nt)), rows_of_band = min(8, p.mt - band * 8);
@@ -163,95 +169,169 @@ __global__ __launch_bounds__(64 * WM *WN) void mm_tile(const Mm p)
     i32x16 acc[FM][FN] = {};
     const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(A), (short)0, rows * p.K, 0x00020000);
     const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(B), (short)0, cols * p.K, 0x00020000);
-    const int piece = (lane % 8) ^ (lane / 8);      // of the row that this lane's 16 bytes go to
+    // A load fills 16 rows: the lane's row of them, and the piece that goes to its place.
+    const int lrow = lane / 4, piece = lane % 4 ^ lrow / 4;
     uint4 held[ALIGNED ? 1 : UA + UB];
 
-    // Stage k0: straight to LDS, or into registers.
-    auto fetch = [&](uint4 *as, uint4 *bs, int k0) {
+    // Stage k0: straight to LDS (past K: zeros), or into registers.
+    auto fetch = [&](uint4 *to, int k0) {
         const int k = 16 * piece;
         if constexpr (ALIGNED) {
             const bool in = k0 + k < p.K;
 #pragma unroll
             for (int i = 0; i < UA; ++i) {
-                const int r = (wave * UA + i) * 8;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (__attribute__((address_space(3))) void *)(as + r * 8), 16,
-                                                         in ? (uint32_t)((r + lane / 8) * p.K + k) : kNowhere, k0, 0, 0);
+                const int r = (wave * UA + i) * 16;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (__attribute__((address_space(3))) void *)(to + r * 4), 16,
+                                                         in ? (uint32_t)((r + lrow) * p.K + k) : kNowhere, k0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < UB; ++i) {
-                const int r = (wave * UB + i) * 8;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (__attribute__((address_space(3))) void *)(bs + r * 8), 16,
-                                                         in ? (uint32_t)((r + lane / 8) * p.K + k) : kNowhere, k0, 0, 0);
+                const int r = (wave * UB + i) * 16;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (__attribute__((address_space(3))) void *)(to + (BM + r) * 4), 16,
+                                                         in ? (uint32_t)((r + lrow) * p.K + k) : kNowhere, k0, 0, 0);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < UA; ++i)
-                held[i] = load16(A + (int64_t)min((wave * UA + i) * 8 + lane / 8, rows - 1) * p.K, k0 + k, p.K);
+            for (int i = 0; i < UA; ++i) held[i] = load16(A + (int64_t)min((wave * UA + i) * 16 + lrow, rows - 1) * p.K, k0 + k, p.K);
 #pragma unroll
-            for (int i = 0; i < UB; ++i)
-                held[UA + i] = load16(B + (int64_t)min((wave * UB + i) * 8 + lane / 8, cols - 1) * p.K, k0 + k, p.K);
+            for (int i = 0; i < UB; ++i) held[UA + i] = load16(B + (int64_t)min((wave * UB + i) * 16 + lrow, cols - 1) * p.K, k0 + k, p.K);
         }
     };
-    auto settle = [&](uint4 *as, uint4 *bs) {
+    auto put = [&](uint4 *to) {
+        if constexpr (!ALIGNED) {
+#pragma unroll
+            for (int i = 0; i < UA; ++i) to[(wave * UA + i) * 64 + lane] = held[i];
+#pragma unroll
+            for (int i = 0; i < UB; ++i) to[BM * 4 + (wave * UB + i) * 64 + lane] = held[UA + i];
+        }
+    };
+    // Every wave's next stage is in LDS, and its reads of this one are done.
+    auto meet = [&] {
         if constexpr (ALIGNED) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            static_assert(UA + UB == 4 || UA + UB == 2, "two stages' loads may stay on their way");
+            if constexpr (UA + UB == 4) asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         } else {
-#pragma unroll
-            for (int i = 0; i < UA; ++i) as[(wave * UA + i) * 64 + lane] = held[i];
-#pragma unroll
-            for (int i = 0; i < UB; ++i) bs[(wave * UB + i) * 64 + lane] = held[UA + i];
+            __syncthreads();
         }
-        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
     };
-    auto products = [&](const uint4 *as, const uint4 *bs) {
+    // Operands of 32 bytes of K, in two sets: one is read while the other is multiplied.
+    uint4 a[2][FM], b[2][FN];
+    auto read = [&](const uint4 *from, int kk) {
 #pragma unroll
-        for (int kk = 0; kk < kStage / 32; ++kk) {
-            uint4 a[FM], b[FN];
-#pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const int r = (wm * FM + i) * 32 + l32;
-                a[i] = as[r * 8 + ((2 * kk + hf) ^ (r & 7))];
-            }
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const int r = (wn * FN + j) * 32 + l32;
-                b[j] = bs[r * 8 + ((2 * kk + hf) ^ (r & 7))];
-            }
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a[i]), __builtin_bit_cast(i32x4, b[j]),
-                                                                      acc[i][j], 0, 0, 0);
+        for (int j = 0; j < FN; ++j) {
+            const int r = (wn * FN + j) * 32 + l32;
+            b[kk][j] = from[(BM + r) * 4 + ((2 * kk + hf) ^ (r / 4 & 3))];
         }
-    };
-
-    // Stages in pairs, one buffer each; one past K holds zeros.
-    fetch(a0, b0, 0);
-    settle(a0, b0);
-    for (int k0 = 0; k0 < p.K; k0 += 2 * kStage) {
-        fetch(a1, b1, k0 + kStage);
-        products(a0, b0);
-        settle(a1, b1);
-        if (k0 + 2 * kStage < p.K) fetch(a0, b0, k0 + 2 * kStage);
-        products(a1, b1);
-        settle(a0, b0);
-    }
-
-    // Lane: column l32 of each 32 x 32 block, rows 8 (r / 4) + 4 hf + r % 4.
-    T *const y = static_cast<T *>(p.y);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-        const int n = n0 + (wn * FN + j) * 32 + l32;
-        if (n >= p.N) continue;
-        const float ws = p.ws[n], bias = bias_of<T>(p, n);
+        for (int i = 0; i < FM; ++i) {
+            const int r = (wm * FM + i) * 32 + l32;
+            a[kk][i] = from[r * 4 + ((2 * kk + hf) ^ (r / 4 & 3))];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto multiply = [&](int kk) {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int m = m0 + (wm * FM + i) * 32 + 8 * (r / 4) + 4 * hf + r % 4;
-                if (m < p.M) y[(int64_t)m * p.N + n] = from_f32<T>((float)acc[i][j][r] * p.qs[m] * ws + bias);
+            for (int j = 0; j < FN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, b[kk][j]), __builtin_bit_cast(i32x4, a[kk][i]),
+                                                                  acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // One stage out of `now`: its last operands are in registers before the waves meet; behind that the
+    // stage four later may come into its place (through registers: the one two later into `second`), and
+    // the next one's first operands are read under its last products.
+    auto stage = [&](uint4 *now, uint4 *next, uint4 *second, int k0) {
+        read(now, 1);
+        multiply(0);
+        put(second);
+        meet();
+        fetch(now, k0 + (ALIGNED ? 4 : 3) * kStage);
+        read(next, 0);
+        multiply(1);
+    };
+
+    // Stages in fours, one buffer each; those past K hold zeros.
+    fetch(s0, 0);
+    put(s0);
+    fetch(s1, kStage);
+    put(s1);
+    fetch(s2, 2 * kStage);
+    if constexpr (ALIGNED) fetch(s3, 3 * kStage);
+    if constexpr (ALIGNED && UA + UB == 4) {
+        asm volatile("s_waitcnt vmcnt(12)\n\ts_barrier" ::: "memory");
+    } else if constexpr (ALIGNED) {
+        asm volatile("s_waitcnt vmcnt(6)\n\ts_barrier" ::: "memory");
+    } else {
+        __syncthreads();
+    }
+    read(s0, 0);
+    for (int k0 = 0; k0 < p.K; k0 += kStages * kStage) {
+        stage(s0, s1, s2, k0);
+        stage(s1, s2, s3, k0 + kStage);
+        stage(s2, s3, s0, k0 + 2 * kStage);
+        stage(s3, s0, s1, k0 + 3 * kStage);
+    }
+    // What is still on its way is zeros for LDS that nobody reads as operands.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+    // Channels are the rows of a block of products: a lane has token l32, channels 8 (r / 4) + 4 hf + r % 4.
+    // 32 tokens at a time go through the wave's own piece of LDS, so that rows leave in whole lines; 16-byte
+    // unit u of token t's row lies at u ^ t.
+    constexpr int CW = FN * 32, UPR = CW * (int)sizeof(T) / 16, PER = (BM + BN) * 4 / (32 * UPR);
+    static_assert(PER * 2 >= NWAVES, "the waves' pieces lie in two stages");
+    uint4 *const rowsout = (wave < PER ? s0 : s1) + wave % PER * (32 * UPR);
+    T *const y = static_cast<T *>(p.y);
+    const int nw = n0 + wn * CW;                    // the wave's first channel
+    if (nw >= p.N) return;
+    const bool whole = nw + CW <= p.N;
+    float ws[FN][16], bias[FN][16];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int n = min(nw + j * 32 + 8 * (r / 4) + 4 * hf + r % 4, p.N - 1);
+            ws[j][r] = p.ws[n];
+            bias[j][r] = bias_of<T>(p, n);
+        }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int mw = m0 + (wm * FM + i) * 32;
+        const float qs = p.qs[min(mw + l32, p.M - 1)];
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                Run<T, 4> v;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v.v[k] = from_f32<T>((float)acc[i][j][4 * g + k] * qs * ws[j][4 * g + k] + bias[j][4 * g + k]);
+                const int byte = (j * 32 + 8 * g + 4 * hf) * (int)sizeof(T);
+                char *const to = (char *)(rowsout + l32 * UPR + ((byte / 16) ^ (l32 & (UPR - 1)))) + byte % 16;
+                if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(to) = __builtin_bit_cast(uint4, v);
+                else *reinterpret_cast<uint2 *>(to) = __builtin_bit_cast(uint2, v);
             }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the wave's own writes, by any lane
+#pragma unroll
+        for (int h = 0; h < UPR / 2; ++h) {
+            const int at = h * 64 + lane, t = at / UPR, u = at % UPR, m = mw + t;
+            const uint4 w = rowsout[t * UPR + (u ^ (t & (UPR - 1)))];
+            if (m >= p.M) continue;
+            T *const to = y + (int64_t)m * p.N + nw + u * (16 / (int)sizeof(T));
+            if (whole) {
+                typedef uint32_t out16 __attribute__((ext_vector_type(4), aligned(2)));
+                *reinterpret_cast<out16 *>(to) = __builtin_bit_cast(out16, w);
+            } else {
+                typedef Run<T, 16 / (int)sizeof(T)> Piece;
+                const Piece v = __builtin_bit_cast(Piece, w);
+#pragma unroll
+                for (int k = 0; k < 16 / (int)sizeof(T); ++k)
+                    if (nw + u * (16 / (int)sizeof(T)) + k < p.N) to[k] = v.v[k];
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // read before the next 32 tokens are written
     }
 }
 
