@@ -38,14 +38,25 @@ template <typename T, int V> __device__ __forceinline__ uint32_t top_of(const Ru
     return top;
 }
 
-template <typename T, int V> __device__ __forceinline__ void store_q(int8_t *dst, int valid, const Run<T, V> &r, float scale)
+// x / scale, rounded to fp32 and then to an integer.  x times inv = 1 / scale is off by at most 2^-22 of
+// itself, 3.1e-5 for quotients up to 127: where it lies further than that from a border between two integers
+// its integer is the quotient's, and only next to one (one vector in some hundred) the quotient is taken.
+// 8192 x 4096 in bf16: 21 us, with a division for every value 27.
+template <typename T, int V> __device__ __forceinline__ void store_q(int8_t *dst, int valid, const Run<T, V> &r, float scale, float inv)
 {
-    uint32_t w[V / 4] = {};
+    float v[V], far = 0.0f;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        const float v = rintf(to_f32(r.v[k]) / scale);
-        w[k / 4] |= ((uint32_t)(int32_t)v & 0xffu) << 8 * (k % 4);
+        const float t = to_f32(r.v[k]) * inv;
+        v[k] = rintf(t);
+        far = fmaxf(far, fabsf(t - v[k]));
     }
+    if (far >= 0.5f - 4e-5f)
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = rintf(to_f32(r.v[k]) / scale);
+    uint32_t w[V / 4] = {};
+#pragma unroll
+    for (int k = 0; k < V; ++k) w[k / 4] |= ((uint32_t)(int32_t)v[k] & 0xffu) << 8 * (k % 4);
     if (valid >= V) {
         if constexpr (V == 8) {
             typedef uint32_t two __attribute__((ext_vector_type(2), aligned(1)));
@@ -92,18 +103,18 @@ __global__ __launch_bounds__(256) void int8_rows(const T *__restrict__ x, int8_t
         __syncthreads();
         top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
     }
-    const float high = __builtin_bit_cast(float, top), scale = (high < kTopFloor ? kTopFloor : high) / 127.0f;
+    const float high = __builtin_bit_cast(float, top), scale = (high < kTopFloor ? kTopFloor : high) / 127.0f, inv = 1.0f / scale;
     if (!on) return;
     if (t == 0) scales[m] = scale;
     int8_t *const out = q + m * K;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int64_t at = ((int64_t)j * TPR + t) * V, left = K - at;
-        if (left > 0) store_q<T, V>(out + at, left < V ? (int)left : V, keep[j], scale);
+        if (left > 0) store_q<T, V>(out + at, left < V ? (int)left : V, keep[j], scale, inv);
     }
     for (int64_t at = ((int64_t)NV * TPR + t) * V; at < K; at += TPR * V) {
         const int valid = K - at < V ? (int)(K - at) : V;
-        store_q<T, V>(out + at, valid, load_raw<T, V>(row + at, valid), scale);
+        store_q<T, V>(out + at, valid, load_raw<T, V>(row + at, valid), scale, inv);
     }
 }
 
@@ -141,10 +152,10 @@ constexpr uint32_t kNowhere = 0x80000000u;
 // Tile BM x BN, waves WM x WN of it.  ALIGNED: K a multiple of 16 and rows on 16 bytes; else
 // the stages go through registers.
 //
-// What bounds it is how early a stage is asked for: a tile of 256 x 256 takes 64 KB for each 2048
-// cycles of products, and the first of an XCD's workgroups to touch a line waits some 4000 for it.
-// So stages are short and three are on their way: 2 stages of 128 bytes took 250 us for 8192 x 6144
-// x 4096, 4 of 64 bytes MEASURED_TILE.
+// Bound by the matrix cores, at the clock that they leave (1.7 GHz over a row of calls; busy 67% of it),
+// and for short K by what stands before and behind the stages of a tile, some 11 us.  8192 x 6144 x 4096
+// takes 190 - 215 us (a library's product of that size without scales 187), 8192^3 464 (460).  Measured
+// on the way: 2 stages of 128 bytes 250, 4 of 64 bytes 243, rows that leave in whole lines 216.
 //
 // LDS holds a stage's rows one after the other, 4 pieces of 16 bytes each, piece c of row r at place
 // c ^ (r / 4 & 3): a wave reads one piece of 32 rows at a time, and any 16 rows next to each other
@@ -171,10 +182,10 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mm_
     const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(B), (short)0, cols * p.K, 0x00020000);
     // A load fills 16 rows: the lane's row of them, and the piece that goes to its place.
     const int lrow = lane / 4, piece = lane % 4 ^ lrow / 4;
-    uint4 held[ALIGNED ? 1 : UA + UB];
+    uint4 held[ALIGNED ? 1 : kStages][UA + UB];      // through registers: four stages on their way
 
     // Stage k0: straight to LDS (past K: zeros), or into registers.
-    auto fetch = [&](uint4 *to, int k0) {
+    auto fetch = [&](uint4 *to, int slot, int k0) {
         const int k = 16 * piece;
         if constexpr (ALIGNED) {
             const bool in = k0 + k < p.K;
@@ -191,18 +202,23 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mm_
                                                          in ? (uint32_t)((r + lrow) * p.K + k) : kNowhere, k0, 0, 0);
             }
         } else {
+auto piece16 = [&](const int8_t *row) {
+                return k0 + kStage <= p.K ? __builtin_bit_cast(uint4, *reinterpret_cast<const any16 *>(row + k0 + k))
+                       : k0 < p.K         ? load16(row, k0 + k, p.K)
+                                          : make_uint4(0, 0, 0, 0);
+            };
 #pragma unroll
-            for (int i = 0; i < UA; ++i) held[i] = load16(A + (int64_t)min((wave * UA + i) * 16 + lrow, rows - 1) * p.K, k0 + k, p.K);
+            for (int i = 0; i < UA; ++i) held[slot][i] = piece16(A + (int64_t)min((wave * UA + i) * 16 + lrow, rows - 1) * p.K);
 #pragma unroll
-            for (int i = 0; i < UB; ++i) held[UA + i] = load16(B + (int64_t)min((wave * UB + i) * 16 + lrow, cols - 1) * p.K, k0 + k, p.K);
+            for (int i = 0; i < UB; ++i) held[slot][UA + i] = piece16(B + (int64_t)min((wave * UB + i) * 16 + lrow, cols - 1) * p.K);
         }
     };
-    auto put = [&](uint4 *to) {
+    auto put = [&](uint4 *to, int slot) {
         if constexpr (!ALIGNED) {
 #pragma unroll
-            for (int i = 0; i < UA; ++i) to[(wave * UA + i) * 64 + lane] = held[i];
+            for (int i = 0; i < UA; ++i) to[(wave * UA + i) * 64 + lane] = held[slot][i];
 #pragma unroll
-            for (int i = 0; i < UB; ++i) to[BM * 4 + (wave * UB + i) * 64 + lane] = held[UA + i];
+            for (int i = 0; i < UB; ++i) to[BM * 4 + (wave * UB + i) * 64 + lane] = held[slot][UA + i];
         }
     };
     // Every wave's next stage is in LDS, and its reads of this one are done.
@@ -212,7 +228,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mm_
             if constexpr (UA + UB == 4) asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             else asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         } else {
-            __syncthreads();
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         }
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -241,39 +257,42 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mm_
         __builtin_amdgcn_sched_barrier(0);
     };
     // One stage out of `now`: its last operands are in registers before the waves meet; behind that the
-    // stage four later may come into its place (through registers: the one two later into `second`), and
-    // the next one's first operands are read under its last products.
-    auto stage = [&](uint4 *now, uint4 *next, uint4 *second, int k0) {
+    // stage four later may come into its place, and the next one's first operands are read under its last
+    // products.  Through registers: the stage two later goes to `second`, its slot takes the one six later.
+    auto stage = [&](uint4 *now, uint4 *next, uint4 *second, int slot, int k0) {
         read(now, 1);
         multiply(0);
-        put(second);
+        put(second, slot);
         meet();
-        fetch(now, k0 + (ALIGNED ? 4 : 3) * kStage);
+        fetch(now, slot, k0 + (ALIGNED ? 4 : 6) * kStage);
         read(next, 0);
         multiply(1);
     };
 
     // Stages in fours, one buffer each; those past K hold zeros.
-    fetch(s0, 0);
-    put(s0);
-    fetch(s1, kStage);
-    put(s1);
-    fetch(s2, 2 * kStage);
-    if constexpr (ALIGNED) fetch(s3, 3 * kStage);
-    if constexpr (ALIGNED && UA + UB == 4) {
+    fetch(s0, 0, 0);
+    put(s0, 0);
+    fetch(s1, 0, kStage);
+    put(s1, 0);
+    fetch(s2, 0, 2 * kStage);
+    fetch(s3, 1, 3 * kStage);
+    if constexpr (!ALIGNED) {
+        fetch(s0, 2, 4 * kStage);
+        fetch(s0, 3, 5 * kStage);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    } else if constexpr (UA + UB == 4) {
         asm volatile("s_waitcnt vmcnt(12)\n\ts_barrier" ::: "memory");
-    } else if constexpr (ALIGNED) {
-        asm volatile("s_waitcnt vmcnt(6)\n\ts_barrier" ::: "memory");
     } else {
-        __syncthreads();
+        asm volatile("s_waitcnt vmcnt(6)\n\ts_barrier" ::: "memory");
     }
     read(s0, 0);
     for (int k0 = 0; k0 < p.K; k0 += kStages * kStage) {
-        stage(s0, s1, s2, k0);
-        stage(s1, s2, s3, k0 + kStage);
-        stage(s2, s3, s0, k0 + 2 * kStage);
-        stage(s3, s0, s1, k0 + 3 * kStage);
+        stage(s0, s1, s2, 0, k0);
+        stage(s1, s2, s3, 1, k0 + kStage);
+        stage(s2, s3, s0, 2, k0 + 2 * kStage);
+        stage(s3, s0, s1, 3, k0 + 3 * kStage);
     }
+
     // What is still on its way is zeros for LDS that nobody reads as operands.
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
