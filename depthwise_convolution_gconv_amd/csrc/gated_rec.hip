@@ -674,20 +674,20 @@ __global__ __launch_bounds__(64 * NW) void gated_bwd_walk(const Walk p)
     GATED_BODY(bwd_body, T, LR, NW);
 }
 
-// Sum over sequences and segments, in order: 16 rows at a time, then those 16.
-__global__ __launch_bounds__(256) void gated_share_sum(const float *__restrict__ part, float *__restrict__ out, int64_t rows,
-                                                       int64_t C)
+// Sum over sequences and segments, in order: 64 rows at a time, then those 64.
+__global__ __launch_bounds__(1024) void gated_share_sum(const float *__restrict__ part, float *__restrict__ out, int64_t rows,
+                                                        int64_t C)
 {
-    __shared__ float s[16][17];
+    __shared__ float s[64][17];
     const int col = threadIdx.x % 16, row = threadIdx.x / 16;
     const int64_t c = (int64_t)blockIdx.x * 16 + col;
     float v = 0.0f;
     if (c < C)
-        for (int64_t r = row; r < rows; r += 16) v += part[r * C + c];
+        for (int64_t r = row; r < rows; r += 64) v += part[r * C + c];
     s[row][col] = v;
     __syncthreads();
     if (row == 0 && c < C) {
-        for (int r = 1; r < 16; ++r) v += s[r][col];
+        for (int r = 1; r < 64; ++r) v += s[r][col];
         out[c] = v;
     }
 }
@@ -751,10 +751,14 @@ template <typename F> hipError_t with_type(int dtype, F &&f)
 template <int N> struct Int { static constexpr int value = N; };
 
 // The kernels that exist: (lanes, waves, rows shorter than a lane's 8 bytes).
+bool short_rows(int64_t C, int dtype) { return C < (dtype == DT_F32 ? 2 : 4); }
 template <typename F> hipError_t with_shape(const GatedPlan &g, int64_t C, int dtype, F &&f)
 {
     constexpr Int<0> whole{};
-    if (C < (dtype == DT_F32 ? 2 : 4)) return f(Int<16>{}, Int<4>{}, Int<1>{});
+    if (short_rows(C, dtype)) return f(Int<32>{}, Int<4>{}, Int<1>{});
+    if (g.lanes == 4) return f(Int<4>{}, Int<8>{}, whole);
+    if (g.lanes == 8) return f(Int<8>{}, Int<8>{}, whole);
+    if (g.lanes == 16) return f(Int<16>{}, Int<8>{}, whole);
     return g.waves == 8 ? f(Int<32>{}, Int<8>{}, whole) : f(Int<32>{}, Int<4>{}, whole);
 }
 
@@ -764,24 +768,52 @@ template <bool BWD> hipError_t launch_states(Walk p, const GatedPlan &g, int dty
     const dim3 grid((unsigned)(8 * ceil_div(p.blocks, 8)));
     return with_type(dtype, [&](auto t) {
         return with_shape(g, p.C, dtype, [&](auto lanes, auto waves, auto one) {
-            gated_states<decltype(t), lanes.value, waves.value, BWD, one.value><<<grid, 64 * waves.value, 0, stream>>>(p);
-            return hipGetLastError();
+            constexpr bool planned = lanes.value == 32 && (!BWD || waves.value == 4);      // of cut sequences
+            if constexpr (planned) gated_states<decltype(t), lanes.value, waves.value, BWD, one.value><<<grid, 64 * waves.value, 0, stream>>>(p);
+            return planned ? hipGetLastError() : hipErrorInvalidValue;
         });
     });
 }
 
 }  // namespace
 
+// Stripes as wide as fill the card without cuts, or cut sequences.  A narrow stripe costs more for each
+// lane: rows of 256, 128, 64 and 32 bytes took 225, 281, 323 and 364 us for 8 x 4096 x 4096 in bf16
+// (factors 1, 1.25, 1.43 and 1.62), since neighbours that share lines are not in step.  A cut reads three of
+// four tensors twice (1.65, and a launch worth 6500 lane-tokens; gradients two of eight, 1.17 and 5000).  With
+// the stripes that this picks, and cut, in bf16: 1 x 4096 x 4096 42 and 63 us, 2 x 8192 x 4096 149 and 214,
+// 6 x 1021 x 1350 24 and 43, 1 x 32768 x 4096 394 and 397, 1 x 32768 x 2048 372 and 217; gradients of 4 x 4096
+// x 2560 335 and 206, of 8 x 1024 x 512 29 and 36.
 GatedPlan gated_plan(int64_t B, int64_t T, int64_t C, int dtype, bool backward)
 {
     GatedPlan g = {32, backward || T <= 256 ? 4 : 8, 1, std::max<int64_t>(T, 1)};
-    if (C < (dtype == DT_F32 ? 2 : 4)) g = {16, 4, 1, g.seg_len};
+    const int64_t lanes = ceil_div(C, dtype == DT_F32 ? 2 : 4);      // of a row
+    const double each = std::max(1.0, (double)std::max<int64_t>(B, 1) * lanes / 256);
+    bool cut = true;
+    if (short_rows(C, dtype)) {
+        g.waves = 4;
+    } else {
+        double least = 0.0;
+        for (int L : {32, 16, 8, 4}) {
+            if (backward && (L == 32 || L == 16)) continue;
+            const double factor = L == 32 ? 1.0 : L == 16 ? 1.25 : L == 8 ? 1.43 : 1.62;
+            const double cost = (double)ceil_div(std::max<int64_t>(B, 1) * ceil_div(lanes, L), 256) * L * factor;
+            if (least == 0.0 || cost < least) {
+                least = cost;
+                g.lanes = L;
+            }
+        }
+        cut = (backward ? 1.17 : 1.65) * each * T + (backward ? 5000 : 6500) < least * T;
+        if (cut) g.lanes = 32;
+        else if (backward || g.lanes < 32) g.waves = 8;
+    }
+    if (!cut) return g;
     const int64_t stripes = std::max<int64_t>(1, B * ceil_div(C, stripe(g, dtype)));
     const int64_t ts = tile_steps(g, backward), tiles = ceil_div(std::max<int64_t>(T, 1), ts);
-    g.nseg = stripes >= 192 ? 1 : (int32_t)std::max<int64_t>(1, std::min<int64_t>({512 / stripes, tiles / 2, 256}));
-    const int64_t each = ceil_div(tiles, (int64_t)g.nseg);
-    g.nseg = (int32_t)ceil_div(tiles, each);
-    g.seg_len = each * ts;
+    g.nseg = (int32_t)std::max<int64_t>(1, std::min<int64_t>({512 / stripes, tiles / 2, 256}));
+    const int64_t per = ceil_div(tiles, (int64_t)g.nseg);
+    g.nseg = (int32_t)ceil_div(tiles, per);
+    g.seg_len = per * ts;
     return g;
 }
 
@@ -835,13 +867,14 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const GatedPlan &g, const char *
         const dim3 grid((unsigned)(8 * ceil_div(p.blocks, 8)));
         const hipError_t err = with_type(a.dtype, [&](auto t) {
             return with_shape(g, a.C, a.dtype, [&](auto lanes, auto waves, auto one) {
-                gated_bwd_walk<decltype(t), lanes.value, waves.value, one.value><<<grid, 64 * waves.value, 0, a.stream>>>(p);
-                return hipGetLastError();
+                constexpr bool planned = lanes.value < 16 || waves.value == 4;
+                if constexpr (planned) gated_bwd_walk<decltype(t), lanes.value, waves.value, one.value><<<grid, 64 * waves.value, 0, a.stream>>>(p);
+                return planned ? hipGetLastError() : hipErrorInvalidValue;
             });
         });
         if (err != hipSuccess) return err;
     }
-    gated_share_sum<<<(unsigned)ceil_div(a.C, 16), 256, 0, a.stream>>>(p.part, a.dlog, a.B * g.nseg, a.C);
+    gated_share_sum<<<(unsigned)ceil_div(a.C, 16), 1024, 0, a.stream>>>(p.part, a.dlog, a.B * g.nseg, a.C);
     return hipGetLastError();
 }
 
