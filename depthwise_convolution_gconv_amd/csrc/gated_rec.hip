@@ -112,7 +112,8 @@ __device__ __forceinline__ void decay(float l, float &a, float &m)
 }
 
 // Tokens of a lane's run: what fits in registers with the next tile's loads beside it.
-constexpr int kRun = 4, kRunBwd = 2;
+template <typename T> constexpr int run_len() { return 4; }
+template <typename T> constexpr int run_len_bwd() { return sizeof(T) == 4 ? 4 : 2; }
 
 // A run's map joined with the one before it.
 __device__ __forceinline__ void join_maps(float &A, float &E, float Ab, float Eb)
@@ -235,13 +236,14 @@ __device__ __forceinline__ float fold(const Walk &p, int64_t b, int seg, int64_t
 
 // ---------------------------------------------------------------- forward
 
-struct RawIn { uint2 x[kRun], r[kRun], i[kRun]; };
+template <int L> struct RawIn { uint2 x[L], r[L], i[L]; };
 
 // step: byte offsets of the lane's run in x, r and i.
 template <typename T, int MODE>
 __device__ __forceinline__ void load_in(const Walk &p, const char *const (&base)[3], int64_t t0, int64_t live, int run, int TS,
-                                        const uint32_t (&step)[3], const Cols &col, RawIn &raw)
+                                        const uint32_t (&step)[3], const Cols &col, RawIn<run_len<T>()> &raw)
 {
+    constexpr int kRun = run_len<T>();
     const char *x = base[0] + t0 * p.xst, *r = base[1] + t0 * p.rst, *i = base[2] + t0 * p.ist;
     if (t0 + TS <= live) {
 #pragma unroll
@@ -266,9 +268,10 @@ __device__ __forceinline__ void load_in(const Walk &p, const char *const (&base)
 }
 
 template <typename T, int MODE, int V>
-__device__ __forceinline__ void gates(const RawIn &raw, const Cols &col, const float (&ld)[V], int rows, float (&a)[kRun][V],
-                                      float (&u)[kRun][V])
+__device__ __forceinline__ void gates(const RawIn<run_len<T>()> &raw, const Cols &col, const float (&ld)[V], int rows, float (&a)[run_len<T>()][V],
+                                      float (&u)[run_len<T>()][V])
 {
+    constexpr int kRun = run_len<T>();
 #pragma unroll
     for (int l = 0; l < kRun; ++l) {
         float x[V], r[V], i[V];
@@ -296,7 +299,7 @@ __device__ __forceinline__ void gates(const RawIn &raw, const Cols &col, const f
 template <typename T, int LR, int NW, int MODE>
 __device__ __forceinline__ void walk_body(const Walk &p, int ct, int seg, int64_t b, Maps<NW, LR, lane_channels<T>()> *maps)
 {
-    constexpr int V = lane_channels<T>(), RW = 64 / LR, TS = NW * RW * kRun;
+    constexpr int V = lane_channels<T>(), RW = 64 / LR, kRun = run_len<T>(), TS = NW * RW * kRun;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int run = wave * RW + lane / LR;
     int64_t c;
@@ -307,7 +310,7 @@ __device__ __forceinline__ void walk_body(const Walk &p, int ct, int seg, int64_
     const uint32_t hrow = (uint32_t)(p.C * sizeof(T)), first = (uint32_t)(run * kRun) * hrow;
     char *const out = p.h + b * p.T * (int64_t)hrow;
 
-    RawIn raw;
+    RawIn<kRun> raw;
     if (begin < live) load_in<T, MODE>(p, base, begin, live, run, TS, step, col, raw);
     float ld[V], carry[V];
 #pragma unroll
@@ -318,7 +321,7 @@ __device__ __forceinline__ void walk_body(const Walk &p, int ct, int seg, int64_
     }
     int buf = 0;
     for (int64_t t0 = begin; t0 < live; t0 += TS, buf ^= 1) {
-        RawIn next;
+        RawIn<kRun> next;
         if (t0 + TS < live) load_in<T, MODE>(p, base, t0 + TS, live, run, TS, step, col, next);
         const bool full = t0 + TS <= live;
         const int rows = full ? kRun : (int)min((int64_t)kRun, max((int64_t)0, live - t0 - run * kRun));
@@ -484,20 +487,20 @@ __global__ __launch_bounds__(64 * NW) void gated_states(const Walk p)
 //     dr = dla log_decay r'(1 - r'),  dlog_decay = sum of dla r'      (s = sqrt(1 - a^2))
 // so each gradient is G times a factor of the token alone.  Where s is 0 (r' underflows, or a
 // log_decay of 0) the root has no derivative, and its term is left out.
-struct RawBwd { uint2 x[kRunBwd], r[kRunBwd], i[kRunBwd], h[kRunBwd], d[kRunBwd]; };
+template <int L> struct RawBwd { uint2 x[L], r[L], i[L], h[L], d[L]; };
 
-// Row l of a lane: token t0 - run kRunBwd - l (tokens fall), its h one token before.
+// Row l of a lane: token t0 - run run_len_bwd<T>() - l (tokens fall), its h one token before.
 // step: byte offsets of the lane's oldest token from the tile's.
 template <typename T, int MODE>
 __device__ __forceinline__ void load_bwd(const Walk &p, const char *const (&base)[5], int64_t t0, int run, int TS,
-                                         const uint32_t (&step)[5], const Cols &col, RawBwd &raw)
+                                         const uint32_t (&step)[5], const Cols &col, RawBwd<run_len_bwd<T>()> &raw)
 {
     const int64_t low = t0 - TS + 1;
     if (low >= 1) {
         const char *x = base[0] + low * p.xst, *r = base[1] + low * p.rst, *i = base[2] + low * p.ist,
                    *h = base[3] + (low - 1) * p.hst, *d = base[4] + low * p.dst;
 #pragma unroll
-        for (int l = kRunBwd - 1; l >= 0; --l) {
+        for (int l = run_len_bwd<T>() - 1; l >= 0; --l) {
             raw.r[l] = load_lane<T, MODE>(r, step[1], col);
             raw.d[l] = load_lane<T, MODE>(d, step[4], col);
             raw.x[l] = load_lane<T, MODE>(x, step[0], col);
@@ -511,8 +514,8 @@ __device__ __forceinline__ void load_bwd(const Walk &p, const char *const (&base
         }
     } else {        // tokens before the first are read from it
 #pragma unroll
-        for (int l = 0; l < kRunBwd; ++l) {
-            const int64_t t = max((int64_t)0, t0 - run * kRunBwd - l);
+        for (int l = 0; l < run_len_bwd<T>(); ++l) {
+            const int64_t t = max((int64_t)0, t0 - run * run_len_bwd<T>() - l);
             raw.r[l] = load_lane<T, MODE>(base[1] + t * p.rst, 0, col);
             raw.d[l] = load_lane<T, MODE>(base[4] + t * p.dst, 0, col);
             raw.x[l] = load_lane<T, MODE>(base[0] + t * p.xst, 0, col);
@@ -525,7 +528,7 @@ __device__ __forceinline__ void load_bwd(const Walk &p, const char *const (&base
 template <typename T, int LR, int NW, int MODE>
 __device__ __forceinline__ void bwd_body(const Walk &p, int ct, int seg, int64_t b, Maps<NW, LR, lane_channels<T>()> *maps)
 {
-    constexpr int V = lane_channels<T>(), RW = 64 / LR, L = kRunBwd, TS = NW * RW * L;
+    constexpr int V = lane_channels<T>(), RW = 64 / LR, L = run_len_bwd<T>(), TS = NW * RW * L;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int run = wave * RW + lane / LR;
     int64_t c;
@@ -539,7 +542,7 @@ __device__ __forceinline__ void bwd_body(const Walk &p, int ct, int seg, int64_t
     const uint32_t orow = (uint32_t)(p.C * sizeof(T)), oldest = (uint32_t)up * orow;
     const int64_t ob = b * p.T * (int64_t)orow;
 
-    RawBwd raw;
+    RawBwd<L> raw;
     if (top >= bottom) load_bwd<T, MODE>(p, base, top, run, TS, step, col, raw);
     float ld[V], carry[V], before[V], share[V];
 #pragma unroll
@@ -552,7 +555,7 @@ __device__ __forceinline__ void bwd_body(const Walk &p, int ct, int seg, int64_t
     }
     int buf = 0;
     for (int64_t t0 = top; t0 >= bottom; t0 -= TS, buf ^= 1) {
-        RawBwd next;
+        RawBwd<L> next;
         if (t0 - TS >= bottom) load_bwd<T, MODE>(p, base, t0 - TS, run, TS, step, col, next);
         const bool full = t0 - TS + 1 >= bottom;
         const int rows = full ? L : (int)min((int64_t)L, max((int64_t)0, t0 - run * L - bottom + 1));
@@ -716,9 +719,10 @@ __global__ __launch_bounds__(256) void gated_step(const T *__restrict__ x, const
 
 // Channels of a stripe, and tokens of a tile.
 int stripe(const GatedPlan &g, int dtype) { return g.lanes * (dtype == DT_F32 ? 2 : 4); }
-int tile_steps(const GatedPlan &g, bool backward)
+int tile_steps(const GatedPlan &g, int dtype, bool backward)
 {
-    return g.waves * (64 / g.lanes) * (backward ? kRunBwd : kRun);
+    return g.waves * (64 / g.lanes) * (dtype == DT_F32 ? (backward ? run_len_bwd<float>() : run_len<float>())
+                                                    : (backward ? run_len_bwd<__bf16>() : run_len<__bf16>()));
 }
 
 Walk make_walk(const GatedArgs &a, const GatedPlan &g)
@@ -809,7 +813,7 @@ GatedPlan gated_plan(int64_t B, int64_t T, int64_t C, int dtype, bool backward)
     }
     if (!cut) return g;
     const int64_t stripes = std::max<int64_t>(1, B * ceil_div(C, stripe(g, dtype)));
-    const int64_t ts = tile_steps(g, backward), tiles = ceil_div(std::max<int64_t>(T, 1), ts);
+    const int64_t ts = tile_steps(g, dtype, backward), tiles = ceil_div(std::max<int64_t>(T, 1), ts);
     g.nseg = (int32_t)std::max<int64_t>(1, std::min<int64_t>({512 / stripes, tiles / 2, 256}));
     const int64_t per = ceil_div(tiles, (int64_t)g.nseg);
     g.nseg = (int32_t)ceil_div(tiles, per);
@@ -824,7 +828,7 @@ size_t gated_workspace(const GatedPlan &g, int64_t B, int64_t C, bool backward)
 
 bool gated_fits(const GatedArgs &a, const GatedPlan &g, bool backward)
 {
-    const int64_t es = a.dtype == DT_F32 ? 4 : 2, ts = tile_steps(g, backward), top = (int64_t(1) << 31) - 1;
+    const int64_t es = a.dtype == DT_F32 ? 4 : 2, ts = tile_steps(g, a.dtype, backward), top = (int64_t(1) << 31) - 1;
     for (int64_t st : {a.xst, a.rst, a.ist, a.C, backward ? a.hst : 0, backward ? a.dst : 0})
         if (ts * es > top / std::max<int64_t>(st, 1)) return false;
     return grid_fits(8 * ceil_div(a.B * g.nseg * ceil_div(a.C, stripe(g, a.dtype)), 8), 64 * g.waves);
