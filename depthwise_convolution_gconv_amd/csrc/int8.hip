@@ -9,7 +9,7 @@
 //   mm_tile  tiles of tokens x channels on the matrix cores (v_mfma_i32_32x32x32_i8), both operands
 //            staged 128 bytes of K at a time by loads that go straight to LDS, the next stage's in
 //            flight over the whole of this one's products;
-//   mm_rows  up to 64 tokens: bound by the weights' one read.  A workgroup takes 16 channels, its
+//   mm_rows  up to 32 tokens: bound by the weights' one read.  A workgroup takes 16 channels, its
 //            waves share K, every wave has all its weights' loads in flight at once
 //            (v_mfma_i32_16x16x64_i8).
 #include <algorithm>
@@ -358,7 +358,7 @@ auto piece16 = [&](const int8_t *row) {
 template <typename T, int MB, int NW>
 __global__ __launch_bounds__(64 * NW) void mm_rows(const Mm p)
 {
-    constexpr int UNROLL = MB == 4 ? 4 : 8;
+    constexpr int UNROLL = 8;
     __shared__ i32x4 sums[NW][MB][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), r = lane % 16, g = lane / 16;
     const int n0 = blockIdx.x * 16;
@@ -474,12 +474,13 @@ hipError_t launch_matmul_int8(const MatmulInt8Args &a, const char **kname)
     Mm p = {};
     p.q = a.q; p.w = a.w; p.qs = a.qs; p.ws = a.ws; p.bias = a.bias; p.y = a.y;
     p.M = (int32_t)a.M; p.N = (int32_t)a.N; p.K = (int32_t)a.K;
-    if (a.M <= 64) {
+    // Few tokens: 16 x 12288 x 4096 14 us; from 17 on tiles overtake where there are channel tiles enough
+    // (32 x 12288 x 4096 21 us and 13, 64 x 12288 x 4096 32 and 13, 32 x 4096 x 4096 8.9 and 9.8).
+    if (a.M <= 16 || (a.M <= 32 && a.N < 8192)) {
         *kname = "mm_rows";
-        const bool few = ceil_div(a.N, 16) < 512;
+        const bool few = ceil_div(a.N, 16) < 512;       // channel groups: more waves share K
         if (a.M <= 16) return few ? run_rows<1, 16>(p, a.dtype, a.stream) : run_rows<1, 4>(p, a.dtype, a.stream);
-        if (a.M <= 32) return few ? run_rows<2, 8>(p, a.dtype, a.stream) : run_rows<2, 4>(p, a.dtype, a.stream);
-        return few ? run_rows<4, 8>(p, a.dtype, a.stream) : run_rows<4, 4>(p, a.dtype, a.stream);
+        return few ? run_rows<2, 8>(p, a.dtype, a.stream) : run_rows<2, 4>(p, a.dtype, a.stream);
     }
     *kname = "mm_tile";
     const bool aligned = a.K % 16 == 0 && (uintptr_t)a.q % 16 == 0 && (uintptr_t)a.w % 16 == 0;
