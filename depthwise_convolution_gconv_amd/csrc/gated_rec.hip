@@ -781,7 +781,33 @@ template <bool BWD> hipError_t launch_states(Walk p, const GatedPlan &g, int dty
 
 }  // namespace
 
-// Stripes as wide as fill the card without cuts, or cut sequences.  A narrow stripe costs more for each
+// Up to 256 tokens: the shape whose tiles take the least time.  A workgroup's tile takes `alone` us where
+// each has a compute unit to itself and `each` us for every one that a compute unit gets, nearly
+// whatever part of the tile the tokens fill: 5 x 16 x 3840 in bf16 took 5.5 us in stripes of 32 lanes on
+// four waves, 13.2 us of 8 and 20.5 us of 4 lanes on eight (gradients 8.8, 23 and 41), 5 x 256 x 3840
+// 21, 15 and 23 us (41, 37 and 47).
+GatedPlan short_plan(int64_t B, int64_t T, int64_t C, int dtype, bool backward)
+{
+    const int64_t lanes = ceil_div(C, dtype == DT_F32 ? 2 : 4);
+    GatedPlan best = {};
+    double least = 0.0;
+    for (int L : {32, 16, 8, 4}) {
+        if (backward && L == 16) continue;
+        const GatedPlan g = {L, L == 32 ? 4 : 8, 1, std::max<int64_t>(T, 1)};
+        const bool four = g.waves == 4;
+        const double start = backward ? 6.5 : 4.0, alone = four ? 2.2 : 3.4,
+                     each = four ? (backward ? 2.4 : 1.8) : backward ? 7.6 : 3.6;
+        const double loads = (double)(std::max<int64_t>(B, 1) * ceil_div(lanes, L)) / 256;
+        const double us = start + (double)ceil_div(std::max<int64_t>(T, 1), tile_steps(g, dtype, backward)) * std::max(alone, each * loads);
+        if (least == 0.0 || us < least) {
+            least = us;
+            best = g;
+        }
+    }
+    return best;
+}
+
+// Longer: stripes as wide as fill the card without cuts, or cut sequences.  A narrow stripe costs more for each
 // lane: rows of 256, 128, 64 and 32 bytes took 225, 281, 323 and 364 us for 8 x 4096 x 4096 in bf16
 // (factors 1, 1.25, 1.43 and 1.62), since neighbours that share lines are not in step.  A cut reads three of
 // four tensors twice (1.65, and a launch worth 6500 lane-tokens; gradients two of eight, 1.17 and 5000).  With
@@ -790,7 +816,8 @@ template <bool BWD> hipError_t launch_states(Walk p, const GatedPlan &g, int dty
 // x 2560 335 and 206, of 8 x 1024 x 512 29 and 36.
 GatedPlan gated_plan(int64_t B, int64_t T, int64_t C, int dtype, bool backward)
 {
-    GatedPlan g = {32, backward || T <= 256 ? 4 : 8, 1, std::max<int64_t>(T, 1)};
+    GatedPlan g = {32, backward ? 4 : 8, 1, std::max<int64_t>(T, 1)};
+    if (T <= 256 && !short_rows(C, dtype)) return short_plan(B, T, C, dtype, backward);
     const int64_t lanes = ceil_div(C, dtype == DT_F32 ? 2 : 4);      // of a row
     const double each = std::max(1.0, (double)std::max<int64_t>(B, 1) * lanes / 256);
     bool cut = true;
