@@ -224,14 +224,33 @@ __device__ __forceinline__ int64_t fresh(int64_t v)
     return v;
 }
 
-// State before a segment: the first one's, through the maps of the segments before it.
-__device__ __forceinline__ float fold(const Walk &p, int64_t b, int seg, int64_t c, float h)
+// carry: the state before the first segment -> before this one, through the maps of those between, shared
+// among the workgroup's runs as a tile's tokens are: 2 x 15147 x 256 in bf16, 79 segments, 43 us; every lane
+// all of them by itself 69 us.
+template <int NW, int LR, int V>
+__device__ __forceinline__ void enter_segment(const Walk &p, int64_t b, int seg, int64_t c, int wave, int lane, Maps<NW, LR, V> &maps,
+                                              float (&carry)[V])
 {
-    for (int s = 0; s < seg; ++s) {
-        const float2 m = *reinterpret_cast<const float2 *>(p.maps + 2 * ((b * p.nseg + s) * p.C + c));
-        h = fmaf(m.x, h, m.y);
+    if (seg == 0) return;
+    constexpr int RUNS = NW * (64 / LR);
+    const int each = (seg + RUNS - 1) / RUNS, from = min(seg, (wave * (64 / LR) + lane / LR) * each), to = min(seg, from + each);
+    float A[V], E[V], Ab[V], Eb[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        A[k] = 1.0f;
+        E[k] = 0.0f;
     }
-    return h;
+    for (int s = from; s < to; ++s)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float2 m = *reinterpret_cast<const float2 *>(p.maps + 2 * ((b * p.nseg + s) * p.C + min(c + k, p.C - 1)));
+            E[k] = fmaf(m.x, E[k], m.y);
+            A[k] *= m.x;
+        }
+    scan_wave<LR>(lane, A, E, Ab, Eb);
+    if (lane >= 64 - LR) put_maps(maps, wave, lane - (64 - LR), A, E);
+    __syncthreads();
+    through_waves(maps, wave, lane % LR, carry, Ab);
 }
 
 // ---------------------------------------------------------------- forward
@@ -317,8 +336,9 @@ __device__ __forceinline__ void walk_body(const Walk &p, int ct, int seg, int64_
     for (int k = 0; k < V; ++k) {
         const int64_t ck = min(c + k, p.C - 1);
         ld[k] = p.log_decay[ck] * kLog2e;
-        carry[k] = fold(p, b, seg, ck, p.s0 ? p.s0[b * p.C + ck] : 0.0f);
+        carry[k] = p.s0 ? p.s0[b * p.C + ck] : 0.0f;
     }
+    enter_segment(p, b, seg, c, wave, lane, maps[1], carry);
     int buf = 0;
     for (int64_t t0 = begin; t0 < live; t0 += TS, buf ^= 1) {
         RawIn<kRun> next;
@@ -549,10 +569,11 @@ __device__ __forceinline__ void bwd_body(const Walk &p, int ct, int seg, int64_t
     for (int k = 0; k < V; ++k) {
         const int64_t ck = min(c + k, p.C - 1);
         ld[k] = p.log_decay[ck];
-        carry[k] = fold(p, b, seg, ck, p.sf ? p.sf[b * p.C + ck] : 0.0f);
+        carry[k] = p.sf ? p.sf[b * p.C + ck] : 0.0f;
         before[k] = p.s0 ? p.s0[b * p.C + ck] : 0.0f;
         share[k] = 0.0f;
     }
+    enter_segment(p, b, seg, c, wave, lane, maps[1], carry);
     int buf = 0;
     for (int64_t t0 = top; t0 >= bottom; t0 -= TS, buf ^= 1) {
         RawBwd<L> next;
