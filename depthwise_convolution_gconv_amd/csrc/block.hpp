@@ -27,7 +27,7 @@ struct GatedArgs {
 };
 // How a call is laid out over workgroups.
 struct GatedPlan {
-    int32_t lanes;                       // lanes that share a row, two channels each
+    int32_t lanes;                       // lanes that share a row, 8 bytes each
     int32_t waves;                       // of a workgroup
     int32_t nseg;                        // segments of a sequence
     int64_t seg_len;                     // tokens of a segment

@@ -5,7 +5,7 @@
 // A recurrence h_t = a_t h_(t-1) + u_t is a composition of affine maps: over any run of tokens
 // it is h_out = A h_in + E with A the product of the a_t and E the run's own result from zero.
 // A workgroup walks the tokens of one sequence for a stripe of channels, tile after tile: each
-// lane takes a run of consecutive tokens for two channels, keeps its a_t and u_t in registers,
+// lane takes a run of consecutive tokens for 8 bytes of channels, keeps its a_t and u_t in registers,
 // and (A, E) of the runs are joined by lane exchanges within a wave and through LDS across the
 // waves.  Then each lane knows the state before its run and writes its h_t.  So the inputs are
 // read once and one barrier is needed for a tile; the next tile's loads are in flight meanwhile.
@@ -13,7 +13,14 @@
 // first (gated_states), and a walk folds those before its own.
 //
 // Bound by HBM and, nearly as much, by vector instructions: six of quarter rate (three
-// exponentials, two reciprocals, a root) and about 30 others for the 8 bytes of an element.
+// exponentials, two reciprocals, a root) and about 30 others for the 8 bytes of an element.  In bf16
+// 8 x 4096 x 4096 takes 224 us (1.07 GB, 4.8 TB/s), 1 x 32768 x 4096, where stripes of 32 bytes fill the
+// card, 385 - 420; gradients of 4 x 4096 x 2560 take 191 us: 48 for the segments' maps, 139 for the walk
+// (0.67 GB, 4.8 TB/s, 188 registers, two waves a SIMD) and 5 for the sum of log_decay's shares.  Tokens of
+// 64 x 4096 take 3 us in gated_step.
+//
+// One pass with a workgroup waiting for its predecessor's state would save the cut's second read; it took
+// 442 us where the narrow stripes take 400.
 #include <algorithm>
 
 #include "block.hpp"

@@ -18,7 +18,12 @@
 //     dw = sum of dz xhat,  db = sum of dz  over samples and positions.
 // dw and db leave each workgroup as fp32 partial sums; a last launch adds them in order.
 //
-// Bound by HBM; with silu two quarter-rate instructions an element, four in gradients.
+// Bound by HBM; with silu two quarter-rate instructions an element, four in gradients.  64 x 784 x 2048
+// in fp16 with silu takes 102 us (0.41 GB, 4.0 TB/s: a workgroup's load, statistics and stores follow one
+// another, two workgroups of 1024 threads share a compute unit); a workgroup that stays and loads its next
+// slab early holds two slabs in registers and took 133 us.  Gradients of 8 x 20480 x 256 in bf16: 47 us for
+// the sums (0.17 GB, 3.6 TB/s), 44 for dx (0.25 GB, 5.7 TB/s, read in part from the last-level cache), 5 for
+// dw and db.
 #include <algorithm>
 
 #include "block.hpp"
@@ -877,7 +882,8 @@ GroupNormPlan gn_plan(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, boo
                 }
         }
     }
-    // Chunks of positions: rows as wide as 64 lanes take.
+    // Chunks of positions: rows as wide as 64 lanes take, 512 workgroups (gradients of 8 x 20480 x 256 in bf16:
+    // sums 48.7 and dx 44.0 us, with 1024 52.8 and 45.4).
     g.kg = g.parts > 1 ? 1 : (int32_t)std::max<int64_t>(1, std::min(G, 64 / cgv));
     g.cols = (int32_t)(g.parts > 1 ? ceil_div(cgv, g.parts) : g.kg * cgv);
     g.threads = (int32_t)std::max<int64_t>(512, 64 * ceil_div(g.cols, 64));

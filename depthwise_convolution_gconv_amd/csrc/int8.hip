@@ -7,8 +7,8 @@
 //
 // Two kernels, by the number of tokens:
 //   mm_tile  tiles of tokens x channels on the matrix cores (v_mfma_i32_32x32x32_i8), both operands
-//            staged 128 bytes of K at a time by loads that go straight to LDS, the next stage's in
-//            flight over the whole of this one's products;
+//            staged 64 bytes of K at a time by loads that go straight to LDS, three stages on their
+//            way while one is multiplied;
 //   mm_rows  up to 32 tokens: bound by the weights' one read.  A workgroup takes 16 channels, its
 //            waves share K, every wave has all its weights' loads in flight at once
 //            (v_mfma_i32_16x16x64_i8).
@@ -484,12 +484,15 @@ hipError_t launch_matmul_int8(const MatmulInt8Args &a, const char **kname)
     }
     *kname = "mm_tile";
     const bool aligned = a.K % 16 == 0 && (uintptr_t)a.q % 16 == 0 && (uintptr_t)a.w % 16 == 0;
+    // Larger tiles where they nearly fill the card.  K = 4096, in bf16: 224 tiles of 256 (3584 x 4096) 60 us and 80
+    // in tiles of 128, 128 of them (2048 x 4096) 53 and 45; 192 tiles of 128 (1536 x 2048) 22 us and 27 in tiles
+    // of 64, 128 of them (1024 x 2048) 21 and 18.  Unaligned rows: 224 tiles of 128 36 and 41, 192 35 and 31.
     auto tiles = [&](int64_t bm, int64_t bn) { return ceil_div(a.M, bm) * ceil_div(a.N, bn); };
     if (!aligned)
-        return tiles(128, 128) >= 256 ? run_tile<128, 128, 2, 2, false>(p, a.dtype, a.stream)
+        return tiles(128, 128) >= 208 ? run_tile<128, 128, 2, 2, false>(p, a.dtype, a.stream)
                                       : run_tile<64, 64, 2, 2, false>(p, a.dtype, a.stream);
     if (tiles(256, 256) >= 224) return run_tile<256, 256, 2, 4, true>(p, a.dtype, a.stream);
-    return tiles(128, 128) >= 224 ? run_tile<128, 128, 2, 2, true>(p, a.dtype, a.stream) : run_tile<64, 64, 2, 2, true>(p, a.dtype, a.stream);
+    return tiles(128, 128) >= 160 ? run_tile<128, 128, 2, 2, true>(p, a.dtype, a.stream) : run_tile<64, 64, 2, 2, true>(p, a.dtype, a.stream);
 }
 
 }  // namespace gconv
