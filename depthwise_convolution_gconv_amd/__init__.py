@@ -1,7 +1,9 @@
 """Grouped-convolution forward engine for AMD Instinct MI355X (gfx950), with the
 backward of the (batch, steps, channels) depthwise conv1d, and the sequence operators
 beside that conv in a mixing block: its causal form with a carried state, linear
-attention with a decay for each head, and RMS norm with the residual's addition.
+attention with a decay for each head, and RMS norm with the residual's addition; and those
+of a recurrent block: a gated linear recurrence, group norm with an activation, and the
+product in 8-bit integers with its quantiser.
 
 The compute runs in libgconv.so (hand-written HIP kernels behind the C ABI in
 include/gconv.h); this package is its Python binding.  Importing the package

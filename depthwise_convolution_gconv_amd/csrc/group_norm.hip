@@ -22,8 +22,7 @@
 // in fp16 with silu takes 102 us (0.41 GB, 4.0 TB/s: a workgroup's load, statistics and stores follow one
 // another, two workgroups of 1024 threads share a compute unit); a workgroup that stays and loads its next
 // slab early holds two slabs in registers and took 133 us.  Gradients of 8 x 20480 x 256 in bf16: 47 us for
-// the sums (0.17 GB, 3.6 TB/s), 44 for dx (0.25 GB, 5.7 TB/s, read in part from the last-level cache), 5 for
-// dw and db.
+// the sums (0.17 GB, 3.6 TB/s), 44 for dx (0.25 GB, 5.7 TB/s), 5 for dw and db.
 #include <algorithm>
 
 #include "block.hpp"
