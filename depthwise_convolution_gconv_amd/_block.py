@@ -101,8 +101,8 @@ def gated_recurrence_backward(x, r, i, log_decay, h, dh, initial_state=None, len
     """(dx, dr, di, dlog_decay, dinitial) of gated_recurrence from its output h, the gradient dh of
     that and dstate (fp32 [B, C], or None: zero) of its final state.  The states before each token
     are taken from h as it was rounded.  dlog_decay is fp32 [C]; dinitial is None without an
-    initial_state.  Where 1 - a^2 is zero (log_decay zero, or a gate that underflows) the root is
-    taken to have no derivative."""
+    initial_state.  Where 1 - a^2 is zero or below 2^-126 (log_decay next to zero, or a gate that
+    underflows) the root is taken as zero, without a derivative."""
     if stream is not None:
         return _on_stream(stream, x, gated_recurrence_backward, x, r, i, log_decay, h, dh, initial_state, lengths, dstate)
     dt, dev, strides, g, n = _gated_args(x, r, i, log_decay, lengths, 3)

@@ -513,7 +513,8 @@ __global__ __launch_bounds__(64 * NW) void gated_states(const Walk p)
 //     dx = G s i',  di = G s x i'(1 - i'),  dla = a G h_(t-1) - (a^2 / s) G i' x,
 //     dr = dla log_decay r'(1 - r'),  dlog_decay = sum of dla r'      (s = sqrt(1 - a^2))
 // so each gradient is G times a factor of the token alone.  Where s is 0 (r' underflows, or a
-// log_decay of 0) the root has no derivative, and its term is left out.
+// log_decay of 0) the root has no derivative, and its term is left out; so it is where 1 - a^2
+// lies below fp32's smallest normal number, 2^-126, which the forward pass's root takes as 0 too.
 template <int L> struct RawBwd { uint2 x[L], r[L], i[L], h[L], d[L]; };
 
 // Row l of a lane: token t0 - run run_len_bwd<T>() - l (tokens fall), its h one token before.
@@ -602,8 +603,8 @@ __device__ __forceinline__ void bwd_body(const Walk &p, int ct, int seg, int64_t
                 const float sr = sigmoid(r[k]), si = sigmoid(i[k]), la = ld[k] * sr;
                 float m;
                 decay(kLog2e * la, a[l][k], m);
-                // 1 / s and s from one root.
-                const float inv = m > 0.0f ? __builtin_amdgcn_rsqf(m) : 0.0f, xi = x[k] * si;
+                // 1 / s and s from one root, which takes a denormal number as zero: its inverse would be infinite.
+                const float inv = m >= 0x1p-126f ? __builtin_amdgcn_rsqf(m) : 0.0f, xi = x[k] * si;
                 const float hp = start ? before[k] : h[k];
                 fx[l][k] = m * inv * si;
                 fi[l][k] = m * inv * xi * (1.0f - si);
