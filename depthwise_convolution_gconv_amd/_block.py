@@ -227,7 +227,7 @@ def group_norm(x, groups: int, weight, bias=None, eps: float = 1e-5, activation:
 def group_norm_backward(dy, x, groups: int, weight, bias, stats, activation: Optional[str] = None, lengths=None,
                         stream=None):
     """(dx, dw, db) of group_norm from the gradient dy of its output and the stats that it returned.
-    db is None without a bias."""
+    db is None without a bias.  A sample without positions adds nothing, whatever its stats are."""
     if stream is not None:
         return _on_stream(stream, x, group_norm_backward, dy, x, groups, weight, bias, stats, activation, lengths)
     dt, dev, shape, strides, w, b, act, n = _norm_args(x, groups, weight, bias, activation, lengths)

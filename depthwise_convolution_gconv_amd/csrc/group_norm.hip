@@ -549,6 +549,15 @@ __device__ __forceinline__ float per_element(const Norm &p, int64_t n)
     return 1.0f / fmaxf((float)all * p.cg, 1.0f);
 }
 
+// (mean, rstd) of a group for the sums over its `live` rows.  Without rows the sums are zero, and rstd, which
+// is infinite where eps is zero, must not multiply them.
+__device__ __forceinline__ float2 group_stats(const Norm &p, int64_t at, int live)
+{
+    float2 st = reinterpret_cast<const float2 *>(p.stats)[at];
+    if (live == 0) st.y = 0.0f;
+    return st;
+}
+
 // Whole samples in registers: a range of them, their dw and db added up on the way.
 template <typename T, int V, int K>
 __global__ __launch_bounds__(kMaxThreads) void gn_backward(const Norm p)
@@ -580,7 +589,7 @@ __global__ __launch_bounds__(kMaxThreads) void gn_backward(const Norm p)
         live = live_rows(p, n, s);
         load_tile<T, V, K>(p.x + n * p.xsb + s.c0 * (int64_t)sizeof(T), p.xst, xat, on, r0, p.R, 0, live, xr);
         load_tile<T, V, K>(p.dy + n * p.dsb + s.c0 * (int64_t)sizeof(T), p.dst, dat, on, r0, p.R, 0, live, dr);
-        st = reinterpret_cast<const float2 *>(p.stats)[n * p.G + s.bundle * p.kg + g];
+        st = group_stats(p, n * p.G + s.bundle * p.kg + g, live);
     };
     if constexpr (K == 1)
         if (from < past) {
@@ -664,7 +673,7 @@ __global__ __launch_bounds__(kMaxThreads) void gn_chunk_sums(const Norm p)
     load_tile<T, V, K>(dy, p.dst, dat, on, r0, p.R, 0, live, dr);
     float a[V], b[V], sd[V] = {}, sz[V] = {}, s1 = 0.0f, s2 = 0.0f;
     load_affine<T, V>(p, on, c, a, b);
-    const float2 st = reinterpret_cast<const float2 *>(p.stats)[at + (on && p.parts == 1 ? col / (p.cg / V) : 0)];
+    const float2 st = group_stats(p, at + (on && p.parts == 1 ? col / (p.cg / V) : 0), live);
 #pragma unroll
     for (int k = 0; k < V; ++k) a[k] *= st.y;
     for (int first = 0; first < live; first += p.R * K) {

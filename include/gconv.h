@@ -437,7 +437,8 @@ gconv_status_t gconv_group_norm(const void *x, const void *weight, const void *b
                                 size_t workspace_bytes, void *hip_stream);
 
 /* Its gradients: dx [N,P,C], dw [C] and db [C] (with a bias, else NULL) from the gradient dy of y and the
- * stats of the forward call.  strides = {dy sample, dy position, x sample, x position}. */
+ * stats of the forward call.  strides = {dy sample, dy position, x sample, x position}.  A sample without
+ * positions adds nothing to dw and db, whatever its stats are. */
 gconv_status_t gconv_group_norm_backward(const void *dy, const void *x, const void *weight, const void *bias,
                                          const float *stats, void *dx, void *dw, void *db, const int64_t *shape,
                                          const int64_t *strides, const int32_t *lengths, gconv_act_t activation,
