@@ -707,12 +707,13 @@ __global__ __launch_bounds__(64 * NW) void gated_bwd_walk(const Walk p)
 }
 
 // Sum over sequences and segments, in order: 64 rows at a time, then those 64.
-__global__ __launch_bounds__(1024) void gated_share_sum(const float *__restrict__ part, float *__restrict__ out, int64_t rows,
-                                                        int64_t C)
+constexpr int kShareCols = 16, kShareThreads = 64 * kShareCols;
+__global__ __launch_bounds__(kShareThreads) void gated_share_sum(const float *__restrict__ part, float *__restrict__ out,
+                                                                 int64_t rows, int64_t C)
 {
-    __shared__ float s[64][17];
-    const int col = threadIdx.x % 16, row = threadIdx.x / 16;
-    const int64_t c = (int64_t)blockIdx.x * 16 + col;
+    __shared__ float s[64][kShareCols + 1];
+    const int col = threadIdx.x % kShareCols, row = threadIdx.x / kShareCols;
+    const int64_t c = (int64_t)blockIdx.x * kShareCols + col;
     float v = 0.0f;
     if (c < C)
         for (int64_t r = row; r < rows; r += 64) v += part[r * C + c];
@@ -887,6 +888,7 @@ bool gated_fits(const GatedArgs &a, const GatedPlan &g, bool backward)
     const int64_t es = a.dtype == DT_F32 ? 4 : 2, ts = tile_steps(g, a.dtype, backward), top = (int64_t(1) << 31) - 1;
     for (int64_t st : {a.xst, a.rst, a.ist, a.C, backward ? a.hst : 0, backward ? a.dst : 0})
         if (ts * es > top / std::max<int64_t>(st, 1)) return false;
+    if (backward && !grid_fits(ceil_div(a.C, kShareCols), kShareThreads)) return false;
     return grid_fits(8 * ceil_div(a.B * g.nseg * ceil_div(a.C, stripe(g, a.dtype)), 8), 64 * g.waves);
 }
 
@@ -934,7 +936,7 @@ hipError_t launch_gated_bwd(const GatedArgs &a, const GatedPlan &g, const char *
         });
         if (err != hipSuccess) return err;
     }
-    gated_share_sum<<<(unsigned)ceil_div(a.C, 16), 1024, 0, a.stream>>>(p.part, a.dlog, a.B * g.nseg, a.C);
+    gated_share_sum<<<(unsigned)ceil_div(a.C, kShareCols), kShareThreads, 0, a.stream>>>(p.part, a.dlog, a.B * g.nseg, a.C);
     return hipGetLastError();
 }
 

@@ -408,6 +408,7 @@ gconv_status_t gconv_gated_recurrence(const void *x, const void *r, const void *
 /* Its gradients: dx, dr, di [B,T,C], dlog_decay [C] (fp32) and, if not NULL, dinitial [B,C] (fp32;
  * only with initial_state) from h as the forward call wrote it, the gradient dh of h and dfinal
  * (fp32 [B,C], or NULL: zero) of final_state.  strides = {x, r, i, h, dh: batch, token}, 10 values.
+ * More than 2^26 - 16 channels are GCONV_ERR_UNSUPPORTED.
  * Where 1 - a^2 is zero or below 2^-126 the root counts as zero, without a derivative. */
 gconv_status_t gconv_gated_recurrence_backward(const void *x, const void *r, const void *i, const float *log_decay,
                                                const void *h, const void *dh, void *dx, void *dr, void *di,

@@ -162,3 +162,11 @@ def test_python_refuses_before_the_library():
         gc.quantize_int8(x.to(torch.int32))
     with pytest.raises(gc.GconvError):
         gc.matmul_int8(x.to(torch.int8), x[..., :1], x[0].to(torch.int8), torch.ones(3), dtype=torch.float64)
+
+
+def test_gated_recurrence_backward_channels():
+    """The sum over log_decay's shares takes 64 threads a channel: with 2^26 - 15 channels and more a launch of
+    2^32 threads, which HIP would cut short."""
+    for C in (2 ** 26 - 15, 2 ** 26 - 1):
+        for shape in ((1, 1, C), (0, 1, C), (1, 0, C)):
+            assert rec_bwd(shape) == UNSUPPORTED, shape
