@@ -278,8 +278,9 @@ def matmul_int8(q, scales, weight, weight_scales, bias=None, dtype: torch.dtype 
 
     q int8 [..., K] and scales fp32 [..., 1] as quantize_int8 gives them; weight int8 [N, K],
     weight_scales fp32 [N] or [N, 1] (quantize_int8 of the weights gives both); bias [N] in `dtype`.  All
-    contiguous, K at most 131071.  The sum is exact; it, the products with the scales (the token's
-    first) and the addition of the bias are rounded to fp32, and the result to the dtype."""
+    contiguous, K at most 131071.  The sum is exact.  It is rounded to fp32, its product with the
+    token's scale too, and that times the channel's scale plus the bias once (a fused multiply and
+    add); the result is rounded to the dtype."""
     if stream is not None:
         return _on_stream(stream, q, matmul_int8, q, scales, weight, weight_scales, bias, dtype)
     dt = DTYPES.get(dtype)

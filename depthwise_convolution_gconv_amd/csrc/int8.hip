@@ -2,8 +2,9 @@
 // the tokens' quantiser:
 //     scale_m = max(max|x_m|, 2^-100) / 127,   q = rint(x / scale_m)
 //     y[m][n] = (sum over k of q[m][k] w[n][k]) scale_m wscale_n + bias_n
-// The sum is exact in int32 (K <= 131071); it is rounded to fp32 once, as are the products with
-// the two scales and the bias's addition, and the result to the dtype.
+// The sum is exact in int32 (K <= 131071).  It is rounded to fp32, and so is its product with the
+// token's scale; that times the channel's scale plus the bias is one fused operation, rounded once,
+// and the result is rounded to the dtype.
 //
 // Two kernels, by the number of tokens:
 //   mm_tile  tiles of tokens x channels on the matrix cores (v_mfma_i32_32x32x32_i8), both operands
@@ -132,6 +133,14 @@ struct Mm {
 template <typename T> __device__ __forceinline__ float bias_of(const Mm &p, int n)
 {
     return p.bias ? to_f32(static_cast<const T *>(p.bias)[n]) : 0.0f;
+}
+
+// The sum, scaled: three roundings, written out so that they do not depend on what the compiler contracts.
+__device__ __forceinline__ float scaled(int32_t sum, float qs, float ws, float bias)
+{
+#pragma clang fp contract(off)
+    const float t = (float)sum * qs;
+    return fmaf(t, ws, bias);
 }
 
 // 16 bytes of a row from byte k on; those past K are zero.  Rows of any alignment.
@@ -326,7 +335,7 @@ auto piece16 = [&](const int8_t *row) {
                 Run<T, 4> v;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    v.v[k] = from_f32<T>((float)acc[i][j][4 * g + k] * qs * ws[j][4 * g + k] + bias[j][4 * g + k]);
+                    v.v[k] = from_f32<T>(scaled(acc[i][j][4 * g + k], qs, ws[j][4 * g + k], bias[j][4 * g + k]));
                 const int byte = (j * 32 + 8 * g + 4 * hf) * (int)sizeof(T);
                 char *const to = (char *)(rowsout + l32 * UPR + ((byte / 16) ^ (l32 & (UPR - 1)))) + byte % 16;
                 if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(to) = __builtin_bit_cast(uint4, v);
@@ -406,7 +415,7 @@ __global__ __launch_bounds__(64 * NW) void mm_rows(const Mm p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int n = n0 + 4 * g + i;
-            if (n < p.N) y[n] = from_f32<T>((float)v[i] * qs * p.ws[n] + bias_of<T>(p, n));
+            if (n < p.N) y[n] = from_f32<T>(scaled(v[i], qs, p.ws[n], bias_of<T>(p, n)));
         }
     }
 }

@@ -456,8 +456,8 @@ gconv_status_t gconv_quantize_int8(const void *x, int8_t *q, float *scales, int6
  * [M,K] and w [N,K] int8, scales [M] and w_scales [N] fp32, bias [N] or NULL and y [M,N] of the dtype,
  * all contiguous:
  *     y[m][n] = (sum over k of q[m][k] w[n][k]) scales[m] w_scales[n] + bias[n]
- * The sum is exact in 32-bit integers (K at most 131071); it and each step after it are rounded to fp32,
- * and the result to the dtype. */
+ * The sum is exact in 32-bit integers (K at most 131071).  It is rounded to fp32, its product with scales[m]
+ * too, and that times w_scales[n] plus the bias once (a fused multiply and add); the result to the dtype. */
 gconv_status_t gconv_matmul_int8(const int8_t *q, const float *scales, const int8_t *w, const float *w_scales,
                                  const void *bias, void *y, const int64_t *shape, gconv_dtype_t dtype,
                                  void *hip_stream);
