@@ -651,8 +651,9 @@ __global__ __launch_bounds__(kMaxThreads) void gn_backward(const Norm p)
     column_sums<V>(p, s, tid, r0, col, db, cells, o + p.C);
 }
 
-// Chunks: S1, S2 and the partial dw, db first, then dx.
-template <typename T, int V>
+// Chunks: S1, S2 and the partial dw, db first, then dx.  RANGES: a chunk is a whole sample, and a workgroup takes
+// a range of samples one after the other, so that they share a row of partial sums.
+template <typename T, int V, bool RANGES>
 __global__ __launch_bounds__(kMaxThreads) void gn_chunk_sums(const Norm p)
 {
     constexpr int K = kTileBwd;
@@ -662,46 +663,55 @@ __global__ __launch_bounds__(kMaxThreads) void gn_chunk_sums(const Norm p)
     Slab s;
     if (!find_slab(p, s)) return;
     slab_columns<V>(p, s);
-    const int tid = threadIdx.x, r0 = tid / p.cols, col = tid - r0 * p.cols, live = live_rows(p, s.n, s);
+    const int tid = threadIdx.x, r0 = tid / p.cols, col = tid - r0 * p.cols;
     const bool on = r0 < p.R && col < s.cols;
-    const int64_t c = s.c0 + (int64_t)col * V, at = s.n * p.G + s.bundle * p.kg;
+    const int64_t c = s.c0 + (int64_t)col * V, past = min((s.n + 1) * p.range, p.N);
     const uint32_t at0 = (uint32_t)(col * V * sizeof(T)), xat = (uint32_t)r0 * (uint32_t)p.xst + at0, dat = (uint32_t)r0 * (uint32_t)p.dst + at0;
-    const char *const x = p.x + s.n * p.xsb + s.first * p.xst + s.c0 * (int64_t)sizeof(T);
-    const char *const dy = p.dy + s.n * p.dsb + s.first * p.dst + s.c0 * (int64_t)sizeof(T);
-    Vec<T, V> xr[K], dr[K], xn[K], dn[K];
-    load_tile<T, V, K>(x, p.xst, xat, on, r0, p.R, 0, live, xr);
-    load_tile<T, V, K>(dy, p.dst, dat, on, r0, p.R, 0, live, dr);
-    float a[V], b[V], sd[V] = {}, sz[V] = {}, s1 = 0.0f, s2 = 0.0f;
-    load_affine<T, V>(p, on, c, a, b);
-    const float2 st = group_stats(p, at + (on && p.parts == 1 ? col / (p.cg / V) : 0), live);
+    float dw[V] = {}, db[V] = {};
+    int64_t n = RANGES ? s.n * p.range : s.n;
+    do {
+        const int live = live_rows(p, n, s);
+        const int64_t at = n * p.G + s.bundle * p.kg;
+        const char *const x = p.x + n * p.xsb + s.first * p.xst + s.c0 * (int64_t)sizeof(T);
+        const char *const dy = p.dy + n * p.dsb + s.first * p.dst + s.c0 * (int64_t)sizeof(T);
+        Vec<T, V> xr[K], dr[K], xn[K], dn[K];
+        load_tile<T, V, K>(x, p.xst, xat, on, r0, p.R, 0, live, xr);
+        load_tile<T, V, K>(dy, p.dst, dat, on, r0, p.R, 0, live, dr);
+        float a[V], b[V], sd[V] = {}, sz[V] = {}, s1 = 0.0f, s2 = 0.0f;
+        load_affine<T, V>(p, on, c, a, b);
+        const float2 st = group_stats(p, at + (on && p.parts == 1 ? col / (p.cg / V) : 0), live);
 #pragma unroll
-    for (int k = 0; k < V; ++k) a[k] *= st.y;
-    for (int first = 0; first < live; first += p.R * K) {
-        load_tile<T, V, K>(x, p.xst, xat, on, r0, p.R, first + p.R * K, live, xn);
-        load_tile<T, V, K>(dy, p.dst, dat, on, r0, p.R, first + p.R * K, live, dn);
+        for (int k = 0; k < V; ++k) a[k] *= st.y;
+        for (int first = 0; first < live; first += p.R * K) {
+            load_tile<T, V, K>(x, p.xst, xat, on, r0, p.R, first + p.R * K, live, xn);
+            load_tile<T, V, K>(dy, p.dst, dat, on, r0, p.R, first + p.R * K, live, dn);
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-            if (on && first + r0 + j * p.R < live) add_sums<T, V>(p, xr[j], dr[j], a, b, st.x, sd, sz);
-            keep_order();
+            for (int j = 0; j < K; ++j) {
+                if (on && first + r0 + j * p.R < live) add_sums<T, V>(p, xr[j], dr[j], a, b, st.x, sd, sz);
+                keep_order();
+            }
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                xr[j] = xn[j];
+                dr[j] = dn[j];
+            }
         }
+        load_affine<T, V>(p, on, c, a, b);
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-            xr[j] = xn[j];
-            dr[j] = dn[j];
+        for (int k = 0; k < V; ++k) {
+            sd[k] *= st.y;
+            dw[k] = RANGES ? dw[k] + sd[k] : sd[k];
+            db[k] = RANGES ? db[k] + sz[k] : sz[k];
+            s1 = fmaf(a[k], sz[k], s1);
+            s2 = fmaf(a[k], sd[k], s2);
         }
-    }
-    load_affine<T, V>(p, on, c, a, b);
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        sd[k] *= st.y;
-        s1 = fmaf(a[k], sz[k], s1);
-        s2 = fmaf(a[k], sd[k], s2);
-    }
-    group_sums<V>(p, s, tid, s1, s2, mine, out);
-    for (int g = tid; g < s.groups; g += blockDim.x) p.chunk[(at + g) * (p.chunks * p.parts) + s.chunk * p.parts + s.part] = out[g];
+        group_sums<V>(p, s, tid, s1, s2, mine, out);
+        // `out` is written next behind the barrier that the next sample's pairs wait at.
+        for (int g = tid; g < s.groups; g += blockDim.x) p.chunk[(at + g) * (p.chunks * p.parts) + s.chunk * p.parts + s.part] = out[g];
+    } while (RANGES && ++n < past);
     float *const o = p.part + (s.n * p.chunks + s.chunk) * 2 * p.C + s.c0;
-    column_sums<V>(p, s, tid, r0, col, sd, cells, o);
-    column_sums<V>(p, s, tid, r0, col, sz, cells, o + p.C);
+    column_sums<V>(p, s, tid, r0, col, dw, cells, o);
+    column_sums<V>(p, s, tid, r0, col, db, cells, o + p.C);
 }
 
 template <typename T, int V>
@@ -901,6 +911,11 @@ GroupNormPlan gn_plan(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, boo
     const int64_t bundles = ceil_div(G, g.kg) * g.parts, want = std::max<int64_t>(1, 512 / std::max<int64_t>(1, N * bundles));
     g.chunk_rows = (int32_t)(tile * ceil_div(tiles, want));
     g.chunks = (int32_t)ceil_div(std::max<int64_t>(P, 1), g.chunk_rows);
+    // Partial sums of dw and db: up to 2 kPartRows rows a sample each, beyond that ranges of samples of 64 positions
+    // in all, whose row of sums is a sixteenth of their x in 16 bits.  16384 rows of 16384 channels in one group in
+    // fp32: 4080 us and 2.1 GB of sums with a row a sample, 2040 us and 0.13 GB; 2050 x 3000 x 64 in bf16 786 us,
+    // in ranges of two samples 825.
+    if (backward && g.chunks == 1) g.range = std::max<int64_t>(1, std::min(N / kPartRows, ceil_div(64, std::max<int64_t>(P, 1))));
     return g;
 }
 
@@ -915,7 +930,8 @@ bool gn_fits(const GroupNormArgs &a, const GroupNormPlan &g)
     const int64_t es = a.dtype == DT_F32 ? 4 : 2, top = ((int64_t(1) << 31) - 1) / es / 2, R = g.threads / g.cols;
     for (int64_t st : {a.P > 1 ? a.xst : 0, a.P > 1 ? a.dst : 0, a.C})
         if (st > top / R) return false;
-    return grid_fits(8 * ceil_div(ceil_div(a.N, g.range) * g.chunks * ceil_div(a.G, g.kg) * g.parts, 8), g.threads);
+    const int64_t samples = g.whole ? ceil_div(a.N, g.range) : a.N;      // (of the launch that has most workgroups)
+    return grid_fits(8 * ceil_div(samples * g.chunks * ceil_div(a.G, g.kg) * g.parts, 8), g.threads);
 }
 
 hipError_t launch_group_norm(const GroupNormArgs &a, const GroupNormPlan &g, const char **kname)
@@ -953,11 +969,16 @@ hipError_t launch_group_norm_bwd(const GroupNormArgs &a, const GroupNormPlan &g,
             });
         } else {
             err = launch_with(p, a, g, [&](auto t, auto v, dim3 grid) {
-                gn_chunk_sums<decltype(t), v.value><<<grid, g.threads, lds_bytes(g.threads, v.value), a.stream>>>(p);
+                const size_t bytes = lds_bytes(g.threads, v.value);
+                if (g.range > 1) gn_chunk_sums<decltype(t), v.value, true><<<grid, g.threads, bytes, a.stream>>>(p);
+                else gn_chunk_sums<decltype(t), v.value, false><<<grid, g.threads, bytes, a.stream>>>(p);
             });
+            Norm each = p;      // a workgroup for each sample's chunk
+            each.range = 1;
+            each.blocks = a.N * g.chunks * p.bundles;
             if (err == hipSuccess)
-                err = launch_with(p, a, g, [&](auto t, auto v, dim3 grid) {
-                    gn_chunk_slopes<decltype(t), v.value><<<grid, g.threads, lds_bytes(g.threads, 0), a.stream>>>(p);
+                err = launch_with(each, a, g, [&](auto t, auto v, dim3 grid) {
+                    gn_chunk_slopes<decltype(t), v.value><<<grid, g.threads, lds_bytes(g.threads, 0), a.stream>>>(each);
                 });
         }
         if (err != hipSuccess) return err;

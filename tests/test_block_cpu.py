@@ -170,3 +170,13 @@ def test_gated_recurrence_backward_channels():
     for C in (2 ** 26 - 15, 2 ** 26 - 1):
         for shape in ((1, 1, C), (0, 1, C), (1, 0, C)):
             assert rec_bwd(shape) == UNSUPPORTED, shape
+
+
+def test_group_norm_workspace_beside_its_tensors():
+    """Gradients of groups wider than a workgroup: 8 bytes a part of a group and sample, and partial sums of dw and
+    db in up to 2048 rows or a sixteenth of x in 16 bits."""
+    w = gc.group_norm_workspace
+    for dtype in (torch.float32, torch.bfloat16):
+        for P, C in ((1, 16384), (3, 1031), (20, 20000), (100, 16384)):
+            for N in (2000, 16384, 1000000):
+                assert w((N, P, C, 1), dtype, True) <= 8 * C * max(2048, N * P // 64 + 1) + 8 * N * 32 + 512, (N, P, C)

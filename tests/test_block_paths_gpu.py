@@ -32,6 +32,8 @@ GN = [  # N, P, C, G, silu, bias, lengths, layout
     (1500, 3, 1031, 1, True, False, [k % 4 for k in range(1500)], "swapped"),
     (1300, 2, 2062, 2, True, True, [2 - k % 3 for k in range(1300)], "plain"),
     (1, 1, 8192, 1, True, True, None, "plain"),
+    (3100, 2, 1031, 1, True, True, [k % 3 for k in range(3100)], "wide"),         # ranges of samples, empty ones in them
+    (4103, 1, 1033, 1, True, False, [k % 5 // 4 for k in range(4103)], "plain"),
 ]
 I8 = [  # M, N, K: stages past the first ring, with rests of K, rows and channels
     (3790, 3810, 1296),      # 225 tiles of 256

@@ -16,6 +16,7 @@ CASES = [  # N, P, C, G, lengths
     (2, 20001, 32, 4, [20001, 0]),                      # chunks of positions
     (3, 20001, 32, 4, [0, 9, 20001]),                   # chunks behind a sample's end
     (3, 5, 1031, 1, [5, 0, 2]),                         # a group wider than a workgroup
+    (3100, 2, 1031, 1, [k % 3 for k in range(3100)]),   # samples one after the other
     (4, 700, 16, 1, [0, 0, 0, 0]),                      # nothing at all
 ]
 
