@@ -81,6 +81,32 @@ def test_tokens_against_the_definition(B, C, slots, dt):
     assert torch.equal(pool[untouched], was[untouched])
 
 
+def test_most_channels_of_a_gradient():
+    """One token of 2^26 - 16 channels, the most that the sum of log_decay's shares takes: every channel's gradients
+    are the same closed form (r = i = 0, log_decay = -1/2: a = exp(-1/4))."""
+    C = 2 ** 26 - 16
+    x, r = torch.ones(1, 1, C, device="cuda").bfloat16(), torch.zeros(1, 1, C, device="cuda").bfloat16()
+    g = torch.full((C,), -0.5, device="cuda")
+    s0 = torch.full((1, C), 3.0, device="cuda")
+    # (of one token only the first state is read, not h)
+    dx, dr, di, dg, ds = gc.gated_recurrence_backward(x, r, r, g, x, x, initial_state=s0)
+    a = torch.tensor(-0.25, dtype=torch.float64).exp()
+    s = (-torch.expm1(torch.tensor(-0.5, dtype=torch.float64))).sqrt()
+    dla = a * 3 - a * a / s * 0.5
+    half = rec.half_step(torch.bfloat16)
+    # A few fp32 roundings (at most 40 u of the terms, which cancel to no less than half), and bf16's own.
+    for name, got, want, off in (("dx", dx, s / 2, half), ("dr", dr, dla * -0.5 / 4, half), ("di", di, s / 4, half),
+                                 ("dlog_decay", dg, dla / 2, 0), ("dinitial", ds, a, 0)):
+        lo, hi = float(got.min()), float(got.max())
+        assert lo == hi and abs(lo - float(want)) <= (off + 80 * U) * abs(float(want)), (name, lo, hi, float(want))
+    with pytest.raises(gc.GconvError):
+        one = torch.zeros(1, 1, C + 1, device="cuda").bfloat16()
+        gc.gated_recurrence_backward(one, one, one, torch.zeros(C + 1, device="cuda"), one, one)
+    del x, r, g, s0, dx, dr, di, dg, ds, got, one
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("case", GN, ids=lambda c: "x".join(map(str, c[:4])))
 def test_groups_wider_than_a_workgroup(case, dt):
