@@ -94,7 +94,7 @@ struct QuantizeArgs {
     int dtype;
     hipStream_t stream;
 };
-bool quantize_fits(int64_t M, int64_t K, int dtype);
+bool quantize_fits(int64_t M);
 hipError_t launch_quantize(const QuantizeArgs &a, const char **kname);
 
 // y = (q w^T) qs ws + bias

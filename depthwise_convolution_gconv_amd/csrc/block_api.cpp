@@ -335,7 +335,7 @@ gconv_status_t gconv_quantize_int8(const void *x, int8_t *q, float *scales, int6
         {"x", x, extent(rows, x_stride, 1, 0, 1, 0, K, elem(dtype)), false},
     };
     if ((st = check_ranges(ranges, sizeof(ranges) / sizeof(ranges[0]))) != GCONV_OK) return st;
-    if (!gconv::quantize_fits(rows, K, (int)dtype))
+    if (!gconv::quantize_fits(rows))
         return fail(GCONV_ERR_UNSUPPORTED, "int8 rows: the call needs more threads than a launch takes");
     const gconv::QuantizeArgs a = {x, q, scales, rows, K, x_stride, (int)dtype, (hipStream_t)hip_stream};
     const char *kname = "";

@@ -16,7 +16,7 @@
 // exponentials, two reciprocals, a root) and about 30 others for the 8 bytes of an element.  In bf16
 // 8 x 4096 x 4096 takes 224 us (1.07 GB, 4.8 TB/s), 1 x 32768 x 4096, where stripes of 32 bytes fill the
 // card, 385 - 420; gradients of 4 x 4096 x 2560 take 191 us: 48 for the segments' maps, 139 for the walk
-// (0.67 GB, 4.8 TB/s, 188 registers, two waves a SIMD) and 5 for the sum of log_decay's shares.  Tokens of
+// (0.67 GB, 4.8 TB/s, 200 registers, two waves a SIMD) and 5 for the sum of log_decay's shares.  Tokens of
 // 64 x 4096 take 3 us in gated_step.
 //
 // One pass with a workgroup waiting for its predecessor's state would save the cut's second read; it took
@@ -841,9 +841,11 @@ GatedPlan short_plan(int64_t B, int64_t T, int64_t C, int dtype, bool backward)
 // lane: rows of 256, 128, 64 and 32 bytes took 225, 281, 323 and 364 us for 8 x 4096 x 4096 in bf16
 // (factors 1, 1.25, 1.43 and 1.62), since neighbours that share lines are not in step.  A cut reads three of
 // four tensors twice (1.65, and a launch worth 6500 lane-tokens; gradients two of eight, 1.17 and 5000).  With
-// the stripes that this picks, and cut, in bf16: 1 x 4096 x 4096 42 and 63 us, 2 x 8192 x 4096 149 and 214,
-// 6 x 1021 x 1350 24 and 43, 1 x 32768 x 4096 394 and 397, 1 x 32768 x 2048 372 and 217; gradients of 4 x 4096
-// x 2560 335 and 206, of 8 x 1024 x 512 29 and 36.
+// narrow stripes uncut, and cut, in bf16: 1 x 4096 x 4096 40 and 54 us, 2 x 8192 x 4096 151 and 190, 6 x 1021 x 1350
+// 24 and 43, 1 x 32768 x 4096 397 and 382, 1 x 32768 x 2048 367 and 203; gradients of 4 x 4096 x 2560 334 and 192,
+// of 8 x 1024 x 512 28 both.  The costs were fitted when a cut's fold was dearer, and are off by up to a quarter
+// where both sides are near: 1 x 32768 x 4096 stays uncut (397), 6 x 5545 x 1024 and 5 x 2360 x 64 are cut (100 and
+// 25 us; uncut 89 and 21).
 GatedPlan gated_plan(int64_t B, int64_t T, int64_t C, int dtype, bool backward)
 {
     GatedPlan g = {32, backward ? 4 : 8, 1, std::max<int64_t>(T, 1)};

@@ -11,7 +11,8 @@
 //
 // Statistics: a thread's sum, and its squares about its own mean; joined exactly,
 //     M2 = sum over threads of M2_t + n_t (mean_t - mean)^2,
-// so an offset much larger than the spread costs nothing.  The order of addition is fixed.
+// so an offset much larger than the spread does not cancel in the variance: it enters only by the square of
+// a mean's rounding (a mean is off by a few 2^-24 of the offset).  The order of addition is fixed.
 //
 // Gradients: with xhat = (x - mean) rstd, dz = dy act'(w xhat + b), m = positions times channels,
 //     dx = rstd (w dz - S1 / m - xhat S2 / m),  S1 = sum of w dz,  S2 = sum of w dz xhat,
@@ -559,6 +560,10 @@ __device__ __forceinline__ float2 group_stats(const Norm &p, int64_t at, int liv
 }
 
 // Whole samples in registers: a range of them, their dw and db added up on the way.
+//
+// With more than four vectors of 16 bytes a thread the sample's x and dy do not fit the 128 registers of a
+// workgroup of 1024 threads: 136 (fp32) to 176 bytes a lane go to scratch memory, and 64 x 784 x 2048 in fp16
+// takes 296 us for the 94 of its bytes.  Eight 16-bit channels in up to four vectors keep 12 bytes there.
 template <typename T, int V, int K>
 __global__ __launch_bounds__(kMaxThreads) void gn_backward(const Norm p)
 {
@@ -652,7 +657,8 @@ __global__ __launch_bounds__(kMaxThreads) void gn_backward(const Norm p)
 }
 
 // Chunks: S1, S2 and the partial dw, db first, then dx.  RANGES: a chunk is a whole sample, and a workgroup takes
-// a range of samples one after the other, so that they share a row of partial sums.
+// a range of samples one after the other, so that they share a row of partial sums (16-bit vectors of 8 channels
+// then keep some 36 bytes a lane in scratch memory).
 template <typename T, int V, bool RANGES>
 __global__ __launch_bounds__(kMaxThreads) void gn_chunk_sums(const Norm p)
 {
@@ -913,7 +919,7 @@ GroupNormPlan gn_plan(int64_t N, int64_t P, int64_t C, int64_t G, int dtype, boo
     g.chunks = (int32_t)ceil_div(std::max<int64_t>(P, 1), g.chunk_rows);
     // Partial sums of dw and db: up to 2 kPartRows rows a sample each, beyond that ranges of samples of 64 positions
     // in all, whose row of sums is a sixteenth of their x in 16 bits.  16384 rows of 16384 channels in one group in
-    // fp32: 4080 us and 2.1 GB of sums with a row a sample, 2040 us and 0.13 GB; 2050 x 3000 x 64 in bf16 786 us,
+    // fp32: 4080 us and 2.1 GB of sums with a row a sample, 2050 us and 0.13 GB; 2050 x 3000 x 64 in bf16 786 us,
     // in ranges of two samples 825.
     if (backward && g.chunks == 1) g.range = std::max<int64_t>(1, std::min(N / kPartRows, ceil_div(64, std::max<int64_t>(P, 1))));
     return g;

@@ -211,7 +211,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM * BN > 128 * 128 ? 1 : 2) void mm_
                                                          in ? (uint32_t)((r + lrow) * p.K + k) : kNowhere, k0, 0, 0);
             }
         } else {
-auto piece16 = [&](const int8_t *row) {
+            auto piece16 = [&](const int8_t *row) {
                 return k0 + kStage <= p.K ? __builtin_bit_cast(uint4, *reinterpret_cast<const any16 *>(row + k0 + k))
                        : k0 < p.K         ? load16(row, k0 + k, p.K)
                                           : make_uint4(0, 0, 0, 0);
@@ -431,7 +431,7 @@ template <typename F> hipError_t with_type(int dtype, F &&f)
 
 }  // namespace
 
-bool quantize_fits(int64_t M, int64_t K, int dtype) { return grid_fits(M, 256); }
+bool quantize_fits(int64_t M) { return grid_fits(M, 256); }
 
 hipError_t launch_quantize(const QuantizeArgs &a, const char **kname)
 {
